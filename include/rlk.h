@@ -493,6 +493,117 @@ rlk_status rlk_selftest_wait_timeout_pair(const void *hidden_bf16, const void *w
                                           const int32_t *targets_i32, rlk_partial *partials,
                                           int mode, rlk_stream_t stream);
 
+/* Element types of the entry points below that take more than one. */
+typedef enum rlk_dtype { RLK_BF16 = 0, RLK_FP16 = 1, RLK_FP32 = 2 } rlk_dtype;
+
+/* Most alternatives rlk_token_logprobs gives per row. */
+#define RLK_MAX_TOP_K 32
+
+/*
+ * Log probabilities of given tokens from LOGITS that the caller holds (of any
+ * head: its own product, a gathered tensor-parallel one, rlk_linear_w4), with
+ * the entropy and the top alternatives.  Per row, with z = logit * inv_temp over
+ * the row's tokens (those the mask allows whose logit is above -inf):
+ *   lse = log sum exp z          logp = z[target] - lse
+ *   entropy = -sum p log p, p = exp(z - lse)
+ *   top: the top_k tokens with the largest logits, larger first, the lower index
+ *        first among equal logits, each with its log probability
+ * Special rows: a token that is masked or at -inf has probability 0 and is never
+ * an alternative; places left over hold id -1 and logp -inf.  A target that is
+ * such a token has logp -inf.  A row without tokens has lse -inf, entropy 0 and
+ * logp -inf.  A target outside [0, V) has logp 0.0f, and one >= V is counted as by
+ * rlk_logprob.  A NaN or +inf logit that is not masked makes its row's floats NaN
+ * (its alternatives are those of the tokens that are not NaN).
+ *   logits      device, [T][V] of `dtype` (rlk_dtype), row t at element t * row_stride
+ *               (row_stride >= V; not read for T == 1), aligned to its element
+ *   targets_i32 device, [T]
+ *   allowed_u32 device, NULL (every token) or [T][>= ceil(V/32)] words, row t at
+ *               word t * allowed_stride: token v is allowed if bit v % 32 of word
+ *               v / 32 is set
+ *   T >= 0 (0: nothing is done), 1 <= V <= 2^31 - 1, inv_temp finite and > 0,
+ *   0 <= top_k <= RLK_MAX_TOP_K (may exceed V)
+ *   out_logp_f32, out_lse_f32, out_entropy_f32   device, [T]
+ *   out_top_ids_i32, out_top_logp_f32            device, [T][top_k] (NULL for 0)
+ * Asynchronous on `stream`; allocates nothing.  Sums are held in fp32 in an order
+ * fixed by V alone: a row's bits depend on that row, its mask and target, V and
+ * inv_temp only, as for rlk_logprob.
+ */
+rlk_status rlk_token_logprobs(const void *logits, int dtype, int64_t row_stride,
+                              const int32_t *targets_i32, const uint32_t *allowed_u32,
+                              int64_t allowed_stride, int64_t T, int64_t V, float inv_temp,
+                              int top_k, float *out_logp_f32, float *out_lse_f32,
+                              float *out_entropy_f32, int32_t *out_top_ids_i32,
+                              float *out_top_logp_f32, rlk_stream_t stream);
+
+/*
+ * The gradient of rlk_token_logprobs' outputs with respect to the logits.  With
+ * p = exp(z - lse) and G = grad_logp + sum_j grad_top[j]:
+ *   grad[v] = inv_temp * ( p[v] (grad_lse - G - grad_entropy (z[v] - lse + entropy))
+ *                          + [v == target] grad_logp + sum_j [v == top_ids[j]] grad_top[j] )
+ * computed in fp32 and rounded once; 0 for masked tokens and tokens at -inf, and in
+ * rows without tokens.  The grad_logp of a row whose target lies outside [0, V) and
+ * the grad_top of an id outside [0, V) count as 0.  Rows whose lse is NaN give NaN.
+ *   logits, targets_i32, allowed_u32, T, V, inv_temp: as given to rlk_token_logprobs
+ *   lse_f32                           device, [T]: its output
+ *   entropy_f32                       device, [T]: its output (NULL without grad_entropy_f32)
+ *   grad_logp_f32, grad_lse_f32, grad_entropy_f32   device, [T], each may be NULL (0)
+ *   top_ids_i32, grad_top_f32         device, [T][top_k]: its ids and the gradient of
+ *                                     its top_logp (NULL for top_k == 0)
+ *   out_grad                          device, [T][V] of `dtype`, row t at element
+ *                                     t * grad_stride (>= V); may be `logits` itself
+ *                                     with the same stride
+ * Asynchronous on `stream`; allocates nothing.
+ */
+rlk_status rlk_token_logprobs_backward(const void *logits, int dtype, int64_t row_stride,
+                                       const int32_t *targets_i32, const uint32_t *allowed_u32,
+                                       int64_t allowed_stride, int64_t T, int64_t V,
+                                       float inv_temp, const float *lse_f32,
+                                       const float *entropy_f32, const float *grad_logp_f32,
+                                       const float *grad_lse_f32, const float *grad_entropy_f32,
+                                       const int32_t *top_ids_i32, const float *grad_top_f32,
+                                       int top_k, void *out_grad, int64_t grad_stride,
+                                       rlk_stream_t stream);
+
+/*
+ * Weights in 4 bits with group scales.  W [N][K] (K % 32 == 0) is cut along K into
+ * G = ceil(K / group) groups of `group` (32, 64 or 128) elements, the last one short
+ * where group does not divide K.  Element (n, k) of group g stands for
+ *   scales[n][g] * (q - zeros[n][g]),   q in 0..15
+ * (zeros NULL: every zero point is 8).
+ *   codes_u32  [N][K/8]: word w of a row holds k = 8w .. 8w+7, the even k in nibbles
+ *              0..3 (from the lowest bits), the odd k in nibbles 4..7
+ *   scales     [N][G] of `dtype` (RLK_BF16 or RLK_FP16)
+ *   zeros_u8   [N][G], 0..15
+ * rlk_quantize_w4 makes them from W of the same `dtype` (finite values):
+ *   zeros NULL:  s = max|w| / 7 rounded to dtype, q = clamp(rint(w / s), -7, 7) + 8
+ *   else:        lo = min(0, min w), hi = max(0, max w), s = (hi - lo) / 15 rounded to
+ *                dtype, zero = clamp(rint(-lo / s), 0, 15), q = clamp(rint(w/s) + zero, 0, 15)
+ * (fp32 arithmetic, rint to even, the rounded s; s = 1 where it would be 0).
+ * rlk_dequantize_w4 writes the values it stands for, as `dtype` or RLK_FP32
+ * (`out_dtype`).  W, codes and scales 16-byte aligned; N >= 0, N * K <= 2^40.
+ * Asynchronous on `stream`; allocate nothing.
+ */
+rlk_status rlk_quantize_w4(const void *W, int dtype, int64_t N, int64_t K, int group,
+                           uint32_t *codes_u32, void *scales, uint8_t *zeros_u8,
+                           rlk_stream_t stream);
+rlk_status rlk_dequantize_w4(const uint32_t *codes_u32, const void *scales,
+                             const uint8_t *zeros_u8, int dtype, int64_t N, int64_t K, int group,
+                             void *out_W, int out_dtype, rlk_stream_t stream);
+
+/*
+ * y [T][N] = x [T][K] . W^T for such a weight: a decode step's LM head or projection.
+ *   y[t][n] = sum_g scales[n][g] * sum_{k in g} (q[n][k] - zeros[n][g]) x[t][k]
+ * with fp32 accumulation (each group's products of a 16-bit x and a small whole number
+ * are exact; a scale is applied once per group, in fp32) and one rounding to out_dtype
+ * (`dtype` or RLK_FP32).  x, scales of `dtype` (RLK_BF16 or RLK_FP16), x and codes
+ * 16-byte aligned, y aligned to its element.  T >= 0, N >= 0.  Asynchronous on
+ * `stream`; allocates nothing.  The order of the sums is fixed by N, K and group: a
+ * row's bits depend on that row of x and the weight only, never on T.
+ */
+rlk_status rlk_linear_w4(const void *x, int dtype, const uint32_t *codes_u32, const void *scales,
+                         const uint8_t *zeros_u8, int64_t T, int64_t N, int64_t K, int group,
+                         void *out_y, int out_dtype, rlk_stream_t stream);
+
 /* Release the library's cached workspaces on every device it used (waits for
  * them to be idle).  Safe to call more than once. */
 rlk_status rlk_shutdown(void);

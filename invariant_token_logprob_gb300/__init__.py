@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional
+from typing import NamedTuple, Optional
 
 __all__ = ["RlkError", "lib", "logprob", "logprob_ws", "logprob_partials", "lse_merge",
            "consistency_stats", "workspace_size", "check_device_error", "take_device_errors", "vocab_tile", "row_tile",
@@ -24,6 +24,9 @@ __all__ = ["RlkError", "lib", "logprob", "logprob_ws", "logprob_partials", "lse_
            "quantize_fp8_weight", "unpack_fp8_weight", "quantize_fp8_row_blocks",
            "quantize_fp8_weight_blocks", "logprob_fp8_block", "fp8_block_workspace_size", "consistency_stats_async",
            "stats_workspace_size", "stats_dict",
+           "TokenLogprobs", "token_logprobs", "token_logprobs_backward",
+           "differentiable_token_logprobs", "MAX_TOP_K",
+           "quantize_w4", "dequantize_w4", "pack_w4", "unpack_w4", "linear_w4", "logprob_w4",
            "header_functions", "STAT_NAMES", "LIB_PATH", "HEADER_PATH"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -128,6 +131,20 @@ def lib() -> ctypes.CDLL:
         L.rlk_logprob_backward.restype = st
         L.rlk_logprob_backward.argtypes = [P, P, P, P, P, i64, i64, i64, f32, P, P, ctypes.c_int,
                                            P, sz, P]
+        L.rlk_token_logprobs.restype = st
+        L.rlk_token_logprobs.argtypes = [P, ctypes.c_int, i64, P, P, i64, i64, i64, f32,
+                                         ctypes.c_int, P, P, P, P, P, P]
+        L.rlk_token_logprobs_backward.restype = st
+        L.rlk_token_logprobs_backward.argtypes = [P, ctypes.c_int, i64, P, P, i64, i64, i64, f32,
+                                                  P, P, P, P, P, P, P, ctypes.c_int, P, i64, P]
+        L.rlk_quantize_w4.restype = st
+        L.rlk_quantize_w4.argtypes = [P, ctypes.c_int, i64, i64, ctypes.c_int, P, P, P, P]
+        L.rlk_dequantize_w4.restype = st
+        L.rlk_dequantize_w4.argtypes = [P, P, P, ctypes.c_int, i64, i64, ctypes.c_int, P,
+                                        ctypes.c_int, P]
+        L.rlk_linear_w4.restype = st
+        L.rlk_linear_w4.argtypes = [P, ctypes.c_int, P, P, P, i64, i64, i64, ctypes.c_int, P,
+                                    ctypes.c_int, P]
         _lib = L
     return _lib
 
@@ -604,3 +621,320 @@ def logprob_fp8_block(h, W_packed, W_scales, targets, V: int, inv_temp: float = 
                                        _ptr(am), _ptr(workspace), workspace.numel(),
                                        _stream(stream)), "rlk_logprob_fp8_block")
     return lp, lse, am
+
+
+# ---------------------------------------------------------------- from logits
+MAX_TOP_K = 32
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs: f32 [T] logp, lse, entropy; the alternatives' ids
+    (i32 [T, top_k], -1 where a row has no more tokens) and log probabilities
+    (f32 [T, top_k])."""
+    logp: object
+    lse: object
+    entropy: object
+    top_ids: object
+    top_logp: object
+
+
+def _dtype_code(dtype):
+    """rlk_dtype of a torch dtype (None for any other)."""
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+
+
+def _rows(t, name, codes=(0, 1, 2)):
+    """A CUDA matrix whose rows are dense but may lie further apart than their length:
+    (rlk_dtype, row stride in elements)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if _dtype_code(t.dtype) not in codes:
+        raise TypeError(f"{name} must be bfloat16, float16{' or float32' if 2 in codes else ''}, "
+                        f"got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims")
+    _need(t[:0].contiguous(), t.dtype, name)  # the device checks
+    dense = t.shape[1] <= 1 or t.stride(1) == 1
+    if not dense or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have dense rows that do not overlap")
+    return _dtype_code(t.dtype), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _logits_args(logits, targets, allowed):
+    """Checked (rlk_dtype, row stride, allowed pointer, allowed stride, T, V)."""
+    import torch
+    code, stride = _rows(logits, "logits")
+    _need(targets, torch.int32, "targets", 1)
+    T, V = logits.shape
+    if targets.shape[0] != T:
+        raise ValueError("shape mismatch: logits [T, V], targets [T]")
+    if allowed is None:
+        return code, stride, None, 0, T, V
+    _need(allowed, torch.int32, "allowed", 2)
+    if allowed.shape[0] != T or allowed.shape[1] < (V + 31) // 32:
+        raise ValueError("allowed must be [T, ceil(V/32)] words of allowed-token bits")
+    return code, stride, _ptr(allowed), allowed.shape[1], T, V
+
+
+def token_logprobs(logits, targets, top_k: int = 0, allowed=None, inv_temp: float = 1.0, out=None,
+                   stream=None):
+    """rlk_token_logprobs: TokenLogprobs(logp, lse, entropy, top_ids, top_logp) of bf16,
+    fp16 or fp32 logits [T, V] (dense rows, any row stride), as a tuple of tensors.
+
+    targets i32 [T] (negative: an ignored row, logp 0); allowed: None or i32
+    [T, ceil(V/32)] words of allowed-token bits (bit v % 32 of word v / 32); top_k up to
+    MAX_TOP_K alternatives, the largest logits first, the lower index first among equals.
+    Pass out=(logp, lse, entropy, top_ids, top_logp) to reuse tensors (the last two may
+    be None for top_k = 0)."""
+    import torch
+    code, stride, bits, bits_stride, T, V = _logits_args(logits, targets, allowed)
+    dev, top_k = logits.device, int(top_k)
+    if not 0 <= top_k <= MAX_TOP_K:
+        raise ValueError(f"top_k must lie in 0..{MAX_TOP_K}")
+    if out is None:
+        f = torch.empty((3, T), dtype=torch.float32, device=dev)
+        lp, lse, ent = f[0], f[1], f[2]
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    else:
+        lp, lse, ent, ids, top = out
+        for name, t in (("logp", lp), ("lse", lse), ("entropy", ent)):
+            _need(t, torch.float32, name, 1)
+            if t.shape[0] != T:
+                raise ValueError(f"{name} must be [T]")
+        if top_k:
+            _need(ids, torch.int32, "top_ids", 2)
+            _need(top, torch.float32, "top_logp", 2)
+            if ids.shape != (T, top_k) or top.shape != (T, top_k):
+                raise ValueError("top_ids and top_logp must be [T, top_k]")
+    _check(lib().rlk_token_logprobs(
+        _ptr(logits), code, stride, _ptr(targets), bits, bits_stride, T, V,
+        ctypes.c_float(inv_temp), top_k, _ptr(lp), _ptr(lse), _ptr(ent),
+        _ptr(ids) if top_k else None, _ptr(top) if top_k else None, _stream(stream)),
+        "rlk_token_logprobs")
+    return TokenLogprobs(lp, lse, ent, ids, top)
+
+
+def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, grad_lse=None,
+                            grad_entropy=None, top_ids=None, grad_top=None, allowed=None,
+                            inv_temp: float = 1.0, out=None, stream=None):
+    """rlk_token_logprobs_backward: the gradient with respect to the logits ([T, V] of
+    their type) from those of token_logprobs' outputs (f32, each may be None).  lse and
+    entropy are its outputs (entropy is needed with grad_entropy), top_ids its ids (needed
+    with grad_top).  out may be a tensor to fill, `logits` itself included."""
+    import torch
+    code, stride, bits, bits_stride, T, V = _logits_args(logits, targets, allowed)
+    _need(lse, torch.float32, "lse", 1)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logp", grad_logp),
+                    ("grad_lse", grad_lse), ("grad_entropy", grad_entropy)):
+        if t is not None:
+            _need(t, torch.float32, name, 1)
+            if t.shape[0] != T:
+                raise ValueError(f"{name} must be [T]")
+    top_k = 0
+    if grad_top is not None:
+        if top_ids is None:
+            raise ValueError("grad_top needs top_ids")
+        _need(top_ids, torch.int32, "top_ids", 2)
+        _need(grad_top, torch.float32, "grad_top", 2)
+        top_k = grad_top.shape[1]
+        if grad_top.shape[0] != T or top_ids.shape != grad_top.shape or top_k > MAX_TOP_K:
+            raise ValueError(f"top_ids and grad_top must be [T, top_k], top_k <= {MAX_TOP_K}")
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    out_code, out_stride = _rows(out, "out")
+    if out_code != code or out.shape != logits.shape:
+        raise ValueError("out must have the logits' shape and type")
+
+    def opt(t):
+        return None if t is None else _ptr(t)
+    _check(lib().rlk_token_logprobs_backward(
+        _ptr(logits), code, stride, _ptr(targets), bits, bits_stride, T, V,
+        ctypes.c_float(inv_temp), _ptr(lse), opt(entropy), opt(grad_logp), opt(grad_lse),
+        opt(grad_entropy), opt(top_ids) if top_k else None, opt(grad_top) if top_k else None, top_k,
+        _ptr(out), out_stride, _stream(stream)), "rlk_token_logprobs_backward")
+    return out
+
+
+def _token_logprobs_function():
+    import torch
+
+    class TokenLogprobsFunction(torch.autograd.Function):
+        """rlk_token_logprobs with rlk_token_logprobs_backward as its gradient."""
+
+        @staticmethod
+        def forward(ctx, logits, targets, top_k, allowed, inv_temp):
+            r = token_logprobs(logits, targets, top_k, allowed, inv_temp)
+            ctx.save_for_backward(logits, targets, r.lse, r.entropy, r.top_ids, allowed)
+            ctx.inv_temp = inv_temp
+            ctx.mark_non_differentiable(r.top_ids)
+            ctx.set_materialize_grads(False)
+            return tuple(r)
+
+        @staticmethod
+        def backward(ctx, g_logp, g_lse, g_entropy, _, g_top):
+            logits, targets, lse, entropy, ids, allowed = ctx.saved_tensors
+
+            def dense(g):
+                return None if g is None else g.contiguous().float()
+            if g_logp is None and g_lse is None and g_entropy is None and g_top is None:
+                return None, None, None, None, None
+            if g_top is not None and g_top.shape[1] == 0:
+                g_top = None
+            return (token_logprobs_backward(logits, targets, lse, entropy, dense(g_logp),
+                                            dense(g_lse), dense(g_entropy),
+                                            None if g_top is None else ids, dense(g_top), allowed,
+                                            ctx.inv_temp), None, None, None, None)
+
+    return TokenLogprobsFunction
+
+
+_TokenLogprobsFunction = None
+
+
+def differentiable_token_logprobs(logits, targets, top_k: int = 0, allowed=None,
+                                  inv_temp: float = 1.0):
+    """token_logprobs under torch autograd: logp, lse, entropy and top_logp carry
+    gradients to the logits (top_ids does not)."""
+    global _TokenLogprobsFunction
+    if _TokenLogprobsFunction is None:
+        _TokenLogprobsFunction = _token_logprobs_function()
+    return TokenLogprobs(*_TokenLogprobsFunction.apply(logits, targets, top_k, allowed, inv_temp))
+
+
+# ---------------------------------------------------------------- 4-bit weights
+# nibble of code k % 8 in its word: the even k in nibbles 0..3, the odd k in 4..7
+_W4_NIBBLE = (0, 4, 1, 5, 2, 6, 3, 7)
+
+
+def pack_w4(q):
+    """Codes one to a byte (uint8 [N, K], 0..15, K % 32 == 0) as the i32 words [N, K/8] of
+    linear_w4, on q's device."""
+    import torch
+    if q.dtype != torch.uint8 or q.dim() != 2 or q.shape[1] % 32:
+        raise ValueError("q must be uint8 [N, K] with K a multiple of 32")
+    words = torch.zeros(q.shape[0], q.shape[1] // 8, dtype=torch.int32, device=q.device)
+    for j, nibble in enumerate(_W4_NIBBLE):
+        words |= q[:, j::8].to(torch.int32) << (4 * nibble)
+    return words
+
+
+def unpack_w4(codes):
+    """The inverse of pack_w4: uint8 [N, K] from i32 words [N, K/8]."""
+    import torch
+    q = torch.empty(codes.shape[0], codes.shape[1] * 8, dtype=torch.uint8, device=codes.device)
+    for j, nibble in enumerate(_W4_NIBBLE):
+        q[:, j::8] = ((codes >> (4 * nibble)) & 15).to(torch.uint8)
+    return q
+
+
+def _w4_args(codes, scales, zeros, group):
+    """Checked (rlk_dtype of the scales, N, K) of a 4-bit weight."""
+    import torch
+    _need(codes, torch.int32, "codes", 2)
+    code = _dtype_code(scales.dtype) if isinstance(scales, torch.Tensor) else None
+    if code not in (0, 1):
+        raise TypeError("scales must be a bfloat16 or float16 tensor")
+    _need(scales, scales.dtype, "scales", 2)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    N, K = codes.shape[0], codes.shape[1] * 8
+    G = (K + group - 1) // group
+    if scales.shape != (N, G):
+        raise ValueError("scales must be [N, ceil(K/group)]")
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", 2)
+        if zeros.shape != (N, G):
+            raise ValueError("zeros must be [N, ceil(K/group)]")
+    return code, N, K
+
+
+def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=None):
+    """rlk_quantize_w4: bf16 or fp16 W [N, K] (K % 32 == 0) -> (i32 codes [N, K/8], scales
+    [N, ceil(K/group)] of W's type, uint8 zero points of the same shape or None).  Pass
+    out=(codes, scales, zeros) to reuse tensors."""
+    import torch
+    if not isinstance(W, torch.Tensor) or _dtype_code(W.dtype) not in (0, 1):
+        raise TypeError("W must be a bfloat16 or float16 tensor")
+    _need(W, W.dtype, "W", 2)
+    N, K = W.shape
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    G = (K + group - 1) // group
+    if out is None:
+        codes = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
+        scales = torch.empty((N, G), dtype=W.dtype, device=W.device)
+        zeros = torch.empty((N, G), dtype=torch.uint8, device=W.device) if asymmetric else None
+    else:
+        codes, scales, zeros = out
+        if (zeros is not None) != bool(asymmetric):
+            raise ValueError("out must hold zero points for asymmetric quantisation, and only then")
+    code, N2, K2 = _w4_args(codes, scales, zeros, group)
+    if (N2, K2) != (N, K) or scales.dtype != W.dtype:
+        raise ValueError("out must hold codes [N, K/8] and scales of W's type")
+    _check(lib().rlk_quantize_w4(_ptr(W), code, N, K, group, _ptr(codes), _ptr(scales),
+                                 None if zeros is None else _ptr(zeros), _stream(stream)),
+           "rlk_quantize_w4")
+    return codes, scales, zeros
+
+
+def dequantize_w4(codes, scales, zeros=None, group: int = 128, out_dtype=None, out=None,
+                  stream=None):
+    """rlk_dequantize_w4: the values a 4-bit weight stands for, [N, K] as the scales' type
+    (default) or float32."""
+    import torch
+    code, N, K = _w4_args(codes, scales, zeros, group)
+    if out is None:
+        out = torch.empty((N, K), dtype=out_dtype or scales.dtype, device=codes.device)
+    out_code = _dtype_code(out.dtype)
+    if out_code not in (code, 2):
+        raise TypeError("out_dtype must be the scales' type or float32")
+    _need(out, out.dtype, "out", 2)
+    if out.shape != (N, K):
+        raise ValueError("out must be [N, K]")
+    _check(lib().rlk_dequantize_w4(_ptr(codes), _ptr(scales), None if zeros is None else _ptr(zeros),
+                                   code, N, K, group, _ptr(out), out_code, _stream(stream)),
+           "rlk_dequantize_w4")
+    return out
+
+
+def linear_w4(x, codes, scales, zeros=None, group: int = 128, out_dtype=None, out=None,
+              stream=None):
+    """rlk_linear_w4: y [T, N] = x [T, K] . W^T for a 4-bit weight; x has the scales' type,
+    y that type or float32 (out_dtype, default float32)."""
+    import torch
+    code, N, K = _w4_args(codes, scales, zeros, group)
+    _need(x, scales.dtype, "x", 2)
+    if x.shape[1] != K:
+        raise ValueError("shape mismatch: x [T, K], codes [N, K/8]")
+    T = x.shape[0]
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=x.device)
+    out_code = _dtype_code(out.dtype)
+    if out_code not in (code, 2):
+        raise TypeError("out_dtype must be the scales' type or float32")
+    _need(out, out.dtype, "out", 2)
+    if out.shape != (T, N):
+        raise ValueError("out must be [T, N]")
+    _check(lib().rlk_linear_w4(_ptr(x), code, _ptr(codes), _ptr(scales),
+                               None if zeros is None else _ptr(zeros), T, N, K, group, _ptr(out),
+                               out_code, _stream(stream)), "rlk_linear_w4")
+    return out
+
+
+def logprob_w4(h, codes, scales, targets, zeros=None, group: int = 128, top_k: int = 0,
+               allowed=None, inv_temp: float = 1.0, logits=None, out=None, stream=None):
+    """A decode step of a 4-bit LM head: linear_w4 into fp32 logits [T, V] (a buffer to
+    reuse may be given), then token_logprobs of them.  Returns its TokenLogprobs."""
+    import torch
+    if logits is not None:
+        _need(logits, torch.float32, "logits", 2)
+    logits = linear_w4(h, codes, scales, zeros, group, out=logits, out_dtype=torch.float32,
+                       stream=stream)
+    return token_logprobs(logits, targets, top_k, allowed, inv_temp, out=out, stream=stream)

@@ -755,6 +755,157 @@ rlk_status rlk_selftest_wait_timeout_pair(const void* hidden_bf16, const void* w
                                                        mode, sms, s));
 }
 
+namespace {
+
+using rlk::ElemType;
+
+int64_t elem_size(int dtype) { return dtype == RLK_FP32 ? 4 : 2; }
+bool aligned_to(const void* p, int64_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & uintptr_t(bytes - 1)) == 0;
+}
+
+// Checks shared by rlk_token_logprobs and its gradient (T >= 1 for the pointers).
+rlk_status check_logits_shape(int dtype, int64_t row_stride, int64_t T, int64_t V, float inv_temp,
+                              int top_k) {
+    if (dtype != RLK_BF16 && dtype != RLK_FP16 && dtype != RLK_FP32) return RLK_ERR_INVALID_ARG;
+    if (T < 0 || T > INT32_MAX || V < 1 || V > INT32_MAX) return RLK_ERR_INVALID_ARG;
+    if (!(inv_temp > 0.0f) || !isfinite(inv_temp)) return RLK_ERR_INVALID_ARG;
+    if (top_k < 0 || top_k > RLK_MAX_TOP_K) return RLK_ERR_INVALID_ARG;
+    if (T > 1 && (row_stride < V || row_stride > INT64_MAX / 8 / T)) return RLK_ERR_INVALID_ARG;
+    return RLK_OK;
+}
+
+rlk_status check_logits_operands(const void* logits, int dtype, const int32_t* targets,
+                                 const uint32_t* allowed, int64_t allowed_stride, int64_t T,
+                                 int64_t V) {
+    if (!logits || !targets) return RLK_ERR_INVALID_ARG;
+    if (allowed && T > 1 &&
+        (allowed_stride < (V + 31) / 32 || allowed_stride > INT64_MAX / 8 / T))
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned_to(logits, elem_size(dtype)) || !aligned4(targets) || !aligned4(allowed))
+        return RLK_ERR_ALIGNMENT;
+    return RLK_OK;
+}
+
+// Checks shared by the 4-bit weight entry points (pointers only where N >= 1).
+rlk_status check_w4(int dtype, int64_t N, int64_t K, int group, const void* codes,
+                    const void* scales) {
+    if (dtype != RLK_BF16 && dtype != RLK_FP16) return RLK_ERR_INVALID_ARG;
+    if (N < 0 || N > INT32_MAX || K < 1 || K > INT32_MAX) return RLK_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return RLK_ERR_INVALID_ARG;
+    if (K % 32 != 0) return RLK_ERR_ALIGNMENT;
+    if (N > (int64_t(1) << 40) / K) return RLK_ERR_INVALID_ARG;
+    if (N == 0) return RLK_OK;
+    if (!codes || !scales) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales)) return RLK_ERR_ALIGNMENT;
+    return RLK_OK;
+}
+
+}  // namespace
+
+rlk_status rlk_token_logprobs(const void* logits, int dtype, int64_t row_stride,
+                              const int32_t* targets_i32, const uint32_t* allowed_u32,
+                              int64_t allowed_stride, int64_t T, int64_t V, float inv_temp,
+                              int top_k, float* out_logp_f32, float* out_lse_f32,
+                              float* out_entropy_f32, int32_t* out_top_ids_i32,
+                              float* out_top_logp_f32, rlk_stream_t stream) {
+    rlk_status st = check_logits_shape(dtype, row_stride, T, V, inv_temp, top_k);
+    if (st != RLK_OK) return st;
+    if (T == 0) return RLK_OK;
+    st = check_logits_operands(logits, dtype, targets_i32, allowed_u32, allowed_stride, T, V);
+    if (st != RLK_OK) return st;
+    if (!out_logp_f32 || !out_lse_f32 || !out_entropy_f32) return RLK_ERR_INVALID_ARG;
+    if (top_k > 0 && (!out_top_ids_i32 || !out_top_logp_f32)) return RLK_ERR_INVALID_ARG;
+    if (!aligned4(out_logp_f32) || !aligned4(out_lse_f32) || !aligned4(out_entropy_f32) ||
+        !aligned4(out_top_ids_i32) || !aligned4(out_top_logp_f32))
+        return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_token_logprobs(
+        logits, ElemType(dtype), T == 1 ? V : row_stride, targets_i32, allowed_u32,
+        T == 1 ? 0 : allowed_stride, T, V, inv_temp, top_k, out_logp_f32, out_lse_f32,
+        out_entropy_f32, out_top_ids_i32, out_top_logp_f32, sms,
+        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rlk_status rlk_token_logprobs_backward(const void* logits, int dtype, int64_t row_stride,
+                                       const int32_t* targets_i32, const uint32_t* allowed_u32,
+                                       int64_t allowed_stride, int64_t T, int64_t V,
+                                       float inv_temp, const float* lse_f32,
+                                       const float* entropy_f32, const float* grad_logp_f32,
+                                       const float* grad_lse_f32, const float* grad_entropy_f32,
+                                       const int32_t* top_ids_i32, const float* grad_top_f32,
+                                       int top_k, void* out_grad, int64_t grad_stride,
+                                       rlk_stream_t stream) {
+    rlk_status st = check_logits_shape(dtype, row_stride, T, V, inv_temp, top_k);
+    if (st != RLK_OK) return st;
+    if (T > 1 && (grad_stride < V || grad_stride > INT64_MAX / 8 / T)) return RLK_ERR_INVALID_ARG;
+    if (T == 0) return RLK_OK;
+    st = check_logits_operands(logits, dtype, targets_i32, allowed_u32, allowed_stride, T, V);
+    if (st != RLK_OK) return st;
+    if (!lse_f32 || !out_grad || (grad_entropy_f32 && !entropy_f32)) return RLK_ERR_INVALID_ARG;
+    if (top_k > 0 && (!top_ids_i32 || !grad_top_f32)) return RLK_ERR_INVALID_ARG;
+    if (out_grad == logits && T > 1 && grad_stride != row_stride) return RLK_ERR_INVALID_ARG;
+    if (!aligned4(lse_f32) || !aligned4(entropy_f32) || !aligned4(grad_logp_f32) ||
+        !aligned4(grad_lse_f32) || !aligned4(grad_entropy_f32) || !aligned4(top_ids_i32) ||
+        !aligned4(grad_top_f32) || !aligned_to(out_grad, elem_size(dtype)))
+        return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_token_logprobs_backward(
+        logits, ElemType(dtype), T == 1 ? V : row_stride, targets_i32, allowed_u32,
+        T == 1 ? 0 : allowed_stride, T, V, inv_temp, lse_f32, entropy_f32, grad_logp_f32,
+        grad_lse_f32, grad_entropy_f32, top_ids_i32, grad_top_f32, top_k, out_grad,
+        T == 1 ? V : grad_stride, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rlk_status rlk_quantize_w4(const void* W, int dtype, int64_t N, int64_t K, int group,
+                           uint32_t* codes_u32, void* scales, uint8_t* zeros_u8,
+                           rlk_stream_t stream) {
+    rlk_status st = check_w4(dtype, N, K, group, codes_u32, scales);
+    if (st != RLK_OK) return st;
+    if (N == 0) return RLK_OK;
+    if (!W) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(W)) return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_quantize_w4(W, ElemType(dtype), N, K, group, codes_u32, scales,
+                                             zeros_u8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rlk_status rlk_dequantize_w4(const uint32_t* codes_u32, const void* scales,
+                             const uint8_t* zeros_u8, int dtype, int64_t N, int64_t K, int group,
+                             void* out_W, int out_dtype, rlk_stream_t stream) {
+    rlk_status st = check_w4(dtype, N, K, group, codes_u32, scales);
+    if (st != RLK_OK) return st;
+    if (out_dtype != dtype && out_dtype != RLK_FP32) return RLK_ERR_INVALID_ARG;
+    if (N == 0) return RLK_OK;
+    if (!out_W) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(out_W)) return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_dequantize_w4(codes_u32, scales, zeros_u8, ElemType(dtype), N, K,
+                                               group, out_W, ElemType(out_dtype),
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rlk_status rlk_linear_w4(const void* x, int dtype, const uint32_t* codes_u32, const void* scales,
+                         const uint8_t* zeros_u8, int64_t T, int64_t N, int64_t K, int group,
+                         void* out_y, int out_dtype, rlk_stream_t stream) {
+    if (T < 0 || T > INT32_MAX) return RLK_ERR_INVALID_ARG;
+    rlk_status st = check_w4(dtype, N, K, group, codes_u32, scales);
+    if (st != RLK_OK) return st;
+    if (out_dtype != dtype && out_dtype != RLK_FP32) return RLK_ERR_INVALID_ARG;
+    if (N == 0 || T == 0) return RLK_OK;
+    if (!x || !out_y) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned_to(out_y, elem_size(out_dtype))) return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_linear_w4(x, ElemType(dtype), codes_u32, scales, zeros_u8, T, N, K,
+                                           group, out_y, ElemType(out_dtype), sms,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
 rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits,
                                   uint64_t* target_range_rows) {
     int dev, sms;
@@ -768,7 +919,10 @@ rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits
     if (rlk::bwd_gemm_take_error(&word_bwd) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::lmhead_fp8b_take_error(&word_fp8b) != cudaSuccess) return RLK_ERR_CUDA;
     word |= word_bwd | word_fp8b;
+    unsigned long long rows_logits = 0;
     if (rlk::take_target_range_rows(&rows) != cudaSuccess) return RLK_ERR_CUDA;
+    if (rlk::token_logprobs_take_range_rows(&rows_logits) != cudaSuccess) return RLK_ERR_CUDA;
+    rows += rows_logits;
     if (wait_error_bits) *wait_error_bits = word;
     if (target_range_rows) *target_range_rows = rows;
     return RLK_OK;
