@@ -638,44 +638,75 @@ class TokenLogprobs(NamedTuple):
     top_logp: object
 
 
+_DTYPE_CODES = {}
+
+
 def _dtype_code(dtype):
     """rlk_dtype of a torch dtype (None for any other)."""
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _DTYPE_CODES.get(dtype)
 
 
-def _rows(t, name, codes=(0, 1, 2)):
-    """A CUDA matrix whose rows are dense but may lie further apart than their length:
-    (rlk_dtype, row stride in elements)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if _dtype_code(t.dtype) not in codes:
-        raise TypeError(f"{name} must be bfloat16, float16{' or float32' if 2 in codes else ''}, "
-                        f"got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims")
-    _need(t[:0].contiguous(), t.dtype, name)  # the device checks
-    dense = t.shape[1] <= 1 or t.stride(1) == 1
-    if not dense or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must have dense rows that do not overlap")
-    return _dtype_code(t.dtype), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+class _Call:
+    """The checks of one call: the device its tensors must be on, found once."""
+    __slots__ = ("torch", "device")
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        # a CUDA tensor exists only after initialisation
+        self.device = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+
+    def arg(self, t, dtype, name, ndim):
+        """Address of a dense tensor of this type and number of dimensions; raises as _need."""
+        if not (isinstance(t, self.torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+                and t.get_device() == self.device and t.is_contiguous()):
+            _need(t, dtype, name, ndim)
+        return t.data_ptr()
+
+    def rows(self, t, name):
+        """A matrix whose rows are dense but may lie further apart than their length:
+        (rlk_dtype, row stride in elements)."""
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        code = _dtype_code(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must have 2 dims")
+        if t.get_device() != self.device:
+            _need(t[:0].contiguous(), t.dtype, name)  # raises
+        n, width = t.shape
+        stride, step = t.stride()
+        if (step != 1 and width > 1) or (n > 1 and stride < width):
+            raise ValueError(f"{name} must have dense rows that do not overlap")
+        return code, stride if n > 1 else width
+
+    def stream(self, stream):
+        if stream is not None:
+            return stream.cuda_stream
+        # the address alone: building the Stream object of torch.cuda.current_stream() takes
+        # longer (2.9 us on Grace) than all checks of a call
+        return self.torch._C._cuda_getCurrentRawStream(self.device)
 
 
-def _logits_args(logits, targets, allowed):
-    """Checked (rlk_dtype, row stride, allowed pointer, allowed stride, T, V)."""
-    import torch
-    code, stride = _rows(logits, "logits")
-    _need(targets, torch.int32, "targets", 1)
+def _logits_args(call, logits, targets, allowed):
+    """Checked leading arguments of the two entry points, and T, V."""
+    code, stride = call.rows(logits, "logits")
+    i32 = call.torch.int32
+    tg = call.arg(targets, i32, "targets", 1)
     T, V = logits.shape
     if targets.shape[0] != T:
         raise ValueError("shape mismatch: logits [T, V], targets [T]")
     if allowed is None:
-        return code, stride, None, 0, T, V
-    _need(allowed, torch.int32, "allowed", 2)
-    if allowed.shape[0] != T or allowed.shape[1] < (V + 31) // 32:
+        return (logits.data_ptr(), code, stride, tg, None, 0, T, V), T, V
+    bits = call.arg(allowed, i32, "allowed", 2)
+    words = allowed.shape[1]
+    if allowed.shape[0] != T or words * 32 < V:
         raise ValueError("allowed must be [T, ceil(V/32)] words of allowed-token bits")
-    return code, stride, _ptr(allowed), allowed.shape[1], T, V
+    return (logits.data_ptr(), code, stride, tg, bits, words, T, V), T, V
 
 
 def token_logprobs(logits, targets, top_k: int = 0, allowed=None, inv_temp: float = 1.0, out=None,
@@ -688,32 +719,34 @@ def token_logprobs(logits, targets, top_k: int = 0, allowed=None, inv_temp: floa
     MAX_TOP_K alternatives, the largest logits first, the lower index first among equals.
     Pass out=(logp, lse, entropy, top_ids, top_logp) to reuse tensors (the last two may
     be None for top_k = 0)."""
-    import torch
-    code, stride, bits, bits_stride, T, V = _logits_args(logits, targets, allowed)
-    dev, top_k = logits.device, int(top_k)
+    call = _Call()
+    torch = call.torch
+    args, T, V = _logits_args(call, logits, targets, allowed)
+    top_k = int(top_k)
     if not 0 <= top_k <= MAX_TOP_K:
         raise ValueError(f"top_k must lie in 0..{MAX_TOP_K}")
+    f32 = torch.float32
     if out is None:
-        f = torch.empty((3, T), dtype=torch.float32, device=dev)
-        lp, lse, ent = f[0], f[1], f[2]
+        # (five allocations: views of one cost five times as much on the host)
+        dev = logits.device
+        lp, lse, ent = (torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev),
+                        torch.empty(T, dtype=f32, device=dev))
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        top = torch.empty((T, top_k), dtype=f32, device=dev)
+        addresses = (lp.data_ptr(), lse.data_ptr(), ent.data_ptr(), ids.data_ptr(), top.data_ptr())
     else:
         lp, lse, ent, ids, top = out
-        for name, t in (("logp", lp), ("lse", lse), ("entropy", ent)):
-            _need(t, torch.float32, name, 1)
-            if t.shape[0] != T:
-                raise ValueError(f"{name} must be [T]")
+        addresses = (call.arg(lp, f32, "logp", 1), call.arg(lse, f32, "lse", 1),
+                     call.arg(ent, f32, "entropy", 1), None, None)
+        if not lp.shape[0] == lse.shape[0] == ent.shape[0] == T:
+            raise ValueError("logp, lse and entropy must be [T]")
         if top_k:
-            _need(ids, torch.int32, "top_ids", 2)
-            _need(top, torch.float32, "top_logp", 2)
+            addresses = addresses[:3] + (call.arg(ids, torch.int32, "top_ids", 2),
+                                         call.arg(top, f32, "top_logp", 2))
             if ids.shape != (T, top_k) or top.shape != (T, top_k):
                 raise ValueError("top_ids and top_logp must be [T, top_k]")
-    _check(lib().rlk_token_logprobs(
-        _ptr(logits), code, stride, _ptr(targets), bits, bits_stride, T, V,
-        ctypes.c_float(inv_temp), top_k, _ptr(lp), _ptr(lse), _ptr(ent),
-        _ptr(ids) if top_k else None, _ptr(top) if top_k else None, _stream(stream)),
-        "rlk_token_logprobs")
+    _check((_lib or lib()).rlk_token_logprobs(*args, inv_temp, top_k, *addresses,
+                                              call.stream(stream)), "rlk_token_logprobs")
     return TokenLogprobs(lp, lse, ent, ids, top)
 
 
@@ -724,39 +757,40 @@ def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, 
     their type) from those of token_logprobs' outputs (f32, each may be None).  lse and
     entropy are its outputs (entropy is needed with grad_entropy), top_ids its ids (needed
     with grad_top).  out may be a tensor to fill, `logits` itself included."""
-    import torch
-    code, stride, bits, bits_stride, T, V = _logits_args(logits, targets, allowed)
-    _need(lse, torch.float32, "lse", 1)
+    call = _Call()
+    torch = call.torch
+    args, T, V = _logits_args(call, logits, targets, allowed)
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
+    f32 = torch.float32
+    vectors = []
     for name, t in (("lse", lse), ("entropy", entropy), ("grad_logp", grad_logp),
                     ("grad_lse", grad_lse), ("grad_entropy", grad_entropy)):
-        if t is not None:
-            _need(t, torch.float32, name, 1)
-            if t.shape[0] != T:
-                raise ValueError(f"{name} must be [T]")
-    top_k = 0
+        if t is None and name != "lse":
+            vectors.append(None)
+            continue
+        vectors.append(call.arg(t, f32, name, 1))
+        if t.shape[0] != T:
+            raise ValueError(f"{name} must be [T]")
+    top_k, ids, g_top = 0, None, None
     if grad_top is not None:
         if top_ids is None:
             raise ValueError("grad_top needs top_ids")
-        _need(top_ids, torch.int32, "top_ids", 2)
-        _need(grad_top, torch.float32, "grad_top", 2)
+        ids = call.arg(top_ids, torch.int32, "top_ids", 2)
+        g_top = call.arg(grad_top, f32, "grad_top", 2)
         top_k = grad_top.shape[1]
         if grad_top.shape[0] != T or top_ids.shape != grad_top.shape or top_k > MAX_TOP_K:
             raise ValueError(f"top_ids and grad_top must be [T, top_k], top_k <= {MAX_TOP_K}")
     if out is None:
         out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
-    out_code, out_stride = _rows(out, "out")
-    if out_code != code or out.shape != logits.shape:
-        raise ValueError("out must have the logits' shape and type")
-
-    def opt(t):
-        return None if t is None else _ptr(t)
-    _check(lib().rlk_token_logprobs_backward(
-        _ptr(logits), code, stride, _ptr(targets), bits, bits_stride, T, V,
-        ctypes.c_float(inv_temp), _ptr(lse), opt(entropy), opt(grad_logp), opt(grad_lse),
-        opt(grad_entropy), opt(top_ids) if top_k else None, opt(grad_top) if top_k else None, top_k,
-        _ptr(out), out_stride, _stream(stream)), "rlk_token_logprobs_backward")
+        out_stride = V
+    else:
+        _, out_stride = call.rows(out, "out")
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must have the logits' shape and type")
+    _check((_lib or lib()).rlk_token_logprobs_backward(
+        *args, inv_temp, *vectors, ids, g_top, top_k, out.data_ptr(), out_stride,
+        call.stream(stream)), "rlk_token_logprobs_backward")
     return out
 
 
@@ -832,35 +866,39 @@ def unpack_w4(codes):
     return q
 
 
-def _w4_args(codes, scales, zeros, group):
-    """Checked (rlk_dtype of the scales, N, K) of a 4-bit weight."""
-    import torch
-    _need(codes, torch.int32, "codes", 2)
+def _w4_args(call, codes, scales, zeros, group):
+    """Checked (codes, scales, zeros) addresses, rlk_dtype of the scales, N, K of a 4-bit
+    weight."""
+    torch = call.torch
+    c = call.arg(codes, torch.int32, "codes", 2)
     code = _dtype_code(scales.dtype) if isinstance(scales, torch.Tensor) else None
     if code not in (0, 1):
         raise TypeError("scales must be a bfloat16 or float16 tensor")
-    _need(scales, scales.dtype, "scales", 2)
+    s = call.arg(scales, scales.dtype, "scales", 2)
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    N, K = codes.shape[0], codes.shape[1] * 8
-    G = (K + group - 1) // group
-    if scales.shape != (N, G):
+    N, words = codes.shape
+    K = words * 8
+    shape = (N, (K + group - 1) // group)
+    if scales.shape != shape:
         raise ValueError("scales must be [N, ceil(K/group)]")
+    z = None
     if zeros is not None:
-        _need(zeros, torch.uint8, "zeros", 2)
-        if zeros.shape != (N, G):
+        z = call.arg(zeros, torch.uint8, "zeros", 2)
+        if zeros.shape != shape:
             raise ValueError("zeros must be [N, ceil(K/group)]")
-    return code, N, K
+    return c, s, z, code, N, K
 
 
 def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=None):
     """rlk_quantize_w4: bf16 or fp16 W [N, K] (K % 32 == 0) -> (i32 codes [N, K/8], scales
     [N, ceil(K/group)] of W's type, uint8 zero points of the same shape or None).  Pass
     out=(codes, scales, zeros) to reuse tensors."""
-    import torch
+    call = _Call()
+    torch = call.torch
     if not isinstance(W, torch.Tensor) or _dtype_code(W.dtype) not in (0, 1):
         raise TypeError("W must be a bfloat16 or float16 tensor")
-    _need(W, W.dtype, "W", 2)
+    w = call.arg(W, W.dtype, "W", 2)
     N, K = W.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
@@ -875,11 +913,10 @@ def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=
         codes, scales, zeros = out
         if (zeros is not None) != bool(asymmetric):
             raise ValueError("out must hold zero points for asymmetric quantisation, and only then")
-    code, N2, K2 = _w4_args(codes, scales, zeros, group)
+    c, s, z, code, N2, K2 = _w4_args(call, codes, scales, zeros, group)
     if (N2, K2) != (N, K) or scales.dtype != W.dtype:
         raise ValueError("out must hold codes [N, K/8] and scales of W's type")
-    _check(lib().rlk_quantize_w4(_ptr(W), code, N, K, group, _ptr(codes), _ptr(scales),
-                                 None if zeros is None else _ptr(zeros), _stream(stream)),
+    _check((_lib or lib()).rlk_quantize_w4(w, code, N, K, group, c, s, z, call.stream(stream)),
            "rlk_quantize_w4")
     return codes, scales, zeros
 
@@ -888,19 +925,18 @@ def dequantize_w4(codes, scales, zeros=None, group: int = 128, out_dtype=None, o
                   stream=None):
     """rlk_dequantize_w4: the values a 4-bit weight stands for, [N, K] as the scales' type
     (default) or float32."""
-    import torch
-    code, N, K = _w4_args(codes, scales, zeros, group)
+    call = _Call()
+    c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
     if out is None:
-        out = torch.empty((N, K), dtype=out_dtype or scales.dtype, device=codes.device)
+        out = call.torch.empty((N, K), dtype=out_dtype or scales.dtype, device=codes.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
-    _need(out, out.dtype, "out", 2)
+    o = call.arg(out, out.dtype, "out", 2)
     if out.shape != (N, K):
         raise ValueError("out must be [N, K]")
-    _check(lib().rlk_dequantize_w4(_ptr(codes), _ptr(scales), None if zeros is None else _ptr(zeros),
-                                   code, N, K, group, _ptr(out), out_code, _stream(stream)),
-           "rlk_dequantize_w4")
+    _check((_lib or lib()).rlk_dequantize_w4(c, s, z, code, N, K, group, o, out_code,
+                                             call.stream(stream)), "rlk_dequantize_w4")
     return out
 
 
@@ -908,23 +944,22 @@ def linear_w4(x, codes, scales, zeros=None, group: int = 128, out_dtype=None, ou
               stream=None):
     """rlk_linear_w4: y [T, N] = x [T, K] . W^T for a 4-bit weight; x has the scales' type,
     y that type or float32 (out_dtype, default float32)."""
-    import torch
-    code, N, K = _w4_args(codes, scales, zeros, group)
-    _need(x, scales.dtype, "x", 2)
+    call = _Call()
+    c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
+    a = call.arg(x, scales.dtype, "x", 2)
+    T = x.shape[0]
     if x.shape[1] != K:
         raise ValueError("shape mismatch: x [T, K], codes [N, K/8]")
-    T = x.shape[0]
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=x.device)
+        out = call.torch.empty((T, N), dtype=out_dtype or call.torch.float32, device=x.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
-    _need(out, out.dtype, "out", 2)
+    o = call.arg(out, out.dtype, "out", 2)
     if out.shape != (T, N):
         raise ValueError("out must be [T, N]")
-    _check(lib().rlk_linear_w4(_ptr(x), code, _ptr(codes), _ptr(scales),
-                               None if zeros is None else _ptr(zeros), T, N, K, group, _ptr(out),
-                               out_code, _stream(stream)), "rlk_linear_w4")
+    _check((_lib or lib()).rlk_linear_w4(a, code, c, s, z, T, N, K, group, o, out_code,
+                                         call.stream(stream)), "rlk_linear_w4")
     return out
 
 

@@ -8,196 +8,747 @@
 //   dx[v] = inv_temp * ( p[v] (g_lse - G - g_H (z[v] - lse + H))
 //                        + [v == target] g_logp + sum_j [v == id_j] g_top_j ),
 //   G = g_logp + sum_j g_top_j
-// One CTA per row; every sum runs in a fixed order over the row's elements, so a
-// row's bits depend on that row alone.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+//
+// Forward: one pass over the row and one launch.  A row is dealt to 64 strips of 32
+// lanes: lane l of strip s takes the eight elements from 256 s + 8 l on, and those
+// 16384, 2 * 16384, ... behind, and keeps a reference and the two sums about it.  A
+// strip is read by one warp.  The 64 x 32 partial sums meet in one binary tree, strips
+// first (inside a block of eight, then the blocks), lanes last.  Strips, lanes and tree
+// follow from V alone, so a row's bits depend on that row only, while the launch is free
+// to give a row to one CTA (many rows) or to a cluster of two, four or eight (few rows).
+//
+// Alternatives: what one lane of one strip reads is a cell, and its maximum is known
+// anyway.  Order tokens by (larger logit, lower index) and cells by (larger maximum,
+// lower place of it).  If K cells reach a bound, the top K tokens lie in cells that
+// reach it and reach it themselves: a token below it would have K tokens before it, one
+// in each of those cells.  So after the pass a bound is taken from the warps' best
+// cells, the cells that reach it (some tens of 2048) are read again, and their tokens
+// that reach it, hardly more, are ranked by counting.
 #include <float.h>
 #include <limits.h>
 
 #include "rlk_internal.h"
+#include "rlk_logits.cuh"
 #include "rlk_lse.cuh"
+#include "rlk_sm103.cuh"
 
 namespace rlk {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kStrips = 64;             // of a row: kBlocks blocks of kWarps
+constexpr int kBlocks = kStrips / kWarps;  // also the largest cluster
+constexpr int kGroup = 8;               // neighbouring elements per lane
+constexpr int kStep = 32 * kGroup;      // elements of a strip side by side
+constexpr int kStride = kStrips * kStep;  // from a lane's group to its next one
+constexpr int kCells = kStrips * 32;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Rows whose target was >= V, counted since the last read on this device.
 __device__ unsigned long long g_range_rows;
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename Elem>
-__device__ __forceinline__ Elem from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Element v of a row as fp32, -inf where the row's allowed bits leave it out.
-template <typename Elem>
-__device__ __forceinline__ float load_logit(const Elem* row, const uint32_t* bits, int v) {
-    if (bits && !((bits[v >> 5] >> (v & 31)) & 1u)) return -INFINITY;
-    return to_float(row[v]);
+// Two fp32 values in a register pair and the packed operations on them, each half
+// rounded like the scalar operation.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
-// Sums about a reference m (a raw logit; -FLT_MAX, the identity, before any
-// token): s = sum e^{c (x - m)}, u = sum e^{c (x - m)} (x - m) with c = inv_temp.
+// Sums about a reference m (a raw logit; -FLT_MAX, the identity, before any token), in
+// units of log 2: t = (x - m) * inv_temp * log2 e, s = sum 2^t, u = sum 2^t t.
 struct Sums {
     float m, s, u;
 };
 
+// Far below: where 2^t is 0, t is cut off there so that 0 * t is 0.  kFar cuts the
+// step between two references, which multiplies a whole sum.
+constexpr float kFarBelow = -200.0f;
+constexpr float kFar = -1e30f;
+
 __device__ __forceinline__ Sums combine(Sums a, Sums b, float c2) {
     const float m = fmaxf(a.m, b.m);
-    const float da = a.m - m, db = b.m - m;
-    const float ea = a.s == 0.0f ? 0.0f : exp2f(da * c2), eb = b.s == 0.0f ? 0.0f : exp2f(db * c2);
+    const float da = max_nan((a.m - m) * c2, kFar), db = max_nan((b.m - m) * c2, kFar);
+    const float ea = ex2(da), eb = ex2(db);
     Sums r;
     r.m = m;
-    r.s = a.s * ea + b.s * eb;
-    // a vanished operand adds nothing, however far (even -inf) its m lies below
-    r.u = (ea == 0.0f ? 0.0f : ea * fmaf(da, a.s, a.u)) +
-          (eb == 0.0f ? 0.0f : eb * fmaf(db, b.s, b.u));
+    r.s = fmaf(a.s, ea, b.s * eb);
+    r.u = fmaf(ea, fmaf(da, a.s, a.u), eb * fmaf(db, b.s, b.u));
     return r;
 }
 
-template <typename Elem>
-__global__ void __launch_bounds__(kThreads)
-    token_logprobs_kernel(const Elem* __restrict__ logits, int64_t row_stride,
-                          const int32_t* __restrict__ targets, const uint32_t* __restrict__ allowed,
-                          int64_t allowed_stride, int V, float inv_temp, int top_k,
-                          float* __restrict__ out_logp, float* __restrict__ out_lse,
-                          float* __restrict__ out_entropy, int32_t* __restrict__ out_ids,
-                          float* __restrict__ out_top) {
-    __shared__ Sums part[kThreads];
-    __shared__ float best_x[kWarps];
-    __shared__ int best_i[kWarps];
-    const int64_t t = blockIdx.x;
-    const Elem* row = logits + t * row_stride;
-    const uint32_t* bits = allowed ? allowed + t * allowed_stride : nullptr;
-    const float c2 = inv_temp * kLog2e;
+// Orders fp32 values as unsigned integers (larger value, larger integer; the zeros are
+// equal; 0 is below every value).
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+// (value, place): larger value first, lower place first among equals; 0 is none.
+__device__ __forceinline__ uint64_t order_key(float x, uint32_t place) {
+    return (uint64_t(ordered(x)) << 32) | (~place);
+}
+__device__ __forceinline__ uint32_t key_place(uint64_t k) { return ~uint32_t(k); }
 
-    Sums a = {-FLT_MAX, 0.0f, 0.0f};
-    for (int v = threadIdx.x; v < V; v += kThreads) {
-        const float x = load_logit(row, bits, v);
-        if (x > a.m) a = combine(a, {x, 0.0f, 0.0f}, c2);
-        const float d = x - a.m;
-        const float e = exp2f(d * c2);
-        a.s += e;
-        a.u = fmaf(e, fmaxf(d, -FLT_MAX), a.u);
-    }
-    part[threadIdx.x] = a;
-    __syncthreads();
-    for (int w = kThreads / 2; w > 0; w >>= 1) {
-        if (threadIdx.x < w) part[threadIdx.x] = combine(part[threadIdx.x], part[threadIdx.x + w], c2);
-        __syncthreads();
-    }
-    a = part[0];
-    const float logs = logf(a.s);
-    const float lse = a.s == 0.0f ? -INFINITY : fmaf(a.m, inv_temp, logs);
-    const bool empty = lse == -INFINITY;
-    if (threadIdx.x == 0) {
-        out_lse[t] = lse;
-        out_entropy[t] = empty ? 0.0f : logs - inv_temp * (a.u / a.s);
-        const int32_t tg = targets[t];
-        float lp = 0.0f;
-        if (tg >= 0 && tg < V) {
-            const float x = load_logit(row, bits, tg);
-            lp = x == -INFINITY || empty ? -INFINITY : (x - a.m) * inv_temp - logs;
-        } else if (tg >= V) {
-            atomicAdd(&g_range_rows, 1ull);
-        }
-        out_logp[t] = lp;
-    }
+constexpr int kCellList = 256;   // cells read again
+constexpr int kTokenList = 512;  // tokens ranked by counting
+constexpr int kGroupsAtOnce = 2 * kThreads;  // groups of cells looked through together
 
-    // The alternatives one after another: the best element behind the last one
-    // in the order (larger x first, lower index first among equals).
-    float last_x = INFINITY;
-    int last_i = -1;
-    for (int k = 0; k < top_k; ++k) {
-        float bx = -INFINITY;
-        int bi = INT_MAX;
-        for (int v = threadIdx.x; v < V; v += kThreads) {
-            const float x = load_logit(row, bits, v);
-            if ((x < last_x || (x == last_x && v > last_i)) && x > bx) {
-                bx = x;
-                bi = v;
-            }
+struct Shared {
+    uint64_t cells[kCells];              // the CTA's cells; 0: no token
+    Sums strip_sums[kBlocks][kWarps][32];
+    Sums block_sums[kBlocks][32];        // rank 0: of the whole row
+    uint64_t cell_list[kCellList];
+    uint32_t group_list[kGroupsAtOnce];
+    uint64_t chosen[kMaxTopK];           // the CTA's, then the row's best tokens
+    uint32_t warp_bound[kWarps];
+    Sums row;
+    int count, tokens, groups;
+
+    // Tokens to rank, in the cells' place once the list of cells is complete.
+    __device__ __forceinline__ uint64_t* token_list() { return cells; }
+    // Rank 0: the best tokens of every CTA, in the place of a block of strip sums that only
+    // a CTA without a cluster has.
+    __device__ __forceinline__ uint64_t* gathered() {
+        return reinterpret_cast<uint64_t*>(strip_sums[kBlocks - 1]);
+    }
+};
+static_assert(sizeof(Shared) <= 48 * 1024, "no opt-in for shared memory");
+static_assert(kBlocks * kMaxTopK * 8 <= sizeof(Sums) * kWarps * 32, "one block of strip sums");
+static_assert(kTokenList <= kCells && kCellList >= kMaxTopK && kTokenList % 4 == 0, "lists");
+
+struct Args {
+    const void* logits;
+    int64_t row_stride;
+    const int32_t* targets;
+    const uint32_t* allowed;
+    int64_t allowed_stride;
+    int V, top_k;
+    float inv_temp;
+    float *out_logp, *out_lse, *out_entropy, *out_top;
+    int32_t* out_ids;
+};
+
+// Adds eight elements to the sums about m.  kCut: elements at -inf may be among them
+// (0 * -inf must not reach u).
+template <bool kCut, typename Elem>
+__device__ __forceinline__ void add_eight(const Packed8<Elem>& x, F2 low, F2 scale, F2& s, F2& u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 xx = x.pair(j);
+        F2 t = mul2(add2(pack2(xx.x, xx.y), low), scale);
+        float2 f = unpack2(t);
+        if (kCut) {
+            f = make_float2(max_nan(f.x, kFarBelow), max_nan(f.y, kFarBelow));
+            t = pack2(f.x, f.y);
         }
-        for (int off = 16; off > 0; off >>= 1) {
-            const float ox = __shfl_xor_sync(0xffffffffu, bx, off);
-            const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
-            if (ox > bx || (ox == bx && oi < bi)) {
-                bx = ox;
-                bi = oi;
-            }
-        }
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-            best_x[threadIdx.x >> 5] = bx;
-            best_i[threadIdx.x >> 5] = bi;
-        }
-        __syncthreads();
-        bx = best_x[0];
-        bi = best_i[0];
-        for (int w = 1; w < kWarps; ++w)
-            if (best_x[w] > bx || (best_x[w] == bx && best_i[w] < bi)) {
-                bx = best_x[w];
-                bi = best_i[w];
-            }
-        if (threadIdx.x == 0) {
-            out_ids[t * top_k + k] = bi == INT_MAX ? -1 : bi;
-            out_top[t * top_k + k] = bi == INT_MAX || empty ? -INFINITY : (bx - a.m) * inv_temp - logs;
-        }
-        last_x = bx;
-        last_i = bi;
+        const F2 p = pack2(ex2(f.x), ex2(f.y));
+        s = add2(s, p);
+        u = fma2(p, t, u);
     }
 }
 
-template <typename Elem>
-__global__ void __launch_bounds__(kThreads)
-    token_logprobs_backward_kernel(const Elem* logits, int64_t row_stride,
-                                   const int32_t* __restrict__ targets,
-                                   const uint32_t* __restrict__ allowed, int64_t allowed_stride,
-                                   int V, float inv_temp, const float* __restrict__ lse_in,
-                                   const float* __restrict__ entropy_in,
-                                   const float* __restrict__ g_logp, const float* __restrict__ g_lse,
-                                   const float* __restrict__ g_entropy,
-                                   const int32_t* __restrict__ top_ids,
-                                   const float* __restrict__ g_top, int top_k, Elem* grad,
-                                   int64_t grad_stride) {
-    const int64_t t = blockIdx.x;
-    const Elem* row = logits + t * row_stride;
-    Elem* out = grad + t * grad_stride;
-    const uint32_t* bits = allowed ? allowed + t * allowed_stride : nullptr;
-    const float lse = lse_in[t];
-    const float H = entropy_in ? entropy_in[t] : 0.0f;
-    const int32_t tg = targets[t];
-    const bool inside = tg >= 0 && tg < V;
-    const float gl = (inside && g_logp) ? g_logp[t] : 0.0f;
-    const float gh = g_entropy ? g_entropy[t] : 0.0f;
-    float total = gl;
-    for (int k = 0; k < top_k; ++k)
-        if (top_ids[t * top_k + k] >= 0) total += g_top[t * top_k + k];
-    const float a = (g_lse ? g_lse[t] : 0.0f) - total;
-    for (int v = threadIdx.x; v < V; v += kThreads) {
-        const float x = load_logit(row, bits, v);
-        float d = 0.0f;
-        if (x != -INFINITY && lse != -INFINITY) {
-            const float lp = fmaf(x, inv_temp, -lse);
-            // e^-200 is 0 in fp32; without the floor 0 * inf could follow
-            d = lp < -200.0f ? 0.0f : expf(lp) * (a - gh * (lp + H));
-            if (inside && v == tg) d += gl;
-            for (int k = 0; k < top_k; ++k)
-                if (top_ids[t * top_k + k] == v) d += g_top[t * top_k + k];
+// The running state of one lane of one strip.  The reference m is the maximum of the
+// first unit of groups with a token; it moves on only where a later unit's maximum lies
+// more than kLead above it (2^kLead times the elements stay far inside fp32), so that the
+// usual unit has no step between references.
+constexpr float kLead = 8.0f;
+
+struct LaneState {
+    float top, m;
+    uint32_t place;
+    F2 s, u;
+
+    // One unit of N groups, the first one e0 / kGroup of the row, kStride apart.
+    template <bool kCut, int N, typename Elem>
+    __device__ __forceinline__ void add(const Packed8<Elem> (&x)[N], uint32_t group, float c2) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float g = x[i].max();
+            if (g > top) {
+                top = g;
+                place = group + i * (kStride / kGroup);
+            }
+            most = fmaxf(most, g);
         }
-        out[v] = from_float<Elem>(d * inv_temp);
+        if ((most - m) * c2 > kLead) {
+            const float d = max_nan((m - most) * c2, kFar);
+            const float f = ex2(d);
+            const F2 ff = pack2(f, f), dd = pack2(d, d);
+            u = mul2(ff, fma2(dd, s, u));
+            s = mul2(ff, s);
+            m = most;
+        }
+        const F2 low = pack2(-m, -m), scale = pack2(c2, c2);
+        F2 us = pack2(0.0f, 0.0f), uu = us;
+#pragma unroll
+        for (int i = 0; i < N; ++i) add_eight<kCut>(x[i], low, scale, us, uu);
+        if (!kCut) {
+            const float2 test = unpack2(uu);
+            if (!(test.x + test.y == test.x + test.y)) {  // an element at -inf, or a NaN
+                us = uu = pack2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) add_eight<true>(x[i], low, scale, us, uu);
+            }
+        }
+        s = add2(s, us);
+        u = add2(u, uu);
+    }
+};
+
+// One strip's lane: its sums, and its cell's key.  Groups are taken two at a time as long
+// as the strip's two rows of groups lie whole in the row, with the next two's loads in
+// flight, then one at a time.  How they are taken follows from V alone (a unit's maximum
+// decides the rounding), not from the row's alignment.
+template <typename Elem, bool kShifted, bool kMasked>
+__device__ __forceinline__ Sums read_strip(const Elem* row, int shift, const uint8_t* bits,
+                                           uint32_t V, uint32_t strip, int lane, float c2,
+                                           uint64_t* cell) {
+    using In = Vectors<Elem, kShifted>;
+    LaneState st = {-INFINITY, -FLT_MAX, 0u, pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+    const uint32_t base = strip * kStep;
+    const uint32_t e = base + lane * kGroup;
+    // rows of groups of this strip whose vectors lie inside the row, and one element more
+    // than the longest shift
+    const uint32_t whole =
+        base + kStep + kGroup <= V ? (V - base - kStep - kGroup) / kStride + 1 : 0;
+    const uint32_t units = whole / 2;
+    // the row's first group has its first vector in front of a shifted row
+    const bool edge = kShifted && e == 0;
+    const Elem* from = row + e;
+    const uint8_t* mask = bits + e / kGroup;
+    In in[2];
+    uint32_t b[2] = {0, 0};
+    if (units > 0) {
+        in[0].load(edge ? from + kStride : from, 0, shift);
+        in[1].load(from + kStride, 0, shift);
+        if (kMasked) {
+            b[0] = mask[0];
+            b[1] = mask[kStride / kGroup];
+        }
+    }
+    uint32_t i = 0;
+    for (uint32_t n = 0; n < units; ++n) {
+        Packed8<Elem> x[2];
+        unshift(in, shift, x);
+        if (edge && n == 0) x[0].load_single(row, 0, V);
+        if (kMasked) {
+            x[0].keep(b[0]);
+            x[1].keep(b[1]);
+        }
+        if (n + 1 < units) {
+            from += 2 * kStride;
+            in[0].load(from, 0, shift);
+            in[1].load(from + kStride, 0, shift);
+            if (kMasked) {
+                mask += 2 * kStride / kGroup;
+                b[0] = mask[0];
+                b[1] = mask[kStride / kGroup];
+            }
+        }
+        st.add<kMasked>(x, e / kGroup + i * (kStride / kGroup), c2);
+        i += 2;
+    }
+    for (; int64_t(base) + int64_t(i) * kStride < V; ++i) {
+        const int64_t e0 = int64_t(e) + int64_t(i) * kStride;
+        Packed8<Elem> x[1];
+        if (In::inside(e0, shift, V)) {
+            In one[1];
+            one[0].load(row, e0, shift);
+            unshift(one, shift, x);
+        } else {
+            x[0].load_single(row, e0, V);
+        }
+        if (kMasked) x[0].keep(e0 < V ? bits[e0 / kGroup] : 0u);
+        st.add<true>(x, uint32_t(e0 / kGroup), c2);
+    }
+    *cell = st.top > -INFINITY ? order_key(st.top, st.place) : 0;
+    const float2 s1 = unpack2(st.s), u1 = unpack2(st.u);
+    return {st.m, s1.x + s1.y, u1.x + u1.y};
+}
+
+// Eight sums of a lane in a binary tree.
+__device__ __forceinline__ Sums combine_eight(const Sums (*w)[32], int lane, float c2) {
+    Sums a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = w[i][lane];
+#pragma unroll
+    for (int n = 1; n < 8; n *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2 * n) a[i] = combine(a[i], a[i + n], c2);
+    return a[0];
+}
+
+// One element of the row, -inf where the mask leaves it out.
+template <typename Elem>
+__device__ __forceinline__ float element(const Elem* row, const uint8_t* bits, int64_t v) {
+    if (bits && !((bits[v >> 3] >> (v & 7)) & 1u)) return -INFINITY;
+    return to_float(row[v]);
+}
+
+// Puts the top_k largest keys of list[0 .. n), larger first, into out (zeroed before); the
+// list is zero up to the next multiple of four.  By the threads from `first` on.
+__device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int top_k, uint64_t* out,
+                                          int first = 0) {
+    for (int i = int(threadIdx.x) - first; i < n; i += kThreads - first) {
+        if (i < 0) return;
+        const uint64_t k = list[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int o = 0; o < n; o += 4) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(list + o);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(list + o + 2);
+            rank += (a.x > k) + (a.y > k) + (b.x > k) + (b.y > k);
+        }
+        if (k != 0 && rank < top_k) out[rank] = k;
+    }
+}
+
+// Collects the keys at or above `bound` out of those that each(f, bound) calls f with, into
+// `list` (of kSize, zero up to the next multiple of four); returns their number.  If they
+// are more than the list holds, the top_k-th of those that it got is a higher bound that
+// still keeps the top_k best, and leaves out all but top_k of the list: the collection
+// starts again with that.  *count and sh.chosen are 0 before and after.
+template <int kSize, typename Each>
+__device__ __forceinline__ int collect(Shared& sh, uint64_t* list, int* count, uint64_t& bound,
+                                       int top_k, Each&& each) {
+    while (true) {
+        each([&](uint64_t k) {
+            const int at = atomicAdd(count, 1);
+            if (at < kSize) list[at] = k;
+        }, bound);
+        __syncthreads();
+        const int n = *count;
+        if (n <= kSize) {
+            if (threadIdx.x < 4 && n + threadIdx.x < kSize) list[n + threadIdx.x] = 0;
+            __syncthreads();
+            return n;
+        }
+        rank_keys(list, kSize, top_k, sh.chosen);
+        __syncthreads();
+        bound = sh.chosen[top_k - 1];
+        __syncthreads();
+        if (threadIdx.x == 0) *count = 0;
+        if (threadIdx.x < kMaxTopK) sh.chosen[threadIdx.x] = 0;
+        __syncthreads();
+    }
+}
+
+// Lists the CTA's cells that may hold one of its top_k best tokens; returns their number and
+// the lowest token key that they are to be searched for.
+__device__ __forceinline__ int best_cells(Shared& sh, int cells, int top_k, uint64_t& bound) {
+    // A value that at least top_k cells reach: the lowest of the warps' r-th best lanes.
+    uint32_t mine = 0;
+    for (int i = threadIdx.x; i < cells; i += kThreads) mine = max(mine, uint32_t(sh.cells[i] >> 32));
+    uint32_t low = 0;
+    for (int r = 0; r < (top_k + kWarps - 1) / kWarps; ++r) {
+        low = __reduce_max_sync(0xffffffffu, mine);
+        if (mine == low) mine = 0;
+    }
+    if ((threadIdx.x & 31) == 0) sh.warp_bound[threadIdx.x >> 5] = low;
+    if (threadIdx.x == 0) sh.count = sh.tokens = sh.groups = 0;
+    if (threadIdx.x < kMaxTopK) sh.chosen[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) low = min(low, sh.warp_bound[w]);
+    bound = max(uint64_t(low) << 32, uint64_t(1));
+    const int n = collect<kCellList>(sh, sh.cell_list, &sh.count, bound, top_k,
+                                     [&](auto&& f, uint64_t at_least) {
+        for (int i = threadIdx.x; i < cells; i += kThreads) {
+            const uint64_t k = sh.cells[i];
+            if (k >= at_least) f(k);
+        }
+    });
+    // a cell's key places its group: the last element of that group
+    bound = uint32_t(bound) == 0 || bound == 1
+                ? bound
+                : (bound & ~uint64_t(0xffffffffu)) | uint32_t(~(key_place(bound) * kGroup + kGroup - 1));
+    return n;
+}
+
+// Calls f(key) for the tokens of the listed cells that are not below `bound`.  The cells'
+// groups are dealt to the threads, kGroupsAtOnce at a time: first the groups whose vectors
+// hold an element that high (their neighbours' elements among them, and forbidden ones) are
+// listed, then the elements of those are looked at one by one.  All threads call it.
+//
+// This and what follows runs once per row, so its instructions are rarely in the cache:
+// short loops beat unrolled code.
+template <typename Elem, typename F>
+__device__ __forceinline__ void each_token(Shared& sh, const Elem* row, int shift,
+                                           const uint8_t* bits, uint32_t V, int cells,
+                                           uint64_t bound, F&& f) {
+    using In = Vectors<Elem, true>;
+    const uint32_t per_cell = (V - 1) / kStride + 1;
+    const uint32_t total = cells * per_cell;
+    for (uint32_t from = 0; from < total; from += kGroupsAtOnce) {
+        uint32_t e0[2];
+        In in[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t g = from + threadIdx.x + i * kThreads;
+            const uint32_t c = g / per_cell;
+            const uint64_t e = uint64_t(key_place(sh.cell_list[min(c, uint32_t(cells - 1))]) % kCells) * kGroup +
+                               uint64_t(g - c * per_cell) * kStride;
+            e0[i] = g < total && e < V ? uint32_t(e) : UINT32_MAX;
+            if (e0[i] != UINT32_MAX && In::inside(e0[i], shift, V)) in[i].load(row, e0[i], shift);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (e0[i] == UINT32_MAX) continue;
+            float top = INFINITY;
+            if (In::inside(e0[i], shift, V)) {
+                top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < In::kVecs; ++j) top = max_of<Elem>(top, in[i].v[j]);
+            }
+            if (ordered(top) >= uint32_t(bound >> 32)) sh.group_list[atomicAdd(&sh.groups, 1)] = e0[i];
+        }
+        __syncthreads();
+        const int n = sh.groups * kGroup;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint32_t e = sh.group_list[i / kGroup] + i % kGroup;
+            const float x = e < V ? element(row, bits, e) : -INFINITY;
+            const uint64_t k = order_key(x, e);
+            if (x > -INFINITY && k >= bound) f(k);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) sh.groups = 0;
+        if (from + kGroupsAtOnce < total) __syncthreads();
+    }
+}
+
+// Grid: T clusters of `ranks` CTAs (1, 2, 4 or 8).
+template <typename Elem, bool kMasked>
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Args p, int ranks) {
+    extern __shared__ uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = ranks > 1 ? int(cluster_ctarank()) : 0;
+    const int64_t t = blockIdx.x / unsigned(ranks);
+    const Elem* row = static_cast<const Elem*>(p.logits) + t * p.row_stride;
+    const uint8_t* bits =
+        kMasked ? reinterpret_cast<const uint8_t*>(p.allowed + t * p.allowed_stride) : nullptr;
+    const float c2 = p.inv_temp * kLog2e;
+    const int shift = row_shift(row);
+    if (ranks > 1) cluster_arrive_relaxed();  // every CTA runs before another writes to it
+    int32_t target = -1;
+    if (rank == 0 && threadIdx.x == 0) target = p.targets[t];
+
+    // A block of eight strips at a time, one strip per warp.
+    const int blocks = kBlocks / ranks;
+    for (int j = 0; j < blocks; ++j) {
+        const int strip = (rank * blocks + j) * kWarps + warp;
+        uint64_t cell = 0;
+        sh.strip_sums[j][warp][lane] =
+            shift == 0 ? read_strip<Elem, false, kMasked>(row, 0, bits, p.V, strip, lane, c2, &cell)
+                       : read_strip<Elem, true, kMasked>(row, shift, bits, p.V, strip, lane, c2, &cell);
+        if (p.top_k > 0) sh.cells[(j * kWarps + warp) * 32 + lane] = cell;
+    }
+    float target_x = -INFINITY;
+    if (target >= 0 && target < p.V) target_x = element(row, bits, target);
+    __syncthreads();
+
+    uint64_t bound = 0;
+    int cells = 0, tokens = 0;
+    if (p.top_k > 0) cells = best_cells(sh, kCells / ranks, p.top_k, bound);
+    Sums sum;
+    if (warp < blocks) {
+        sum = combine_eight(sh.strip_sums[warp], lane, c2);
+        if (ranks == 1) sh.block_sums[warp][lane] = sum;
+    }
+    if (p.top_k > 0)
+        tokens = collect<kTokenList>(sh, sh.token_list(), &sh.tokens, bound, p.top_k,
+                                     [&](auto&& f, uint64_t at_least) {
+            each_token(sh, row, shift, bits, uint32_t(p.V), cells, at_least, f);
+        });
+
+    const int handed = (p.top_k + 3) / 4 * 4;  // keys each CTA hands over, zeros at the end
+    if (ranks > 1) {
+        if (p.top_k > 0) {
+            rank_keys(sh.token_list(), tokens, p.top_k, sh.chosen);
+            __syncthreads();
+        }
+        cluster_wait();
+        if (warp < blocks) {
+            const uint32_t to = mapa_shared(smem_u32(&sh.block_sums[rank * blocks + warp][lane]), 0);
+            st_shared_cluster_u32(to, __float_as_uint(sum.m));
+            st_shared_cluster_u32(to + 4, __float_as_uint(sum.s));
+            st_shared_cluster_u32(to + 8, __float_as_uint(sum.u));
+        }
+        if (warp == kWarps - 1 && lane < handed) {
+            const uint64_t k = sh.chosen[lane];
+            const uint32_t to = mapa_shared(smem_u32(&sh.gathered()[rank * handed + lane]), 0);
+            st_shared_cluster_u32(to, uint32_t(k));
+            st_shared_cluster_u32(to + 4, uint32_t(k >> 32));
+        }
+        cluster_sync();
+        if (rank != 0) return;
+        if (threadIdx.x < kMaxTopK) sh.chosen[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    if (warp > 0) {  // the other warps rank the tokens while the first one ends the sums
+        if (ranks == 1)
+            rank_keys(sh.token_list(), tokens, p.top_k, sh.chosen, 32);
+        else
+            rank_keys(sh.gathered(), ranks * handed, p.top_k, sh.chosen, 32);
+    } else {
+        sum = combine_eight(sh.block_sums, lane, c2);
+#pragma unroll 1
+        for (int off = 16; off > 0; off >>= 1) {
+            Sums o;
+            o.m = __shfl_xor_sync(0xffffffffu, sum.m, off);
+            o.s = __shfl_xor_sync(0xffffffffu, sum.s, off);
+            o.u = __shfl_xor_sync(0xffffffffu, sum.u, off);
+            sum = combine(sum, o, c2);
+        }
+        if (lane == 0) {
+            sh.row = sum;
+            const float logs = logf(sum.s);
+            const float lse = fmaf(sum.m, p.inv_temp, logs);
+            const bool empty = sum.s == 0.0f || lse == -INFINITY;
+            p.out_lse[t] = empty ? -INFINITY : lse;
+            p.out_entropy[t] = empty ? 0.0f : logs - kLn2 * (sum.u / sum.s);
+            float lp = 0.0f;
+            if (target >= 0 && target < p.V)
+                lp = target_x == -INFINITY || empty ? -INFINITY
+                                                    : (target_x - sum.m) * p.inv_temp - logs;
+            else if (target >= p.V)
+                atomicAdd(&g_range_rows, 1ull);
+            p.out_logp[t] = lp;
+        }
+    }
+    if (p.top_k == 0) return;
+    __syncthreads();
+    if (threadIdx.x < p.top_k) {
+        const uint64_t k = sh.chosen[threadIdx.x];
+        const float logs = logf(sh.row.s);
+        const bool empty = fmaf(sh.row.m, p.inv_temp, logs) == -INFINITY;
+        const int64_t at = t * p.top_k + threadIdx.x;
+        p.out_ids[at] = k == 0 ? -1 : int32_t(key_place(k));
+        p.out_top[at] = k == 0 || empty
+                            ? -INFINITY
+                            : (from_ordered(uint32_t(k >> 32)) - sh.row.m) * p.inv_temp - logs;
+    }
+}
+
+struct BackwardArgs {
+    const void* logits;
+    int64_t row_stride;
+    const int32_t* targets;
+    const uint32_t* allowed;
+    int64_t allowed_stride;
+    int V, top_k;
+    float inv_temp;
+    const float *lse, *entropy, *g_logp, *g_lse, *g_entropy, *g_top;
+    const int32_t* top_ids;
+    void* grad;
+    int64_t grad_stride;
+    int parts, part_length;  // CTAs per row and elements of each (a multiple of kGroup)
+};
+
+// dx = p (a - b (z - lse)) with a, b scaled by inv_temp, for the tokens of a row.
+struct RowGradient {
+    float it, lse, a, b;
+    __device__ __forceinline__ float operator()(float x) const {
+        const float lp = max_nan(fmaf(x, it, -lse), kFarBelow);
+        return ex2(lp * kLog2e) * fmaf(lp, -b, a);
+    }
+    template <typename Elem>
+    __device__ __forceinline__ void operator()(const Packed8<Elem>& in, float (&x)[8]) const {
+        const F2 it2 = pack2(it, it), lse2 = pack2(-lse, -lse), a2 = pack2(a, a), b2 = pack2(-b, -b);
+        const F2 l2e = pack2(kLog2e, kLog2e);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2 xx = in.pair(j / 2);
+            const float2 lp = unpack2(fma2(pack2(xx.x, xx.y), it2, lse2));
+            const F2 l = pack2(max_nan(lp.x, kFarBelow), max_nan(lp.y, kFarBelow));
+            const float2 t = unpack2(mul2(l, l2e));
+            const float2 d = unpack2(mul2(pack2(ex2(t.x), ex2(t.y)), fma2(l, b2, a2)));
+            x[j] = d.x;
+            x[j + 1] = d.y;
+        }
+    }
+};
+
+__device__ __forceinline__ void store_eight(float* out, const float (&x)[8]) {
+    reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store_eight(__half* out, const float (&x)[8]) {
+    __half2 h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ void store_eight(__nv_bfloat16* out, const float (&x)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+}
+
+// Eight mask bits from element e0 on (e0 + 7 lies in the row).
+__device__ __forceinline__ uint32_t eight_bits(const uint8_t* bits, int64_t e0) {
+    const int64_t b = e0 >> 3;
+    const int off = int(e0 & 7);
+    return off ? (uint32_t(bits[b]) | uint32_t(bits[b + 1]) << 8) >> off : bits[b];
+}
+
+// One part of a row: elementwise in groups of eight that start at 16-byte boundaries of
+// the gradient's row, then the few tokens with a gradient of their own (the target, the
+// alternatives) once more, whole.  Those are read before anything is written, so the
+// gradient may take the logits' place.
+template <typename Elem, bool kMasked>
+__global__ void __launch_bounds__(kThreads, 4)
+    token_logprobs_backward_kernel(const BackwardArgs p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = blockIdx.x / unsigned(p.parts);
+    const int part = int(blockIdx.x - t * p.parts);
+    const Elem* row = static_cast<const Elem*>(p.logits) + t * p.row_stride;
+    Elem* out = static_cast<Elem*>(p.grad) + t * p.grad_stride;
+    const uint8_t* bits =
+        kMasked ? reinterpret_cast<const uint8_t*>(p.allowed + t * p.allowed_stride) : nullptr;
+    const int head = (kVecElems<Elem> - row_shift(out)) % kVecElems<Elem>;
+    const int begin = part == 0 ? 0 : head + part * p.part_length;
+    const int end = int(min(int64_t(head) + int64_t(part + 1) * p.part_length, int64_t(p.V)));
+
+    const int32_t target = p.targets[t];
+    const float g_target = p.g_logp && target >= 0 && target < p.V ? p.g_logp[t] : 0.0f;
+    int32_t id = -1;
+    float g_id = 0.0f;
+    if (lane < p.top_k) {
+        id = p.top_ids[t * p.top_k + lane];
+        if (id >= 0 && id < p.V)
+            g_id = p.g_top[t * p.top_k + lane];
+        else
+            id = -1;
+    }
+    float total = g_id;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    total += g_target;
+    const float g_ent = p.g_entropy ? p.g_entropy[t] : 0.0f;
+    const float H = p.g_entropy ? p.entropy[t] : 0.0f;
+    RowGradient f;
+    f.it = p.inv_temp;
+    f.lse = p.lse[t];
+    f.b = p.inv_temp * g_ent;
+    f.a = p.inv_temp * ((p.g_lse ? p.g_lse[t] : 0.0f) - total - g_ent * H);
+    const bool empty = f.lse == -INFINITY;
+
+    // Tokens of this part with a gradient of their own: lane j the j-th alternative (the
+    // first of equal ids for all of them), lane 0 of warp 1 the target.
+    const bool own_target = target >= begin && target < end;
+    int own = -1;
+    float own_x = -INFINITY, own_g = 0.0f;
+    if (p.top_k > 0 || own_target) {
+        bool taken = false;
+        for (int j = 0; j < p.top_k; ++j) {
+            const int32_t other = __shfl_sync(0xffffffffu, id, j);
+            const float g = __shfl_sync(0xffffffffu, g_id, j);
+            taken |= other == target;
+            if (other == id) {
+                own_g += g;
+                if (j < lane) own_g = NAN;  // an earlier lane has it
+            }
+        }
+        if (threadIdx.x < 32) {
+            if (id >= begin && id < end && own_g == own_g) own = id;
+            if (id == target) own_g += g_target;
+        } else if (threadIdx.x == 32 && own_target && !taken) {
+            own = target;
+            own_g = g_target;
+        }
+        if (own >= 0) own_x = element(row, bits, own);
+        __syncthreads();
+    }
+
+    const int first = head + part * p.part_length;
+    const int shift = (row_shift(row) + head) % kVecElems<Elem>;
+    auto body = [&](auto shifted) {
+        using In = Vectors<Elem, decltype(shifted)::value>;
+        constexpr int kBatch = 8 / int(sizeof(Elem));
+        for (int64_t e = int64_t(first) + threadIdx.x * kGroup; e < end;
+             e += kBatch * kThreads * kGroup) {
+            In in[kBatch];
+            Packed8<Elem> raw[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t e0 = e + i * kThreads * kGroup;
+                if (e0 < end && In::inside(e0, shift, p.V)) in[i].load(row, e0, shift);
+            }
+            unshift(in, shift, raw);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t e0 = e + i * kThreads * kGroup;
+                if (e0 >= end) break;
+                if (In::inside(e0, shift, p.V)) {
+                    if (kMasked) raw[i].keep(eight_bits(bits, e0));
+                    float x[8];
+                    f(raw[i], x);
+                    if (empty) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+                    }
+                    store_eight(out + e0, x);
+                } else {
+                    for (int j = 0; j < 8 && e0 + j < p.V; ++j)
+                        out[e0 + j] = from_float<Elem>(empty ? 0.0f : f(element(row, bits, e0 + j)));
+                }
+            }
+        }
+    };
+    if (shift == 0)
+        body(std::false_type());
+    else
+        body(std::true_type());
+    if (part == 0 && threadIdx.x < min(head, p.V))
+        out[threadIdx.x] = from_float<Elem>(empty ? 0.0f : f(element(row, bits, threadIdx.x)));
+
+    if (p.top_k > 0 || own_target) {
+        __syncthreads();
+        if (own >= 0 && own_x != -INFINITY && !empty)
+            out[own] = from_float<Elem>(fmaf(f.it, own_g, f(own_x)));
     }
 }
 
@@ -217,16 +768,38 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
                                   int64_t allowed_stride, int64_t T, int64_t V, float inv_temp,
                                   int top_k, float* out_logp, float* out_lse, float* out_entropy,
                                   int32_t* out_ids, float* out_top, int num_sms, cudaStream_t stream) {
-    auto go = [&](auto elem) {
-        using Elem = decltype(elem);
-        token_logprobs_kernel<Elem><<<unsigned(T), kThreads, 0, stream>>>(
-            static_cast<const Elem*>(logits), row_stride, targets, allowed, allowed_stride, int(V),
-            inv_temp, top_k, out_logp, out_lse, out_entropy, out_ids, out_top);
-        return cudaGetLastError();
+    const Args p = {logits, row_stride, targets, allowed, allowed_stride, int(V), top_k, inv_temp,
+                    out_logp, out_lse, out_entropy, out_top, out_ids};
+    // CTAs per row: as many as keep the launch within what the SMs hold at once (four
+    // CTAs each; a little less with alternatives, whose selection every CTA pays for, and
+    // then at least 8192 elements per CTA).
+    int ranks = 8;
+    while (ranks > 1 && (2 * T * ranks > (top_k ? 7 : 8) * int64_t(num_sms) ||
+                         (top_k && V < 8192 * int64_t(ranks))))
+        ranks /= 2;
+    auto go = [&](auto kernel) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(ranks);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(unsigned(T * ranks), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = sizeof(Shared);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = ranks > 1 ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, ranks);
+        return e != cudaSuccess ? e : cudaGetLastError();
     };
-    if (type == ElemType::kBf16) return go(__nv_bfloat16());
-    if (type == ElemType::kFp16) return go(__half());
-    return go(float());
+    if (type == ElemType::kBf16)
+        return allowed ? go(token_logprobs_kernel<__nv_bfloat16, true>)
+                       : go(token_logprobs_kernel<__nv_bfloat16, false>);
+    if (type == ElemType::kFp16)
+        return allowed ? go(token_logprobs_kernel<__half, true>)
+                       : go(token_logprobs_kernel<__half, false>);
+    return allowed ? go(token_logprobs_kernel<float, true>)
+                   : go(token_logprobs_kernel<float, false>);
 }
 
 cudaError_t launch_token_logprobs_backward(const void* logits, ElemType type, int64_t row_stride,
@@ -237,17 +810,24 @@ cudaError_t launch_token_logprobs_backward(const void* logits, ElemType type, in
                                            const float* g_entropy, const int32_t* top_ids,
                                            const float* g_top, int top_k, void* grad,
                                            int64_t grad_stride, int num_sms, cudaStream_t stream) {
-    auto go = [&](auto elem) {
-        using Elem = decltype(elem);
-        token_logprobs_backward_kernel<Elem><<<unsigned(T), kThreads, 0, stream>>>(
-            static_cast<const Elem*>(logits), row_stride, targets, allowed, allowed_stride, int(V),
-            inv_temp, lse, entropy, g_logp, g_lse, g_entropy, top_ids, g_top, top_k,
-            static_cast<Elem*>(grad), grad_stride);
+    BackwardArgs p = {logits, row_stride, targets, allowed, allowed_stride, int(V), top_k, inv_temp,
+                      lse, entropy, g_logp, g_lse, g_entropy, g_top, top_ids, grad, grad_stride, 1, 0};
+    int64_t want = 32768;
+    while (want > 2048 && T * ((V + want - 1) / want) < 8 * int64_t(num_sms)) want /= 2;
+    p.part_length = int(want);
+    p.parts = int((V + want - 1) / want);
+    auto go = [&](auto kernel) {
+        kernel<<<unsigned(T * p.parts), kThreads, 0, stream>>>(p);
         return cudaGetLastError();
     };
-    if (type == ElemType::kBf16) return go(__nv_bfloat16());
-    if (type == ElemType::kFp16) return go(__half());
-    return go(float());
+    if (type == ElemType::kBf16)
+        return allowed ? go(token_logprobs_backward_kernel<__nv_bfloat16, true>)
+                       : go(token_logprobs_backward_kernel<__nv_bfloat16, false>);
+    if (type == ElemType::kFp16)
+        return allowed ? go(token_logprobs_backward_kernel<__half, true>)
+                       : go(token_logprobs_backward_kernel<__half, false>);
+    return allowed ? go(token_logprobs_backward_kernel<float, true>)
+                   : go(token_logprobs_backward_kernel<float, false>);
 }
 
 }  // namespace rlk

@@ -8,29 +8,13 @@
 // group.  Eight codes k = 8w .. 8w+7 make word w of a row: the even k in nibbles
 // 0..3, the odd k in nibbles 4..7, so that (word >> 4i) & 0x000f000f is the pair
 // (8w + 2i, 8w + 2i + 1) in the halves of a register.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "rlk_internal.h"
+#include "rlk_logits.cuh"
 
 namespace rlk {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename Elem>
-__device__ __forceinline__ Elem from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
-}
 
 // Bit position of code k of a word (k = 0..7).
 __host__ __device__ constexpr int code_shift(int k) { return 4 * ((k & 1) * 4 + k / 2); }
