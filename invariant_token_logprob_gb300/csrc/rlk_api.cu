@@ -918,7 +918,9 @@ rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits
     if (rlk::lmhead_take_error(&word) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::bwd_gemm_take_error(&word_bwd) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::lmhead_fp8b_take_error(&word_fp8b) != cudaSuccess) return RLK_ERR_CUDA;
-    word |= word_bwd | word_fp8b;
+    unsigned int word_w4 = 0;
+    if (rlk::linear_w4_take_error(&word_w4) != cudaSuccess) return RLK_ERR_CUDA;
+    word |= word_bwd | word_fp8b | word_w4;
     unsigned long long rows_logits = 0;
     if (rlk::take_target_range_rows(&rows) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::token_logprobs_take_range_rows(&rows_logits) != cudaSuccess) return RLK_ERR_CUDA;

@@ -236,6 +236,9 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
                              const void* scales, const uint8_t* zeros, int64_t T, int64_t N,
                              int64_t K, int group, void* y, ElemType y_type, int num_sms,
                              cudaStream_t stream);
+// Reads and clears the product kernel's per-device error word (bit 0: a bounded wait ran
+// out; bit 1: a teardown wait ran out).
+cudaError_t linear_w4_take_error(unsigned int* out);
 cudaError_t launch_quantize_w4(const void* W, ElemType type, int64_t N, int64_t K, int group,
                                uint32_t* codes, void* scales, uint8_t* zeros, cudaStream_t stream);
 cudaError_t launch_dequantize_w4(const uint32_t* codes, const void* scales, const uint8_t* zeros,

@@ -1,5 +1,5 @@
-// rlk_w4.cu -- weights in 4 bits with group scales: quantising, reading back, and
-// the product y = x . W^T.
+// rlk_w4.cu -- weights in 4 bits with group scales: quantising and reading back (the
+// product is in rlk_w4_linear.cu).
 //
 // Format: W [N][K] is cut along K into groups of `group` (32, 64 or 128) elements;
 // the last group of a row is short where group does not divide K (K % 32 == 0).
@@ -96,41 +96,6 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < int(sizeof(Out) / 2); ++j) reinterpret_cast<uint4*>(W + i * 8)[j] = o.v[j];
 }
 
-constexpr int kCols = 8;  // rows of x per thread
-
-// One row of W per thread, kCols rows of x: a group's products are summed in fp32
-// in the order of k, scaled, and the groups summed in order.
-template <typename Elem, typename Out>
-__global__ void __launch_bounds__(kThreads)
-    linear_w4_kernel(const Elem* __restrict__ x, const uint32_t* __restrict__ codes,
-                     const Elem* __restrict__ scales, const uint8_t* __restrict__ zeros, int64_t T,
-                     int64_t N, int K, int group, int num_groups, Out* __restrict__ y) {
-    const int64_t n = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t t0 = int64_t(blockIdx.y) * kCols;
-    if (n >= N) return;
-    float acc[kCols] = {};
-    for (int g = 0; g < num_groups; ++g) {
-        const float s = to_float(scales[n * num_groups + g]);
-        const int z = zeros ? zeros[n * num_groups + g] : 8;
-        float part[kCols] = {};
-        for (int k = g * group; k < min((g + 1) * group, K); k += 8) {
-            const uint32_t word = codes[n * (K / 8) + k / 8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float w = float(int((word >> code_shift(j)) & 15u) - z);
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (t0 + c < T) part[c] = fmaf(w, to_float(x[(t0 + c) * K + k + j]), part[c]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = fmaf(s, part[c], acc[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kCols; ++c)
-        if (t0 + c < T) y[(t0 + c) * N + n] = from_float<Out>(acc[c]);
-}
-
 template <typename Elem>
 cudaError_t quantize(const void* W, int64_t N, int64_t K, int group, uint32_t* codes, void* scales,
                      uint8_t* zeros, cudaStream_t stream) {
@@ -156,16 +121,6 @@ cudaError_t dequantize(const uint32_t* codes, const void* scales, const uint8_t*
     return cudaGetLastError();
 }
 
-template <typename Elem, typename Out>
-cudaError_t linear(const void* x, const uint32_t* codes, const void* scales, const uint8_t* zeros,
-                   int64_t T, int64_t N, int64_t K, int group, void* y, cudaStream_t stream) {
-    const dim3 grid(unsigned((N + kThreads - 1) / kThreads), unsigned((T + kCols - 1) / kCols));
-    linear_w4_kernel<Elem, Out><<<grid, kThreads, 0, stream>>>(
-        static_cast<const Elem*>(x), codes, static_cast<const Elem*>(scales), zeros, T, N, int(K),
-        group, int((K + group - 1) / group), static_cast<Out*>(y));
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_quantize_w4(const void* W, ElemType type, int64_t N, int64_t K, int group,
@@ -185,20 +140,6 @@ cudaError_t launch_dequantize_w4(const uint32_t* codes, const void* scales, cons
                                                                stream);
     return wide ? dequantize<__half, float>(codes, scales, zeros, N, K, group, W, stream)
                 : dequantize<__half, __half>(codes, scales, zeros, N, K, group, W, stream);
-}
-
-cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes,
-                             const void* scales, const uint8_t* zeros, int64_t T, int64_t N,
-                             int64_t K, int group, void* y, ElemType y_type, int num_sms,
-                             cudaStream_t stream) {
-    (void)num_sms;
-    const bool wide = y_type == ElemType::kFp32;
-    if (type == ElemType::kBf16)
-        return wide ? linear<__nv_bfloat16, float>(x, codes, scales, zeros, T, N, K, group, y, stream)
-                    : linear<__nv_bfloat16, __nv_bfloat16>(x, codes, scales, zeros, T, N, K, group,
-                                                           y, stream);
-    return wide ? linear<__half, float>(x, codes, scales, zeros, T, N, K, group, y, stream)
-                : linear<__half, __half>(x, codes, scales, zeros, T, N, K, group, y, stream);
 }
 
 }  // namespace rlk

@@ -1,0 +1,587 @@
+// rlk_w4_linear.cu -- y [T][N] = x [T][K] . W^T for a weight in 4 bits with group scales
+// (the format of rlk_w4.cu), on the tensor cores:
+//   y[t][n] = sum_g s[n][g] * sum_{k in g} (q[n][k] - z[n][g]) x[t][k]
+// q - z is a whole number up to 15 in magnitude, exact in bf16 and fp16, so a group's sum
+// runs on the tensor core on 16-bit operands with exact products, and the group's scale
+// meets it once, in fp32, on the CUDA cores.
+//
+// What bounds it: the codes, N K / 2 bytes, read once.  x is small.  The codes must become
+// 16-bit numbers on the way (11 instructions per 8 codes), so a plain row-times-vector
+// kernel would spend twice the instructions on the products alone; and a tile of numbers
+// written to shared memory for the tensor core and read back by it would take more
+// shared-memory time than the codes take from HBM.  So the tile goes through tensor memory:
+// a thread owns one row of a 128-row tile, turns the row's codes into numbers in registers
+// and stores them to its TMEM lane, from where they are the A operand.  x is B (N = the
+// rows of x, 16, 32 or 64).
+//
+// One CTA per SM, 10 warps:
+//   warp 0      TMA producer: stages of 256 k, the tile's codes (16 KB) and x
+//   warp 1      MMA issuer: per block of 128 k and group its MMAs into a D buffer, fresh
+//   warps 2..9  two warpgroups, the first takes the even blocks, the second the odd ones:
+//               codes -> numbers -> A buffer; then, while the tensor core works on that
+//               block, the products of the block before: acc = fma(D, scale, acc), one
+//               accumulator per row of x.  At the end the second hands its sums to the first.
+// Two A and two D buffers per warpgroup fill tensor memory (512 columns), and no separate
+// barrier frees a buffer: a warpgroup writes block b into the buffers of block b - 2 after
+// it has read that block's products.
+//
+// Few tiles (N of some thousands): the K range of a tile is cut into `splits` parts, one
+// per CTA of a cluster, whose sums meet through distributed shared memory in the order of k.
+// The cut follows from N and K; tiles, stages and blocks are fixed; a row of x is one column
+// of D.  So a row's bits do not depend on T.
+//
+// Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
+#include "rlk_internal.h"
+#include "rlk_logits.cuh"
+#include "rlk_sm103.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int kTileN = 128;                  // rows of W per tile = UMMA M = TMEM lanes
+constexpr int kStageK = 256;                 // k per stage
+constexpr int kBlockK = 128;                 // k per A buffer
+constexpr int kCodeBytes = kTileN * kStageK / 2;
+constexpr int kDequantWarps = 8;
+constexpr int kThreads = 32 * (2 + kDequantWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kABufCols = kBlockK / 2;  // two 16-bit numbers per column
+constexpr uint32_t kDBase = 4 * kABufCols;   // D buffers behind the four A buffers
+constexpr uint32_t kDBufCols = 64;           // groups per block times columns
+constexpr int kMaxSplits = 8;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 200000000ull;
+
+__device__ unsigned int g_w4_error;  // bit 0: a wait ran out; bit 1: a teardown wait ran out
+
+// Rows of x a CTA takes at a time, and the MMA's N (at least 16).
+constexpr int mma_n(int cols) { return cols < 16 ? 16 : cols; }
+constexpr int stage_bytes(int cols) { return kCodeBytes + mma_n(cols) * kStageK * 2; }
+constexpr int stages(int cols) { return cols <= 16 ? 7 : cols == 32 ? 5 : 4; }
+constexpr int barriers(int cols) { return 2 * stages(cols) + 8 + 1; }
+// The exchange buffer: the second warpgroup's sums.
+constexpr int exchange_bytes(int cols) { return cols * kTileN * 4; }
+constexpr size_t smem_bytes(int cols) {
+    return 1024 + size_t(stages(cols)) * stage_bytes(cols) + exchange_bytes(cols) +
+           barriers(cols) * 8 + 16;
+}
+static_assert(smem_bytes(64) <= 227 * 1024 && smem_bytes(32) <= 227 * 1024 &&
+                  smem_bytes(16) <= 227 * 1024,
+              "shared memory per CTA");
+static_assert((64 + kMaxSplits) * kTileN * 4 <= stages(8) * stage_bytes(8) &&
+                  (64 + kMaxSplits) * kTileN * 4 <= stages(64) * stage_bytes(64),
+              "the parts' sums take the stages' place");
+
+struct Args {
+    const void* scales;
+    const uint8_t* zeros;
+    void* y;
+    int64_t T;
+    int N, num_groups;
+    int chunks;        // of `cols` rows of x
+    int items;         // tiles * chunks
+    int num_stages;    // of the whole K
+    int splits;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
+                                             volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    uint32_t spins = 0;
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((++spins & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                atomicOr(&g_w4_error, 1u);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > kDrainLimitNs) {
+            atomicOr(&g_w4_error, 2u);
+            return;
+        }
+    }
+}
+
+// One lane waits, the warp learns the outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int lane) {
+    int got = 1;
+    if (lane == 0) got = wait_bounded(bar, parity, abort_flag) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+
+// Whole numbers 0..15 next to a constant whose last place is 1 (bf16: 128, fp16: 1024): the
+// code sits in the low bits of the pattern; subtracting the constant plus the zero point
+// leaves q - z, exactly.
+__device__ __forceinline__ uint32_t base_pattern(__nv_bfloat16) { return 0x43004300u; }
+__device__ __forceinline__ uint32_t base_pattern(__half) { return 0x64006400u; }
+__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b, __half) {
+    const __half2 r =
+        __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 32 codes (four words) as 16 registers of two numbers, in the order of k.
+template <typename Elem>
+__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero_pattern,
+                                        uint32_t (&r)[16]) {
+    const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+    const uint32_t base = base_pattern(Elem());
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r[4 * i + j] = minus(((w[i] >> (4 * j)) & 0x000f000fu) | base, zero_pattern, Elem());
+}
+
+template <int kCols>
+__device__ __forceinline__ void load_products(uint32_t taddr, uint32_t (&r)[kCols < 16 ? 8 : 16]) {
+    if constexpr (kCols < 16)
+        tmem_ld8(taddr, r);
+    else
+        tmem_ld16(taddr, r);
+}
+
+// Per block of 128 k: this row's scales (and zero points), one per group.
+template <typename Elem, int kGroups, bool kZeros>
+struct BlockScales {
+    float s[kGroups];
+    uint32_t z[kGroups];  // the pattern to subtract, in both halves
+    __device__ __forceinline__ void load(const Elem* scales, const uint8_t* zeros, int g,
+                                         int num_groups, bool live) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const bool in = live && g + i < num_groups;
+            s[i] = in ? to_float(scales[g + i]) : 0.0f;
+            const uint32_t zero = kZeros ? (in ? uint32_t(zeros[g + i]) : 0u) : 8u;
+            z[i] = base_pattern(Elem()) + zero * 0x00010001u;
+        }
+    }
+};
+
+template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_w4_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                     const __grid_constant__ CUtensorMap tmap_x, const Args p) {
+    constexpr int kN = mma_n(kCols);
+    constexpr int kStages = stages(kCols);
+    constexpr int kStageBytes = stage_bytes(kCols);
+    constexpr uint32_t kIdesc =
+        std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
+    static_assert(kGroups * kN <= int(kDBufCols), "a D buffer");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t stage0 = raw_addr + pad;
+    float* exchange = reinterpret_cast<float*>(smem + size_t(kStages) * kStageBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(exchange) +
+                                                 exchange_bytes(kCols));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + barriers(kCols));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    auto full_bar = [&](int s) { return smem_u32(bars + s); };
+    auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
+    auto a_full = [&](int wg, int buf) { return smem_u32(bars + 2 * kStages + wg * 2 + buf); };
+    auto d_full = [&](int wg, int buf) { return smem_u32(bars + 2 * kStages + 4 + wg * 2 + buf); };
+    const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), kDequantWarps + 1);  // the codes' readers, and the MMAs
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(a_full(i >> 1, i & 1), kDequantWarps / 2);
+            mbar_init(d_full(i >> 1, i & 1), 1);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_w);
+        tma_prefetch_desc(&tmap_x);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // A cluster takes one item, a CTA alone every gridDim.x-th; either way these stages of K.
+    const int rank = p.splits > 1 ? int(cluster_ctarank()) : 0;
+    const int first_item = p.splits > 1 ? int(blockIdx.x) / p.splits : int(blockIdx.x);
+    const int item_step = p.splits > 1 ? p.items : int(gridDim.x);
+    const int k_first = int(int64_t(p.num_stages) * rank / p.splits);
+    const int k_last = int(int64_t(p.num_stages) * (rank + 1) / p.splits);
+
+    float acc[kCols];  // of the dequant warps
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int issued = 0;
+            bool ok = true;
+            for (int item = first_item; ok && item < p.items; item += item_step) {
+                const int tile = item / p.chunks;
+                const int chunk = item - tile * p.chunks;
+                for (int ks = k_first; ks < k_last; ++ks) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = stage0 + stage * kStageBytes;
+                    mbar_arrive_expect_tx(full_bar(stage), kStageBytes);
+                    tma_load_2d(&tmap_w, full_bar(stage), at, ks * (kStageK / 2), tile * kTileN);
+#pragma unroll
+                    for (int i = 0; i < kStageK / 64; ++i)
+                        tma_load_2d(&tmap_x, full_bar(stage), at + kCodeBytes + i * kN * 128,
+                                    ks * kStageK + i * 64, chunk * kCols);
+                    ++issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {  // let the copies this thread started land before the CTA exits
+                const int first = issued > kStages ? issued - kStages : 0;
+                for (int i = first; i < issued; ++i)
+                    wait_drain(full_bar(i % kStages), uint32_t(i / kStages) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            bool ok = true;
+            for (int item = first_item; ok && item < p.items; item += item_step) {
+                for (int ks = k_first; ok && ks < k_last; ++ks) {
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t x_desc =
+                        sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
+#pragma unroll
+                    for (int wg = 0; wg < 2; ++wg) {
+                        if (!wait_bounded(a_full(wg, buf), buf_phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t a = tmem_base + (wg * 2 + buf) * kABufCols;
+                        const uint32_t d = tmem_base + kDBase + (wg * 2 + buf) * kDBufCols;
+#pragma unroll
+                        for (int i = 0; i < kBlockK / 16; ++i) {
+                            constexpr int kPerGroup = kBlockK / 16 / kGroups;
+                            const int kk = wg * kBlockK + i * 16;  // k inside the stage
+                            const uint64_t off =
+                                uint64_t(((kk / 64) * kN * 128 + (kk % 64) * 2) >> 4);
+                            umma_f16_tmem_a(d + (i / kPerGroup) * kN, a + i * 8, x_desc + off, kIdesc,
+                                            i % kPerGroup != 0 ? 1u : 0u);
+                        }
+                        umma_commit(d_full(wg, buf));
+                    }
+                    if (!ok) break;
+                    umma_commit(empty_bar(stage));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    buf ^= 1u;
+                    if (buf == 0) buf_phase ^= 1u;
+                }
+            }
+            umma_commit(drain_bar);  // no MMA may still run when TMEM is freed
+            wait_drain(drain_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ numbers and sums
+        const int q = warp & 3;            // TMEM lane quadrant this warp may access
+        const int wg = (warp - 2) >> 2;
+        const int row_in_tile = q * 32 + lane;
+        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true, first = true;
+        // After a wait that ran out a warp does no more work but keeps the barriers' count.
+        for (int item = first_item; item < p.items; item += item_step) {
+            const int tile = item / p.chunks;
+            const int chunk = item - tile * p.chunks;
+            const int n = tile * kTileN + row_in_tile;
+            const bool live = n < p.N;
+            const Elem* scales =
+                static_cast<const Elem*>(p.scales) + int64_t(live ? n : 0) * p.num_groups;
+            const uint8_t* zeros = kZeros ? p.zeros + int64_t(live ? n : 0) * p.num_groups : nullptr;
+#pragma unroll
+            for (int t = 0; t < kCols; ++t) acc[t] = 0.0f;
+            BlockScales<Elem, kGroups, kZeros> now, next;
+            next.load(scales, zeros, (k_first * 2 + wg) * kGroups, p.num_groups, live);
+            float prev[kGroups];  // the scales of the block whose products come next
+
+            // the products of the block in D buffer `b`, scaled into the sums
+            auto take_products = [&](uint32_t b, uint32_t parity) {
+                if (!warp_wait(d_full(wg, b), parity, abort_flag, lane)) return false;
+                tc_fence_after_sync();
+                constexpr int kChunk = kCols < 16 ? 8 : 16;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                    for (int c = 0; c < kCols; c += kChunk) {
+                        uint32_t r[kChunk];
+                        load_products<kCols>(
+                            lane_base + kDBase + (wg * 2 + b) * kDBufCols + g * kN + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < kChunk; ++j)
+                            acc[c + j] = fmaf(__uint_as_float(r[j]), prev[g], acc[c + j]);
+                    }
+                return true;
+            };
+
+            for (int ks = k_first; ok && ks < k_last; ++ks) {
+                now = next;
+                if (ks + 1 < k_last)
+                    next.load(scales, zeros, ((ks + 1) * 2 + wg) * kGroups, p.num_groups, live);
+                ok = warp_wait(full_bar(stage), phase, abort_flag, lane);
+                if (!ok) break;
+                // 16-byte pieces of the row, swizzled by its place among eight
+                const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
+                uint4 words[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    words[c] = *reinterpret_cast<const uint4*>(
+                        codes + (((wg * 4 + c) ^ (row_in_tile & 7)) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[16];
+                    numbers<Elem>(words[c], now.z[c * kGroups / 4], r);
+                    tmem_st16(lane_base + (wg * 2 + buf) * kABufCols + c * 16, r);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty_bar(stage));
+                    mbar_arrive(a_full(wg, buf));
+                }
+                // block ks - 1 lies in the other buffer, whose phase turns with buffer 0
+                if (ks > k_first)
+                    ok = take_products(buf ^ 1u, buf == 0 ? buf_phase ^ 1u : buf_phase);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) prev[g] = now.s[g];
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                buf ^= 1u;
+                if (buf == 0) buf_phase ^= 1u;
+            }
+            if (ok) ok = take_products(buf ^ 1u, buf == 0 ? buf_phase ^ 1u : buf_phase);
+
+            // The second warpgroup's sums meet the first's.
+            if (!first) named_barrier_sync(2, 32 * kDequantWarps);  // the last ones are read
+            if (wg == 1) {
+#pragma unroll
+                for (int t = 0; t < kCols; ++t) exchange[t * kTileN + row_in_tile] = acc[t];
+            }
+            named_barrier_sync(1, 32 * kDequantWarps);
+            if (wg == 0) {
+#pragma unroll
+                for (int t = 0; t < kCols; ++t) acc[t] += exchange[t * kTileN + row_in_tile];
+                if (p.splits == 1 && live && ok) {
+                    Out* y = static_cast<Out*>(p.y) + int64_t(chunk) * kCols * p.N + n;
+                    const int64_t rows = p.T - int64_t(chunk) * kCols;
+#pragma unroll
+                    for (int t = 0; t < kCols; ++t)
+                        if (t < rows) y[int64_t(t) * p.N] = from_float<Out>(acc[t]);
+                }
+            }
+            first = false;
+        }
+    }
+
+    if (p.splits > 1) {
+        // Each CTA ends a share of the columns: sums of all parts, in the order of k, in
+        // the place of the stages.
+        float* parts = reinterpret_cast<float*>(smem);
+        cluster_sync();  // no CTA uses its stages any more
+        const int share = (kCols + p.splits - 1) / p.splits;
+        const int wg_row = (warp & 3) * 32 + lane;
+        if (warp >= 2 && warp < 6) {
+#pragma unroll
+            for (int t = 0; t < kCols; ++t) {
+                const int owner = t / share;
+                const uint32_t to = mapa_shared(
+                    smem_u32(parts + (rank * share + (t - owner * share)) * kTileN + wg_row), owner);
+                st_shared_cluster_u32(to, __float_as_uint(acc[t]));
+            }
+        }
+        cluster_sync();
+        const int tile = first_item / p.chunks;
+        const int chunk = first_item - tile * p.chunks;
+        const int n = tile * kTileN + wg_row;
+        if (warp >= 2 && n < p.N) {
+            for (int i = (warp - 2) >> 2; i < share; i += 2) {
+                const int64_t t = int64_t(chunk) * kCols + rank * share + i;
+                if (rank * share + i >= kCols || t >= p.T) break;
+                float sum = parts[i * kTileN + wg_row];
+                for (int s = 1; s < p.splits; ++s)
+                    sum += parts[(s * share + i) * kTileN + wg_row];
+                static_cast<Out*>(p.y)[t * p.N + n] = from_float<Out>(sum);
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem_base, kTmemCols);
+    }
+}
+
+// Parts of K per tile: the fewest rounds of stages over the SMs, counting a few stages'
+// time for a part's beginning and end.  A function of the weight's shape alone.
+int num_splits(int tiles, int num_stages, int num_sms) {
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; s <= kMaxSplits && s <= num_stages; ++s) {
+        const int64_t rounds = (int64_t(tiles) * s + num_sms - 1) / num_sms;
+        const int64_t cost = rounds * ((num_stages + s - 1) / s + 3 + (s > 1 ? 1 : 0));
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, int num_sms,
+                   cudaStream_t stream) {
+    auto kernel = linear_w4_kernel<Elem, Out, kCols, kGroups, kZeros>;
+    constexpr size_t smem = smem_bytes(kCols);
+    static int configured[64];  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        configured[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(p.splits);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    const int64_t ctas = p.splits > 1 ? int64_t(p.items) * p.splits
+                                      : (p.items < num_sms ? p.items : num_sms);
+    cfg.gridDim = dim3(unsigned(ctas), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+// Columns per pass: the rows of x, at most what a D buffer holds of each group.
+int columns(int64_t T, int groups_per_block) {
+    const int most = int(kDBufCols) / groups_per_block;
+    const int want = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    return want < most ? want : most;
+}
+
+template <typename Elem, typename Out, bool kZeros>
+cudaError_t launch_cols(int cols, int groups, const CUtensorMap& tw, const CUtensorMap& tx,
+                        const Args& p, int num_sms, cudaStream_t s) {
+    if (groups == 1) {
+        if (cols == 8) return launch<Elem, Out, 8, 1, kZeros>(tw, tx, p, num_sms, s);
+        if (cols == 16) return launch<Elem, Out, 16, 1, kZeros>(tw, tx, p, num_sms, s);
+        if (cols == 32) return launch<Elem, Out, 32, 1, kZeros>(tw, tx, p, num_sms, s);
+        return launch<Elem, Out, 64, 1, kZeros>(tw, tx, p, num_sms, s);
+    }
+    if (groups == 2) {
+        if (cols == 8) return launch<Elem, Out, 8, 2, kZeros>(tw, tx, p, num_sms, s);
+        if (cols == 16) return launch<Elem, Out, 16, 2, kZeros>(tw, tx, p, num_sms, s);
+        return launch<Elem, Out, 32, 2, kZeros>(tw, tx, p, num_sms, s);
+    }
+    if (cols == 8) return launch<Elem, Out, 8, 4, kZeros>(tw, tx, p, num_sms, s);
+    return launch<Elem, Out, 16, 4, kZeros>(tw, tx, p, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes,
+                             const void* scales, const uint8_t* zeros, int64_t T, int64_t N,
+                             int64_t K, int group, void* y, ElemType y_type, int num_sms,
+                             cudaStream_t stream) {
+    const int groups = kBlockK / group;
+    const int cols = columns(T, groups);
+    const int64_t tiles = (N + kTileN - 1) / kTileN;
+    const int64_t chunks = (T + cols - 1) / cols;
+    if (tiles * chunks * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
+    Args p = {scales, zeros, y, T, int(N), int((K + group - 1) / group), int(chunks),
+              int(tiles * chunks), int((K + kStageK - 1) / kStageK), 1};
+    p.splits = num_splits(int(tiles), p.num_stages, num_sms);
+    CUtensorMap tw, tx;
+    // (fp16 and bf16 are copied alike)
+    if (!encode_tensor_map_2d(&tw, codes, uint64_t(K / 2), uint64_t(N), uint64_t(K / 2),
+                              kStageK / 2, kTileN, true) ||
+        !encode_tensor_map_2d(&tx, x, uint64_t(K), uint64_t(T), uint64_t(K) * 2, 64,
+                              uint32_t(mma_n(cols)), false))
+        return cudaErrorInvalidValue;
+    auto go = [&](auto elem, auto out) {
+        using Elem = decltype(elem);
+        using Out = decltype(out);
+        return zeros ? launch_cols<Elem, Out, true>(cols, groups, tw, tx, p, num_sms, stream)
+                     : launch_cols<Elem, Out, false>(cols, groups, tw, tx, p, num_sms, stream);
+    };
+    const bool wide = y_type == ElemType::kFp32;
+    if (type == ElemType::kBf16)
+        return wide ? go(__nv_bfloat16(), float()) : go(__nv_bfloat16(), __nv_bfloat16());
+    return wide ? go(__half(), float()) : go(__half(), __half());
+}
+
+cudaError_t linear_w4_take_error(unsigned int* out) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_w4_error, sizeof v);
+    if (e != cudaSuccess) return e;
+    if (v) e = cudaMemcpyToSymbol(g_w4_error, &zero, sizeof zero);
+    *out = v;
+    return e;
+}
+
+}  // namespace rlk
