@@ -21,6 +21,17 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // Block until the grids this one depends on have completed and their memory
 // is visible (a no-op when the launch did not allow programmatic overlap).

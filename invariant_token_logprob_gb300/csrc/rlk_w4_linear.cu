@@ -157,20 +157,27 @@ __device__ __forceinline__ void load_products(uint32_t taddr, uint32_t (&r)[kCol
         tmem_ld16(taddr, r);
 }
 
-// Per block of 128 k: this row's scales (and zero points), one per group.
+// Per block of 128 k: this row's scales (and zero points), one per group, as they lie in
+// memory: they are loaded a block ahead, and a conversion here would wait for them.
 template <typename Elem, int kGroups, bool kZeros>
 struct BlockScales {
-    float s[kGroups];
-    uint32_t z[kGroups];  // the pattern to subtract, in both halves
+    Elem s[kGroups];
+    uint8_t z[kGroups];
     __device__ __forceinline__ void load(const Elem* scales, const uint8_t* zeros, int g,
                                          int num_groups, bool live) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const bool in = live && g + i < num_groups;
-            s[i] = in ? to_float(scales[g + i]) : 0.0f;
-            const uint32_t zero = kZeros ? (in ? uint32_t(zeros[g + i]) : 0u) : 8u;
-            z[i] = base_pattern(Elem()) + zero * 0x00010001u;
+            s[i] = from_float<Elem>(0.0f);
+            z[i] = 0;
+            if (live && g + i < num_groups) {
+                s[i] = scales[g + i];
+                if (kZeros) z[i] = zeros[g + i];
+            }
         }
+    }
+    // The pattern to subtract, in both halves.
+    __device__ __forceinline__ uint32_t zero_pattern(int i) const {
+        return base_pattern(Elem()) + (kZeros ? uint32_t(z[i]) : 8u) * 0x00010001u;
     }
 };
 
@@ -276,26 +283,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
-            bool ok = true;
-            for (int item = first_item; ok && item < p.items; item += item_step) {
-                for (int ks = k_first; ok && ks < k_last; ++ks) {
-                    if (!wait_bounded(full_bar(stage), phase, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint64_t x_desc =
-                        sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
+        // The whole warp runs the loop and one elected lane issues: addresses and
+        // descriptors then are warp-uniform, which single-lane code does not let them be.
+        const bool leader = elect_one();
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int item = first_item; ok && item < p.items; item += item_step) {
+            for (int ks = k_first; ok && ks < k_last; ++ks) {
+                ok = warp_wait(full_bar(stage), phase, abort_flag, lane);
+                const uint64_t x_desc = sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
 #pragma unroll
-                    for (int wg = 0; wg < 2; ++wg) {
-                        if (!wait_bounded(a_full(wg, buf), buf_phase, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        const uint32_t a = tmem_base + (wg * 2 + buf) * kABufCols;
-                        const uint32_t d = tmem_base + kDBase + (wg * 2 + buf) * kDBufCols;
+                for (int wg = 0; wg < 2; ++wg) {
+                    if (ok) ok = warp_wait(a_full(wg, buf), buf_phase, abort_flag, lane);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t a = tmem_base + (wg * 2 + buf) * kABufCols;
+                    const uint32_t d = tmem_base + kDBase + (wg * 2 + buf) * kDBufCols;
+                    if (leader) {
 #pragma unroll
                         for (int i = 0; i < kBlockK / 16; ++i) {
                             constexpr int kPerGroup = kBlockK / 16 / kGroups;
@@ -306,17 +310,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             i % kPerGroup != 0 ? 1u : 0u);
                         }
                         umma_commit(d_full(wg, buf));
+                        if (wg == 1) umma_commit(empty_bar(stage));
                     }
-                    if (!ok) break;
-                    umma_commit(empty_bar(stage));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    buf ^= 1u;
-                    if (buf == 0) buf_phase ^= 1u;
+                    __syncwarp();
                 }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                buf ^= 1u;
+                if (buf == 0) buf_phase ^= 1u;
             }
+        }
+        if (leader) {
             umma_commit(drain_bar);  // no MMA may still run when TMEM is freed
             wait_drain(drain_bar, 0);
         }
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r[16];
-                    numbers<Elem>(words[c], now.z[c * kGroups / 4], r);
+                    numbers<Elem>(words[c], now.zero_pattern(c * kGroups / 4), r);
                     tmem_st16(lane_base + (wg * 2 + buf) * kABufCols + c * 16, r);
                 }
                 tmem_st_wait();
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ks > k_first)
                     ok = take_products(buf ^ 1u, buf == 0 ? buf_phase ^ 1u : buf_phase);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) prev[g] = now.s[g];
+                for (int g = 0; g < kGroups; ++g) prev[g] = to_float(now.s[g]);
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
