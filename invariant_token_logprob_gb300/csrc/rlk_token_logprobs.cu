@@ -60,37 +60,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Two fp32 values in a register pair and the packed operations on them, each half
-// rounded like the scalar operation.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 pack2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // Sums about a reference m (a raw logit; -FLT_MAX, the identity, before any token), in
 // units of log 2: t = (x - m) * inv_temp * log2 e, s = sum 2^t, u = sum 2^t t.
 struct Sums {

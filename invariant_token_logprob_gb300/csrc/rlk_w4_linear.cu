@@ -14,20 +14,27 @@
 // and stores them to its TMEM lane, from where they are the A operand.  x is B (N = the
 // rows of x, 16, 32 or 64).
 //
-// One CTA per SM, 10 warps:
-//   warp 0      TMA producer: stages of 256 k, the tile's codes (16 KB) and x
-//   warp 1      MMA issuer: per block of 128 k and group its MMAs into a D buffer, fresh
-//   warps 2..9  two warpgroups, the first takes the even blocks, the second the odd ones:
-//               codes -> numbers -> A buffer; then, while the tensor core works on that
-//               block, the products of the block before: acc = fma(D, scale, acc), one
-//               accumulator per row of x.  At the end the second hands its sums to the first.
-// Two A and two D buffers per warpgroup fill tensor memory (512 columns), and no separate
-// barrier frees a buffer: a warpgroup writes block b into the buffers of block b - 2 after
-// it has read that block's products.
+// One CTA per SM, 19 warps:
+//   warp 0       TMA producer: stages of 256 k, the tile's codes (16 KB) and x
+//   warp 1       MMA issuer: per stage and group its MMAs into a D buffer, fresh
+//   warps 2..17  two teams of eight, the first takes the even stages of a tile, the second
+//                the odd ones.  A row has two threads per team: each turns its half of the
+//                stage's codes into numbers and stores them to the team's A buffer, and
+//                each keeps the running sums of half the rows of x:
+//                acc = fma(D, scale, acc) once the stage's products are there.  At the end
+//                the second team hands its sums to the first.
+//   warp 18      copies the scales and zero points, 32 groups of the tile's rows at a time,
+//                into shared memory, where a thread finds its row's: straight from global
+//                memory every lane of a warp would touch another row, 32 sectors a load.
+//                Word by word, so that any number of groups per row will do: a row's words
+//                are those that hold its groups, its values lie from its own shift on
+// No barrier frees an A or D buffer: a team stores a stage's numbers only after it has
+// waited for the products of its stage before, and lets the MMAs of a stage start only
+// after it has read them.  One team's numbers overlap the other's MMAs.
 //
 // Few tiles (N of some thousands): the K range of a tile is cut into `splits` parts, one
 // per CTA of a cluster, whose sums meet through distributed shared memory in the order of k.
-// The cut follows from N and K; tiles, stages and blocks are fixed; a row of x is one column
+// The cut follows from N and K; tiles, stages and teams are fixed; a row of x is one column
 // of D.  So a row's bits do not depend on T.
 //
 // Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
@@ -40,30 +47,42 @@ namespace {
 
 constexpr int kTileN = 128;                  // rows of W per tile = UMMA M = TMEM lanes
 constexpr int kStageK = 256;                 // k per stage
-constexpr int kBlockK = 128;                 // k per A buffer
 constexpr int kCodeBytes = kTileN * kStageK / 2;
-constexpr int kDequantWarps = 8;
-constexpr int kThreads = 32 * (2 + kDequantWarps);
+constexpr int kTeams = 2;
+constexpr int kTeamWarps = 8;
+constexpr int kNumberWarps = kTeams * kTeamWarps;
+constexpr int kNumberThreads = 32 * kNumberWarps;
+constexpr int kThreads = 32 * (3 + kNumberWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kABufCols = kBlockK / 2;  // two 16-bit numbers per column
-constexpr uint32_t kDBase = 4 * kABufCols;   // D buffers behind the four A buffers
-constexpr uint32_t kDBufCols = 64;           // groups per block times columns
+constexpr uint32_t kABufCols = kStageK / 2;  // two 16-bit numbers per column
+constexpr uint32_t kDBase = kTeams * kABufCols;
+constexpr uint32_t kDBufCols = 128;          // groups per stage times columns
+static_assert(kDBase + kTeams * kDBufCols == kTmemCols, "tensor memory");
 constexpr int kMaxSplits = 8;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 
 __device__ unsigned int g_w4_error;  // bit 0: a wait ran out; bit 1: a teardown wait ran out
 
+// Scales and zero points of kScaleGroups groups of a tile's rows, in words (one more than
+// they fill, for rows that start inside a word).  The rows lie an odd number of words apart,
+// so 32 rows' values of one group lie in 32 banks.
+constexpr int kScaleGroups = 32;
+constexpr int kScaleWords = kScaleGroups / 2 + 1;
+constexpr int kZeroWords = kScaleGroups / 4 + 1;
+static_assert(kScaleWords % 2 == 1 && kZeroWords % 2 == 1, "banks");
+constexpr int kScaleBytes = kTileN * (kScaleWords + kZeroWords) * 4;
+
 // Rows of x a CTA takes at a time, and the MMA's N (at least 16).
 constexpr int mma_n(int cols) { return cols < 16 ? 16 : cols; }
 constexpr int stage_bytes(int cols) { return kCodeBytes + mma_n(cols) * kStageK * 2; }
-constexpr int stages(int cols) { return cols <= 16 ? 7 : cols == 32 ? 5 : 4; }
-constexpr int barriers(int cols) { return 2 * stages(cols) + 8 + 1; }
-// The exchange buffer: the second warpgroup's sums.
+constexpr int stages(int cols) { return cols <= 16 ? 7 : cols == 32 ? 5 : 3; }
+constexpr int barriers(int cols) { return 2 * stages(cols) + 2 * kTeams + 4 + 1; }
+// The exchange buffer: the second team's sums.
 constexpr int exchange_bytes(int cols) { return cols * kTileN * 4; }
 constexpr size_t smem_bytes(int cols) {
     return 1024 + size_t(stages(cols)) * stage_bytes(cols) + exchange_bytes(cols) +
-           barriers(cols) * 8 + 16;
+           2 * kScaleBytes + barriers(cols) * 8 + 16;
 }
 static_assert(smem_bytes(64) <= 227 * 1024 && smem_bytes(32) <= 227 * 1024 &&
                   smem_bytes(16) <= 227 * 1024,
@@ -84,6 +103,7 @@ struct Args {
     int splits;
 };
 
+// By whole warps or single lanes; the usual wait finds its phase complete.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -110,14 +130,6 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
             return;
         }
     }
-}
-
-// One lane waits, the warp learns the outcome.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          int lane) {
-    int got = 1;
-    if (lane == 0) got = wait_bounded(bar, parity, abort_flag) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
 // Whole numbers 0..15 next to a constant whose last place is 1 (bf16: 128, fp16: 1024): the
@@ -149,45 +161,38 @@ __device__ __forceinline__ void numbers(const uint4& words, uint32_t zero_patter
             r[4 * i + j] = minus(((w[i] >> (4 * j)) & 0x000f000fu) | base, zero_pattern, Elem());
 }
 
-template <int kCols>
-__device__ __forceinline__ void load_products(uint32_t taddr, uint32_t (&r)[kCols < 16 ? 8 : 16]) {
-    if constexpr (kCols < 16)
-        tmem_ld8(taddr, r);
-    else
-        tmem_ld16(taddr, r);
+// N (4, 8 or a multiple of 16) fp32 columns of this thread's lane, scaled into acc.
+template <int N>
+__device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&acc)[N / 2]) {
+    constexpr int kPiece = N < 16 ? N : 16;
+    const F2 s = pack2(scale, scale);
+#pragma unroll
+    for (int c = 0; c < N; c += kPiece) {
+        uint32_t r[kPiece];
+        if constexpr (kPiece == 4)
+            tmem_ld4(taddr + c, r);
+        else if constexpr (kPiece == 8)
+            tmem_ld8(taddr + c, r);
+        else
+            tmem_ld16(taddr + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < kPiece; j += 2)
+            acc[(c + j) / 2] = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s,
+                                    acc[(c + j) / 2]);
+    }
 }
 
-// Per block of 128 k: this row's scales (and zero points), one per group, as they lie in
-// memory: they are loaded a block ahead, and a conversion here would wait for them.
-template <typename Elem, int kGroups, bool kZeros>
-struct BlockScales {
-    Elem s[kGroups];
-    uint8_t z[kGroups];
-    __device__ __forceinline__ void load(const Elem* scales, const uint8_t* zeros, int g,
-                                         int num_groups, bool live) {
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            s[i] = from_float<Elem>(0.0f);
-            z[i] = 0;
-            if (live && g + i < num_groups) {
-                s[i] = scales[g + i];
-                if (kZeros) z[i] = zeros[g + i];
-            }
-        }
-    }
-    // The pattern to subtract, in both halves.
-    __device__ __forceinline__ uint32_t zero_pattern(int i) const {
-        return base_pattern(Elem()) + (kZeros ? uint32_t(z[i]) : 8u) * 0x00010001u;
-    }
-};
-
+// kCols: rows of x at a time; kGroups: groups per stage.
 template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap tmap_w,
                      const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     constexpr int kN = mma_n(kCols);
+    constexpr int kMine = kCols / 2;  // running sums per thread
     constexpr int kStages = stages(kCols);
     constexpr int kStageBytes = stage_bytes(kCols);
+    constexpr int kChunkStages = kScaleGroups / kGroups;  // stages per chunk of scales
     constexpr uint32_t kIdesc =
         std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
     static_assert(kGroups * kN <= int(kDBufCols), "a D buffer");
@@ -196,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
     uint8_t* smem = smem_raw + pad;
     const uint32_t stage0 = raw_addr + pad;
-    float* exchange = reinterpret_cast<float*>(smem + size_t(kStages) * kStageBytes);
+    uint8_t* scale_bufs = smem + size_t(kStages) * kStageBytes;
+    float* exchange = reinterpret_cast<float*>(scale_bufs + 2 * kScaleBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(exchange) +
                                                  exchange_bytes(kCols));
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + barriers(kCols));
@@ -204,9 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
     auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
-    auto a_full = [&](int wg, int buf) { return smem_u32(bars + 2 * kStages + wg * 2 + buf); };
-    auto d_full = [&](int wg, int buf) { return smem_u32(bars + 2 * kStages + 4 + wg * 2 + buf); };
-    const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 8);
+    auto a_full = [&](int team) { return smem_u32(bars + 2 * kStages + team); };
+    auto d_full = [&](int team) { return smem_u32(bars + 2 * kStages + kTeams + team); };
+    auto s_full = [&](int buf) { return smem_u32(bars + 2 * kStages + 2 * kTeams + buf); };
+    auto s_empty = [&](int buf) { return smem_u32(bars + 2 * kStages + 2 * kTeams + 2 + buf); };
+    const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 2 * kTeams + 4);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -214,11 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), kDequantWarps + 1);  // the codes' readers, and the MMAs
+            mbar_init(empty_bar(s), kTeamWarps + 1);  // the codes' readers, and the MMAs
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(a_full(i >> 1, i & 1), kDequantWarps / 2);
-            mbar_init(d_full(i >> 1, i & 1), 1);
+        for (int i = 0; i < kTeams; ++i) {
+            mbar_init(a_full(i), kTeamWarps);
+            mbar_init(d_full(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 32);  // the copying warp's lanes
+            mbar_init(s_empty(i), kNumberWarps);
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -244,7 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int k_first = int(int64_t(p.num_stages) * rank / p.splits);
     const int k_last = int(int64_t(p.num_stages) * (rank + 1) / p.splits);
 
-    float acc[kCols];  // of the dequant warps
+    // Of the number warps: the team, the half of a stage's k and of the rows of x, the row.
+    const int team = (warp - 2) / kTeamWarps;
+    const int half = (warp - 2) / 4 & 1;
+    const int row_in_tile = (warp & 3) * 32 + lane;  // (a warp reaches the lanes of its quadrant)
+    F2 acc[kMine / 2];
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -286,40 +302,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs the loop and one elected lane issues: addresses and
         // descriptors then are warp-uniform, which single-lane code does not let them be.
         const bool leader = elect_one();
-        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        uint32_t stage = 0, phase = 0, team_phases = 0;  // (one bit per team)
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
-            for (int ks = k_first; ok && ks < k_last; ++ks) {
-                ok = warp_wait(full_bar(stage), phase, abort_flag, lane);
+            for (int ks = k_first; ks < k_last; ++ks) {
+                const int tm = (ks - k_first) & 1;
+                ok = wait_bounded(full_bar(stage), phase, abort_flag) &&
+                     wait_bounded(a_full(tm), (team_phases >> tm) & 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
                 const uint64_t x_desc = sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
+                const uint32_t a = tmem_base + tm * kABufCols;
+                const uint32_t d = tmem_base + kDBase + tm * kDBufCols;
+                if (leader) {
 #pragma unroll
-                for (int wg = 0; wg < 2; ++wg) {
-                    if (ok) ok = warp_wait(a_full(wg, buf), buf_phase, abort_flag, lane);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t a = tmem_base + (wg * 2 + buf) * kABufCols;
-                    const uint32_t d = tmem_base + kDBase + (wg * 2 + buf) * kDBufCols;
-                    if (leader) {
-#pragma unroll
-                        for (int i = 0; i < kBlockK / 16; ++i) {
-                            constexpr int kPerGroup = kBlockK / 16 / kGroups;
-                            const int kk = wg * kBlockK + i * 16;  // k inside the stage
-                            const uint64_t off =
-                                uint64_t(((kk / 64) * kN * 128 + (kk % 64) * 2) >> 4);
-                            umma_f16_tmem_a(d + (i / kPerGroup) * kN, a + i * 8, x_desc + off, kIdesc,
-                                            i % kPerGroup != 0 ? 1u : 0u);
-                        }
-                        umma_commit(d_full(wg, buf));
-                        if (wg == 1) umma_commit(empty_bar(stage));
+                    for (int i = 0; i < kStageK / 16; ++i) {
+                        constexpr int kPerGroup = kStageK / 16 / kGroups;
+                        const uint64_t off = uint64_t((i / 4 * kN * 128 + i % 4 * 32) >> 4);
+                        umma_f16_tmem_a(d + (i / kPerGroup) * kN, a + i * 8, x_desc + off, kIdesc,
+                                        i % kPerGroup != 0 ? 1u : 0u);
                     }
-                    __syncwarp();
+                    umma_commit(d_full(tm));
+                    umma_commit(empty_bar(stage));
                 }
+                __syncwarp();
+                team_phases ^= 1u << tm;
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                buf ^= 1u;
-                if (buf == 0) buf_phase ^= 1u;
             }
         }
         if (leader) {
@@ -327,105 +339,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_drain(drain_bar, 0);
         }
         __syncwarp();
+    } else if (warp == kNumberWarps + 2) {
+        // ------------------------------------------------------------ scales
+        uint32_t buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int item = first_item; ok && item < p.items; item += item_step) {
+            const int64_t n0 = int64_t(item / p.chunks) * kTileN;
+            const uint8_t* scales = static_cast<const uint8_t*>(p.scales);
+            const int64_t all = int64_t(p.N) * p.num_groups;
+            for (int ks = k_first; ks < k_last; ks += kChunkStages) {
+                ok = wait_bounded(s_empty(buf), buf_phase ^ 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t to = smem_u32(scale_bufs + buf * kScaleBytes);
+                const int64_t from = n0 * p.num_groups + ks * kGroups;  // the first row's first group
+                auto copy = [&](const uint8_t* base, int size, int words, uint32_t dst) {
+                    for (int i = lane; i < kTileN * words; i += 32) {
+                        const int r = i / words;
+                        const int64_t at =
+                            ((from + int64_t(r) * p.num_groups) * size & ~int64_t(3)) + (i - r * words) * 4;
+                        const int64_t left = all * size - at;
+                        const uint32_t bytes = left <= 0 ? 0u : left < 4 ? uint32_t(left) : 4u;
+                        copy_word_async(dst + i * 4, bytes ? base + at : base, bytes);
+                    }
+                };
+                copy(scales, 2, kScaleWords, to);
+                if (kZeros) copy(p.zeros, 1, kZeroWords, to + kTileN * kScaleWords * 4);
+                copy_words_arrive(s_full(buf));
+                buf ^= 1u;
+                if (buf == 0) buf_phase ^= 1u;
+            }
+        }
+        copy_words_wait_all();  // (no copy outlives the CTA)
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ numbers and sums
-        const int q = warp & 3;            // TMEM lane quadrant this warp may access
-        const int wg = (warp - 2) >> 2;
-        const int row_in_tile = q * 32 + lane;
-        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
-        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        const uint32_t lane_base = tmem_base + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t my_a = lane_base + team * kABufCols + half * (kABufCols / 2);
+        const uint32_t my_d = lane_base + kDBase + team * kDBufCols + half * kMine;
+        uint32_t stage = 0, phase = 0, d_phase = 0, buf = 0, buf_phase = 0;
         bool ok = true, first = true;
         // After a wait that ran out a warp does no more work but keeps the barriers' count.
         for (int item = first_item; item < p.items; item += item_step) {
             const int tile = item / p.chunks;
             const int chunk = item - tile * p.chunks;
             const int n = tile * kTileN + row_in_tile;
-            const bool live = n < p.N;
-            const Elem* scales =
-                static_cast<const Elem*>(p.scales) + int64_t(live ? n : 0) * p.num_groups;
-            const uint8_t* zeros = kZeros ? p.zeros + int64_t(live ? n : 0) * p.num_groups : nullptr;
+            const uint32_t row_first = uint32_t(n) * uint32_t(p.num_groups);  // (its low bits count)
 #pragma unroll
-            for (int t = 0; t < kCols; ++t) acc[t] = 0.0f;
-            BlockScales<Elem, kGroups, kZeros> now, next;
-            next.load(scales, zeros, (k_first * 2 + wg) * kGroups, p.num_groups, live);
-            float prev[kGroups];  // the scales of the block whose products come next
+            for (int t = 0; t < kMine / 2; ++t) acc[t] = pack2(0.0f, 0.0f);
+            float scale[kGroups];  // of the stage whose products come next
 
-            // the products of the block in D buffer `b`, scaled into the sums
-            auto take_products = [&](uint32_t b, uint32_t parity) {
-                if (!warp_wait(d_full(wg, b), parity, abort_flag, lane)) return false;
+            auto take_products = [&]() {
+                if (!__all_sync(0xffffffffu, wait_bounded(d_full(team), d_phase, abort_flag)))
+                    return false;
+                d_phase ^= 1u;
                 tc_fence_after_sync();
-                constexpr int kChunk = kCols < 16 ? 8 : 16;
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                    for (int c = 0; c < kCols; c += kChunk) {
-                        uint32_t r[kChunk];
-                        load_products<kCols>(
-                            lane_base + kDBase + (wg * 2 + b) * kDBufCols + g * kN + c, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j)
-                            acc[c + j] = fmaf(__uint_as_float(r[j]), prev[g], acc[c + j]);
-                    }
+                for (int g = 0; g < kGroups; ++g) add_products<kMine>(my_d + g * kN, scale[g], acc);
                 return true;
             };
 
             for (int ks = k_first; ok && ks < k_last; ++ks) {
-                now = next;
-                if (ks + 1 < k_last)
-                    next.load(scales, zeros, ((ks + 1) * 2 + wg) * kGroups, p.num_groups, live);
-                ok = warp_wait(full_bar(stage), phase, abort_flag, lane);
-                if (!ok) break;
-                // 16-byte pieces of the row, swizzled by its place among eight
-                const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
-                uint4 words[4];
+                const int i = ks - k_first;
+                const int in_chunk = i % kChunkStages;
+                if (in_chunk == 0)
+                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(buf), buf_phase, abort_flag));
+                if (ok && (i & 1) == team) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, abort_flag));
+                    if (!ok) break;
+                    // 16-byte pieces of the row, swizzled by its place among eight
+                    const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
+                    uint4 words[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    words[c] = *reinterpret_cast<const uint4*>(
-                        codes + (((wg * 4 + c) ^ (row_in_tile & 7)) << 4));
+                    for (int c = 0; c < 4; ++c)
+                        words[c] = *reinterpret_cast<const uint4*>(
+                            codes + (((half * 4 + c) ^ (row_in_tile & 7)) << 4));
+                    // this stage's groups of the row: behind the shift of the row's first word
+                    const int chunk_g = (ks - in_chunk) * kGroups;
+                    const uint32_t shift = row_first + uint32_t(chunk_g);
+                    const Elem* row_scales =
+                        reinterpret_cast<const Elem*>(scale_bufs + buf * kScaleBytes +
+                                                      row_in_tile * kScaleWords * 4) +
+                        (shift & 1u) + in_chunk * kGroups;
+                    const uint8_t* row_zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
+                                               row_in_tile * kZeroWords * 4 + (shift & 3u) +
+                                               in_chunk * kGroups;
+                    uint32_t zero[(kGroups + 1) / 2];  // patterns to subtract: this half's groups
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                    for (int g = 0; g < kGroups / 2; ++g)
+                        zero[g] = base_pattern(Elem()) +
+                                  (kZeros ? uint32_t(row_zeros[half * (kGroups / 2) + g]) : 8u) * 0x00010001u;
                     uint32_t r[16];
-                    numbers<Elem>(words[c], now.zero_pattern(c * kGroups / 4), r);
-                    tmem_st16(lane_base + (wg * 2 + buf) * kABufCols + c * 16, r);
-                }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(empty_bar(stage));
-                    mbar_arrive(a_full(wg, buf));
-                }
-                // block ks - 1 lies in the other buffer, whose phase turns with buffer 0
-                if (ks > k_first)
-                    ok = take_products(buf ^ 1u, buf == 0 ? buf_phase ^ 1u : buf_phase);
+                    numbers<Elem>(words[0], zero[0], r);
+                    if (i >= kTeams) ok = take_products();  // of this team's stage before
+                    if (!ok) break;
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) prev[g] = to_float(now.s[g]);
+                    for (int c = 0; c < 4; ++c) {
+                        if (c > 0) numbers<Elem>(words[c], zero[c * (kGroups / 2) / 4], r);
+                        tmem_st16(my_a + c * 16, r);
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)  // (0 behind the row's last group)
+                        scale[g] = ks * kGroups + g < p.num_groups ? to_float(row_scales[g]) : 0.0f;
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(a_full(team));
+                        mbar_arrive(empty_bar(stage));
+                    }
+                }
+                if (in_chunk == kChunkStages - 1 || ks + 1 == k_last) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty(buf));
+                    buf ^= 1u;
+                    if (buf == 0) buf_phase ^= 1u;
+                }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                buf ^= 1u;
-                if (buf == 0) buf_phase ^= 1u;
             }
-            if (ok) ok = take_products(buf ^ 1u, buf == 0 ? buf_phase ^ 1u : buf_phase);
+            if (ok && k_last - k_first > team) ok = take_products();
 
-            // The second warpgroup's sums meet the first's.
-            if (!first) named_barrier_sync(2, 32 * kDequantWarps);  // the last ones are read
-            if (wg == 1) {
+            // The second team's sums meet the first's.
+            if (!first) named_barrier_sync(2, kNumberThreads);  // the last ones are read
+            float* mine = exchange + half * kMine * kTileN + row_in_tile;
+            if (team == 1) {
 #pragma unroll
-                for (int t = 0; t < kCols; ++t) exchange[t * kTileN + row_in_tile] = acc[t];
+                for (int t = 0; t < kMine; t += 2) {
+                    const float2 v = unpack2(acc[t / 2]);
+                    mine[t * kTileN] = v.x;
+                    mine[(t + 1) * kTileN] = v.y;
+                }
             }
-            named_barrier_sync(1, 32 * kDequantWarps);
-            if (wg == 0) {
+            named_barrier_sync(1, kNumberThreads);
+            if (team == 0) {
+                const int64_t t0 = int64_t(chunk) * kCols + half * kMine;
+                Out* y = static_cast<Out*>(p.y) + t0 * p.N + n;
+                const bool store = p.splits == 1 && n < p.N && ok;
 #pragma unroll
-                for (int t = 0; t < kCols; ++t) acc[t] += exchange[t * kTileN + row_in_tile];
-                if (p.splits == 1 && live && ok) {
-                    Out* y = static_cast<Out*>(p.y) + int64_t(chunk) * kCols * p.N + n;
-                    const int64_t rows = p.T - int64_t(chunk) * kCols;
-#pragma unroll
-                    for (int t = 0; t < kCols; ++t)
-                        if (t < rows) y[int64_t(t) * p.N] = from_float<Out>(acc[t]);
+                for (int t = 0; t < kMine; t += 2) {
+                    acc[t / 2] = add2(acc[t / 2], pack2(mine[t * kTileN], mine[(t + 1) * kTileN]));
+                    const float2 v = unpack2(acc[t / 2]);
+                    if (store && t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x);
+                    if (store && t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y);
                 }
             }
             first = false;
@@ -438,27 +496,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* parts = reinterpret_cast<float*>(smem);
         cluster_sync();  // no CTA uses its stages any more
         const int share = (kCols + p.splits - 1) / p.splits;
-        const int wg_row = (warp & 3) * 32 + lane;
-        if (warp >= 2 && warp < 6) {
+        const bool numbers_warp = warp >= 2 && warp < 2 + kNumberWarps;
+        if (numbers_warp && team == 0) {
 #pragma unroll
-            for (int t = 0; t < kCols; ++t) {
+            for (int i = 0; i < kMine; ++i) {
+                const int t = half * kMine + i;
                 const int owner = t / share;
                 const uint32_t to = mapa_shared(
-                    smem_u32(parts + (rank * share + (t - owner * share)) * kTileN + wg_row), owner);
-                st_shared_cluster_u32(to, __float_as_uint(acc[t]));
+                    smem_u32(parts + (rank * share + (t - owner * share)) * kTileN + row_in_tile), owner);
+                const float2 v = unpack2(acc[i / 2]);
+                st_shared_cluster_u32(to, __float_as_uint(i & 1 ? v.y : v.x));
             }
         }
         cluster_sync();
         const int tile = first_item / p.chunks;
         const int chunk = first_item - tile * p.chunks;
-        const int n = tile * kTileN + wg_row;
-        if (warp >= 2 && n < p.N) {
-            for (int i = (warp - 2) >> 2; i < share; i += 2) {
+        const int n = tile * kTileN + row_in_tile;
+        if (numbers_warp && n < p.N) {
+            for (int i = (warp - 2) / 4; i < share; i += kNumberWarps / 4) {
                 const int64_t t = int64_t(chunk) * kCols + rank * share + i;
                 if (rank * share + i >= kCols || t >= p.T) break;
-                float sum = parts[i * kTileN + wg_row];
+                float sum = parts[i * kTileN + row_in_tile];
                 for (int s = 1; s < p.splits; ++s)
-                    sum += parts[(s * share + i) * kTileN + wg_row];
+                    sum += parts[(s * share + i) * kTileN + row_in_tile];
                 static_cast<Out*>(p.y)[t * p.N + n] = from_float<Out>(sum);
             }
         }
@@ -524,8 +584,8 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
 }
 
 // Columns per pass: the rows of x, at most what a D buffer holds of each group.
-int columns(int64_t T, int groups_per_block) {
-    const int most = int(kDBufCols) / groups_per_block;
+int columns(int64_t T, int groups_per_stage) {
+    const int most = int(kDBufCols) / groups_per_stage;
     const int want = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
     return want < most ? want : most;
 }
@@ -533,19 +593,19 @@ int columns(int64_t T, int groups_per_block) {
 template <typename Elem, typename Out, bool kZeros>
 cudaError_t launch_cols(int cols, int groups, const CUtensorMap& tw, const CUtensorMap& tx,
                         const Args& p, int num_sms, cudaStream_t s) {
-    if (groups == 1) {
-        if (cols == 8) return launch<Elem, Out, 8, 1, kZeros>(tw, tx, p, num_sms, s);
-        if (cols == 16) return launch<Elem, Out, 16, 1, kZeros>(tw, tx, p, num_sms, s);
-        if (cols == 32) return launch<Elem, Out, 32, 1, kZeros>(tw, tx, p, num_sms, s);
-        return launch<Elem, Out, 64, 1, kZeros>(tw, tx, p, num_sms, s);
-    }
     if (groups == 2) {
         if (cols == 8) return launch<Elem, Out, 8, 2, kZeros>(tw, tx, p, num_sms, s);
         if (cols == 16) return launch<Elem, Out, 16, 2, kZeros>(tw, tx, p, num_sms, s);
-        return launch<Elem, Out, 32, 2, kZeros>(tw, tx, p, num_sms, s);
+        if (cols == 32) return launch<Elem, Out, 32, 2, kZeros>(tw, tx, p, num_sms, s);
+        return launch<Elem, Out, 64, 2, kZeros>(tw, tx, p, num_sms, s);
     }
-    if (cols == 8) return launch<Elem, Out, 8, 4, kZeros>(tw, tx, p, num_sms, s);
-    return launch<Elem, Out, 16, 4, kZeros>(tw, tx, p, num_sms, s);
+    if (groups == 4) {
+        if (cols == 8) return launch<Elem, Out, 8, 4, kZeros>(tw, tx, p, num_sms, s);
+        if (cols == 16) return launch<Elem, Out, 16, 4, kZeros>(tw, tx, p, num_sms, s);
+        return launch<Elem, Out, 32, 4, kZeros>(tw, tx, p, num_sms, s);
+    }
+    if (cols == 8) return launch<Elem, Out, 8, 8, kZeros>(tw, tx, p, num_sms, s);
+    return launch<Elem, Out, 16, 8, kZeros>(tw, tx, p, num_sms, s);
 }
 
 }  // namespace
@@ -554,7 +614,7 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
                              const void* scales, const uint8_t* zeros, int64_t T, int64_t N,
                              int64_t K, int group, void* y, ElemType y_type, int num_sms,
                              cudaStream_t stream) {
-    const int groups = kBlockK / group;
+    const int groups = kStageK / group;  // per stage
     const int cols = columns(T, groups);
     const int64_t tiles = (N + kTileN - 1) / kTileN;
     const int64_t chunks = (T + cols - 1) / cols;
