@@ -14,28 +14,26 @@
 // and stores them to its TMEM lane, from where they are the A operand.  x is B (N = the
 // rows of x, 16, 32 or 64).
 //
-// One CTA per SM, 19 warps:
-//   warp 0       TMA producer: stages of 256 k, the tile's codes (16 KB) and x
+// One CTA per SM; a tile's K goes by in stages of 256 k:
+//   warp 0       TMA producer: the stage's codes (16 KB) and x
 //   warp 1       MMA issuer: per stage and group its MMAs into a D buffer, fresh
-//   warps 2..17  two teams of eight, the first takes the even stages of a tile, the second
-//                the odd ones.  A row has two threads per team: each turns its half of the
-//                stage's codes into numbers and stores them to the team's A buffer, and
-//                each keeps the running sums of half the rows of x:
-//                acc = fma(D, scale, acc) once the stage's products are there.  At the end
-//                the second team hands its sums to the first.
-//   warp 18      copies the scales and zero points, 32 groups of the tile's rows at a time,
+//   warp 2       copies the scales and zero points, 32 groups of the tile's rows at a time,
 //                into shared memory, where a thread finds its row's: straight from global
 //                memory every lane of a warp would touch another row, 32 sectors a load.
 //                Word by word, so that any number of groups per row will do: a row's words
 //                are those that hold its groups, its values lie from its own shift on
-// No barrier frees an A or D buffer: a team stores a stage's numbers only after it has
-// waited for the products of its stage before, and lets the MMAs of a stage start only
-// after it has read them.  One team's numbers overlap the other's MMAs.
+//   warps 3..6   products: a thread keeps a row's running sums, one per row of x:
+//                acc = fma(D, scale, acc), stage after stage, group after group
+//   the others   two or three teams of four warps, which take the stages in turn: a thread
+//                turns its row's codes into numbers and stores them to the team's A buffer
+// Turning codes into numbers takes 7 instructions of the half-rate integer pipe per 8 codes
+// (bf16), about 30 us of the SMs' time for 622 M codes next to 47 us of HBM's: the teams are
+// there so that one's waits are the others' work.
 //
 // Few tiles (N of some thousands): the K range of a tile is cut into `splits` parts, one
 // per CTA of a cluster, whose sums meet through distributed shared memory in the order of k.
-// The cut follows from N and K; tiles, stages and teams are fixed; a row of x is one column
-// of D.  So a row's bits do not depend on T.
+// The cut follows from N and K; tiles, stages and the order of the sums are fixed; a row of
+// x is one column of D.  So a row's bits do not depend on T.
 //
 // Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
 #include "rlk_internal.h"
@@ -48,16 +46,12 @@ namespace {
 constexpr int kTileN = 128;                  // rows of W per tile = UMMA M = TMEM lanes
 constexpr int kStageK = 256;                 // k per stage
 constexpr int kCodeBytes = kTileN * kStageK / 2;
-constexpr int kTeams = 2;
-constexpr int kTeamWarps = 8;
-constexpr int kNumberWarps = kTeams * kTeamWarps;
-constexpr int kNumberThreads = 32 * kNumberWarps;
-constexpr int kThreads = 32 * (3 + kNumberWarps);
+constexpr int kTeamWarps = 4;
+constexpr int kProductWarps = 4;
+constexpr int kFirstProductWarp = 3;
+constexpr int kFirstTeamWarp = kFirstProductWarp + kProductWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kABufCols = kStageK / 2;  // two 16-bit numbers per column
-constexpr uint32_t kDBase = kTeams * kABufCols;
-constexpr uint32_t kDBufCols = 128;          // groups per stage times columns
-static_assert(kDBase + kTeams * kDBufCols == kTmemCols, "tensor memory");
 constexpr int kMaxSplits = 8;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
@@ -76,13 +70,19 @@ constexpr int kScaleBytes = kTileN * (kScaleWords + kZeroWords) * 4;
 // Rows of x a CTA takes at a time, and the MMA's N (at least 16).
 constexpr int mma_n(int cols) { return cols < 16 ? 16 : cols; }
 constexpr int stage_bytes(int cols) { return kCodeBytes + mma_n(cols) * kStageK * 2; }
-constexpr int stages(int cols) { return cols <= 16 ? 7 : cols == 32 ? 5 : 3; }
-constexpr int barriers(int cols) { return 2 * stages(cols) + 2 * kTeams + 4 + 1; }
-// The exchange buffer: the second team's sums.
-constexpr int exchange_bytes(int cols) { return cols * kTileN * 4; }
+constexpr int stages(int cols) { return cols <= 16 ? 8 : cols == 32 ? 6 : 4; }
+// Tensor memory: A buffers (one per team) first, then the D buffers, `cols` columns for
+// each of a stage's groups.
+constexpr int d_cols(int cols, int groups) { return mma_n(cols) * groups; }
+constexpr int num_teams(int cols, int groups) { return d_cols(cols, groups) <= 64 ? 3 : 2; }
+constexpr int num_d(int cols, int groups) {
+    return (int(kTmemCols) - num_teams(cols, groups) * int(kABufCols)) / d_cols(cols, groups) < 4
+               ? (int(kTmemCols) - num_teams(cols, groups) * int(kABufCols)) / d_cols(cols, groups)
+               : 4;
+}
+constexpr int kMaxBarriers = 2 * 8 + 2 * 3 + 2 * 4 + 4 + 1;
 constexpr size_t smem_bytes(int cols) {
-    return 1024 + size_t(stages(cols)) * stage_bytes(cols) + exchange_bytes(cols) +
-           2 * kScaleBytes + barriers(cols) * 8 + 16;
+    return 1024 + size_t(stages(cols)) * stage_bytes(cols) + 2 * kScaleBytes + kMaxBarriers * 8 + 16;
 }
 static_assert(smem_bytes(64) <= 227 * 1024 && smem_bytes(32) <= 227 * 1024 &&
                   smem_bytes(16) <= 227 * 1024,
@@ -132,36 +132,50 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
     }
 }
 
-// Whole numbers 0..15 next to a constant whose last place is 1 (bf16: 128, fp16: 1024): the
-// code sits in the low bits of the pattern; subtracting the constant plus the zero point
-// leaves q - z, exactly.
-__device__ __forceinline__ uint32_t base_pattern(__nv_bfloat16) { return 0x43004300u; }
-__device__ __forceinline__ uint32_t base_pattern(__half) { return 0x64006400u; }
-__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b, __nv_bfloat16) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// 32 codes (four words) as 16 registers of two numbers q - z, in the order of k, exactly: a
+// code put into the low places of a constant's pattern adds its value to the constant, and
+// the constant and the zero point are subtracted.
+__device__ __forceinline__ uint32_t pattern_of(uint32_t zero, __nv_bfloat16) {
+    return 0x43004300u + zero * 0x00010001u;  // 128 + zero, twice
 }
-__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b, __half) {
-    const __half2 r =
-        __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// 32 codes (four words) as 16 registers of two numbers, in the order of k.
-template <typename Elem>
-__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero_pattern,
+__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __nv_bfloat16,
                                         uint32_t (&r)[16]) {
     const uint32_t w[4] = {words.x, words.y, words.z, words.w};
-    const uint32_t base = base_pattern(Elem());
+    const __nv_bfloat162 less = *reinterpret_cast<const __nv_bfloat162*>(&zero);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            r[4 * i + j] = minus(((w[i] >> (4 * j)) & 0x000f000fu) | base, zero_pattern, Elem());
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = ((w[i] >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), less);
+            r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+}
+// fp16 has room for two codes in the places of 1024: one shift per word instead of three.
+__device__ __forceinline__ uint32_t pattern_of(uint32_t zero, __half) {
+    return 0x64006400u + zero * 0x00010001u;  // 1024 + zero, twice
+}
+__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __half,
+                                        uint32_t (&r)[16]) {
+    const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+    const __half2 less = *reinterpret_cast<const __half2*>(&zero);
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    const __half2 less16 = __hsub2(__float2half2_rn(960.0f), less);  // -(64 + zero)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const uint32_t v = j == 0 ? w[i] : w[i] >> 8;
+            const uint32_t lo = (v & 0x000f000fu) | 0x64006400u;  // 1024 + q
+            const uint32_t hi = (v & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 q
+            const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), less);
+            const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, less16);
+            r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&a);
+            r[4 * i + j + 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
 }
 
-// N (4, 8 or a multiple of 16) fp32 columns of this thread's lane, scaled into acc.
+// N (8 or a multiple of 16) fp32 columns of this thread's lane, scaled into acc.
 template <int N>
 __device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&acc)[N / 2]) {
     constexpr int kPiece = N < 16 ? N : 16;
@@ -169,9 +183,7 @@ __device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&a
 #pragma unroll
     for (int c = 0; c < N; c += kPiece) {
         uint32_t r[kPiece];
-        if constexpr (kPiece == 4)
-            tmem_ld4(taddr + c, r);
-        else if constexpr (kPiece == 8)
+        if constexpr (kPiece == 8)
             tmem_ld8(taddr + c, r);
         else
             tmem_ld16(taddr + c, r);
@@ -185,36 +197,42 @@ __device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&a
 
 // kCols: rows of x at a time; kGroups: groups per stage.
 template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(kCols, kGroups)), 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap tmap_w,
                      const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     constexpr int kN = mma_n(kCols);
-    constexpr int kMine = kCols / 2;  // running sums per thread
     constexpr int kStages = stages(kCols);
     constexpr int kStageBytes = stage_bytes(kCols);
+    constexpr int kTeams = num_teams(kCols, kGroups);
+    constexpr int kDs = num_d(kCols, kGroups);
+    constexpr uint32_t kDBase = kTeams * kABufCols;
+    constexpr uint32_t kDBufCols = d_cols(kCols, kGroups);
     constexpr int kChunkStages = kScaleGroups / kGroups;  // stages per chunk of scales
     constexpr uint32_t kIdesc =
         std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
-    static_assert(kGroups * kN <= int(kDBufCols), "a D buffer");
+    static_assert(kDs >= 1 && kDBase + kDs * kDBufCols <= kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
     uint8_t* smem = smem_raw + pad;
     const uint32_t stage0 = raw_addr + pad;
     uint8_t* scale_bufs = smem + size_t(kStages) * kStageBytes;
-    float* exchange = reinterpret_cast<float*>(scale_bufs + 2 * kScaleBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(exchange) +
-                                                 exchange_bytes(kCols));
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + barriers(kCols));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(scale_bufs + 2 * kScaleBytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kMaxBarriers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    auto full_bar = [&](int s) { return smem_u32(bars + s); };
-    auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
-    auto a_full = [&](int team) { return smem_u32(bars + 2 * kStages + team); };
-    auto d_full = [&](int team) { return smem_u32(bars + 2 * kStages + kTeams + team); };
-    auto s_full = [&](int buf) { return smem_u32(bars + 2 * kStages + 2 * kTeams + buf); };
-    auto s_empty = [&](int buf) { return smem_u32(bars + 2 * kStages + 2 * kTeams + 2 + buf); };
-    const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 2 * kTeams + 4);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (kStages + s); };
+    constexpr int kA = 2 * kStages, kD = kA + 2 * kTeams, kS = kD + 2 * kDs;
+    static_assert(kS + 5 <= kMaxBarriers, "barriers");
+    auto a_full = [&](uint32_t team) { return bar0 + 8 * (kA + team); };
+    auto a_empty = [&](uint32_t team) { return bar0 + 8 * (kA + kTeams + team); };
+    auto d_full = [&](uint32_t d) { return bar0 + 8 * (kD + d); };
+    auto d_empty = [&](uint32_t d) { return bar0 + 8 * (kD + kDs + d); };
+    auto s_full = [&](uint32_t buf) { return bar0 + 8 * (kS + buf); };
+    auto s_empty = [&](uint32_t buf) { return bar0 + 8 * (kS + 2 + buf); };
+    const uint32_t drain_bar = bar0 + 8 * (kS + 4);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -226,11 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kTeams; ++i) {
             mbar_init(a_full(i), kTeamWarps);
+            mbar_init(a_empty(i), 1);
+        }
+        for (int i = 0; i < kDs; ++i) {
             mbar_init(d_full(i), 1);
+            mbar_init(d_empty(i), kProductWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 32);  // the copying warp's lanes
-            mbar_init(s_empty(i), kNumberWarps);
+            mbar_init(s_empty(i), kProductWarps + (kZeros ? kTeams * kTeamWarps : 0));
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -256,11 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int k_first = int(int64_t(p.num_stages) * rank / p.splits);
     const int k_last = int(int64_t(p.num_stages) * (rank + 1) / p.splits);
 
-    // Of the number warps: the team, the half of a stage's k and of the rows of x, the row.
-    const int team = (warp - 2) / kTeamWarps;
-    const int half = (warp - 2) / 4 & 1;
     const int row_in_tile = (warp & 3) * 32 + lane;  // (a warp reaches the lanes of its quadrant)
-    F2 acc[kMine / 2];
+    const uint32_t lane_base = tmem_base + (uint32_t((warp & 3) * 32) << 16);
+    F2 acc[kCols / 2];  // of the product warps
+
+    // By a whole warp: all lanes wait, all learn the outcome.
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag)) != 0;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -302,35 +327,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs the loop and one elected lane issues: addresses and
         // descriptors then are warp-uniform, which single-lane code does not let them be.
         const bool leader = elect_one();
-        uint32_t stage = 0, phase = 0, team_phases = 0;  // (one bit per team)
+        uint32_t stage = 0, phase = 0, team = 0, team_phase = 0, d = 0, d_phase = 0;
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
-                const int tm = (ks - k_first) & 1;
-                ok = wait_bounded(full_bar(stage), phase, abort_flag) &&
-                     wait_bounded(a_full(tm), (team_phases >> tm) & 1u, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(full_bar(stage), phase) && warp_wait(d_empty(d), d_phase ^ 1u) &&
+                     warp_wait(a_full(team), team_phase);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint64_t x_desc = sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
-                const uint32_t a = tmem_base + tm * kABufCols;
-                const uint32_t d = tmem_base + kDBase + tm * kDBufCols;
+                const uint32_t a_tmem = tmem_base + team * kABufCols;
+                const uint32_t d_tmem = tmem_base + kDBase + d * kDBufCols;
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < kStageK / 16; ++i) {
                         constexpr int kPerGroup = kStageK / 16 / kGroups;
                         const uint64_t off = uint64_t((i / 4 * kN * 128 + i % 4 * 32) >> 4);
-                        umma_f16_tmem_a(d + (i / kPerGroup) * kN, a + i * 8, x_desc + off, kIdesc,
-                                        i % kPerGroup != 0 ? 1u : 0u);
+                        umma_f16_tmem_a(d_tmem + (i / kPerGroup) * kN, a_tmem + i * 8, x_desc + off,
+                                        kIdesc, i % kPerGroup != 0 ? 1u : 0u);
                     }
-                    umma_commit(d_full(tm));
+                    umma_commit(d_full(d));
+                    umma_commit(a_empty(team));
                     umma_commit(empty_bar(stage));
                 }
                 __syncwarp();
-                team_phases ^= 1u << tm;
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
+                }
+                if (++team == kTeams) {
+                    team = 0;
+                    team_phase ^= 1u;
+                }
+                if (++d == kDs) {
+                    d = 0;
+                    d_phase ^= 1u;
                 }
             }
         }
@@ -339,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_drain(drain_bar, 0);
         }
         __syncwarp();
-    } else if (warp == kNumberWarps + 2) {
+    } else if (warp == 2) {
         // ------------------------------------------------------------ scales
         uint32_t buf = 0, buf_phase = 0;
         bool ok = true;
@@ -348,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* scales = static_cast<const uint8_t*>(p.scales);
             const int64_t all = int64_t(p.N) * p.num_groups;
             for (int ks = k_first; ks < k_last; ks += kChunkStages) {
-                ok = wait_bounded(s_empty(buf), buf_phase ^ 1u, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(s_empty(buf), buf_phase ^ 1u);
                 if (!ok) break;
                 const uint32_t to = smem_u32(scale_bufs + buf * kScaleBytes);
                 const int64_t from = n0 * p.num_groups + ks * kGroups;  // the first row's first group
@@ -372,75 +402,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         copy_words_wait_all();  // (no copy outlives the CTA)
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ numbers and sums
-        const uint32_t lane_base = tmem_base + (uint32_t((warp & 3) * 32) << 16);
-        const uint32_t my_a = lane_base + team * kABufCols + half * (kABufCols / 2);
-        const uint32_t my_d = lane_base + kDBase + team * kDBufCols + half * kMine;
-        uint32_t stage = 0, phase = 0, d_phase = 0, buf = 0, buf_phase = 0;
-        bool ok = true, first = true;
-        // After a wait that ran out a warp does no more work but keeps the barriers' count.
-        for (int item = first_item; item < p.items; item += item_step) {
+    } else if (warp < kFirstTeamWarp) {
+        // ------------------------------------------------------------ products
+        uint32_t d = 0, d_phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int item = first_item; ok && item < p.items; item += item_step) {
             const int tile = item / p.chunks;
             const int chunk = item - tile * p.chunks;
             const int n = tile * kTileN + row_in_tile;
+            const uint32_t row_first = uint32_t(n) * uint32_t(p.num_groups);  // (its low bit counts)
+#pragma unroll
+            for (int t = 0; t < kCols / 2; ++t) acc[t] = pack2(0.0f, 0.0f);
+            for (int ks0 = k_first; ok && ks0 < k_last; ks0 += kChunkStages) {
+                ok = warp_wait(s_full(buf), buf_phase);
+                const Elem* scales = reinterpret_cast<const Elem*>(scale_bufs + buf * kScaleBytes +
+                                                                   row_in_tile * kScaleWords * 4) +
+                                     ((row_first + uint32_t(ks0 * kGroups)) & 1u);
+                const int stop = min(k_last, ks0 + kChunkStages);
+                for (int ks = ks0; ok && ks < stop; ++ks) {
+                    float scale[kGroups];
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)  // (0 behind the row's last group)
+                        scale[g] = ks * kGroups + g < p.num_groups
+                                       ? to_float(scales[(ks - ks0) * kGroups + g]) : 0.0f;
+                    ok = warp_wait(d_full(d), d_phase);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        add_products<kCols>(lane_base + kDBase + d * kDBufCols + g * kN, scale[g], acc);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(d_empty(d));
+                    if (++d == kDs) {
+                        d = 0;
+                        d_phase ^= 1u;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty(buf));
+                buf ^= 1u;
+                if (buf == 0) buf_phase ^= 1u;
+            }
+            if (p.splits == 1 && n < p.N && ok) {
+                const int64_t t0 = int64_t(chunk) * kCols;
+                Out* y = static_cast<Out*>(p.y) + t0 * p.N + n;
+#pragma unroll
+                for (int t = 0; t < kCols; t += 2) {
+                    const float2 v = unpack2(acc[t / 2]);
+                    if (t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x);
+                    if (t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y);
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ numbers
+        const int team = (warp - kFirstTeamWarp) / kTeamWarps;
+        const uint32_t a_tmem = lane_base + team * kABufCols;
+        // The CTA's stages are numbered through all items; number i lies in ring place
+        // i % kStages and belongs to team i % kTeams.
+        uint32_t stage = 0, phase = 0, turn = 0, a_phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int item = first_item; ok && item < p.items; item += item_step) {
+            const int n = item / p.chunks * kTileN + row_in_tile;
             const uint32_t row_first = uint32_t(n) * uint32_t(p.num_groups);  // (its low bits count)
-#pragma unroll
-            for (int t = 0; t < kMine / 2; ++t) acc[t] = pack2(0.0f, 0.0f);
-            float scale[kGroups];  // of the stage whose products come next
-
-            auto take_products = [&]() {
-                if (!__all_sync(0xffffffffu, wait_bounded(d_full(team), d_phase, abort_flag)))
-                    return false;
-                d_phase ^= 1u;
-                tc_fence_after_sync();
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) add_products<kMine>(my_d + g * kN, scale[g], acc);
-                return true;
-            };
-
             for (int ks = k_first; ok && ks < k_last; ++ks) {
-                const int i = ks - k_first;
-                const int in_chunk = i % kChunkStages;
-                if (in_chunk == 0)
-                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(buf), buf_phase, abort_flag));
-                if (ok && (i & 1) == team) {
-                    ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, abort_flag));
+                const int in_chunk = (ks - k_first) % kChunkStages;
+                if (kZeros && in_chunk == 0) ok = warp_wait(s_full(buf), buf_phase);
+                if (ok && turn == uint32_t(team)) {
+                    ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
                     if (!ok) break;
                     // 16-byte pieces of the row, swizzled by its place among eight
                     const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
-                    uint4 words[4];
+                    uint4 words[8];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 8; ++c)
                         words[c] = *reinterpret_cast<const uint4*>(
-                            codes + (((half * 4 + c) ^ (row_in_tile & 7)) << 4));
+                            codes + ((c ^ (row_in_tile & 7)) << 4));
                     // this stage's groups of the row: behind the shift of the row's first word
-                    const int chunk_g = (ks - in_chunk) * kGroups;
-                    const uint32_t shift = row_first + uint32_t(chunk_g);
-                    const Elem* row_scales =
-                        reinterpret_cast<const Elem*>(scale_bufs + buf * kScaleBytes +
-                                                      row_in_tile * kScaleWords * 4) +
-                        (shift & 1u) + in_chunk * kGroups;
-                    const uint8_t* row_zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
-                                               row_in_tile * kZeroWords * 4 + (shift & 3u) +
-                                               in_chunk * kGroups;
-                    uint32_t zero[(kGroups + 1) / 2];  // patterns to subtract: this half's groups
+                    const uint8_t* zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
+                                           row_in_tile * kZeroWords * 4 +
+                                           ((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
+                                           in_chunk * kGroups;
 #pragma unroll
-                    for (int g = 0; g < kGroups / 2; ++g)
-                        zero[g] = base_pattern(Elem()) +
-                                  (kZeros ? uint32_t(row_zeros[half * (kGroups / 2) + g]) : 8u) * 0x00010001u;
-                    uint32_t r[16];
-                    numbers<Elem>(words[0], zero[0], r);
-                    if (i >= kTeams) ok = take_products();  // of this team's stage before
-                    if (!ok) break;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c > 0) numbers<Elem>(words[c], zero[c * (kGroups / 2) / 4], r);
-                        tmem_st16(my_a + c * 16, r);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t r[16];
+                        numbers(words[c],
+                                pattern_of(kZeros ? uint32_t(zeros[c * kGroups / 8]) : 8u, Elem()),
+                                Elem(), r);
+                        tmem_st16(a_tmem + c * 16, r);
                     }
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g)  // (0 behind the row's last group)
-                        scale[g] = ks * kGroups + g < p.num_groups ? to_float(row_scales[g]) : 0.0f;
                     tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
@@ -448,8 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(a_full(team));
                         mbar_arrive(empty_bar(stage));
                     }
+                    a_phase ^= 1u;
                 }
-                if (in_chunk == kChunkStages - 1 || ks + 1 == k_last) {
+                if (kZeros && (in_chunk == kChunkStages - 1 || ks + 1 == k_last)) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty(buf));
                     buf ^= 1u;
@@ -459,34 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     stage = 0;
                     phase ^= 1u;
                 }
+                if (++turn == kTeams) turn = 0;
             }
-            if (ok && k_last - k_first > team) ok = take_products();
-
-            // The second team's sums meet the first's.
-            if (!first) named_barrier_sync(2, kNumberThreads);  // the last ones are read
-            float* mine = exchange + half * kMine * kTileN + row_in_tile;
-            if (team == 1) {
-#pragma unroll
-                for (int t = 0; t < kMine; t += 2) {
-                    const float2 v = unpack2(acc[t / 2]);
-                    mine[t * kTileN] = v.x;
-                    mine[(t + 1) * kTileN] = v.y;
-                }
-            }
-            named_barrier_sync(1, kNumberThreads);
-            if (team == 0) {
-                const int64_t t0 = int64_t(chunk) * kCols + half * kMine;
-                Out* y = static_cast<Out*>(p.y) + t0 * p.N + n;
-                const bool store = p.splits == 1 && n < p.N && ok;
-#pragma unroll
-                for (int t = 0; t < kMine; t += 2) {
-                    acc[t / 2] = add2(acc[t / 2], pack2(mine[t * kTileN], mine[(t + 1) * kTileN]));
-                    const float2 v = unpack2(acc[t / 2]);
-                    if (store && t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x);
-                    if (store && t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y);
-                }
-            }
-            first = false;
         }
     }
 
@@ -496,24 +522,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* parts = reinterpret_cast<float*>(smem);
         cluster_sync();  // no CTA uses its stages any more
         const int share = (kCols + p.splits - 1) / p.splits;
-        const bool numbers_warp = warp >= 2 && warp < 2 + kNumberWarps;
-        if (numbers_warp && team == 0) {
+        if (warp >= kFirstProductWarp && warp < kFirstTeamWarp) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int t = half * kMine + i;
+            for (int t = 0; t < kCols; ++t) {
                 const int owner = t / share;
                 const uint32_t to = mapa_shared(
                     smem_u32(parts + (rank * share + (t - owner * share)) * kTileN + row_in_tile), owner);
-                const float2 v = unpack2(acc[i / 2]);
-                st_shared_cluster_u32(to, __float_as_uint(i & 1 ? v.y : v.x));
+                const float2 v = unpack2(acc[t / 2]);
+                st_shared_cluster_u32(to, __float_as_uint(t & 1 ? v.y : v.x));
             }
         }
         cluster_sync();
         const int tile = first_item / p.chunks;
         const int chunk = first_item - tile * p.chunks;
         const int n = tile * kTileN + row_in_tile;
-        if (numbers_warp && n < p.N) {
-            for (int i = (warp - 2) / 4; i < share; i += kNumberWarps / 4) {
+        if (warp >= kFirstProductWarp && n < p.N) {
+            for (int i = (warp - kFirstProductWarp) / 4; i < share; i += 1 + kTeams) {
                 const int64_t t = int64_t(chunk) * kCols + rank * share + i;
                 if (rank * share + i >= kCols || t >= p.T) break;
                 float sum = parts[i * kTileN + row_in_tile];
@@ -573,7 +597,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
     const int64_t ctas = p.splits > 1 ? int64_t(p.items) * p.splits
                                       : (p.items < num_sms ? p.items : num_sms);
     cfg.gridDim = dim3(unsigned(ctas), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(32 * (kFirstTeamWarp + kTeamWarps * num_teams(kCols, kGroups)), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -583,9 +607,9 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
     return cudaGetLastError();
 }
 
-// Columns per pass: the rows of x, at most what a D buffer holds of each group.
+// Columns per pass: the rows of x, at most what half of tensor memory holds of each group.
 int columns(int64_t T, int groups_per_stage) {
-    const int most = int(kDBufCols) / groups_per_stage;
+    const int most = 256 / groups_per_stage;
     const int want = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
     return want < most ? want : most;
 }
@@ -593,19 +617,18 @@ int columns(int64_t T, int groups_per_stage) {
 template <typename Elem, typename Out, bool kZeros>
 cudaError_t launch_cols(int cols, int groups, const CUtensorMap& tw, const CUtensorMap& tx,
                         const Args& p, int num_sms, cudaStream_t s) {
-    if (groups == 2) {
-        if (cols == 8) return launch<Elem, Out, 8, 2, kZeros>(tw, tx, p, num_sms, s);
-        if (cols == 16) return launch<Elem, Out, 16, 2, kZeros>(tw, tx, p, num_sms, s);
-        if (cols == 32) return launch<Elem, Out, 32, 2, kZeros>(tw, tx, p, num_sms, s);
-        return launch<Elem, Out, 64, 2, kZeros>(tw, tx, p, num_sms, s);
-    }
-    if (groups == 4) {
-        if (cols == 8) return launch<Elem, Out, 8, 4, kZeros>(tw, tx, p, num_sms, s);
-        if (cols == 16) return launch<Elem, Out, 16, 4, kZeros>(tw, tx, p, num_sms, s);
-        return launch<Elem, Out, 32, 4, kZeros>(tw, tx, p, num_sms, s);
-    }
-    if (cols == 8) return launch<Elem, Out, 8, 8, kZeros>(tw, tx, p, num_sms, s);
-    return launch<Elem, Out, 16, 8, kZeros>(tw, tx, p, num_sms, s);
+    auto go = [&](auto c) {
+        constexpr int kCols = decltype(c)::value;
+        if (groups == 2) return launch<Elem, Out, kCols, 2, kZeros>(tw, tx, p, num_sms, s);
+        if (groups == 4) return launch<Elem, Out, kCols, 4, kZeros>(tw, tx, p, num_sms, s);
+        if constexpr (kCols <= 32)
+            if (groups == 8) return launch<Elem, Out, kCols, 8, kZeros>(tw, tx, p, num_sms, s);
+        return cudaErrorInvalidValue;
+    };
+    if (cols == 8) return go(std::integral_constant<int, 8>());
+    if (cols == 16) return go(std::integral_constant<int, 16>());
+    if (cols == 32) return go(std::integral_constant<int, 32>());
+    return go(std::integral_constant<int, 64>());
 }
 
 }  // namespace
