@@ -195,6 +195,38 @@ __device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&a
     }
 }
 
+// Copies kScaleGroups values of kSize bytes of each of a tile's rows, value `from` of an
+// array of `all` on and row_values further per row, as the words that hold them.  A warp
+// takes whole rows side by side: rows four (kSize 1) or two apart start at the same place
+// of a word, so a lane's words lie a fixed step apart.  The word behind comes at the end.
+template <int kSize>
+__device__ __forceinline__ void copy_groups(const uint8_t* base, int64_t from, int row_values,
+                                            int64_t all, bool inner, int lane, uint32_t to) {
+    constexpr int kWords = kScaleGroups * kSize / 4;  // and one more
+    constexpr int kRows = 32 / kWords;                // at once
+    static_assert(kRows * kSize % 4 == 0, "the rows of a step start at the same place of a word");
+    auto word = [&](int row, int w) {  // byte offset
+        return ((from + int64_t(row) * row_values) * kSize & ~int64_t(3)) + w * 4;
+    };
+    int64_t at = word(lane / kWords, lane % kWords);
+    uint32_t dst = to + ((lane / kWords) * (kWords + 1) + lane % kWords) * 4;
+    const int64_t step = int64_t(kRows) * row_values * kSize;
+    auto copy = [&](int64_t src, uint32_t d) {
+        const int64_t left = inner ? 4 : all * kSize - src;
+        const uint32_t bytes = left <= 0 ? 0u : left < 4 ? uint32_t(left) : 4u;
+        copy_word_async(d, bytes ? base + src : base, bytes);
+    };
+#pragma unroll 4
+    for (int r = 0; r < kTileN; r += kRows) {
+        copy(at, dst);
+        at += step;
+        dst += kRows * (kWords + 1) * 4;
+    }
+#pragma unroll
+    for (int r = lane; r < kTileN; r += 32)
+        copy(word(r, kWords), to + (r * (kWords + 1) + kWords) * 4);
+}
+
 // kCols: rows of x at a time; kGroups: groups per stage.
 template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
 __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(kCols, kGroups)), 1)
@@ -376,25 +408,18 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
             const int64_t n0 = int64_t(item / p.chunks) * kTileN;
-            const uint8_t* scales = static_cast<const uint8_t*>(p.scales);
-            const int64_t all = int64_t(p.N) * p.num_groups;
+            // no word of the tile, with the one behind a row's last, lies behind the arrays
+            const bool inner = n0 + kTileN + 1 < p.N;
             for (int ks = k_first; ks < k_last; ks += kChunkStages) {
                 ok = warp_wait(s_empty(buf), buf_phase ^ 1u);
                 if (!ok) break;
                 const uint32_t to = smem_u32(scale_bufs + buf * kScaleBytes);
                 const int64_t from = n0 * p.num_groups + ks * kGroups;  // the first row's first group
-                auto copy = [&](const uint8_t* base, int size, int words, uint32_t dst) {
-                    for (int i = lane; i < kTileN * words; i += 32) {
-                        const int r = i / words;
-                        const int64_t at =
-                            ((from + int64_t(r) * p.num_groups) * size & ~int64_t(3)) + (i - r * words) * 4;
-                        const int64_t left = all * size - at;
-                        const uint32_t bytes = left <= 0 ? 0u : left < 4 ? uint32_t(left) : 4u;
-                        copy_word_async(dst + i * 4, bytes ? base + at : base, bytes);
-                    }
-                };
-                copy(scales, 2, kScaleWords, to);
-                if (kZeros) copy(p.zeros, 1, kZeroWords, to + kTileN * kScaleWords * 4);
+                copy_groups<2>(static_cast<const uint8_t*>(p.scales), from, p.num_groups,
+                               int64_t(p.N) * p.num_groups, inner, lane, to);
+                if (kZeros)
+                    copy_groups<1>(p.zeros, from, p.num_groups, int64_t(p.N) * p.num_groups, inner,
+                                   lane, to + kTileN * kScaleWords * 4);
                 copy_words_arrive(s_full(buf));
                 buf ^= 1u;
                 if (buf == 0) buf_phase ^= 1u;
