@@ -132,6 +132,14 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
     }
 }
 
+// (a & mask) | set in one instruction: with both constants as immediates it would be two,
+// and this is the instruction the whole kernel waits for.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t set) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(mask), "r"(set));
+    return r;
+}
+
 // 32 codes (four words) as 16 registers of two numbers q - z, in the order of k, exactly: a
 // code put into the low places of a constant's pattern adds its value to the constant, and
 // the constant and the zero point are subtracted.
@@ -146,7 +154,7 @@ __device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __nv_
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t v = ((w[i] >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+            const uint32_t v = and_or(w[i] >> (4 * j), 0x000f000fu, 0x43004300u);
             const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), less);
             r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&d);
         }
@@ -166,8 +174,8 @@ __device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __hal
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
             const uint32_t v = j == 0 ? w[i] : w[i] >> 8;
-            const uint32_t lo = (v & 0x000f000fu) | 0x64006400u;  // 1024 + q
-            const uint32_t hi = (v & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 q
+            const uint32_t lo = and_or(v, 0x000f000fu, 0x64006400u);  // 1024 + q
+            const uint32_t hi = and_or(v, 0x00f000f0u, 0x64006400u);  // 1024 + 16 q
             const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), less);
             const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, less16);
             r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&a);
@@ -499,21 +507,21 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                     if (!ok) break;
                     // 16-byte pieces of the row, swizzled by its place among eight
                     const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
-                    uint4 words[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        words[c] = *reinterpret_cast<const uint4*>(
-                            codes + ((c ^ (row_in_tile & 7)) << 4));
                     // this stage's groups of the row: behind the shift of the row's first word
                     const uint8_t* zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
                                            row_in_tile * kZeroWords * 4 +
                                            ((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
                                            in_chunk * kGroups;
+                    auto piece = [&](int c) {
+                        return *reinterpret_cast<const uint4*>(codes + ((c ^ (row_in_tile & 7)) << 4));
+                    };
+                    uint4 next = piece(0);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
+                        const uint4 words = next;
+                        next = piece(c < 7 ? c + 1 : 7);
                         uint32_t r[16];
-                        numbers(words[c],
-                                pattern_of(kZeros ? uint32_t(zeros[c * kGroups / 8]) : 8u, Elem()),
+                        numbers(words, pattern_of(kZeros ? uint32_t(zeros[c * kGroups / 8]) : 8u, Elem()),
                                 Elem(), r);
                         tmem_st16(a_tmem + c * 16, r);
                     }
