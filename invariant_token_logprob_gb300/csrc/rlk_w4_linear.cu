@@ -26,9 +26,9 @@
 //                acc = fma(D, scale, acc), stage after stage, group after group
 //   the others   two or three teams of four warps, which take the stages in turn: a thread
 //                turns its row's codes into numbers and stores them to the team's A buffer
-// Turning codes into numbers takes 7 instructions of the half-rate integer pipe per 8 codes
-// (bf16), about 30 us of the SMs' time for 622 M codes next to 47 us of HBM's: the teams are
-// there so that one's waits are the others' work.
+// Turning codes into numbers takes 5 instructions of the half-rate integer pipe per 8 codes,
+// about 21 us of the SMs' time for 622 M codes next to 47 us of HBM's: the teams are there so
+// that one's waits are the others' work.
 //
 // Few tiles (N of some thousands): the K range of a tile is cut into `splits` parts, one
 // per CTA of a cluster, whose sums meet through distributed shared memory in the order of k.
@@ -140,47 +140,61 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t s
     return r;
 }
 
-// 32 codes (four words) as 16 registers of two numbers q - z, in the order of k, exactly: a
-// code put into the low places of a constant's pattern adds its value to the constant, and
-// the constant and the zero point are subtracted.
-__device__ __forceinline__ uint32_t pattern_of(uint32_t zero, __nv_bfloat16) {
-    return 0x43004300u + zero * 0x00010001u;  // 128 + zero, twice
-}
-__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __nv_bfloat16,
+// 32 codes (four words) as 16 registers of two numbers kUnit (q - z), in the order of k,
+// exactly.  A code in the low places of a constant's pattern adds its value to the constant:
+// the multiply-add that subtracts the constant and the zero point brings the unit along.  A
+// code four places higher needs no shift: fp16's 1024 has room for it too (16 q), and in
+// bf16 the bare bits are a subnormal number, 16 q * 2^-133, that 2^127 brings to q / 4.  So a
+// word takes one shift and four cuts; the integer pipe's time goes into nothing else.
+template <typename Elem>
+struct Numbers;
+template <>
+struct Numbers<__nv_bfloat16> {
+    static constexpr float kUnit = 0.25f;
+    uint32_t less_low, less_high;  // -(32 + z / 4) and -z / 4, twice
+    __device__ __forceinline__ explicit Numbers(uint32_t zero) {
+        less_low = 0xc200c200u + zero * 0x00010001u;  // (the last place of 32 is 1/4)
+        const __nv_bfloat162 q = __float2bfloat162_rn(-0.25f * float(zero));
+        less_high = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    __device__ __forceinline__ void pair(uint32_t v, uint32_t& low, uint32_t& high) const {
+        low = fma(and_or(v, 0x000f000fu, 0x43004300u), 0x3e803e80u, less_low);  // (128 + q) / 4
+        high = fma(v & 0x00f000f0u, 0x7f007f00u, less_high);                    // times 2^127
+    }
+};
+template <>
+struct Numbers<__half> {
+    static constexpr float kUnit = 1.0f;
+    uint32_t less_low, less_high;  // -(1024 + z) and -(64 + z), twice
+    __device__ __forceinline__ explicit Numbers(uint32_t zero) {
+        less_low = 0xe400e400u + zero * 0x00010001u;
+        less_high = 0xd400d400u + zero * 0x00100010u;  // (that of 64 is 1/16)
+    }
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    __device__ __forceinline__ void pair(uint32_t v, uint32_t& low, uint32_t& high) const {
+        low = fma(and_or(v, 0x000f000fu, 0x64006400u), 0x3c003c00u, less_low);    // 1024 + q
+        high = fma(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, less_high);  // (1024 + 16 q) / 16
+    }
+};
+
+template <typename Elem>
+__device__ __forceinline__ void numbers(const uint4& words, const Numbers<Elem>& minus,
                                         uint32_t (&r)[16]) {
     const uint32_t w[4] = {words.x, words.y, words.z, words.w};
-    const __nv_bfloat162 less = *reinterpret_cast<const __nv_bfloat162*>(&zero);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = and_or(w[i] >> (4 * j), 0x000f000fu, 0x43004300u);
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), less);
-            r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&d);
-        }
-}
-// fp16 has room for two codes in the places of 1024: one shift per word instead of three.
-__device__ __forceinline__ uint32_t pattern_of(uint32_t zero, __half) {
-    return 0x64006400u + zero * 0x00010001u;  // 1024 + zero, twice
-}
-__device__ __forceinline__ void numbers(const uint4& words, uint32_t zero, __half,
-                                        uint32_t (&r)[16]) {
-    const uint32_t w[4] = {words.x, words.y, words.z, words.w};
-    const __half2 less = *reinterpret_cast<const __half2*>(&zero);
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-    const __half2 less16 = __hsub2(__float2half2_rn(960.0f), less);  // -(64 + zero)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            const uint32_t v = j == 0 ? w[i] : w[i] >> 8;
-            const uint32_t lo = and_or(v, 0x000f000fu, 0x64006400u);  // 1024 + q
-            const uint32_t hi = and_or(v, 0x00f000f0u, 0x64006400u);  // 1024 + 16 q
-            const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), less);
-            const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, less16);
-            r[4 * i + j] = *reinterpret_cast<const uint32_t*>(&a);
-            r[4 * i + j + 1] = *reinterpret_cast<const uint32_t*>(&b);
-        }
+    for (int i = 0; i < 4; ++i) {
+        minus.pair(w[i], r[4 * i], r[4 * i + 1]);
+        minus.pair(w[i] >> 8, r[4 * i + 2], r[4 * i + 3]);
+    }
 }
 
 // N (8 or a multiple of 16) fp32 columns of this thread's lane, scaled into acc.
@@ -248,6 +262,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     constexpr uint32_t kDBase = kTeams * kABufCols;
     constexpr uint32_t kDBufCols = d_cols(kCols, kGroups);
     constexpr int kChunkStages = kScaleGroups / kGroups;  // stages per chunk of scales
+    constexpr float kUnit = Numbers<Elem>::kUnit;  // (a power of two: dividing is exact)
     constexpr uint32_t kIdesc =
         std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
     static_assert(kDs >= 1 && kDBase + kDs * kDBufCols <= kTmemCols, "tensor memory");
@@ -483,8 +498,8 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
 #pragma unroll
                 for (int t = 0; t < kCols; t += 2) {
                     const float2 v = unpack2(acc[t / 2]);
-                    if (t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x);
-                    if (t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y);
+                    if (t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x / kUnit);
+                    if (t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y / kUnit);
                 }
             }
         }
@@ -502,28 +517,30 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
             for (int ks = k_first; ok && ks < k_last; ++ks) {
                 const int in_chunk = (ks - k_first) % kChunkStages;
                 if (kZeros && in_chunk == 0) ok = warp_wait(s_full(buf), buf_phase);
+                const uint8_t* zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
+                                       row_in_tile * kZeroWords * 4;
                 if (ok && turn == uint32_t(team)) {
                     ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
                     if (!ok) break;
                     // 16-byte pieces of the row, swizzled by its place among eight
-                    const uint8_t* codes = smem + stage * kStageBytes + row_in_tile * 128;
-                    // this stage's groups of the row: behind the shift of the row's first word
-                    const uint8_t* zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
-                                           row_in_tile * kZeroWords * 4 +
-                                           ((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
-                                           in_chunk * kGroups;
-                    auto piece = [&](int c) {
-                        return *reinterpret_cast<const uint4*>(codes + ((c ^ (row_in_tile & 7)) << 4));
-                    };
-                    uint4 next = piece(0);
+                    const uint32_t codes = stage0 + stage * kStageBytes + row_in_tile * 128 +
+                                           ((row_in_tile & 7) << 4);
+                    uint4 next = load_shared_v4(codes);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint4 words = next;
-                        next = piece(c < 7 ? c + 1 : 7);
-                        uint32_t r[16];
-                        numbers(words, pattern_of(kZeros ? uint32_t(zeros[c * kGroups / 8]) : 8u, Elem()),
-                                Elem(), r);
-                        tmem_st16(a_tmem + c * 16, r);
+                    for (int g = 0; g < kGroups; ++g) {
+                        // (the row's values lie behind the shift of its first word)
+                        const Numbers<Elem> minus(
+                            kZeros ? uint32_t(zeros[((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
+                                                    in_chunk * kGroups + g])
+                                   : 8u);
+#pragma unroll
+                        for (int c = g * 8 / kGroups; c < (g + 1) * 8 / kGroups; ++c) {
+                            const uint4 words = next;
+                            next = load_shared_v4(codes ^ ((c < 7 ? c + 1 : 7) << 4));
+                            uint32_t r[16];
+                            numbers<Elem>(words, minus, r);
+                            tmem_st16(a_tmem + c * 16, r);
+                        }
                     }
                     tmem_st_wait();
                     tc_fence_before_sync();
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 float sum = parts[i * kTileN + row_in_tile];
                 for (int s = 1; s < p.splits; ++s)
                     sum += parts[(s * share + i) * kTileN + row_in_tile];
-                static_cast<Out*>(p.y)[t * p.N + n] = from_float<Out>(sum);
+                static_cast<Out*>(p.y)[t * p.N + n] = from_float<Out>(sum / kUnit);
             }
         }
     }
