@@ -70,7 +70,11 @@ constexpr int kScaleBytes = kTileN * (kScaleWords + kZeroWords) * 4;
 // Rows of x a CTA takes at a time, and the MMA's N (at least 16).
 constexpr int mma_n(int cols) { return cols < 16 ? 16 : cols; }
 constexpr int stage_bytes(int cols) { return kCodeBytes + mma_n(cols) * kStageK * 2; }
-constexpr int stages(int cols) { return cols <= 16 ? 8 : cols == 32 ? 6 : 4; }
+// Groups of 32 run through a chunk of scales in four stages: two more buffers, a stage less.
+constexpr int scale_bufs_of(int groups) { return groups == 8 ? 4 : 2; }
+constexpr int stages(int cols, int groups) {
+    return (cols <= 16 ? 8 : cols == 32 ? 6 : 4) - (groups == 8 ? 1 : 0);
+}
 // Tensor memory: A buffers (one per team) first, then the D buffers, `cols` columns for
 // each of a stage's groups.
 constexpr int d_cols(int cols, int groups) { return mma_n(cols) * groups; }
@@ -80,15 +84,17 @@ constexpr int num_d(int cols, int groups) {
                ? (int(kTmemCols) - num_teams(cols, groups) * int(kABufCols)) / d_cols(cols, groups)
                : 4;
 }
-constexpr int kMaxBarriers = 2 * 8 + 2 * 3 + 2 * 4 + 4 + 1;
-constexpr size_t smem_bytes(int cols) {
-    return 1024 + size_t(stages(cols)) * stage_bytes(cols) + 2 * kScaleBytes + kMaxBarriers * 8 + 16;
+constexpr int kMaxBarriers = 2 * 8 + 2 * 3 + 2 * 4 + 2 * 4 + 1;
+constexpr size_t smem_bytes(int cols, int groups) {
+    return 1024 + size_t(stages(cols, groups)) * stage_bytes(cols) +
+           scale_bufs_of(groups) * kScaleBytes + kMaxBarriers * 8 + 16;
 }
-static_assert(smem_bytes(64) <= 227 * 1024 && smem_bytes(32) <= 227 * 1024 &&
-                  smem_bytes(16) <= 227 * 1024,
+static_assert(smem_bytes(64, 4) <= 227 * 1024 && smem_bytes(32, 8) <= 227 * 1024 &&
+                  smem_bytes(16, 8) <= 227 * 1024 && smem_bytes(32, 4) <= 227 * 1024 &&
+                  smem_bytes(16, 4) <= 227 * 1024,
               "shared memory per CTA");
-static_assert((64 + kMaxSplits) * kTileN * 4 <= stages(8) * stage_bytes(8) &&
-                  (64 + kMaxSplits) * kTileN * 4 <= stages(64) * stage_bytes(64),
+static_assert((64 + kMaxSplits) * kTileN * 4 <= stages(8, 8) * stage_bytes(8) &&
+                  (64 + kMaxSplits) * kTileN * 4 <= stages(64, 4) * stage_bytes(64),
               "the parts' sums take the stages' place");
 
 struct Args {
@@ -101,6 +107,8 @@ struct Args {
     int items;         // tiles * chunks
     int num_stages;    // of the whole K
     int splits;
+    int x_rows;        // rows of an x box: fewer than the MMA's N where T is (the others'
+                       // columns hold what the shared memory held and are never read)
 };
 
 // By whole warps or single lanes; the usual wait finds its phase complete.
@@ -154,8 +162,7 @@ struct Numbers<__nv_bfloat16> {
     uint32_t less_low, less_high;  // -(32 + z / 4) and -z / 4, twice
     __device__ __forceinline__ explicit Numbers(uint32_t zero) {
         less_low = 0xc200c200u + zero * 0x00010001u;  // (the last place of 32 is 1/4)
-        const __nv_bfloat162 q = __float2bfloat162_rn(-0.25f * float(zero));
-        less_high = *reinterpret_cast<const uint32_t*>(&q);
+        less_high = fma(0x43004300u + zero * 0x00010001u, 0xbe80be80u, 0x42004200u);  // 32 - (128 + z)/4
     }
     static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
         uint32_t r;
@@ -230,19 +237,37 @@ __device__ __forceinline__ void copy_groups(const uint8_t* base, int64_t from, i
     auto word = [&](int row, int w) {  // byte offset
         return ((from + int64_t(row) * row_values) * kSize & ~int64_t(3)) + w * 4;
     };
-    int64_t at = word(lane / kWords, lane % kWords);
-    uint32_t dst = to + ((lane / kWords) * (kWords + 1) + lane % kWords) * 4;
+    const int64_t at = word(lane / kWords, lane % kWords);
+    const uint32_t dst = to + ((lane / kWords) * (kWords + 1) + lane % kWords) * 4;
     const int64_t step = int64_t(kRows) * row_values * kSize;
+    if (inner) {  // one warp keeps up with all others only with few instructions per word
+        const uint8_t* src = base + at;
+        uint32_t d = dst;
+#pragma unroll 8
+        for (int r = 0; r < kTileN; r += kRows) {
+            copy_word_async(d, src, 4);
+            src += step;
+            d += kRows * (kWords + 1) * 4;
+        }
+#pragma unroll 1
+        for (int r = 0; r < kTileN; r += 32)
+            copy_word_async(to + ((r + lane) * (kWords + 1) + kWords) * 4,
+                            base + word(r + lane, kWords), 4);
+        return;
+    }
+    const int64_t end = all * kSize;
     auto copy = [&](int64_t src, uint32_t d) {
-        const int64_t left = inner ? 4 : all * kSize - src;
+        const int64_t left = end - src;
         const uint32_t bytes = left <= 0 ? 0u : left < 4 ? uint32_t(left) : 4u;
         copy_word_async(d, bytes ? base + src : base, bytes);
     };
+    int64_t src = at;
+    uint32_t d = dst;
 #pragma unroll 4
     for (int r = 0; r < kTileN; r += kRows) {
-        copy(at, dst);
-        at += step;
-        dst += kRows * (kWords + 1) * 4;
+        copy(src, d);
+        src += step;
+        d += kRows * (kWords + 1) * 4;
     }
 #pragma unroll
     for (int r = lane; r < kTileN; r += 32)
@@ -255,7 +280,8 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     linear_w4_kernel(const __grid_constant__ CUtensorMap tmap_w,
                      const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     constexpr int kN = mma_n(kCols);
-    constexpr int kStages = stages(kCols);
+    constexpr int kStages = stages(kCols, kGroups);
+    constexpr int kScaleBufs = scale_bufs_of(kGroups);
     constexpr int kStageBytes = stage_bytes(kCols);
     constexpr int kTeams = num_teams(kCols, kGroups);
     constexpr int kDs = num_d(kCols, kGroups);
@@ -272,7 +298,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     uint8_t* smem = smem_raw + pad;
     const uint32_t stage0 = raw_addr + pad;
     uint8_t* scale_bufs = smem + size_t(kStages) * kStageBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(scale_bufs + 2 * kScaleBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(scale_bufs + kScaleBufs * kScaleBytes);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kMaxBarriers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -280,14 +306,14 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
     auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (kStages + s); };
     constexpr int kA = 2 * kStages, kD = kA + 2 * kTeams, kS = kD + 2 * kDs;
-    static_assert(kS + 5 <= kMaxBarriers, "barriers");
+    static_assert(kS + 2 * kScaleBufs + 1 <= kMaxBarriers, "barriers");
     auto a_full = [&](uint32_t team) { return bar0 + 8 * (kA + team); };
     auto a_empty = [&](uint32_t team) { return bar0 + 8 * (kA + kTeams + team); };
     auto d_full = [&](uint32_t d) { return bar0 + 8 * (kD + d); };
     auto d_empty = [&](uint32_t d) { return bar0 + 8 * (kD + kDs + d); };
     auto s_full = [&](uint32_t buf) { return bar0 + 8 * (kS + buf); };
-    auto s_empty = [&](uint32_t buf) { return bar0 + 8 * (kS + 2 + buf); };
-    const uint32_t drain_bar = bar0 + 8 * (kS + 4);
+    auto s_empty = [&](uint32_t buf) { return bar0 + 8 * (kS + kScaleBufs + buf); };
+    const uint32_t drain_bar = bar0 + 8 * (kS + 2 * kScaleBufs);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -305,7 +331,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
             mbar_init(d_full(i), 1);
             mbar_init(d_empty(i), kProductWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kScaleBufs; ++i) {
             mbar_init(s_full(i), 32);  // the copying warp's lanes
             mbar_init(s_empty(i), kProductWarps + (kZeros ? kTeams * kTeamWarps : 0));
         }
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                         break;
                     }
                     const uint32_t at = stage0 + stage * kStageBytes;
-                    mbar_arrive_expect_tx(full_bar(stage), kStageBytes);
+                    mbar_arrive_expect_tx(full_bar(stage), kCodeBytes + uint32_t(p.x_rows) * kStageK * 2);
                     tma_load_2d(&tmap_w, full_bar(stage), at, ks * (kStageK / 2), tile * kTileN);
 #pragma unroll
                     for (int i = 0; i < kStageK / 64; ++i)
@@ -444,8 +470,10 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                     copy_groups<1>(p.zeros, from, p.num_groups, int64_t(p.N) * p.num_groups, inner,
                                    lane, to + kTileN * kScaleWords * 4);
                 copy_words_arrive(s_full(buf));
-                buf ^= 1u;
-                if (buf == 0) buf_phase ^= 1u;
+                if (++buf == kScaleBufs) {
+                    buf = 0;
+                    buf_phase ^= 1u;
+                }
             }
         }
         copy_words_wait_all();  // (no copy outlives the CTA)
@@ -489,8 +517,10 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty(buf));
-                buf ^= 1u;
-                if (buf == 0) buf_phase ^= 1u;
+                if (++buf == kScaleBufs) {
+                    buf = 0;
+                    buf_phase ^= 1u;
+                }
             }
             if (p.splits == 1 && n < p.N && ok) {
                 const int64_t t0 = int64_t(chunk) * kCols;
@@ -520,6 +550,12 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 const uint8_t* zeros = scale_bufs + buf * kScaleBytes + kTileN * kScaleWords * 4 +
                                        row_in_tile * kZeroWords * 4;
                 if (ok && turn == uint32_t(team)) {
+                    uint32_t zero[kGroups];  // (the row's values lie behind the shift of its first word)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        zero[g] = kZeros ? zeros[((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
+                                                 in_chunk * kGroups + g]
+                                         : 8u;
                     ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
                     if (!ok) break;
                     // 16-byte pieces of the row, swizzled by its place among eight
@@ -528,11 +564,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                     uint4 next = load_shared_v4(codes);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        // (the row's values lie behind the shift of its first word)
-                        const Numbers<Elem> minus(
-                            kZeros ? uint32_t(zeros[((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
-                                                    in_chunk * kGroups + g])
-                                   : 8u);
+                        const Numbers<Elem> minus(zero[g]);
 #pragma unroll
                         for (int c = g * 8 / kGroups; c < (g + 1) * 8 / kGroups; ++c) {
                             const uint4 words = next;
@@ -554,8 +586,10 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 if (kZeros && (in_chunk == kChunkStages - 1 || ks + 1 == k_last)) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty(buf));
-                    buf ^= 1u;
-                    if (buf == 0) buf_phase ^= 1u;
+                    if (++buf == kScaleBufs) {
+                        buf = 0;
+                        buf_phase ^= 1u;
+                    }
                 }
                 if (++stage == kStages) {
                     stage = 0;
@@ -626,7 +660,7 @@ template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
 cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, int num_sms,
                    cudaStream_t stream) {
     auto kernel = linear_w4_kernel<Elem, Out, kCols, kGroups, kZeros>;
-    constexpr size_t smem = smem_bytes(kCols);
+    constexpr size_t smem = smem_bytes(kCols, kGroups);
     static int configured[64];  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -693,14 +727,15 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
     const int64_t chunks = (T + cols - 1) / cols;
     if (tiles * chunks * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
     Args p = {scales, zeros, y, T, int(N), int((K + group - 1) / group), int(chunks),
-              int(tiles * chunks), int((K + kStageK - 1) / kStageK), 1};
+              int(tiles * chunks), int((K + kStageK - 1) / kStageK), 1,
+              int(T < mma_n(cols) ? T : mma_n(cols))};
     p.splits = num_splits(int(tiles), p.num_stages, num_sms);
     CUtensorMap tw, tx;
     // (fp16 and bf16 are copied alike)
     if (!encode_tensor_map_2d(&tw, codes, uint64_t(K / 2), uint64_t(N), uint64_t(K / 2),
                               kStageK / 2, kTileN, true) ||
         !encode_tensor_map_2d(&tx, x, uint64_t(K), uint64_t(T), uint64_t(K) * 2, 64,
-                              uint32_t(mma_n(cols)), false))
+                              uint32_t(p.x_rows), false))
         return cudaErrorInvalidValue;
     auto go = [&](auto elem, auto out) {
         using Elem = decltype(elem);
