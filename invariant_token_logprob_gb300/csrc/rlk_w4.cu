@@ -10,6 +10,7 @@
 // (8w + 2i, 8w + 2i + 1) in the halves of a register.
 #include "rlk_internal.h"
 #include "rlk_logits.cuh"
+#include "rlk_w4.cuh"
 
 namespace rlk {
 namespace {
@@ -19,106 +20,223 @@ constexpr int kThreads = 256;
 // Bit position of code k of a word (k = 0..7).
 __host__ __device__ constexpr int code_shift(int k) { return 4 * ((k & 1) * 4 + k / 2); }
 
-// One group of kGroup elements is held by kGroup / 8 neighbouring lanes, eight
-// elements (16 bytes of W, one word of codes) each.
-template <typename Elem, int kGroup>
-__global__ void __launch_bounds__(kThreads)
+// Pieces of eight elements (16 bytes of W, one word of codes) per thread whose loads are in
+// flight together: 64 KB per SM.
+constexpr int kPieces = 4;
+
+// Quotients x / s of 16-bit numbers of up to 16 in magnitude, exactly rounded at ties: with
+// the reciprocal r, t = x r is off by some units of the last place; the remainder x - t s,
+// exact in a multiply-add, corrects it (Newton's step for the quotient), so a quotient that
+// is a whole number and a half comes out as that.  No other quotient of two numbers with 11
+// significant bits lies closer to a half than 2^-13, far above what is left of the error.
+// Scales below 2^-64 (whose reciprocals or remainders could leave fp32's range) divide.
+constexpr float kFastScale = 5.42101086e-20f;  // 2^-64
+struct Quotient {
+    float s, r;
+    bool fast;
+    __device__ __forceinline__ explicit Quotient(float scale)
+        : s(scale), r(1.0f / scale), fast(scale >= kFastScale) {}
+    __device__ __forceinline__ float operator()(float x) const {
+        if (!fast) return x / s;
+        const float t = x * r;
+        return fmaf(fmaf(-t, s, x), r, t);
+    }
+};
+
+// One group is held by kGroup / 8 neighbouring lanes, a piece each.  HBM-bound: reads W and
+// writes a quarter of its bytes; a division per element would take longer than the bytes.
+// kWhole: group divides K, so the pieces of W are dealt to the threads in memory order.
+template <typename Elem, int kGroup, bool kZeros, bool kWhole>
+__global__ void __launch_bounds__(kThreads, 4)
     quantize_w4_kernel(const Elem* __restrict__ W, int64_t N, int K, int num_groups,
                        uint32_t* __restrict__ codes, Elem* __restrict__ scales,
                        uint8_t* __restrict__ zeros) {
     constexpr int kLanes = kGroup / 8;
-    const int64_t piece = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;  // (n, g)
-    const int sub = threadIdx.x % kLanes;
-    const bool act = piece < N * num_groups;
-    const int64_t n = act ? piece / num_groups : 0;
-    const int g = act ? int(piece - n * num_groups) : 0;
-    const int k = g * kGroup + sub * 8;
-    const bool in_row = act && k < K;
-    float x[8];
-    union {
-        uint4 v;
-        Elem e[8];
-    } raw;
-    raw.v = make_uint4(0u, 0u, 0u, 0u);
-    if (in_row) raw.v = *reinterpret_cast<const uint4*>(W + n * K + k);
-    float lo = 0.0f, hi = 0.0f;
+    const int64_t groups = N * num_groups;
+    // (!kWhole) the row of the block's first group; the others by a 32-bit division from there
+    const int64_t group0 = int64_t(blockIdx.x) * (kPieces * kThreads / kLanes);
+    const int64_t row0 = kWhole ? 0 : group0 / num_groups;
+    uint4 raw[kPieces];
+    int64_t at[kPieces];  // piece of W, or -1 behind a row's end
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = to_float(raw.e[i]);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+    for (int i = 0; i < kPieces; ++i) {
+        const int64_t p = (int64_t(blockIdx.x) * kPieces + i) * kThreads + threadIdx.x;
+        const int64_t group = p / kLanes;
+        at[i] = -1;
+        if (group < groups) {
+            if (kWhole) {
+                at[i] = p;
+            } else {
+                const uint32_t from_row0 = uint32_t(group - row0 * num_groups);
+                const uint32_t rows = from_row0 / uint32_t(num_groups);
+                const int k8 = int(from_row0 - rows * uint32_t(num_groups)) * kLanes + int(p % kLanes);
+                if (k8 < K / 8) at[i] = (row0 + rows) * (K / 8) + k8;
+            }
+        }
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at[i] >= 0) raw[i] = __ldcs(reinterpret_cast<const uint4*>(W) + at[i]);
     }
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    }
-    Elem s16 = from_float<Elem>(zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f);
-    if (to_float(s16) == 0.0f) s16 = from_float<Elem>(1.0f);
-    const float s = to_float(s16);
-    const float z = zeros ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 8.0f;
-    uint32_t word = 0;
+    for (int i = 0; i < kPieces; ++i) {
+        const Elem* e = reinterpret_cast<const Elem*>(&raw[i]);
+        float x[8], lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = rintf(x[i] / s);
-        const float q = zeros ? fminf(fmaxf(r + z, 0.0f), 15.0f) : fminf(fmaxf(r, -7.0f), 7.0f) + 8.0f;
-        word |= uint32_t(int(q)) << code_shift(i);
-    }
-    if (in_row) codes[n * (K / 8) + k / 8] = word;
-    if (act && sub == 0) {
-        scales[piece] = s16;
-        if (zeros) zeros[piece] = uint8_t(int(z));
+        for (int j = 0; j < 8; ++j) {
+            x[j] = to_float(e[j]);
+            if (kZeros) lo = fminf(lo, x[j]);
+            hi = fmaxf(hi, kZeros ? x[j] : fabsf(x[j]));
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) {
+            if (kZeros) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+        }
+        Elem s16 = from_float<Elem>(kZeros ? (hi - lo) / 15.0f : hi / 7.0f);
+        if (to_float(s16) == 0.0f) s16 = from_float<Elem>(1.0f);
+        const Quotient over(to_float(s16));
+        const float z = kZeros ? fminf(fmaxf(rintf(over(-lo)), 0.0f), 15.0f) : 8.0f;
+        // 2^23 + 2^22 + q has q in its low bits; the words' constant part is subtracted at
+        // the end.  Adding the (even) constant rounds a half to the even code.
+        constexpr float kMagic = 12582912.0f;
+        constexpr uint32_t kMagicBits = 0x4b400000u;
+        uint32_t word = 0, constant = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float q = over(x[j]);
+            if (kZeros)
+                q = fminf(fmaxf((q + kMagic) - kMagic + z, 0.0f), 15.0f) + kMagic;
+            else
+                q = fminf(fmaxf(q, -7.0f), 7.0f) + (kMagic + 8.0f);
+            word += __float_as_uint(q) * (1u << code_shift(j));
+            constant += kMagicBits * (1u << code_shift(j));
+        }
+        if (at[i] >= 0) {
+            __stcs(codes + at[i], word - constant);
+            const int64_t p = (int64_t(blockIdx.x) * kPieces + i) * kThreads + threadIdx.x;
+            if (p % kLanes == 0) {
+                scales[p / kLanes] = s16;
+                if (kZeros) zeros[p / kLanes] = uint8_t(int(z));
+            }
+        }
     }
 }
 
-// One word of codes per thread.
-template <typename Elem, typename Out>
+// Words of codes per thread whose loads are in flight together.
+constexpr int kWords = 8;
+
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b, __nv_bfloat16) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b, __half) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Values of a word, in order: scale * (q - zero) rounded once.  HBM-bound: writes four times
+// what it reads.
+template <typename Elem>
+__device__ __forceinline__ void values(uint32_t word, Elem scale, uint32_t zero, Elem* out) {
+    const Numbers<Elem> minus(zero);
+    const Elem two[2] = {scale, scale};
+    const Elem four = from_float<Elem>(1.0f / Numbers<Elem>::kUnit);
+    const Elem fours[2] = {four, four};
+    const uint32_t s = *reinterpret_cast<const uint32_t*>(two);
+    const uint32_t f = *reinterpret_cast<const uint32_t*>(fours);
+    uint32_t r[4];
+    minus.pair(word, r[0], r[1]);
+    minus.pair(word >> 8, r[2], r[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = times(times(r[j], f, Elem()), s, Elem());
+    __stcs(reinterpret_cast<uint4*>(out), make_uint4(r[0], r[1], r[2], r[3]));
+}
+template <typename Elem>
+__device__ __forceinline__ void values(uint32_t word, Elem scale, uint32_t zero, float* out) {
+    const float s = to_float(scale);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = float(int((word >> code_shift(j)) & 15u) - int(zero)) * s;
+    __stcs(reinterpret_cast<float4*>(out), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+
+template <typename Elem, typename Out, bool kWhole>
 __global__ void __launch_bounds__(kThreads)
     dequantize_w4_kernel(const uint32_t* __restrict__ codes, const Elem* __restrict__ scales,
-                         const uint8_t* __restrict__ zeros, int64_t N, int K, int group,
-                         int num_groups, Out* __restrict__ W) {
-    const int words = K / 8;
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= N * words) return;
-    const int64_t n = i / words;
-    const int g = int(i - n * words) * 8 / group;
-    const float s = to_float(scales[n * num_groups + g]);
-    const int z = zeros ? zeros[n * num_groups + g] : 8;
-    const uint32_t word = codes[i];
-    union {
-        uint4 v[sizeof(Out) / 2];
-        Out e[8];
-    } o;
+                         const uint8_t* __restrict__ zeros, int64_t N, int K, int group_shift,
+                         int num_groups, Out* __restrict__ W) {  // groups of 2^group_shift words
+    const int row_words = K / 8;
+    const int64_t all = N * row_words;
+    const int64_t block0 = int64_t(blockIdx.x) * (kWords * kThreads);
+    const int64_t row0 = kWhole ? 0 : block0 / row_words;  // (!kWhole) of the block's first word
+    const int64_t first = block0 + threadIdx.x;
+    uint32_t word[kWords], zero[kWords];
+    Elem scale[kWords];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        o.e[j] = from_float<Out>(float(int((word >> code_shift(j)) & 15u) - z) * s);
+    for (int i = 0; i < kWords; ++i) {
+        const int64_t w = first + i * kThreads;
+        if (w < all) {
+            word[i] = __ldcs(codes + w);
+            int64_t g = w >> group_shift;
+            if (!kWhole) {
+                const uint32_t from_row0 = uint32_t(w - row0 * row_words);
+                const uint32_t rows = from_row0 / uint32_t(row_words);
+                g = (row0 + rows) * num_groups +
+                    ((from_row0 - rows * uint32_t(row_words)) >> group_shift);
+            }
+            scale[i] = scales[g];
+            zero[i] = zeros ? zeros[g] : 8u;
+        }
+    }
 #pragma unroll
-    for (int j = 0; j < int(sizeof(Out) / 2); ++j) reinterpret_cast<uint4*>(W + i * 8)[j] = o.v[j];
+    for (int i = 0; i < kWords; ++i) {
+        const int64_t w = first + i * kThreads;
+        if (w < all) values(word[i], scale[i], zero[i], W + w * 8);
+    }
+}
+
+template <typename Elem, int kGroup>
+cudaError_t quantize(const void* W, int64_t N, int64_t K, uint32_t* codes, void* scales,
+                     uint8_t* zeros, cudaStream_t stream) {
+    const int64_t G = (K + kGroup - 1) / kGroup;
+    const int64_t pieces = N * G * (kGroup / 8);
+    const int64_t blocks = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
+    auto go = [&](auto kernel) {
+        kernel<<<unsigned(blocks), kThreads, 0, stream>>>(static_cast<const Elem*>(W), N, int(K),
+                                                          int(G), codes, static_cast<Elem*>(scales),
+                                                          zeros);
+        return cudaGetLastError();
+    };
+    if (K % kGroup == 0)
+        return zeros ? go(quantize_w4_kernel<Elem, kGroup, true, true>)
+                     : go(quantize_w4_kernel<Elem, kGroup, false, true>);
+    return zeros ? go(quantize_w4_kernel<Elem, kGroup, true, false>)
+                 : go(quantize_w4_kernel<Elem, kGroup, false, false>);
 }
 
 template <typename Elem>
-cudaError_t quantize(const void* W, int64_t N, int64_t K, int group, uint32_t* codes, void* scales,
-                     uint8_t* zeros, cudaStream_t stream) {
-    const int G = int((K + group - 1) / group);
-    const int64_t blocks = (N * G * (group / 8) + kThreads - 1) / kThreads;
-    auto go = [&](auto kernel) {
-        kernel<<<unsigned(blocks), kThreads, 0, stream>>>(static_cast<const Elem*>(W), N, int(K), G,
-                                                          codes, static_cast<Elem*>(scales), zeros);
-        return cudaGetLastError();
-    };
-    if (group == 32) return go(quantize_w4_kernel<Elem, 32>);
-    if (group == 64) return go(quantize_w4_kernel<Elem, 64>);
-    return go(quantize_w4_kernel<Elem, 128>);
+cudaError_t quantize_group(const void* W, int64_t N, int64_t K, int group, uint32_t* codes,
+                           void* scales, uint8_t* zeros, cudaStream_t stream) {
+    if (group == 32) return quantize<Elem, 32>(W, N, K, codes, scales, zeros, stream);
+    if (group == 64) return quantize<Elem, 64>(W, N, K, codes, scales, zeros, stream);
+    return quantize<Elem, 128>(W, N, K, codes, scales, zeros, stream);
 }
 
 template <typename Elem, typename Out>
 cudaError_t dequantize(const uint32_t* codes, const void* scales, const uint8_t* zeros, int64_t N,
                        int64_t K, int group, void* W, cudaStream_t stream) {
-    const int64_t blocks = (N * (K / 8) + kThreads - 1) / kThreads;
-    dequantize_w4_kernel<Elem, Out><<<unsigned(blocks), kThreads, 0, stream>>>(
-        codes, static_cast<const Elem*>(scales), zeros, N, int(K), group,
-        int((K + group - 1) / group), static_cast<Out*>(W));
-    return cudaGetLastError();
+    const int64_t blocks = (N * (K / 8) + kThreads * kWords - 1) / (kThreads * kWords);
+    auto go = [&](auto kernel) {
+        kernel<<<unsigned(blocks), kThreads, 0, stream>>>(
+            codes, static_cast<const Elem*>(scales), zeros, N, int(K),
+            group == 32 ? 2 : group == 64 ? 3 : 4,
+            int((K + group - 1) / group), static_cast<Out*>(W));
+        return cudaGetLastError();
+    };
+    return K % group == 0 ? go(dequantize_w4_kernel<Elem, Out, true>)
+                          : go(dequantize_w4_kernel<Elem, Out, false>);
 }
 
 }  // namespace
@@ -126,8 +244,8 @@ cudaError_t dequantize(const uint32_t* codes, const void* scales, const uint8_t*
 cudaError_t launch_quantize_w4(const void* W, ElemType type, int64_t N, int64_t K, int group,
                                uint32_t* codes, void* scales, uint8_t* zeros, cudaStream_t stream) {
     return type == ElemType::kBf16
-               ? quantize<__nv_bfloat16>(W, N, K, group, codes, scales, zeros, stream)
-               : quantize<__half>(W, N, K, group, codes, scales, zeros, stream);
+               ? quantize_group<__nv_bfloat16>(W, N, K, group, codes, scales, zeros, stream)
+               : quantize_group<__half>(W, N, K, group, codes, scales, zeros, stream);
 }
 
 cudaError_t launch_dequantize_w4(const uint32_t* codes, const void* scales, const uint8_t* zeros,
