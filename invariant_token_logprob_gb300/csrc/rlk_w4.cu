@@ -8,8 +8,11 @@
 // group.  Eight codes k = 8w .. 8w+7 make word w of a row: the even k in nibbles
 // 0..3, the odd k in nibbles 4..7, so that (word >> 4i) & 0x000f000f is the pair
 // (8w + 2i, 8w + 2i + 1) in the halves of a register.
+#include <float.h>
+
 #include "rlk_internal.h"
 #include "rlk_logits.cuh"
+#include "rlk_sm103.cuh"
 #include "rlk_w4.cuh"
 
 namespace rlk {
@@ -24,24 +27,89 @@ __host__ __device__ constexpr int code_shift(int k) { return 4 * ((k & 1) * 4 + 
 // flight together: 64 KB per SM.
 constexpr int kPieces = 4;
 
-// Quotients x / s of 16-bit numbers of up to 16 in magnitude, exactly rounded at ties: with
-// the reciprocal r, t = x r is off by some units of the last place; the remainder x - t s,
-// exact in a multiply-add, corrects it (Newton's step for the quotient), so a quotient that
-// is a whole number and a half comes out as that.  No other quotient of two numbers with 11
+// a / b for a constant b with r = 1 / b rounded: t = a r is off by a unit of the last place
+// at most, and the remainder a - t b, exact in a multiply-add, corrects it (Newton's step for
+// the quotient) to the correctly rounded one.
+__device__ __forceinline__ float divide(float a, float b, float r) {
+    const float t = a * r;
+    return fmaf(fmaf(-t, b, a), r, t);
+}
+__device__ __forceinline__ float reciprocal(float a) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+
+// Largest |x| of the four pairs of a piece.
+__device__ __forceinline__ float max_abs(const uint4& v, __nv_bfloat16) {
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w);
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return fmaxf(m.x, m.y);
+}
+__device__ __forceinline__ float max_abs(const uint4& v, __half) {
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+    const __half2* p = reinterpret_cast<const __half2*>(w);
+    const float2 m = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return fmaxf(m.x, m.y);
+}
+
+// The smallest scale whose own rounding is a small part of it (and whose reciprocal and
+// remainders stay inside fp32's range): from here on |x / scale| exceeds 7 (or a span 15) by
+// less than half a code, so no code needs clamping at its end.
+__device__ __forceinline__ float normal_scale(__nv_bfloat16) { return 7.8886090522101181e-31f; }  // 2^-100
+__device__ __forceinline__ float normal_scale(__half) { return 1.220703125e-4f; }                 // 2^-13
+
+// The word of eight codes.  2^23 + 2^22 + q has the whole number q in its low bits; adding the
+// constant, which is even, rounds a half to the even code.  The words' constant part is
+// subtracted at the end.
+constexpr float kMagic = 12582912.0f;
+constexpr uint32_t kMagicBits = 0x4b400000u;
+__host__ __device__ constexpr uint32_t magic_word() {
+    uint32_t c = 0;
+    for (int j = 0; j < 8; ++j) c += kMagicBits * (1u << code_shift(j));
+    return c;
+}
+
+// Quotients x / s, exactly rounded at ties: with an approximate reciprocal r, t = x r is off
+// by some units of the last place; the remainder x - t s corrects it, so a quotient that is a
+// whole number and a half comes out as that.  No other quotient of two numbers with 11
 // significant bits lies closer to a half than 2^-13, far above what is left of the error.
-// Scales below 2^-64 (whose reciprocals or remainders could leave fp32's range) divide.
-constexpr float kFastScale = 5.42101086e-20f;  // 2^-64
-struct Quotient {
-    float s, r;
-    bool fast;
-    __device__ __forceinline__ explicit Quotient(float scale)
-        : s(scale), r(1.0f / scale), fast(scale >= kFastScale) {}
-    __device__ __forceinline__ float operator()(float x) const {
-        if (!fast) return x / s;
-        const float t = x * r;
-        return fmaf(fmaf(-t, s, x), r, t);
+template <bool kZeros>
+__device__ __forceinline__ uint32_t code_word(const float2 (&x)[4], float s, float z) {
+    const float r = reciprocal(s);
+    const F2 rr = pack2(r, r), ss = pack2(-s, -s);
+    const float add = kZeros ? kMagic : kMagic + 8.0f;
+    const F2 magic = pack2(add, add);
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const F2 v = pack2(x[j].x, x[j].y);
+        const F2 t = mul2(v, rr);
+        F2 q = add2(fma2(fma2(t, ss, v), rr, t), magic);
+        if (kZeros) {  // the two ends' roundings may add up to one code more than 15
+            const float2 f = unpack2(add2(q, pack2(z, z)));
+            q = pack2(fminf(f.x, kMagic + 15.0f), fminf(f.y, kMagic + 15.0f));
+        }
+        const float2 f = unpack2(q);
+        word += __float_as_uint(f.x) * (1u << code_shift(2 * j));
+        word += __float_as_uint(f.y) * (1u << code_shift(2 * j + 1));
     }
-};
+    return word - magic_word();
+}
+// The same by division and with both ends clamped, for scales near the end of their range.
+template <bool kZeros>
+__device__ __noinline__ uint32_t code_word_small(float2 x0, float2 x1, float2 x2, float2 x3, float s,
+                                                 float z) {
+    const float x[8] = {x0.x, x0.y, x1.x, x1.y, x2.x, x2.y, x3.x, x3.y};
+    uint32_t word = 0;
+    for (int j = 0; j < 8; ++j) {
+        const float q = rintf(x[j] / s);
+        const float c = kZeros ? fminf(fmaxf(q + z, 0.0f), 15.0f) : fminf(fmaxf(q, -7.0f), 7.0f) + 8.0f;
+        word |= uint32_t(int(c)) << code_shift(j);
+    }
+    return word;
+}
 
 // One group is held by kGroup / 8 neighbouring lanes, a piece each.  HBM-bound: reads W and
 // writes a quarter of its bytes; a division per element would take longer than the bytes.
@@ -78,40 +146,44 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const Elem* e = reinterpret_cast<const Elem*>(&raw[i]);
-        float x[8], lo = 0.0f, hi = 0.0f;
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float2 x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = to_float(e[j]);
-            if (kZeros) lo = fminf(lo, x[j]);
-            hi = fmaxf(hi, kZeros ? x[j] : fabsf(x[j]));
+        for (int j = 0; j < 4; ++j) x[j] = pair_to_float(w[j], Elem());
+        float lo = 0.0f, hi = 0.0f;
+        if (kZeros) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo = fminf(fminf(lo, x[j].x), x[j].y);
+                hi = fmaxf(fmaxf(hi, x[j].x), x[j].y);
+            }
+        } else {
+            hi = max_abs(raw[i], Elem());
         }
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1) {
             if (kZeros) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
         }
-        Elem s16 = from_float<Elem>(kZeros ? (hi - lo) / 15.0f : hi / 7.0f);
-        if (to_float(s16) == 0.0f) s16 = from_float<Elem>(1.0f);
-        const Quotient over(to_float(s16));
-        const float z = kZeros ? fminf(fmaxf(rintf(over(-lo)), 0.0f), 15.0f) : 8.0f;
-        // 2^23 + 2^22 + q has q in its low bits; the words' constant part is subtracted at
-        // the end.  Adding the (even) constant rounds a half to the even code.
-        constexpr float kMagic = 12582912.0f;
-        constexpr uint32_t kMagicBits = 0x4b400000u;
-        uint32_t word = 0, constant = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float q = over(x[j]);
-            if (kZeros)
-                q = fminf(fmaxf((q + kMagic) - kMagic + z, 0.0f), 15.0f) + kMagic;
-            else
-                q = fminf(fmaxf(q, -7.0f), 7.0f) + (kMagic + 8.0f);
-            word += __float_as_uint(q) * (1u << code_shift(j));
-            constant += kMagicBits * (1u << code_shift(j));
+        Elem s16 = from_float<Elem>(kZeros ? divide(hi - lo, 15.0f, 1.0f / 15.0f)
+                                           : divide(hi, 7.0f, 1.0f / 7.0f));
+        if (kZeros && isinf(hi - lo)) s16 = from_float<Elem>(INFINITY);  // (bf16: a span beyond fp32)
+        float s = to_float(s16);
+        float z = 8.0f;
+        uint32_t word;
+        if (s >= normal_scale(Elem()) && s <= FLT_MAX) {
+            if (kZeros) z = rintf(divide(-lo, s, reciprocal(s)));
+            word = code_word<kZeros>(x, s, z);
+        } else {
+            if (s == 0.0f) {
+                s = 1.0f;
+                s16 = from_float<Elem>(1.0f);
+            }
+            if (kZeros) z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
+            word = code_word_small<kZeros>(x[0], x[1], x[2], x[3], s, z);
         }
         if (at[i] >= 0) {
-            __stcs(codes + at[i], word - constant);
+            __stcs(codes + at[i], word);
             const int64_t p = (int64_t(blockIdx.x) * kPieces + i) * kThreads + threadIdx.x;
             if (p % kLanes == 0) {
                 scales[p / kLanes] = s16;

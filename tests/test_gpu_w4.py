@@ -98,6 +98,24 @@ def test_quantize_every_step_of_the_grid():
         assert torch.equal(scales.cpu(), s) and torch.equal(rlk.unpack_w4(codes).cpu(), q)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quantize_every_maximum(dtype):
+    """Every finite positive value of the type as a group's maximum (subnormal ones too): the
+    scales' rounding, and codes at whole and half steps of them."""
+    import invariant_token_logprob_gb300 as rlk
+    top = torch.arange(1, 0x7f80 if dtype == "bf16" else 0x7c00, dtype=torch.int32).to(torch.int16)
+    m = top.view(DTYPES[dtype])
+    f = torch.linspace(-1, 1, 31)
+    f[15] = 0.0
+    W = torch.cat([m.float()[:, None], m.float()[:, None] * f], 1).to(DTYPES[dtype])
+    for asym in (False, True):
+        codes, scales, zeros = rlk.quantize_w4(W.cuda(), 32, asym)
+        q, s, z = ref_quantize(W, 32, asym)
+        assert torch.equal(scales.cpu(), s), asym
+        assert torch.equal(rlk.unpack_w4(codes).cpu(), q), asym
+        assert z is None or torch.equal(zeros.cpu(), z)
+
+
 def make(T, N, K, group, dtype, zeros, seed):
     """Codes over the whole range, scales over some binades, zero points of every value."""
     g = torch.Generator().manual_seed(seed)
