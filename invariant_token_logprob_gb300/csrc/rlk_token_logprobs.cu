@@ -43,6 +43,7 @@ constexpr int kGroup = 8;               // neighbouring elements per lane
 constexpr int kStep = 32 * kGroup;      // elements of a strip side by side
 constexpr int kStride = kStrips * kStep;  // from a lane's group to its next one
 constexpr int kCells = kStrips * 32;
+constexpr uint32_t kNoStrip = uint32_t(INT_MAX) / kStep + 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Rows whose target was >= V, counted since the last read on this device.
@@ -204,61 +205,75 @@ struct LaneState {
     }
 };
 
-// One strip's lane: its sums, and its cell's key.  Groups are taken two at a time as long
-// as the strip's two rows of groups lie whole in the row, with the next two's loads in
-// flight, then one at a time.  How they are taken follows from V alone (a unit's maximum
-// decides the rounding), not from the row's alignment.
-template <typename Elem, bool kShifted, bool kMasked>
+// How a strip's groups are taken: rows of 32 groups (one per lane, kStride apart) two at a
+// time, a unit, as long as they lie whole in the row, the last one alone where their number
+// is odd, and then the row's end.  It follows from V alone (a unit's maximum decides the
+// rounding), not from the row's alignment.
+struct StripPlan {
+    uint32_t base;   // the strip's first element
+    uint32_t whole;  // rows of groups whose vectors, and the longest shift, lie in the row
+    __device__ __forceinline__ StripPlan(uint32_t strip, uint32_t V)
+        : base(strip * kStep),
+          whole(base + kStep + kGroup <= V ? (V - base - kStep - kGroup) / kStride + 1 : 0) {}
+};
+
+// One unit's loads.
+template <typename Elem, bool kShifted>
+struct Unit {
+    Vectors<Elem, kShifted> in[2];
+    uint32_t b[2];
+    // Row `first` of the strip and, if it is whole too, the next one.
+    template <bool kMasked>
+    __device__ __forceinline__ void load(const Elem* row, const uint8_t* bits, int shift, int lane,
+                                         const StripPlan& plan, uint32_t first) {
+        const uint32_t e = plan.base + lane * kGroup + first * kStride;
+        // the row's first group has its first vector in front of a shifted row: read apart
+        in[0].load(row, kShifted && e == 0 ? kStep : e, shift);
+        if (kMasked) b[0] = bits[e / kGroup];
+        if (first + 1 < plan.whole) {
+            in[1].load(row, e + kStride, shift);
+            if (kMasked) b[1] = bits[(e + kStride) / kGroup];
+        }
+    }
+};
+
+// One strip's lane: its sums, and its cell's key.  `unit` holds the loads of its first unit;
+// on return those of the next strip's.
+template <bool kMasked, typename Elem, bool kShifted>
 __device__ __forceinline__ Sums read_strip(const Elem* row, int shift, const uint8_t* bits,
-                                           uint32_t V, uint32_t strip, int lane, float c2,
+                                           uint32_t V, const StripPlan& plan, const StripPlan& next,
+                                           Unit<Elem, kShifted>& unit, int lane, float c2,
                                            uint64_t* cell) {
     using In = Vectors<Elem, kShifted>;
+    constexpr uint32_t kRow = kStride / kGroup;
     LaneState st = {-INFINITY, -FLT_MAX, 0u, pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
-    const uint32_t base = strip * kStep;
-    const uint32_t e = base + lane * kGroup;
-    // rows of groups of this strip whose vectors lie inside the row, and one element more
-    // than the longest shift
-    const uint32_t whole =
-        base + kStep + kGroup <= V ? (V - base - kStep - kGroup) / kStride + 1 : 0;
-    const uint32_t units = whole / 2;
-    // the row's first group has its first vector in front of a shifted row
-    const bool edge = kShifted && e == 0;
-    const Elem* from = row + e;
-    const uint8_t* mask = bits + e / kGroup;
-    In in[2];
-    uint32_t b[2] = {0, 0};
-    if (units > 0) {
-        in[0].load(edge ? from + kStride : from, 0, shift);
-        in[1].load(from + kStride, 0, shift);
-        if (kMasked) {
-            b[0] = mask[0];
-            b[1] = mask[kStride / kGroup];
-        }
-    }
+    const uint32_t group = (plan.base + lane * kGroup) / kGroup;
     uint32_t i = 0;
-    for (uint32_t n = 0; n < units; ++n) {
+    for (; i + 1 < plan.whole; i += 2) {
         Packed8<Elem> x[2];
-        unshift(in, shift, x);
-        if (edge && n == 0) x[0].load_single(row, 0, V);
+        unshift(unit.in, shift, x);
+        if (kShifted && group + i == 0) x[0].load_single(row, 0, V);
         if (kMasked) {
-            x[0].keep(b[0]);
-            x[1].keep(b[1]);
+            x[0].keep(unit.b[0]);
+            x[1].keep(unit.b[1]);
         }
-        if (n + 1 < units) {
-            from += 2 * kStride;
-            in[0].load(from, 0, shift);
-            in[1].load(from + kStride, 0, shift);
-            if (kMasked) {
-                mask += 2 * kStride / kGroup;
-                b[0] = mask[0];
-                b[1] = mask[kStride / kGroup];
-            }
-        }
-        st.add<kMasked>(x, e / kGroup + i * (kStride / kGroup), c2);
-        i += 2;
+        const bool more = i + 2 < plan.whole;
+        if (more || next.whole > 0)
+            unit.template load<kMasked>(row, bits, shift, lane, more ? plan : next, more ? i + 2 : 0);
+        st.add<kMasked>(x, group + i * kRow, c2);
     }
-    for (; int64_t(base) + int64_t(i) * kStride < V; ++i) {
-        const int64_t e0 = int64_t(e) + int64_t(i) * kStride;
+    if (i < plan.whole) {
+        Packed8<Elem> x[2];
+        unshift(unit.in, shift, x);
+        if (kShifted && group + i == 0) x[0].load_single(row, 0, V);
+        if (kMasked) x[0].keep(unit.b[0]);
+        if (next.whole > 0) unit.template load<kMasked>(row, bits, shift, lane, next, 0);
+        Packed8<Elem> one[1] = {x[0]};
+        st.add<kMasked>(one, group + i * kRow, c2);
+        ++i;
+    }
+    for (; int64_t(plan.base) + int64_t(i) * kStride < V; ++i) {  // the row's end
+        const int64_t e0 = int64_t(group) * kGroup + int64_t(i) * kStride;
         Packed8<Elem> x[1];
         if (In::inside(e0, shift, V)) {
             In one[1];
@@ -445,14 +460,25 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Args 
 
     // A block of eight strips at a time, one strip per warp.
     const int blocks = kBlocks / ranks;
-    for (int j = 0; j < blocks; ++j) {
-        const int strip = (rank * blocks + j) * kWarps + warp;
-        uint64_t cell = 0;
-        sh.strip_sums[j][warp][lane] =
-            shift == 0 ? read_strip<Elem, false, kMasked>(row, 0, bits, p.V, strip, lane, c2, &cell)
-                       : read_strip<Elem, true, kMasked>(row, shift, bits, p.V, strip, lane, c2, &cell);
-        if (p.top_k > 0) sh.cells[(j * kWarps + warp) * 32 + lane] = cell;
-    }
+    auto read = [&](auto shifted) {
+        Unit<Elem, decltype(shifted)::value> unit;
+        const int first = rank * blocks * kWarps + warp;
+        StripPlan plan(first, p.V);
+        if (plan.whole > 0) unit.template load<kMasked>(row, bits, shift, lane, plan, 0);
+        for (int j = 0; j < blocks; ++j) {
+            // (behind the last block: a strip behind every row's end)
+            const StripPlan next(j + 1 < blocks ? first + (j + 1) * kWarps : kNoStrip, p.V);
+            uint64_t cell = 0;
+            sh.strip_sums[j][warp][lane] = read_strip<kMasked>(row, shift, bits, uint32_t(p.V), plan,
+                                                               next, unit, lane, c2, &cell);
+            if (p.top_k > 0) sh.cells[(j * kWarps + warp) * 32 + lane] = cell;
+            plan = next;
+        }
+    };
+    if (shift == 0)
+        read(std::false_type());
+    else
+        read(std::true_type());
     float target_x = -INFINITY;
     if (target >= 0 && target < p.V) target_x = element(row, bits, target);
     __syncthreads();
