@@ -447,6 +447,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Args 
     extern __shared__ uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Launched with programmatic overlap: the kernel ahead in the stream may still be writing
+    // the logits (or reading the outputs) until here.
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int rank = ranks > 1 ? int(cluster_ctarank()) : 0;
     const int64_t t = blockIdx.x / unsigned(ranks);
     const Elem* row = static_cast<const Elem*>(p.logits) + t * p.row_stride;
@@ -637,6 +641,8 @@ template <typename Elem, bool kMasked>
 __global__ void __launch_bounds__(kThreads, 4)
     token_logprobs_backward_kernel(const BackwardArgs p) {
     const int lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int64_t t = blockIdx.x / unsigned(p.parts);
     const int part = int(blockIdx.x - t * p.parts);
     const Elem* row = static_cast<const Elem*>(p.logits) + t * p.row_stride;
@@ -774,16 +780,18 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
         ranks /= 2;
     auto go = [&](auto kernel) {
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = unsigned(ranks);
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = unsigned(ranks);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.gridDim = dim3(unsigned(T * ranks), 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = sizeof(Shared);
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = ranks > 1 ? 1 : 0;
+        cfg.numAttrs = ranks > 1 ? 2 : 1;
         cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, ranks);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
@@ -812,8 +820,17 @@ cudaError_t launch_token_logprobs_backward(const void* logits, ElemType type, in
     p.part_length = int(want);
     p.parts = int((V + want - 1) / want);
     auto go = [&](auto kernel) {
-        kernel<<<unsigned(T * p.parts), kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(unsigned(T * p.parts), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+        return e != cudaSuccess ? e : cudaGetLastError();
     };
     if (type == ElemType::kBf16)
         return allowed ? go(token_logprobs_backward_kernel<__nv_bfloat16, true>)
