@@ -596,9 +596,12 @@ rlk_status rlk_dequantize_w4(const uint32_t *codes_u32, const void *scales,
  * with fp32 accumulation (each group's products of a 16-bit x and a small whole number
  * are exact; a scale is applied once per group, in fp32) and one rounding to out_dtype
  * (`dtype` or RLK_FP32).  x, scales of `dtype` (RLK_BF16 or RLK_FP16), x and codes
- * 16-byte aligned, y aligned to its element.  T >= 0, N >= 0.  Asynchronous on
- * `stream`; allocates nothing.  The order of the sums is fixed by N, K and group: a
- * row's bits depend on that row of x and the weight only, never on T.
+ * 16-byte aligned, y aligned to its element.  T >= 0, N >= 0, T * N <= 2^39.
+ * Asynchronous on `stream`; allocates nothing.  The order of the sums is fixed by N, K
+ * and group: a row's bits depend on that row of x and the weight only, never on T.  A
+ * bounded wait that runs out is reported by rlk_check_device_error.  Callers that capture
+ * graphs make one call of each class before (T up to 8, 16, 32, more; group; with or
+ * without zeros; types): the first one sets its kernel's shared-memory size.
  */
 rlk_status rlk_linear_w4(const void *x, int dtype, const uint32_t *codes_u32, const void *scales,
                          const uint8_t *zeros_u8, int64_t T, int64_t N, int64_t K, int group,

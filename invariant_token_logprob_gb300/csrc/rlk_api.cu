@@ -15,6 +15,7 @@
 
 #include "rlk.h"
 #include "rlk_internal.h"
+#include "rlk_logits_w4.h"
 
 namespace {
 
@@ -896,6 +897,7 @@ rlk_status rlk_linear_w4(const void* x, int dtype, const uint32_t* codes_u32, co
     rlk_status st = check_w4(dtype, N, K, group, codes_u32, scales);
     if (st != RLK_OK) return st;
     if (out_dtype != dtype && out_dtype != RLK_FP32) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && N > (int64_t(1) << 39) / T) return RLK_ERR_INVALID_ARG;
     if (N == 0 || T == 0) return RLK_OK;
     if (!x || !out_y) return RLK_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned_to(out_y, elem_size(out_dtype))) return RLK_ERR_ALIGNMENT;

@@ -27,10 +27,10 @@
 #include <float.h>
 #include <limits.h>
 
-#include "rlk_internal.h"
 #include "rlk_logits.cuh"
+#include "rlk_logits_w4.h"
 #include "rlk_lse.cuh"
-#include "rlk_sm103.cuh"
+#include "rlk_ptx.cuh"
 
 namespace rlk {
 namespace {

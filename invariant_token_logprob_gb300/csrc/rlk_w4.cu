@@ -10,9 +10,9 @@
 // (8w + 2i, 8w + 2i + 1) in the halves of a register.
 #include <float.h>
 
-#include "rlk_internal.h"
 #include "rlk_logits.cuh"
-#include "rlk_sm103.cuh"
+#include "rlk_logits_w4.h"
+#include "rlk_ptx.cuh"
 #include "rlk_w4.cuh"
 
 namespace rlk {

@@ -36,9 +36,9 @@
 // x is one column of D.  So a row's bits do not depend on T.
 //
 // Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
-#include "rlk_internal.h"
 #include "rlk_logits.cuh"
-#include "rlk_sm103.cuh"
+#include "rlk_logits_w4.h"
+#include "rlk_ptx.cuh"
 #include "rlk_w4.cuh"
 
 namespace rlk {

@@ -59,6 +59,7 @@ def linear(L, x=A16, dtype=0, c=A16, s=A16, T=2, N=10, K=64, group=32, y=A16, od
 @pytest.mark.parametrize("kw,expect", [
     (dict(dtype=2), 1), (dict(odt=1), 1), (dict(odt=5), 1), (dict(T=-1), 1), (dict(N=-1), 1), (dict(K=0), 1),
     (dict(K=48), 2), (dict(group=16), 1), (dict(group=0), 1), (dict(N=1 << 31), 1), (dict(N=1 << 30, K=1 << 20), 1),
+    (dict(T=1 << 30, N=1 << 20), 1),
     (dict(x=None), 1), (dict(c=None), 1), (dict(s=None), 1), (dict(y=None), 1), (dict(x=A4), 2), (dict(c=A4), 2),
     (dict(s=A4), 2), (dict(y=A2), 2),
 ])
