@@ -128,7 +128,7 @@ struct Packed8 {
 };
 
 // The aligned vectors that cover eight elements e0 .. e0 + 7 of a row that starts `shift`
-// elements behind a 16-byte boundary (kShifted: shift > 0).
+// elements behind a 16-byte boundary (not kShifted: shift is 0).
 template <typename Elem, bool kShifted>
 struct Vectors {
     static constexpr int E = kVecElems<Elem>;
@@ -162,7 +162,7 @@ struct Vectors {
     }
 };
 
-// The eight elements of each of N groups out of their vectors (kShifted: any shift but 0).
+// The eight elements of each of N groups out of their vectors (kShifted: any shift, 0 too).
 // The amount of the shift
 // picks one of a few short pieces of code that only move registers, not a copy of the
 // caller: an odd vocabulary has rows of every shift on an SM at once, and copies of a whole
@@ -178,12 +178,14 @@ __device__ __forceinline__ void unshift(const Vectors<Elem, kShifted> (&in)[N], 
         all(std::integral_constant<int, 0>());
     } else if constexpr (sizeof(Elem) == 4) {
         switch (shift) {
+            case 0: all(std::integral_constant<int, 0>()); break;
             case 1: all(std::integral_constant<int, 1>()); break;
             case 2: all(std::integral_constant<int, 2>()); break;
             default: all(std::integral_constant<int, 3>()); break;
         }
     } else {
         switch (shift) {
+            case 0: all(std::integral_constant<int, 0>()); break;
             case 1: all(std::integral_constant<int, 1>()); break;
             case 2: all(std::integral_constant<int, 2>()); break;
             case 3: all(std::integral_constant<int, 3>()); break;

@@ -77,6 +77,10 @@ __device__ __forceinline__ void copy_word_async(uint32_t dst, const void* src, u
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
+// 16 bytes of global memory into shared memory, both 16-byte aligned.
+__device__ __forceinline__ void copy_vector_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrive on `bar` once this thread's copies so far have landed (the barrier's count
 // includes this arrival).
 __device__ __forceinline__ void copy_words_arrive(uint32_t bar) {

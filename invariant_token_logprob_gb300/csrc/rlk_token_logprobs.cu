@@ -24,6 +24,11 @@
 // in each of those cells.  So after the pass a bound is taken from the warps' best
 // cells, the cells that reach it (some tens of 2048) are read again, and their tokens
 // that reach it, hardly more, are ranked by counting.
+//
+// The pass is bound by the reads of the logits where rows are many (T = 4096, V = 151936,
+// bf16: 205 us, 6.1 TB/s; with 20 alternatives 249 us; T = 1024, fp32: 94 us, 6.6 TB/s),
+// by the latency of its steps where they are few (T = 1, fp32, 20 alternatives: 8.5 us).
+// The gradient reads and writes each logit once (T = 4096, bf16: 366 us, 6.8 TB/s).
 #include <float.h>
 #include <limits.h>
 
@@ -167,9 +172,9 @@ struct LaneState {
     uint32_t place;
     F2 s, u;
 
-    // One unit of N groups, the first one e0 / kGroup of the row, kStride apart.
-    template <bool kCut, int N, typename Elem>
-    __device__ __forceinline__ void add(const Packed8<Elem> (&x)[N], uint32_t group, float c2) {
+    // Looks at a unit of N groups, the first one `group` of the row, kStride apart.
+    template <int N, typename Elem>
+    __device__ __forceinline__ void look(const Packed8<Elem>* x, uint32_t group, float c2) {
         float most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -188,27 +193,44 @@ struct LaneState {
             s = mul2(ff, s);
             m = most;
         }
+    }
+    // Adds them.  summed(k) follows the k-th group; again(group) loads one that holds an
+    // element at -inf, which is cut then.
+    template <bool kCut, typename Elem, int N, typename Summed, typename Again>
+    __device__ __forceinline__ void add(const Packed8<Elem> (&x)[N], uint32_t group, float c2,
+                                        Summed&& summed, Again&& again) {
+        look<N>(x, group, c2);
         const F2 low = pack2(-m, -m), scale = pack2(c2, c2);
         F2 us = pack2(0.0f, 0.0f), uu = us;
 #pragma unroll
-        for (int i = 0; i < N; ++i) add_eight<kCut>(x[i], low, scale, us, uu);
-        if (!kCut) {
-            const float2 test = unpack2(uu);
-            if (!(test.x + test.y == test.x + test.y)) {  // an element at -inf, or a NaN
-                us = uu = pack2(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < N; ++i) add_eight<true>(x[i], low, scale, us, uu);
-            }
+        for (int k = 0; k < N; ++k) {
+            add_eight<kCut>(x[k], low, scale, us, uu);
+            summed(k);
+        }
+        if (!kCut && !finite(uu)) {
+            us = uu = pack2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int k = 0; k < N; ++k)
+                add_eight<true>(again(group + k * (kStride / kGroup)), low, scale, us, uu);
         }
         s = add2(s, us);
         u = add2(u, uu);
     }
+    // False where an element at -inf (or a NaN) was added without a cut.
+    static __device__ __forceinline__ bool finite(F2 uu) {
+        const float2 test = unpack2(uu);
+        return test.x + test.y == test.x + test.y;
+    }
 };
 
-// How a strip's groups are taken: rows of 32 groups (one per lane, kStride apart) two at a
-// time, a unit, as long as they lie whole in the row, the last one alone where their number
-// is odd, and then the row's end.  It follows from V alone (a unit's maximum decides the
-// rounding), not from the row's alignment.
+// How a strip's groups are taken: rows of 32 groups (one per lane, kStride apart) in units of
+// kUnitOf<Elem> rows as long as they lie whole in the row, what is left of the whole ones one
+// at a time, and then the row's end.  It follows from V and the type alone (a unit's maximum
+// decides the rounding), not from the row's alignment.
+template <typename Elem>
+constexpr int kUnitOf = 8 / int(sizeof(Elem));  // 64 bytes per lane; bf16, T = 4096,
+                                                // V = 151936: 205 us, with 32 bytes 240 us
+
 struct StripPlan {
     uint32_t base;   // the strip's first element
     uint32_t whole;  // rows of groups whose vectors, and the longest shift, lie in the row
@@ -217,73 +239,157 @@ struct StripPlan {
           whole(base + kStep + kGroup <= V ? (V - base - kStep - kGroup) / kStride + 1 : 0) {}
 };
 
-// One unit's loads.
-template <typename Elem, bool kShifted>
+// The loads of one unit (or of the whole rows left behind the last one), under way from load()
+// until take() gives their elements.  Rows at 16-byte boundaries wait in registers.
+template <typename Elem, bool kShifted, bool kMasked>
 struct Unit {
-    Vectors<Elem, kShifted> in[2];
-    uint32_t b[2];
-    // Row `first` of the strip and, if it is whole too, the next one.
-    template <bool kMasked>
-    __device__ __forceinline__ void load(const Elem* row, const uint8_t* bits, int shift, int lane,
+    static constexpr int N = kUnitOf<Elem>;
+    Vectors<Elem, false> in[N];
+    uint32_t b[N];
+    // Row first + k of the strip, if it is whole.
+    __device__ __forceinline__ void load(int k, const Elem* row, const uint8_t* bits, int lane,
                                          const StripPlan& plan, uint32_t first) {
-        const uint32_t e = plan.base + lane * kGroup + first * kStride;
-        // the row's first group has its first vector in front of a shifted row: read apart
-        in[0].load(row, kShifted && e == 0 ? kStep : e, shift);
-        if (kMasked) b[0] = bits[e / kGroup];
-        if (first + 1 < plan.whole) {
-            in[1].load(row, e + kStride, shift);
-            if (kMasked) b[1] = bits[(e + kStride) / kGroup];
-        }
+        if (first + k >= plan.whole) return;
+        const uint32_t e = plan.base + lane * kGroup + (first + k) * kStride;
+        in[k].load(row, e, 0);
+        if (kMasked) b[k] = bits[e / kGroup];
     }
 };
 
-// One strip's lane: its sums, and its cell's key.  `unit` holds the loads of its first unit;
+// Shifted rows wait in the warp's slots in shared memory: a second vector per lane would make
+// their loads too many registers (T = 4096, V = 151935, bf16: 262 us; in registers 294 us, and
+// 443 us with spills at four CTAs per SM).  The lanes copy the strip's vectors and lane 0 the
+// one behind it; each then reads those that cover its elements.
+template <typename Elem, bool kMasked>
+struct Unit<Elem, true, kMasked> {
+    static constexpr int N = kUnitOf<Elem>;
+    static constexpr int kOwn = kGroup / kVecElems<Elem>;    // vectors of a lane
+    static constexpr int kVecs = 32 * kOwn + 1;              // of a row of groups
+    uint4* slots;
+    uint32_t b[N];
+    __device__ __forceinline__ Unit(uint4* ring, int warp) : slots(ring + warp * (N * kVecs)) {}
+    __device__ __forceinline__ void load(const Elem* row, const uint8_t* bits, int shift, int lane,
+                                         const StripPlan& plan, uint32_t first) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (first + k >= plan.whole) break;
+            const uint32_t e = plan.base + (first + k) * kStride;
+            const uint4* from = reinterpret_cast<const uint4*>(row + e - shift);
+            const uint32_t to = smem_u32(slots + k * kVecs);
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                // (the row's first vector may begin in front of the tensor)
+                const int v = i * 32 + lane;
+                if (e + v > 0) copy_vector_async(to + v * 16, from + v);
+            }
+            if (lane == 0) copy_vector_async(to + 32 * kOwn * 16, from + 32 * kOwn);
+            if (kMasked) b[k] = bits[e / kGroup + lane];
+        }
+    }
+    template <int M>
+    __device__ __forceinline__ void take(Packed8<Elem> (&x)[M], uint32_t first, int shift, int lane) {
+        copy_words_wait_all();
+        __syncwarp();
+        Vectors<Elem, true> in[M];
+#pragma unroll
+        for (int k = 0; k < M; ++k)
+#pragma unroll
+            for (int i = 0; i <= kOwn; ++i) in[k].v[i] = slots[(first + k) * kVecs + lane * kOwn + i];
+        unshift(in, shift, x);
+        __syncwarp();  // the slots may be loaded again
+    }
+};
+
+// The eight elements from e0 on, wherever they lie in the row.
+template <typename Elem, bool kShifted>
+__device__ __forceinline__ Packed8<Elem> load_group(const Elem* row, int64_t e0, int shift, int64_t V) {
+    Packed8<Elem> x[1];
+    if (Vectors<Elem, kShifted>::inside(e0, shift, V)) {
+        Vectors<Elem, kShifted> in[1];
+        in[0].load(row, e0, shift);
+        unshift(in, shift, x);
+    } else {
+        x[0].load_single(row, e0, V);
+    }
+    return x[0];
+}
+
+// One strip's lane: its sums, and its cell's key.  `unit` holds the loads of its first unit,
 // on return those of the next strip's.
-template <bool kMasked, typename Elem, bool kShifted>
+template <typename Elem, bool kShifted, bool kMasked>
 __device__ __forceinline__ Sums read_strip(const Elem* row, int shift, const uint8_t* bits,
                                            uint32_t V, const StripPlan& plan, const StripPlan& next,
-                                           Unit<Elem, kShifted>& unit, int lane, float c2,
+                                           Unit<Elem, kShifted, kMasked>& unit, int lane, float c2,
                                            uint64_t* cell) {
-    using In = Vectors<Elem, kShifted>;
+    constexpr int N = kUnitOf<Elem>;
     constexpr uint32_t kRow = kStride / kGroup;
     LaneState st = {-INFINITY, -FLT_MAX, 0u, pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
     const uint32_t group = (plan.base + lane * kGroup) / kGroup;
-    uint32_t i = 0;
-    for (; i + 1 < plan.whole; i += 2) {
-        Packed8<Elem> x[2];
-        unshift(unit.in, shift, x);
-        if (kShifted && group + i == 0) x[0].load_single(row, 0, V);
-        if (kMasked) {
-            x[0].keep(unit.b[0]);
-            x[1].keep(unit.b[1]);
-        }
-        const bool more = i + 2 < plan.whole;
-        if (more || next.whole > 0)
-            unit.template load<kMasked>(row, bits, shift, lane, more ? plan : next, more ? i + 2 : 0);
-        st.add<kMasked>(x, group + i * kRow, c2);
-    }
-    if (i < plan.whole) {
-        Packed8<Elem> x[2];
-        unshift(unit.in, shift, x);
-        if (kShifted && group + i == 0) x[0].load_single(row, 0, V);
-        if (kMasked) x[0].keep(unit.b[0]);
-        if (next.whole > 0) unit.template load<kMasked>(row, bits, shift, lane, next, 0);
-        Packed8<Elem> one[1] = {x[0]};
-        st.add<kMasked>(one, group + i * kRow, c2);
-        ++i;
-    }
-    for (; int64_t(plan.base) + int64_t(i) * kStride < V; ++i) {  // the row's end
-        const int64_t e0 = int64_t(group) * kGroup + int64_t(i) * kStride;
-        Packed8<Elem> x[1];
-        if (In::inside(e0, shift, V)) {
-            In one[1];
-            one[0].load(row, e0, shift);
-            unshift(one, shift, x);
+    // The unit's groups from the k-th on, which is row i + k; `last`: loads what comes next.
+    auto take = [&](auto& x, uint32_t i, auto k, bool last, bool more) {
+        constexpr int K = decltype(k)::value, M = sizeof(x) / sizeof(x[0]);
+        if constexpr (kShifted) {
+            unit.take(x, K, shift, lane);
+            if (group + i + K == 0) x[0].load_single(row, 0, V);
         } else {
-            x[0].load_single(row, e0, V);
+#pragma unroll
+            for (int j = 0; j < M; ++j) unit.in[K + j].template get<0>(x[j]);
         }
-        if (kMasked) x[0].keep(e0 < V ? bits[e0 / kGroup] : 0u);
-        st.add<true>(x, uint32_t(e0 / kGroup), c2);
+        if (kMasked) {
+#pragma unroll
+            for (int j = 0; j < M; ++j) x[j].keep(unit.b[K + j]);
+        }
+        if constexpr (kShifted) {
+            if (last) unit.load(row, bits, shift, lane, more ? plan : next, more ? i + N : 0);
+        }
+    };
+    constexpr std::integral_constant<int, 0> k0;
+    constexpr std::integral_constant<int, (N > 2 ? 2 : 0)> k2;
+    auto again = [&](uint32_t g) {
+        return load_group<Elem, kShifted>(row, int64_t(g) * kGroup, shift, V);
+    };
+    uint32_t i = 0;
+    for (; i + N <= plan.whole; i += N) {
+        const bool more = i + N < plan.whole;
+        Packed8<Elem> x[N];
+        take(x, i, k0, true, more);
+        st.template add<kMasked>(x, group + i * kRow, c2, [&](int k) {
+            // (a group's registers take the next unit's loads once it is summed)
+            if constexpr (!kShifted) {
+                if (more)
+                    unit.load(k, row, bits, lane, plan, i + N);
+                else
+                    unit.load(k, row, bits, lane, next, 0);
+            }
+        }, again);
+    }
+    // What is left of the whole rows, and the next strip's first unit.
+    const uint32_t left = plan.whole - i;
+    if (left > 0) {
+        if (N > 2 && left >= 2) {
+            Packed8<Elem> x[2];
+            take(x, i, k0, left == 2, false);
+            st.template add<kMasked>(x, group + i * kRow, c2, [](int) {}, again);
+        }
+        if (left % 2 != 0) {
+            Packed8<Elem> x[1];
+            if (left > 1)
+                take(x, i, k2, true, false);
+            else
+                take(x, i, k0, true, false);
+            st.template add<kMasked>(x, group + (plan.whole - 1) * kRow, c2, [](int) {}, again);
+        }
+        if constexpr (!kShifted) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) unit.load(k, row, bits, lane, next, 0);
+        }
+    }
+    for (i = plan.whole; int64_t(plan.base) + int64_t(i) * kStride < V; ++i) {  // the row's end
+        const int64_t e0 = (int64_t(group) + i * kRow) * kGroup;
+        Packed8<Elem> x = load_group<Elem, kShifted>(row, e0, shift, V);
+        if (kMasked) x.keep(e0 < V ? bits[e0 / kGroup] : 0u);
+        Packed8<Elem> one[1] = {x};
+        st.template add<true>(one, uint32_t(e0 / kGroup), c2, [](int) {}, again);
     }
     *cell = st.top > -INFINITY ? order_key(st.top, st.place) : 0;
     const float2 s1 = unpack2(st.s), u1 = unpack2(st.u);
@@ -441,10 +547,18 @@ __device__ __forceinline__ void each_token(Shared& sh, const Elem* row, int shif
     }
 }
 
-// Grid: T clusters of `ranks` CTAs (1, 2, 4 or 8).
-template <typename Elem, bool kMasked>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Args p, int ranks) {
-    extern __shared__ uint8_t smem[];
+// CTAs per SM: four by registers; the slots of shifted rows leave shared memory for three.
+template <bool kShifted>
+constexpr int kCtasPerSm = kShifted ? 3 : 4;
+// Shared memory of a CTA.
+constexpr int kSharedBytes = (int(sizeof(Shared)) + 15) / 16 * 16;
+
+// Grid: T clusters of `ranks` CTAs (1, 2, 4 or 8).  kShifted: not every row starts at a
+// 16-byte boundary.
+template <typename Elem, bool kShifted, bool kMasked>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<kShifted>)
+    token_logprobs_kernel(const Args p, int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Launched with programmatic overlap: the kernel ahead in the stream may still be writing
@@ -457,32 +571,35 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Args 
     const uint8_t* bits =
         kMasked ? reinterpret_cast<const uint8_t*>(p.allowed + t * p.allowed_stride) : nullptr;
     const float c2 = p.inv_temp * kLog2e;
-    const int shift = row_shift(row);
+    const int shift = kShifted ? row_shift(row) : 0;
     if (ranks > 1) cluster_arrive_relaxed();  // every CTA runs before another writes to it
     int32_t target = -1;
     if (rank == 0 && threadIdx.x == 0) target = p.targets[t];
 
     // A block of eight strips at a time, one strip per warp.
     const int blocks = kBlocks / ranks;
-    auto read = [&](auto shifted) {
-        Unit<Elem, decltype(shifted)::value> unit;
-        const int first = rank * blocks * kWarps + warp;
-        StripPlan plan(first, p.V);
-        if (plan.whole > 0) unit.template load<kMasked>(row, bits, shift, lane, plan, 0);
-        for (int j = 0; j < blocks; ++j) {
-            // (behind the last block: a strip behind every row's end)
-            const StripPlan next(j + 1 < blocks ? first + (j + 1) * kWarps : kNoStrip, p.V);
-            uint64_t cell = 0;
-            sh.strip_sums[j][warp][lane] = read_strip<kMasked>(row, shift, bits, uint32_t(p.V), plan,
-                                                               next, unit, lane, c2, &cell);
-            if (p.top_k > 0) sh.cells[(j * kWarps + warp) * 32 + lane] = cell;
-            plan = next;
-        }
-    };
-    if (shift == 0)
-        read(std::false_type());
-    else
-        read(std::true_type());
+    const int first = rank * blocks * kWarps + warp;
+    StripPlan plan(first, p.V);
+    using Loads = Unit<Elem, kShifted, kMasked>;
+    Loads unit = [&] {
+        if constexpr (kShifted) return Loads(reinterpret_cast<uint4*>(smem + kSharedBytes), warp);
+        else return Loads();
+    }();
+    if constexpr (kShifted) {
+        unit.load(row, bits, shift, lane, plan, 0);
+    } else {
+#pragma unroll
+        for (int k = 0; k < Loads::N; ++k) unit.load(k, row, bits, lane, plan, 0);
+    }
+    for (int j = 0; j < blocks; ++j) {
+        // (behind the last block: a strip behind every row's end)
+        const StripPlan next(j + 1 < blocks ? first + (j + 1) * kWarps : kNoStrip, p.V);
+        uint64_t cell = 0;
+        sh.strip_sums[j][warp][lane] = read_strip<Elem, kShifted, kMasked>(
+            row, shift, bits, uint32_t(p.V), plan, next, unit, lane, c2, &cell);
+        if (p.top_k > 0) sh.cells[(j * kWarps + warp) * 32 + lane] = cell;
+        plan = next;
+    }
     float target_x = -INFINITY;
     if (target >= 0 && target < p.V) target_x = element(row, bits, target);
     __syncthreads();
@@ -771,6 +888,9 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
                                   int32_t* out_ids, float* out_top, int num_sms, cudaStream_t stream) {
     const Args p = {logits, row_stride, targets, allowed, allowed_stride, int(V), top_k, inv_temp,
                     out_logp, out_lse, out_entropy, out_top, out_ids};
+    const int64_t elem = type == ElemType::kFp32 ? 4 : 2;
+    const bool shifted = reinterpret_cast<uintptr_t>(logits) % 16 != 0 ||
+                         (T > 1 && row_stride * elem % 16 != 0);
     // CTAs per row: as many as keep the launch within what the SMs hold at once (four
     // CTAs each; a little less with alternatives, whose selection every CTA pays for, and
     // then at least 8192 elements per CTA).
@@ -778,7 +898,20 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
     while (ranks > 1 && (2 * T * ranks > (top_k ? 7 : 8) * int64_t(num_sms) ||
                          (top_k && V < 8192 * int64_t(ranks))))
         ranks /= 2;
-    auto go = [&](auto kernel) {
+    auto go = [&](auto kernel, int slots, int which) {
+        const int smem = kSharedBytes + slots;
+        static uint8_t configured[64];  // per device: the kernels that may have that much
+        if (slots > 0) {
+            int dev = 0;
+            cudaError_t e = cudaGetDevice(&dev);
+            if (e != cudaSuccess) return e;
+            if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+            if (!(configured[dev] >> which & 1)) {
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (e != cudaSuccess) return e;
+                configured[dev] |= uint8_t(1 << which);
+            }
+        }
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -788,21 +921,26 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.gridDim = dim3(unsigned(T * ranks), 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = sizeof(Shared);
+        cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = ranks > 1 ? 2 : 1;
         cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, ranks);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
-    if (type == ElemType::kBf16)
-        return allowed ? go(token_logprobs_kernel<__nv_bfloat16, true>)
-                       : go(token_logprobs_kernel<__nv_bfloat16, false>);
-    if (type == ElemType::kFp16)
-        return allowed ? go(token_logprobs_kernel<__half, true>)
-                       : go(token_logprobs_kernel<__half, false>);
-    return allowed ? go(token_logprobs_kernel<float, true>)
-                   : go(token_logprobs_kernel<float, false>);
+    auto pick = [&](auto elem) {
+        using Elem = decltype(elem);
+        constexpr int kSlots = kWarps * kUnitOf<Elem> * Unit<Elem, true, false>::kVecs * 16;
+        const int which = int(type) * 2;
+        if (shifted)
+            return allowed ? go(token_logprobs_kernel<Elem, true, true>, kSlots, which + 1)
+                           : go(token_logprobs_kernel<Elem, true, false>, kSlots, which);
+        return allowed ? go(token_logprobs_kernel<Elem, false, true>, 0, 0)
+                       : go(token_logprobs_kernel<Elem, false, false>, 0, 0);
+    };
+    if (type == ElemType::kBf16) return pick(__nv_bfloat16());
+    if (type == ElemType::kFp16) return pick(__half());
+    return pick(float());
 }
 
 cudaError_t launch_token_logprobs_backward(const void* logits, ElemType type, int64_t row_stride,

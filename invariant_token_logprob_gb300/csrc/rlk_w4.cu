@@ -28,8 +28,8 @@ __host__ __device__ constexpr int code_shift(int k) { return 4 * ((k & 1) * 4 + 
 constexpr int kPieces = 4;
 
 // a / b for a constant b with r = 1 / b rounded: t = a r is off by a unit of the last place
-// at most, and the remainder a - t b, exact in a multiply-add, corrects it (Newton's step for
-// the quotient) to the correctly rounded one.
+// at most, and the remainder a - t b, exact in a multiply-add, corrects it to the correctly
+// rounded one (P. Markstein, IBM Journal of Research and Development 34, 1990).
 __device__ __forceinline__ float divide(float a, float b, float r) {
     const float t = a * r;
     return fmaf(fmaf(-t, b, a), r, t);
