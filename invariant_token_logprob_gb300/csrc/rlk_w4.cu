@@ -24,7 +24,7 @@ constexpr int kThreads = 256;
 __host__ __device__ constexpr int code_shift(int k) { return 4 * ((k & 1) * 4 + k / 2); }
 
 // Pieces of eight elements (16 bytes of W, one word of codes) per thread whose loads are in
-// flight together: 64 KB per SM.
+// flight together: 96 KB per SM.
 constexpr int kPieces = 4;
 
 // a / b for a constant b with r = 1 / b rounded: t = a r is off by a unit of the last place
@@ -40,18 +40,32 @@ __device__ __forceinline__ float reciprocal(float a) {
     return r;
 }
 
-// Largest |x| of the four pairs of a piece.
-__device__ __forceinline__ float max_abs(const uint4& v, __nv_bfloat16) {
-    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
-    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w);
-    const float2 m = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
-    return fmaxf(m.x, m.y);
+// The larger of the halves of (a, b) each: the largest of a's pair and of b's.
+template <typename Pair>
+__device__ __forceinline__ uint32_t max_halves(Pair a, Pair b) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(&a), y = *reinterpret_cast<const uint32_t*>(&b);
+    const uint32_t low = __byte_perm(x, y, 0x5410), high = __byte_perm(x, y, 0x7632);
+    const Pair m = max_pair(*reinterpret_cast<const Pair*>(&low), *reinterpret_cast<const Pair*>(&high));
+    return *reinterpret_cast<const uint32_t*>(&m);
 }
-__device__ __forceinline__ float max_abs(const uint4& v, __half) {
-    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
-    const __half2* p = reinterpret_cast<const __half2*>(w);
-    const float2 m = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
-    return fmaxf(m.x, m.y);
+template <typename Elem>
+__device__ __forceinline__ typename PairOf<Elem>::type max_of_pairs(const uint4& v, uint32_t keep,
+                                                                    uint32_t flip, Elem) {
+    using Pair = typename PairOf<Elem>::type;
+    const uint32_t w[4] = {(v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip,
+                           (v.w & keep) ^ flip};
+    const Pair* p = reinterpret_cast<const Pair*>(w);
+    return max_pair(max_pair(p[0], p[1]), max_pair(p[2], p[3]));
+}
+// The largest |x| of two pieces (NaN counts as nothing).
+template <typename Elem>
+__device__ __forceinline__ uint32_t max_abs_pair(const uint4& a, const uint4& b, Elem e) {
+    return max_halves(max_of_pairs(a, 0x7fff7fffu, 0u, e), max_of_pairs(b, 0x7fff7fffu, 0u, e));
+}
+// The largest x and the largest -x of a piece.
+template <typename Elem>
+__device__ __forceinline__ uint32_t max_both(const uint4& a, Elem e) {
+    return max_halves(max_of_pairs(a, 0xffffffffu, 0u, e), max_of_pairs(a, 0xffffffffu, 0x80008000u, e));
 }
 
 // The smallest scale whose own rounding is a small part of it (and whose reciprocal and
@@ -61,15 +75,9 @@ __device__ __forceinline__ float normal_scale(__nv_bfloat16) { return 7.88860905
 __device__ __forceinline__ float normal_scale(__half) { return 1.220703125e-4f; }                 // 2^-13
 
 // The word of eight codes.  2^23 + 2^22 + q has the whole number q in its low bits; adding the
-// constant, which is even, rounds a half to the even code.  The words' constant part is
-// subtracted at the end.
+// constant, which is even, rounds a half to the even code.  Four codes become 16 bits of one
+// such number by exact multiply-adds, the even and the odd ones side by side.
 constexpr float kMagic = 12582912.0f;
-constexpr uint32_t kMagicBits = 0x4b400000u;
-__host__ __device__ constexpr uint32_t magic_word() {
-    uint32_t c = 0;
-    for (int j = 0; j < 8; ++j) c += kMagicBits * (1u << code_shift(j));
-    return c;
-}
 
 // Quotients x / s, exactly rounded at ties: with an approximate reciprocal r, t = x r is off
 // by some units of the last place; the remainder x - t s corrects it, so a quotient that is a
@@ -81,7 +89,8 @@ __device__ __forceinline__ uint32_t code_word(const float2 (&x)[4], float s, flo
     const F2 rr = pack2(r, r), ss = pack2(-s, -s);
     const float add = kZeros ? kMagic : kMagic + 8.0f;
     const F2 magic = pack2(add, add);
-    uint32_t word = 0;
+    const F2 off = pack2(-kMagic, -kMagic);
+    F2 four = magic;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const F2 v = pack2(x[j].x, x[j].y);
@@ -91,11 +100,11 @@ __device__ __forceinline__ uint32_t code_word(const float2 (&x)[4], float s, flo
             const float2 f = unpack2(add2(q, pack2(z, z)));
             q = pack2(fminf(f.x, kMagic + 15.0f), fminf(f.y, kMagic + 15.0f));
         }
-        const float2 f = unpack2(q);
-        word += __float_as_uint(f.x) * (1u << code_shift(2 * j));
-        word += __float_as_uint(f.y) * (1u << code_shift(2 * j + 1));
+        const float place = float(1 << 4 * j);
+        four = j == 0 ? q : fma2(add2(q, off), pack2(place, place), four);
     }
-    return word - magic_word();
+    const float2 f = unpack2(four);
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x5410);
 }
 // The same by division and with both ends clamped, for scales near the end of their range.
 template <bool kZeros>
@@ -112,37 +121,58 @@ __device__ __noinline__ uint32_t code_word_small(float2 x0, float2 x1, float2 x2
 }
 
 // One group is held by kGroup / 8 neighbouring lanes, a piece each.  HBM-bound: reads W and
-// writes a quarter of its bytes; a division per element would take longer than the bytes.
-// kWhole: group divides K, so the pieces of W are dealt to the threads in memory order.
+// writes a quarter of its bytes.  A division per element would take longer than the bytes;
+// the arithmetic is kept to packed pairs, and the groups' maxima go across lanes together
+// (N = 151936, K = 4096, bf16, group 128: 233 us, 6.7 TB/s; with zero points 279 us).
+// kWhole: group divides K, so the pieces of W are dealt to the threads in memory order, six
+// CTAs to an SM (five: 241 us); the search for the rows otherwise would spill with six.
 template <typename Elem, int kGroup, bool kZeros, bool kWhole>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kWhole ? 6 : 5)
     quantize_w4_kernel(const Elem* __restrict__ W, int64_t N, int K, int num_groups,
                        uint32_t* __restrict__ codes, Elem* __restrict__ scales,
                        uint8_t* __restrict__ zeros) {
     constexpr int kLanes = kGroup / 8;
-    const int64_t groups = N * num_groups;
+    const int64_t first = int64_t(blockIdx.x) * (kPieces * kThreads) + threadIdx.x;
+    const int left = int(min(N * num_groups * kLanes - first, int64_t(kPieces * kThreads)));
     // (!kWhole) the row of the block's first group; the others by a 32-bit division from there
     const int64_t group0 = int64_t(blockIdx.x) * (kPieces * kThreads / kLanes);
     const int64_t row0 = kWhole ? 0 : group0 / num_groups;
+    const uint32_t col0 = uint32_t(group0 - row0 * num_groups);
+    const uint4* src = reinterpret_cast<const uint4*>(W) + (kWhole ? first : row0 * (K / 8));
+    codes += kWhole ? first : row0 * (K / 8);
+    scales += first / kLanes;
+    if (kZeros) zeros += first / kLanes;
     uint4 raw[kPieces];
-    int64_t at[kPieces];  // piece of W, or -1 behind a row's end
+    int at[kPieces];  // piece of W from src on, or -1 behind a row's end
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int64_t p = (int64_t(blockIdx.x) * kPieces + i) * kThreads + threadIdx.x;
-        const int64_t group = p / kLanes;
-        at[i] = -1;
-        if (group < groups) {
-            if (kWhole) {
-                at[i] = p;
-            } else {
-                const uint32_t from_row0 = uint32_t(group - row0 * num_groups);
-                const uint32_t rows = from_row0 / uint32_t(num_groups);
-                const int k8 = int(from_row0 - rows * uint32_t(num_groups)) * kLanes + int(p % kLanes);
-                if (k8 < K / 8) at[i] = (row0 + rows) * (K / 8) + k8;
-            }
+        at[i] = i * kThreads < left ? i * kThreads : -1;
+        if (!kWhole && at[i] >= 0) {
+            const uint32_t group = col0 + (threadIdx.x + i * kThreads) / kLanes;
+            const uint32_t rows = group / uint32_t(num_groups);
+            const int k8 = int(group - rows * uint32_t(num_groups)) * kLanes + int(threadIdx.x % kLanes);
+            at[i] = k8 < K / 8 ? int(rows) * (K / 8) + k8 : -1;
         }
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at[i] >= 0) raw[i] = __ldcs(reinterpret_cast<const uint4*>(W) + at[i]);
+        if (at[i] >= 0) raw[i] = __ldcs(src + at[i]);
+    }
+    // Every piece's largest element and largest negated one, or two pieces' largest |x|, as a
+    // pair of the elements' own type: exact, and all groups' steps across lanes run together.
+    using Pair = typename PairOf<Elem>::type;
+    constexpr int kPairs = kZeros ? kPieces : kPieces / 2;
+    uint32_t most[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+        most[i] = kZeros ? max_both(raw[i], Elem()) : max_abs_pair(raw[2 * i], raw[2 * i + 1], Elem());
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, most[i], off);
+            const Pair m = max_pair(*reinterpret_cast<const Pair*>(&most[i]),
+                                    *reinterpret_cast<const Pair*>(&o));
+            most[i] = *reinterpret_cast<const uint32_t*>(&m);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -150,21 +180,9 @@ __global__ void __launch_bounds__(kThreads, 4)
         float2 x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = pair_to_float(w[j], Elem());
-        float lo = 0.0f, hi = 0.0f;
-        if (kZeros) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo = fminf(fminf(lo, x[j].x), x[j].y);
-                hi = fmaxf(fmaxf(hi, x[j].x), x[j].y);
-            }
-        } else {
-            hi = max_abs(raw[i], Elem());
-        }
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) {
-            if (kZeros) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        }
+        const float2 both = pair_to_float(most[kZeros ? i : i / 2], Elem());
+        const float hi = kZeros ? fmaxf(both.x, 0.0f) : i % 2 ? both.y : both.x;
+        const float lo = kZeros ? fminf(-both.y, 0.0f) : 0.0f;
         Elem s16 = from_float<Elem>(kZeros ? divide(hi - lo, 15.0f, 1.0f / 15.0f)
                                            : divide(hi, 7.0f, 1.0f / 7.0f));
         if (kZeros && isinf(hi - lo)) s16 = from_float<Elem>(INFINITY);  // (bf16: a span beyond fp32)
@@ -184,16 +202,16 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
         if (at[i] >= 0) {
             __stcs(codes + at[i], word);
-            const int64_t p = (int64_t(blockIdx.x) * kPieces + i) * kThreads + threadIdx.x;
-            if (p % kLanes == 0) {
-                scales[p / kLanes] = s16;
-                if (kZeros) zeros[p / kLanes] = uint8_t(int(z));
+            if (threadIdx.x % kLanes == 0) {
+                scales[i * (kThreads / kLanes)] = s16;
+                if (kZeros) zeros[i * (kThreads / kLanes)] = uint8_t(int(z));
             }
         }
     }
 }
 
-// Words of codes per thread whose loads are in flight together.
+// Words of codes per thread whose loads are in flight together.  HBM-bound on what it writes
+// (N = 151936, K = 4096, bf16, group 128: 226 us, 6.9 TB/s).
 constexpr int kWords = 8;
 
 __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b, __nv_bfloat16) {
