@@ -77,8 +77,13 @@ constexpr int stages(int cols, int groups) {
     return (cols <= 16 ? 8 : cols == 32 ? 6 : 4) - (groups == 8 ? 1 : 0);
 }
 // Tensor memory: A buffers (one per team) first, then the D buffers, `cols` columns for
-// each of a stage's groups.
-constexpr int d_cols(int cols, int groups) { return mma_n(cols) * groups; }
+// each of some groups of a stage, 128 columns at most: two buffers have to fit, or the products
+// wait for the MMAs and the MMAs for them (N = 151936, K = 4096, T = 64, a stage's groups
+// together: group 64 126 us, by twos 108 us).
+constexpr int d_groups(int cols, int groups) {
+    return groups < 128 / mma_n(cols) ? groups : 128 / mma_n(cols);
+}
+constexpr int d_cols(int cols, int groups) { return mma_n(cols) * d_groups(cols, groups); }
 constexpr int num_teams(int cols, int groups) { return d_cols(cols, groups) <= 64 ? 3 : 2; }
 constexpr int num_d(int cols, int groups) {
     return (int(kTmemCols) - num_teams(cols, groups) * int(kABufCols)) / d_cols(cols, groups) < 4
@@ -90,12 +95,13 @@ constexpr size_t smem_bytes(int cols, int groups) {
     return 1024 + size_t(stages(cols, groups)) * stage_bytes(cols) +
            scale_bufs_of(groups) * kScaleBytes + kMaxBarriers * 8 + 16;
 }
-static_assert(smem_bytes(64, 4) <= 227 * 1024 && smem_bytes(32, 8) <= 227 * 1024 &&
+static_assert(smem_bytes(64, 4) <= 227 * 1024 && smem_bytes(64, 8) <= 227 * 1024 &&
+                  smem_bytes(64, 2) <= 227 * 1024 && smem_bytes(32, 8) <= 227 * 1024 &&
                   smem_bytes(16, 8) <= 227 * 1024 && smem_bytes(32, 4) <= 227 * 1024 &&
                   smem_bytes(16, 4) <= 227 * 1024,
               "shared memory per CTA");
 static_assert((64 + kMaxSplits) * kTileN * 4 <= stages(8, 8) * stage_bytes(8) &&
-                  (64 + kMaxSplits) * kTileN * 4 <= stages(64, 4) * stage_bytes(64),
+                  (64 + kMaxSplits) * kTileN * 4 <= stages(64, 8) * stage_bytes(64),
               "the parts' sums take the stages' place");
 
 struct Args {
@@ -152,23 +158,34 @@ __device__ __forceinline__ void numbers(const uint4& words, const Numbers<Elem>&
     }
 }
 
-// N (8 or a multiple of 16) fp32 columns of this thread's lane, scaled into acc.
-template <int N>
-__device__ __forceinline__ void add_products(uint32_t taddr, float scale, F2 (&acc)[N / 2]) {
-    constexpr int kPiece = N < 16 ? N : 16;
-    const F2 s = pack2(scale, scale);
-#pragma unroll
-    for (int c = 0; c < N; c += kPiece) {
-        uint32_t r[kPiece];
+// kGroups groups of N (8 or a multiple of 16) fp32 columns of this thread's lane, each group
+// scaled into acc.  With fewer than 64 columns, whose sums leave registers for it, a piece is
+// loaded while the one before is added.
+template <int N, int kGroups>
+__device__ __forceinline__ void add_products(uint32_t taddr, const float* scale, F2 (&acc)[N / 2]) {
+    constexpr int kPiece = N < 16 ? N : 16, kPieces = N / kPiece;
+    constexpr bool kAhead = N < 64;
+    uint32_t r[kAhead ? 2 : 1][kPiece];
+    auto load = [&](int i) {
+        const uint32_t at = taddr + i / kPieces * mma_n(N) + i % kPieces * kPiece;
         if constexpr (kPiece == 8)
-            tmem_ld8(taddr + c, r);
+            tmem_ld8(at, r[kAhead ? i % 2 : 0]);
         else
-            tmem_ld16(taddr + c, r);
+            tmem_ld16(at, r[kAhead ? i % 2 : 0]);
+    };
+    if (kAhead) load(0);
+#pragma unroll
+    for (int i = 0; i < kGroups * kPieces; ++i) {
+        if (!kAhead) load(i);
         tmem_ld_wait();
+        if (kAhead && i + 1 < kGroups * kPieces) load(i + 1);
+        const F2 s = pack2(scale[i / kPieces], scale[i / kPieces]);
+        const int c = i % kPieces * kPiece;
 #pragma unroll
         for (int j = 0; j < kPiece; j += 2)
-            acc[(c + j) / 2] = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s,
-                                    acc[(c + j) / 2]);
+            acc[(c + j) / 2] = fma2(pack2(__uint_as_float(r[kAhead ? i % 2 : 0][j]),
+                                          __uint_as_float(r[kAhead ? i % 2 : 0][j + 1])),
+                                    s, acc[(c + j) / 2]);
     }
 }
 
@@ -235,11 +252,12 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     constexpr int kDs = num_d(kCols, kGroups);
     constexpr uint32_t kDBase = kTeams * kABufCols;
     constexpr uint32_t kDBufCols = d_cols(kCols, kGroups);
+    constexpr int kDGroups = d_groups(kCols, kGroups);
     constexpr int kChunkStages = kScaleGroups / kGroups;  // stages per chunk of scales
     constexpr float kUnit = Numbers<Elem>::kUnit;  // (a power of two: dividing is exact)
     constexpr uint32_t kIdesc =
         std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
-    static_assert(kDs >= 1 && kDBase + kDs * kDBufCols <= kTmemCols, "tensor memory");
+    static_assert(kDs >= 2 && kGroups % kDGroups == 0 && kDBase + kDs * kDBufCols <= kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -360,22 +378,33 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
-                ok = warp_wait(full_bar(stage), phase) && warp_wait(d_empty(d), d_phase ^ 1u) &&
-                     warp_wait(a_full(team), team_phase);
+                ok = warp_wait(full_bar(stage), phase) && warp_wait(a_full(team), team_phase);
                 if (!ok) break;
-                tc_fence_after_sync();
                 const uint64_t x_desc = sw128_kmajor_desc(stage0 + stage * kStageBytes + kCodeBytes);
                 const uint32_t a_tmem = tmem_base + team * kABufCols;
-                const uint32_t d_tmem = tmem_base + kDBase + d * kDBufCols;
-                if (leader) {
 #pragma unroll
-                    for (int i = 0; i < kStageK / 16; ++i) {
+                for (int g0 = 0; g0 < kGroups; g0 += kDGroups) {
+                    ok = warp_wait(d_empty(d), d_phase ^ 1u);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t d_tmem = tmem_base + kDBase + d * kDBufCols;
+                    if (leader) {
                         constexpr int kPerGroup = kStageK / 16 / kGroups;
-                        const uint64_t off = uint64_t((i / 4 * kN * 128 + i % 4 * 32) >> 4);
-                        umma_f16_tmem_a(d_tmem + (i / kPerGroup) * kN, a_tmem + i * 8, x_desc + off,
-                                        kIdesc, i % kPerGroup != 0 ? 1u : 0u);
+#pragma unroll
+                        for (int i = g0 * kPerGroup; i < (g0 + kDGroups) * kPerGroup; ++i) {
+                            const uint64_t off = uint64_t((i / 4 * kN * 128 + i % 4 * 32) >> 4);
+                            umma_f16_tmem_a(d_tmem + (i / kPerGroup - g0) * kN, a_tmem + i * 8,
+                                            x_desc + off, kIdesc, i % kPerGroup != 0 ? 1u : 0u);
+                        }
+                        umma_commit(d_full(d));
                     }
-                    umma_commit(d_full(d));
+                    if (++d == kDs) {
+                        d = 0;
+                        d_phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (leader) {
                     umma_commit(a_empty(team));
                     umma_commit(empty_bar(stage));
                 }
@@ -387,10 +416,6 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 if (++team == kTeams) {
                     team = 0;
                     team_phase ^= 1u;
-                }
-                if (++d == kDs) {
-                    d = 0;
-                    d_phase ^= 1u;
                 }
             }
         }
@@ -444,23 +469,24 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                                      ((row_first + uint32_t(ks0 * kGroups)) & 1u);
                 const int stop = min(k_last, ks0 + kChunkStages);
                 for (int ks = ks0; ok && ks < stop; ++ks) {
-                    float scale[kGroups];
+#pragma unroll 1
+                    for (int g0 = 0; g0 < kGroups; g0 += kDGroups) {
+                        float scale[kDGroups];
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)  // (0 behind the row's last group)
-                        scale[g] = ks * kGroups + g < p.num_groups
-                                       ? to_float(scales[(ks - ks0) * kGroups + g]) : 0.0f;
-                    ok = warp_wait(d_full(d), d_phase);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        add_products<kCols>(lane_base + kDBase + d * kDBufCols + g * kN, scale[g], acc);
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(d_empty(d));
-                    if (++d == kDs) {
-                        d = 0;
-                        d_phase ^= 1u;
+                        for (int g = 0; g < kDGroups; ++g)  // (0 behind the row's last group)
+                            scale[g] = ks * kGroups + g0 + g < p.num_groups
+                                           ? to_float(scales[(ks - ks0) * kGroups + g0 + g]) : 0.0f;
+                        ok = warp_wait(d_full(d), d_phase);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        add_products<kCols, kDGroups>(lane_base + kDBase + d * kDBufCols, scale, acc);
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(d_empty(d));
+                        if (++d == kDs) {
+                            d = 0;
+                            d_phase ^= 1u;
+                        }
                     }
                 }
                 __syncwarp();
@@ -639,12 +665,8 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
     return cudaGetLastError();
 }
 
-// Columns per pass: the rows of x, at most what half of tensor memory holds of each group.
-int columns(int64_t T, int groups_per_stage) {
-    const int most = 256 / groups_per_stage;
-    const int want = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
-    return want < most ? want : most;
-}
+// Rows of x per pass over the codes.
+int columns(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 template <typename Elem, typename Out, bool kZeros>
 cudaError_t launch_cols(int cols, int groups, const CUtensorMap& tw, const CUtensorMap& tx,
@@ -653,8 +675,7 @@ cudaError_t launch_cols(int cols, int groups, const CUtensorMap& tw, const CUten
         constexpr int kCols = decltype(c)::value;
         if (groups == 2) return launch<Elem, Out, kCols, 2, kZeros>(tw, tx, p, num_sms, s);
         if (groups == 4) return launch<Elem, Out, kCols, 4, kZeros>(tw, tx, p, num_sms, s);
-        if constexpr (kCols <= 32)
-            if (groups == 8) return launch<Elem, Out, kCols, 8, kZeros>(tw, tx, p, num_sms, s);
+        if (groups == 8) return launch<Elem, Out, kCols, 8, kZeros>(tw, tx, p, num_sms, s);
         return cudaErrorInvalidValue;
     };
     if (cols == 8) return go(std::integral_constant<int, 8>());
@@ -670,7 +691,7 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
                              int64_t K, int group, void* y, ElemType y_type, int num_sms,
                              cudaStream_t stream) {
     const int groups = kStageK / group;  // per stage
-    const int cols = columns(T, groups);
+    const int cols = columns(T);
     const int64_t tiles = (N + kTileN - 1) / kTileN;
     const int64_t chunks = (T + cols - 1) / cols;
     if (tiles * chunks * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
