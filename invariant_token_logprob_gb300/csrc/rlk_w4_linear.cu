@@ -12,7 +12,10 @@
 // shared-memory time than the codes take from HBM.  So the tile goes through tensor memory:
 // a thread owns one row of a 128-row tile, turns the row's codes into numbers in registers
 // and stores them to its TMEM lane, from where they are the A operand.  x is B (N = the
-// rows of x, 16, 32 or 64).
+// rows of x, 16, 32 or 64 at a time).
+// N = 151936, K = 4096, group 128, bf16: T = 1 59 us (5.5 TB/s, 0.81 of a copy), T = 32 65 us,
+// T = 64 80 us, where the x that comes in again for every tile, 32 KB a stage next to 16 KB of
+// codes, costs more than the codes.  N = K = 4096, T = 1: 6.4 us.
 //
 // One CTA per SM; a tile's K goes by in stages of 256 k:
 //   warp 0       TMA producer: the stage's codes (16 KB) and x
@@ -22,7 +25,8 @@
 //                memory every lane of a warp would touch another row, 32 sectors a load.
 //                Word by word, so that any number of groups per row will do: a row's words
 //                are those that hold its groups, its values lie from its own shift on
-//   warps 3..6   products: a thread keeps a row's running sums, one per row of x:
+//   warps 3..    products, one or two sets of four: a thread keeps a row's running sums, one
+//                per row of x (of half of them):
 //                acc = fma(D, scale, acc), stage after stage, group after group
 //   the others   two or three teams of four warps, which take the stages in turn: a thread
 //                turns its row's codes into numbers and stores them to the team's A buffer
@@ -48,9 +52,12 @@ constexpr int kTileN = 128;                  // rows of W per tile = UMMA M = TM
 constexpr int kStageK = 256;                 // k per stage
 constexpr int kCodeBytes = kTileN * kStageK / 2;
 constexpr int kTeamWarps = 4;
-constexpr int kProductWarps = 4;
 constexpr int kFirstProductWarp = 3;
-constexpr int kFirstTeamWarp = kFirstProductWarp + kProductWarps;
+// Sets of four product warps, which share the columns: 64 in one set's registers leave none to
+// load ahead with (N = 151936, K = 4096, T = 64: group 128 83 us, group 32 176 us; two sets
+// 80 and 166 us).
+constexpr int product_sets(int cols) { return cols < 64 ? 1 : 2; }
+constexpr int first_team_warp(int cols) { return kFirstProductWarp + 4 * product_sets(cols); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kABufCols = kStageK / 2;  // two 16-bit numbers per column
 constexpr int kMaxSplits = 8;
@@ -158,33 +165,29 @@ __device__ __forceinline__ void numbers(const uint4& words, const Numbers<Elem>&
     }
 }
 
-// kGroups groups of N (8 or a multiple of 16) fp32 columns of this thread's lane, each group
-// scaled into acc.  With fewer than 64 columns, whose sums leave registers for it, a piece is
-// loaded while the one before is added.
-template <int N, int kGroups>
+// kGroups groups, kStride columns apart, of N (8, 16 or 32) fp32 columns of this thread's lane,
+// each group scaled into acc.  A piece is loaded while the one before is added.
+template <int N, int kGroups, int kStride>
 __device__ __forceinline__ void add_products(uint32_t taddr, const float* scale, F2 (&acc)[N / 2]) {
     constexpr int kPiece = N < 16 ? N : 16, kPieces = N / kPiece;
-    constexpr bool kAhead = N < 64;
-    uint32_t r[kAhead ? 2 : 1][kPiece];
+    uint32_t r[2][kPiece];
     auto load = [&](int i) {
-        const uint32_t at = taddr + i / kPieces * mma_n(N) + i % kPieces * kPiece;
+        const uint32_t at = taddr + i / kPieces * kStride + i % kPieces * kPiece;
         if constexpr (kPiece == 8)
-            tmem_ld8(at, r[kAhead ? i % 2 : 0]);
+            tmem_ld8(at, r[i % 2]);
         else
-            tmem_ld16(at, r[kAhead ? i % 2 : 0]);
+            tmem_ld16(at, r[i % 2]);
     };
-    if (kAhead) load(0);
+    load(0);
 #pragma unroll
     for (int i = 0; i < kGroups * kPieces; ++i) {
-        if (!kAhead) load(i);
         tmem_ld_wait();
-        if (kAhead && i + 1 < kGroups * kPieces) load(i + 1);
+        if (i + 1 < kGroups * kPieces) load(i + 1);
         const F2 s = pack2(scale[i / kPieces], scale[i / kPieces]);
         const int c = i % kPieces * kPiece;
 #pragma unroll
         for (int j = 0; j < kPiece; j += 2)
-            acc[(c + j) / 2] = fma2(pack2(__uint_as_float(r[kAhead ? i % 2 : 0][j]),
-                                          __uint_as_float(r[kAhead ? i % 2 : 0][j + 1])),
+            acc[(c + j) / 2] = fma2(pack2(__uint_as_float(r[i % 2][j]), __uint_as_float(r[i % 2][j + 1])),
                                     s, acc[(c + j) / 2]);
     }
 }
@@ -241,7 +244,7 @@ __device__ __forceinline__ void copy_groups(const uint8_t* base, int64_t from, i
 
 // kCols: rows of x at a time; kGroups: groups per stage.
 template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
-__global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(kCols, kGroups)), 1)
+__global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * num_teams(kCols, kGroups)), 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap tmap_w,
                      const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     constexpr int kN = mma_n(kCols);
@@ -253,6 +256,8 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
     constexpr uint32_t kDBase = kTeams * kABufCols;
     constexpr uint32_t kDBufCols = d_cols(kCols, kGroups);
     constexpr int kDGroups = d_groups(kCols, kGroups);
+    constexpr int kSets = product_sets(kCols), kMine = kCols / kSets;  // a product warp's columns
+    constexpr int kProductWarps = 4 * kSets, kFirstTeamWarp = first_team_warp(kCols);
     constexpr int kChunkStages = kScaleGroups / kGroups;  // stages per chunk of scales
     constexpr float kUnit = Numbers<Elem>::kUnit;  // (a power of two: dividing is exact)
     constexpr uint32_t kIdesc =
@@ -327,7 +332,8 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
 
     const int row_in_tile = (warp & 3) * 32 + lane;  // (a warp reaches the lanes of its quadrant)
     const uint32_t lane_base = tmem_base + (uint32_t((warp & 3) * 32) << 16);
-    F2 acc[kCols / 2];  // of the product warps
+    F2 acc[kMine / 2];  // of the product warps: the sums of columns mine0 ..
+    const int mine0 = kSets > 1 ? (warp - kFirstProductWarp) / 4 * kMine : 0;
 
     // By a whole warp: all lanes wait, all learn the outcome.
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
             const int n = tile * kTileN + row_in_tile;
             const uint32_t row_first = uint32_t(n) * uint32_t(p.num_groups);  // (its low bit counts)
 #pragma unroll
-            for (int t = 0; t < kCols / 2; ++t) acc[t] = pack2(0.0f, 0.0f);
+            for (int t = 0; t < kMine / 2; ++t) acc[t] = pack2(0.0f, 0.0f);
             for (int ks0 = k_first; ok && ks0 < k_last; ks0 += kChunkStages) {
                 ok = warp_wait(s_full(buf), buf_phase);
                 const Elem* scales = reinterpret_cast<const Elem*>(scale_bufs + buf * kScaleBytes +
@@ -479,7 +485,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                         ok = warp_wait(d_full(d), d_phase);
                         if (!ok) break;
                         tc_fence_after_sync();
-                        add_products<kCols, kDGroups>(lane_base + kDBase + d * kDBufCols, scale, acc);
+                        add_products<kMine, kDGroups, kN>(lane_base + kDBase + d * kDBufCols + mine0, scale, acc);
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(d_empty(d));
@@ -497,10 +503,10 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
                 }
             }
             if (p.splits == 1 && n < p.N && ok) {
-                const int64_t t0 = int64_t(chunk) * kCols;
+                const int64_t t0 = int64_t(chunk) * kCols + mine0;
                 Out* y = static_cast<Out*>(p.y) + t0 * p.N + n;
 #pragma unroll
-                for (int t = 0; t < kCols; t += 2) {
+                for (int t = 0; t < kMine; t += 2) {
                     const float2 v = unpack2(acc[t / 2]);
                     if (t0 + t < p.T) y[int64_t(t) * p.N] = from_float<Out>(v.x / kUnit);
                     if (t0 + t + 1 < p.T) y[int64_t(t + 1) * p.N] = from_float<Out>(v.y / kUnit);
@@ -582,10 +588,10 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
         const int share = (kCols + p.splits - 1) / p.splits;
         if (warp >= kFirstProductWarp && warp < kFirstTeamWarp) {
 #pragma unroll
-            for (int t = 0; t < kCols; ++t) {
-                const int owner = t / share;
-                const uint32_t to = mapa_shared(
-                    smem_u32(parts + (rank * share + (t - owner * share)) * kTileN + row_in_tile), owner);
+            for (int t = 0; t < kMine; ++t) {
+                const int owner = (mine0 + t) / share;
+                const int place = rank * share + (mine0 + t - owner * share);
+                const uint32_t to = mapa_shared(smem_u32(parts + place * kTileN + row_in_tile), owner);
                 const float2 v = unpack2(acc[t / 2]);
                 st_shared_cluster_u32(to, __float_as_uint(t & 1 ? v.y : v.x));
             }
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(32 * (kFirstTeamWarp + kTeamWarps * num_teams(
         const int chunk = first_item - tile * p.chunks;
         const int n = tile * kTileN + row_in_tile;
         if (warp >= kFirstProductWarp && n < p.N) {
-            for (int i = (warp - kFirstProductWarp) / 4; i < share; i += 1 + kTeams) {
+            for (int i = (warp - kFirstProductWarp) / 4; i < share; i += kSets + kTeams) {
                 const int64_t t = int64_t(chunk) * kCols + rank * share + i;
                 if (rank * share + i >= kCols || t >= p.T) break;
                 float sum = parts[i * kTileN + row_in_tile];
@@ -655,7 +661,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
     const int64_t ctas = p.splits > 1 ? int64_t(p.items) * p.splits
                                       : (p.items < num_sms ? p.items : num_sms);
     cfg.gridDim = dim3(unsigned(ctas), 1, 1);
-    cfg.blockDim = dim3(32 * (kFirstTeamWarp + kTeamWarps * num_teams(kCols, kGroups)), 1, 1);
+    cfg.blockDim = dim3(32 * (first_team_warp(kCols) + kTeamWarps * num_teams(kCols, kGroups)), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
