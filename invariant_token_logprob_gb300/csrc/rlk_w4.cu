@@ -125,7 +125,7 @@ __device__ __noinline__ uint32_t code_word_small(float2 x0, float2 x1, float2 x2
 // the arithmetic is kept to packed pairs, and the groups' maxima go across lanes together
 // (N = 151936, K = 4096, bf16, group 128: 233 us, 6.7 TB/s; with zero points 279 us).
 // kWhole: group divides K, so the pieces of W are dealt to the threads in memory order, six
-// CTAs to an SM (five: 241 us); the search for the rows otherwise would spill with six.
+// CTAs to an SM (five: 241 us); the rows' places otherwise would spill with six.
 template <typename Elem, int kGroup, bool kZeros, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kWhole ? 6 : 5)
     quantize_w4_kernel(const Elem* __restrict__ W, int64_t N, int K, int num_groups,
@@ -134,10 +134,18 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 6 : 5)
     constexpr int kLanes = kGroup / 8;
     const int64_t first = int64_t(blockIdx.x) * (kPieces * kThreads) + threadIdx.x;
     const int left = int(min(N * num_groups * kLanes - first, int64_t(kPieces * kThreads)));
-    // (!kWhole) the row of the block's first group; the others by a 32-bit division from there
-    const int64_t group0 = int64_t(blockIdx.x) * (kPieces * kThreads / kLanes);
-    const int64_t row0 = kWhole ? 0 : group0 / num_groups;
-    const uint32_t col0 = uint32_t(group0 - row0 * num_groups);
+    // (!kWhole) the row of the block's first group, and the thread's first group from there;
+    // its other groups lie kStep apart
+    constexpr uint32_t kStep = kThreads / kLanes;
+    const int64_t group0 = int64_t(blockIdx.x) * (kPieces * kStep);
+    const uint32_t per_row = uint32_t(num_groups);
+    const int64_t row0 = kWhole ? 0
+                         : N * num_groups <= UINT32_MAX ? int64_t(uint32_t(group0) / per_row)
+                                                        : group0 / num_groups;
+    uint32_t col = uint32_t(group0 - row0 * num_groups) + threadIdx.x / kLanes;
+    uint32_t row = kWhole ? 0 : col / per_row;
+    col -= row * per_row;
+    const uint32_t step_rows = kWhole ? 0 : kStep / per_row, step_cols = kStep - step_rows * per_row;
     const uint4* src = reinterpret_cast<const uint4*>(W) + (kWhole ? first : row0 * (K / 8));
     codes += kWhole ? first : row0 * (K / 8);
     scales += first / kLanes;
@@ -147,11 +155,15 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 6 : 5)
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
         at[i] = i * kThreads < left ? i * kThreads : -1;
-        if (!kWhole && at[i] >= 0) {
-            const uint32_t group = col0 + (threadIdx.x + i * kThreads) / kLanes;
-            const uint32_t rows = group / uint32_t(num_groups);
-            const int k8 = int(group - rows * uint32_t(num_groups)) * kLanes + int(threadIdx.x % kLanes);
-            at[i] = k8 < K / 8 ? int(rows) * (K / 8) + k8 : -1;
+        if (!kWhole) {
+            const int k8 = int(col) * kLanes + int(threadIdx.x % kLanes);
+            at[i] = at[i] >= 0 && k8 < K / 8 ? int(row) * (K / 8) + k8 : -1;
+            row += step_rows;
+            col += step_cols;
+            if (col >= per_row) {
+                col -= per_row;
+                ++row;
+            }
         }
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
         if (at[i] >= 0) raw[i] = __ldcs(src + at[i]);
