@@ -44,11 +44,12 @@
 #include "rlk_logits_w4.h"
 #include "rlk_ptx.cuh"
 #include "rlk_w4.cuh"
+#include "rlk_w4_plan.h"
 
 namespace rlk {
 namespace {
 
-constexpr int kTileN = 128;                  // rows of W per tile = UMMA M = TMEM lanes
+constexpr int kTileN = kW4TileN;             // rows of W per tile = UMMA M = TMEM lanes
 constexpr int kStageK = 256;                 // k per stage
 constexpr int kCodeBytes = kTileN * kStageK / 2;
 constexpr int kTeamWarps = 4;
@@ -69,9 +70,9 @@ __device__ unsigned int g_w4_error;  // bit 0: a wait ran out; bit 1: a teardown
 // Scales and zero points of kScaleGroups groups of a tile's rows, in words (one more than
 // they fill, for rows that start inside a word).  The rows lie an odd number of words apart,
 // so 32 rows' values of one group lie in 32 banks.
-constexpr int kScaleGroups = 32;
-constexpr int kScaleWords = kScaleGroups / 2 + 1;
-constexpr int kZeroWords = kScaleGroups / 4 + 1;
+constexpr int kScaleGroups = kW4ScaleGroups;
+constexpr int kScaleWords = w4_chunk_words(2);
+constexpr int kZeroWords = w4_chunk_words(1);
 static_assert(kScaleWords % 2 == 1 && kZeroWords % 2 == 1, "banks");
 constexpr int kScaleBytes = kTileN * (kScaleWords + kZeroWords) * 4;
 
@@ -193,22 +194,21 @@ __device__ __forceinline__ void add_products(uint32_t taddr, const float* scale,
 }
 
 // Copies kScaleGroups values of kSize bytes of each of a tile's rows, value `from` of an
-// array of `all` on and row_values further per row, as the words that hold them.  A warp
+// array of n_rows rows on and row_values further per row, as the words that hold them.  A warp
 // takes whole rows side by side: rows four (kSize 1) or two apart start at the same place
 // of a word, so a lane's words lie a fixed step apart.  The word behind comes at the end.
 template <int kSize>
 __device__ __forceinline__ void copy_groups(const uint8_t* base, int64_t from, int row_values,
-                                            int64_t all, bool inner, int lane, uint32_t to) {
+                                            int64_t n_rows, int lane, uint32_t to) {
     constexpr int kWords = kScaleGroups * kSize / 4;  // and one more
     constexpr int kRows = 32 / kWords;                // at once
     static_assert(kRows * kSize % 4 == 0, "the rows of a step start at the same place of a word");
-    auto word = [&](int row, int w) {  // byte offset
-        return ((from + int64_t(row) * row_values) * kSize & ~int64_t(3)) + w * 4;
-    };
+    auto word = [&](int row, int w) { return w4_chunk_word(from, row, row_values, kSize, w); };
     const int64_t at = word(lane / kWords, lane % kWords);
     const uint32_t dst = to + ((lane / kWords) * (kWords + 1) + lane % kWords) * 4;
     const int64_t step = int64_t(kRows) * row_values * kSize;
-    if (inner) {  // one warp keeps up with all others only with few instructions per word
+    // one warp keeps up with all others only with few instructions per word
+    if (w4_chunk_inside(from, row_values, n_rows, kSize)) {
         const uint8_t* src = base + at;
         uint32_t d = dst;
 #pragma unroll 8
@@ -223,7 +223,7 @@ __device__ __forceinline__ void copy_groups(const uint8_t* base, int64_t from, i
                             base + word(r + lane, kWords), 4);
         return;
     }
-    const int64_t end = all * kSize;
+    const int64_t end = n_rows * row_values * kSize;
     auto copy = [&](int64_t src, uint32_t d) {
         const int64_t left = end - src;
         const uint32_t bytes = left <= 0 ? 0u : left < 4 ? uint32_t(left) : 4u;
@@ -436,18 +436,14 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
             const int64_t n0 = int64_t(item / p.chunks) * kTileN;
-            // no word of the tile, with the one behind a row's last, lies behind the arrays
-            const bool inner = n0 + kTileN + 1 < p.N;
             for (int ks = k_first; ks < k_last; ks += kChunkStages) {
                 ok = warp_wait(s_empty(buf), buf_phase ^ 1u);
                 if (!ok) break;
                 const uint32_t to = smem_u32(scale_bufs + buf * kScaleBytes);
                 const int64_t from = n0 * p.num_groups + ks * kGroups;  // the first row's first group
-                copy_groups<2>(static_cast<const uint8_t*>(p.scales), from, p.num_groups,
-                               int64_t(p.N) * p.num_groups, inner, lane, to);
+                copy_groups<2>(static_cast<const uint8_t*>(p.scales), from, p.num_groups, p.N, lane, to);
                 if (kZeros)
-                    copy_groups<1>(p.zeros, from, p.num_groups, int64_t(p.N) * p.num_groups, inner,
-                                   lane, to + kTileN * kScaleWords * 4);
+                    copy_groups<1>(p.zeros, from, p.num_groups, p.N, lane, to + kTileN * kScaleWords * 4);
                 copy_words_arrive(s_full(buf));
                 if (++buf == kScaleBufs) {
                     buf = 0;

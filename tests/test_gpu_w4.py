@@ -280,3 +280,16 @@ def test_refusals():
         rlk.linear_w4(flat[1:].view(T, K), c, s, z, group)
     assert rlk.linear_w4(x[:0], c, s, z, group).shape == (0, N)
     assert rlk.linear_w4(x, c[:0], s[:0], z[:0], group).shape == (T, 0)
+
+
+@pytest.mark.parametrize("T,N,K,group", [(1, 130, 1024, 128), (3, 258, 128, 128), (20, 130, 256, 128),
+                                         (64, 1154, 768, 128), (9, 163, 32, 32), (2, 32002, 1024, 128)])
+def test_linear_with_few_groups_per_row(T, N, K, group):
+    """Few groups per row and a few rows behind a multiple of 128: the words copied for the
+    scales and zero points of a tile's last rows span more rows than are left."""
+    import invariant_token_logprob_gb300 as rlk
+    for zeros in (False, True):
+        x, q, s, z = make(T, N, K, group, "bf16", zeros, N + K)
+        y = rlk.linear_w4(x.cuda(), rlk.pack_w4(q.cuda()), s.cuda(), None if z is None else z.cuda(), group)
+        rlk.check_device_error()
+        check_linear(y, x, q, s, z, group, "fp32", str((T, N, K, group, zeros)))
