@@ -595,8 +595,9 @@ rlk_status rlk_dequantize_w4(const uint32_t *codes_u32, const void *scales,
  *   y[t][n] = sum_g scales[n][g] * sum_{k in g} (q[n][k] - zeros[n][g]) x[t][k]
  * with fp32 accumulation (each group's products of a 16-bit x and a small whole number
  * are exact; a scale is applied once per group, in fp32) and one rounding to out_dtype
- * (`dtype` or RLK_FP32).  x, scales of `dtype` (RLK_BF16 or RLK_FP16), x and codes
- * 16-byte aligned, y aligned to its element.  T >= 0, N >= 0, T * N <= 2^39.
+ * (`dtype` or RLK_FP32).  x, scales of `dtype` (RLK_BF16 or RLK_FP16), x, codes and
+ * scales 16-byte aligned, zeros_u8 4-byte aligned (it is copied in words), y aligned to
+ * its element; else RLK_ERR_ALIGNMENT.  T >= 0, N >= 0, T * N <= 2^39.
  * Asynchronous on `stream`; allocates nothing.  The order of the sums is fixed by N, K
  * and group: a row's bits depend on that row of x and the weight only, never on T.  A
  * bounded wait that runs out is reported by rlk_check_device_error.  Callers that capture

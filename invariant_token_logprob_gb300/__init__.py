@@ -943,7 +943,8 @@ def dequantize_w4(codes, scales, zeros=None, group: int = 128, out_dtype=None, o
 def linear_w4(x, codes, scales, zeros=None, group: int = 128, out_dtype=None, out=None,
               stream=None):
     """rlk_linear_w4: y [T, N] = x [T, K] . W^T for a 4-bit weight; x has the scales' type,
-    y that type or float32 (out_dtype, default float32)."""
+    y that type or float32 (out_dtype, default float32).  x, codes and scales start at
+    16-byte boundaries, zeros at a 4-byte one."""
     call = _Call()
     c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
     a = call.arg(x, scales.dtype, "x", 2)

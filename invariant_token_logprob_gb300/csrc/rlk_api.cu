@@ -900,7 +900,8 @@ rlk_status rlk_linear_w4(const void* x, int dtype, const uint32_t* codes_u32, co
     if (T > 0 && N > (int64_t(1) << 39) / T) return RLK_ERR_INVALID_ARG;
     if (N == 0 || T == 0) return RLK_OK;
     if (!x || !out_y) return RLK_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned_to(out_y, elem_size(out_dtype))) return RLK_ERR_ALIGNMENT;
+    if (!aligned16(x) || !aligned4(zeros_u8) || !aligned_to(out_y, elem_size(out_dtype)))
+        return RLK_ERR_ALIGNMENT;
     int dev, sms;
     if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
     return from_cuda(rlk::launch_linear_w4(x, ElemType(dtype), codes_u32, scales, zeros_u8, T, N, K,

@@ -293,3 +293,23 @@ def test_linear_with_few_groups_per_row(T, N, K, group):
         y = rlk.linear_w4(x.cuda(), rlk.pack_w4(q.cuda()), s.cuda(), None if z is None else z.cuda(), group)
         rlk.check_device_error()
         check_linear(y, x, q, s, z, group, "fp32", str((T, N, K, group, zeros)))
+
+
+def test_zero_points_off_a_word():
+    """A view into a packed buffer: read back as it is, refused by the product."""
+    import invariant_token_logprob_gb300 as rlk
+    T, N, K, group = 2, 40, 256, 64
+    x, q, s, z = make(T, N, K, group, "bf16", True, 11)
+    x, c, s, z = x.cuda(), rlk.pack_w4(q.cuda()), s.cuda(), z.cuda()
+    flat = torch.zeros(z.numel() + 4, dtype=torch.uint8, device="cuda")
+    want = rlk.dequantize_w4(c, s, z, group)
+    y = rlk.linear_w4(x, c, s, z, group)
+    for off in (1, 2, 3, 4):
+        view = flat[off:off + z.numel()].view_as(z)
+        view.copy_(z)
+        assert torch.equal(rlk.dequantize_w4(c, s, view, group), want)
+        if off < 4:
+            with pytest.raises(rlk.RlkError):
+                rlk.linear_w4(x, c, s, view, group)
+        else:
+            assert torch.equal(rlk.linear_w4(x, c, s, view, group), y)

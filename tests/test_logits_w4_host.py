@@ -109,3 +109,14 @@ def test_binding_refuses_cpu_tensors():
                       torch.zeros(2, 1, dtype=torch.bfloat16), group=32)
     with pytest.raises(ValueError, match="CUDA"):
         rlk.quantize_w4(torch.zeros(2, 32, dtype=torch.bfloat16), 32)
+
+
+@pytest.mark.parametrize("zeros", [A1, A2, ctypes.c_void_p((1 << 20) + 3)])
+def test_linear_refuses_zero_points_off_a_word(L, zeros):
+    """The product copies zero points in words of four bytes."""
+    assert L.rlk_linear_w4(A16, 0, A16, A16, zeros, 2, 10, 64, 32, A16, 2, None) == 2
+    assert L.rlk_linear_w4(A16, 0, A16, A16, zeros, 0, 10, 64, 32, A16, 2, None) == 0  # nothing to do
+    if not torch.cuda.is_available():  # byte by byte elsewhere: any address goes on to the device's check
+        assert L.rlk_linear_w4(A16, 0, A16, A16, A4, 2, 10, 64, 32, A16, 2, None) == 3
+        assert L.rlk_quantize_w4(A16, 0, 4, 64, 32, A16, A16, zeros, None) == 3
+        assert L.rlk_dequantize_w4(A16, A16, zeros, 0, 4, 64, 32, A16, 0, None) == 3
