@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
                                          : 8u;
                     ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
                     if (!ok) break;
+                    tc_fence_after_sync();  // the MMAs that read the buffer come before the stores
                     // 16-byte pieces of the row, swizzled by its place among eight
                     const uint32_t codes = stage0 + stage * kStageBytes + row_in_tile * 128 +
                                            ((row_in_tile & 7) << 4);

@@ -3,6 +3,7 @@
 lies outside the scales or the zero points."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -80,3 +81,16 @@ def test_every_chunk_that_lies_inside_is_held_to(plan):
     for n, g in ((151936, 32), (151936, 64), (5120, 40), (1000, 9), (4096, 1), (129, 32)):
         for size in (1, 2):
             assert plan.counts(n, g, size, ctypes.byref(held)) == held.value, (n, g, size)
+
+
+def test_tensor_memory_is_fenced_behind_every_wait():
+    """tcgen05 accesses are ordered behind what a barrier's phase reports (other tcgen05 work
+    of the issuing warp among it) only by a fence after the wait.  No run can show a missing
+    one, so the source is read: between each access and the wait before it there is one."""
+    text = open(os.path.join(CSRC, "rlk_w4_linear.cu")).read()
+    body = re.sub(r"//[^\n]*", "", text[text.index("linear_w4_kernel("):])
+    accesses = [m.start() for m in re.finditer(r"\b(tmem_st16|add_products|umma_f16_tmem_a)\b", body)]
+    assert len(accesses) >= 3
+    for at in accesses:
+        wait = max(body.rfind("warp_wait(", 0, at), body.rfind("wait_bounded(", 0, at))
+        assert "tc_fence_after_sync()" in body[wait:at], body[wait:at][:200]
