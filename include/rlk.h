@@ -608,6 +608,22 @@ rlk_status rlk_linear_w4(const void *x, int dtype, const uint32_t *codes_u32, co
                          const uint8_t *zeros_u8, int64_t T, int64_t N, int64_t K, int group,
                          void *out_y, int out_dtype, rlk_stream_t stream);
 
+/*
+ * Self-test of rlk_linear_w4's bounded waits, as rlk_selftest_wait_timeout: a product with
+ * T = 1, N = 128, K = 1024, group 128 and no zero points that cannot end.
+ *   mode 1: the copy engine issues nothing, and the first wait for data runs out.
+ *   mode 2: all copies are issued (and land) but no stage is consumed: the waits for its
+ *           products run out after the copy engine's thread has issued its last copy.
+ * The kernel records the timeout, waits for its copies, releases its tensor memory and
+ * returns after about 2 s; rlk_check_device_error(stream) then returns RLK_ERR_TIMEOUT and
+ * the context stays usable.
+ *   x_bf16 [1][1024], codes_u32 [128][128], scales_bf16 [128][8] (16-byte aligned),
+ *   y_f32 [128] (left unwritten): device buffers.  Another mode: RLK_ERR_INVALID_ARG.
+ */
+rlk_status rlk_selftest_wait_timeout_w4(const void *x_bf16, const uint32_t *codes_u32,
+                                        const void *scales_bf16, float *y_f32, int mode,
+                                        rlk_stream_t stream);
+
 /* Release the library's cached workspaces on every device it used (waits for
  * them to be idle).  Safe to call more than once. */
 rlk_status rlk_shutdown(void);

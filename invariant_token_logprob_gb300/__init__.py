@@ -145,6 +145,8 @@ def lib() -> ctypes.CDLL:
         L.rlk_linear_w4.restype = st
         L.rlk_linear_w4.argtypes = [P, ctypes.c_int, P, P, P, i64, i64, i64, ctypes.c_int, P,
                                     ctypes.c_int, P]
+        L.rlk_selftest_wait_timeout_w4.restype = st
+        L.rlk_selftest_wait_timeout_w4.argtypes = [P, P, P, P, ctypes.c_int, P]
         _lib = L
     return _lib
 

@@ -909,6 +909,21 @@ rlk_status rlk_linear_w4(const void* x, int dtype, const uint32_t* codes_u32, co
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
+rlk_status rlk_selftest_wait_timeout_w4(const void* x_bf16, const uint32_t* codes_u32,
+                                        const void* scales_bf16, float* y_f32, int mode,
+                                        rlk_stream_t stream) {
+    if (mode != 1 && mode != 2) return RLK_ERR_INVALID_ARG;
+    if (!x_bf16 || !codes_u32 || !scales_bf16 || !y_f32) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(codes_u32) || !aligned16(scales_bf16) || !aligned4(y_f32))
+        return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    rlk_status st = current_device(&dev, &sms);
+    if (st != RLK_OK) return st;
+    return from_cuda(rlk::launch_linear_w4_stall_selftest(x_bf16, codes_u32, scales_bf16, y_f32,
+                                                          mode, sms,
+                                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
 rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits,
                                   uint64_t* target_range_rows) {
     int dev, sms;

@@ -33,6 +33,11 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
                              const void* scales, const uint8_t* zeros, int64_t T, int64_t N,
                              int64_t K, int group, void* y, ElemType y_type, int num_sms,
                              cudaStream_t stream);
+// Its bounded-wait self-test (T = 1, N = 128, K = 1024, group 128, bf16, fp32 output); mode 1:
+// no copy is issued, 2: no stage is consumed.
+cudaError_t launch_linear_w4_stall_selftest(const void* x, const uint32_t* codes,
+                                            const void* scales, float* y, int mode, int num_sms,
+                                            cudaStream_t stream);
 // Reads and clears the product kernel's per-device error word (bit 0: a bounded wait ran
 // out; bit 1: a teardown wait ran out).
 cudaError_t linear_w4_take_error(unsigned int* out);

@@ -124,6 +124,8 @@ struct Args {
     int splits;
     int x_rows;        // rows of an x box: fewer than the MMA's N where T is (the others'
                        // columns hold what the shared memory held and are never read)
+    int stall_selftest;  // bounded-wait self-test: 1, the producer issues no copies; 2, the MMA
+                         // issuer consumes no stage
 };
 
 // By whole warps or single lanes; the usual wait finds its phase complete.
@@ -346,7 +348,8 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
             uint32_t stage = 0, phase = 0;
             int issued = 0;
             bool ok = true;
-            for (int item = first_item; ok && item < p.items; item += item_step) {
+            const int items = p.stall_selftest == 1 ? 0 : p.items;
+            for (int item = first_item; ok && item < items; item += item_step) {
                 const int tile = item / p.chunks;
                 const int chunk = item - tile * p.chunks;
                 for (int ks = k_first; ks < k_last; ++ks) {
@@ -368,10 +371,12 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
                     }
                 }
             }
-            if (!ok) {  // let the copies this thread started land before the CTA exits
-                const int first = issued > kStages ? issued - kStages : 0;
-                for (int i = first; i < issued; ++i)
-                    wait_drain(full_bar(i % kStages), uint32_t(i / kStages) & 1u);
+            // The copies this thread started land before the CTA exits, whichever role gave up:
+            // the others may stop waiting for them after the last one was issued.  (Usually
+            // they have landed, or the others wait for them too.)
+            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+                const uint32_t bar = full_bar(i % kStages), parity = uint32_t(i / kStages) & 1u;
+                if (!wait_bounded(bar, parity, abort_flag)) wait_drain(bar, parity);
             }
         }
         __syncwarp();
@@ -382,7 +387,8 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
         const bool leader = elect_one();
         uint32_t stage = 0, phase = 0, team = 0, team_phase = 0, d = 0, d_phase = 0;
         bool ok = true;
-        for (int item = first_item; ok && item < p.items; item += item_step) {
+        const int items = p.stall_selftest == 2 ? 0 : p.items;
+        for (int item = first_item; ok && item < items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
                 ok = warp_wait(full_bar(stage), phase) && warp_wait(a_full(team), team_phase);
                 if (!ok) break;
@@ -668,6 +674,15 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
     return cudaGetLastError();
 }
 
+// (fp16 and bf16 are copied alike)
+bool encode_maps(const uint32_t* codes, const void* x, int64_t T, int64_t N, int64_t K, int x_rows,
+                 CUtensorMap* tw, CUtensorMap* tx) {
+    return encode_tensor_map_2d(tw, codes, uint64_t(K / 2), uint64_t(N), uint64_t(K / 2),
+                                kStageK / 2, kTileN, true) &&
+           encode_tensor_map_2d(tx, x, uint64_t(K), uint64_t(T), uint64_t(K) * 2, 64,
+                                uint32_t(x_rows), false);
+}
+
 // Rows of x per pass over the codes.
 int columns(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
@@ -700,15 +715,10 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
     if (tiles * chunks * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
     Args p = {scales, zeros, y, T, int(N), int((K + group - 1) / group), int(chunks),
               int(tiles * chunks), int((K + kStageK - 1) / kStageK), 1,
-              int(T < mma_n(cols) ? T : mma_n(cols))};
+              int(T < mma_n(cols) ? T : mma_n(cols)), 0};
     p.splits = num_splits(int(tiles), p.num_stages, num_sms);
     CUtensorMap tw, tx;
-    // (fp16 and bf16 are copied alike)
-    if (!encode_tensor_map_2d(&tw, codes, uint64_t(K / 2), uint64_t(N), uint64_t(K / 2),
-                              kStageK / 2, kTileN, true) ||
-        !encode_tensor_map_2d(&tx, x, uint64_t(K), uint64_t(T), uint64_t(K) * 2, 64,
-                              uint32_t(p.x_rows), false))
-        return cudaErrorInvalidValue;
+    if (!encode_maps(codes, x, T, N, K, p.x_rows, &tw, &tx)) return cudaErrorInvalidValue;
     auto go = [&](auto elem, auto out) {
         using Elem = decltype(elem);
         using Out = decltype(out);
@@ -719,6 +729,19 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
     if (type == ElemType::kBf16)
         return wide ? go(__nv_bfloat16(), float()) : go(__nv_bfloat16(), __nv_bfloat16());
     return wide ? go(__half(), float()) : go(__half(), __half());
+}
+
+cudaError_t launch_linear_w4_stall_selftest(const void* x, const uint32_t* codes,
+                                            const void* scales, float* y, int mode, int num_sms,
+                                            cudaStream_t stream) {
+    // one tile and four stages: all copies are issued before a wait can run out
+    constexpr int64_t T = 1, N = kTileN, K = 4 * kStageK;
+    constexpr int kCols = 8, kGroup = 128;
+    static_assert(K / kStageK <= stages(kCols, kStageK / kGroup), "the ring holds every stage");
+    const Args p = {scales, nullptr, y, T, int(N), int(K / kGroup), 1, 1, int(K / kStageK), 1, 1, mode};
+    CUtensorMap tw, tx;
+    if (!encode_maps(codes, x, T, N, K, p.x_rows, &tw, &tx)) return cudaErrorInvalidValue;
+    return launch<__nv_bfloat16, float, kCols, kStageK / kGroup, false>(tw, tx, p, num_sms, stream);
 }
 
 cudaError_t linear_w4_take_error(unsigned int* out) {

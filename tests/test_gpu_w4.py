@@ -313,3 +313,32 @@ def test_zero_points_off_a_word():
                 rlk.linear_w4(x, c, s, view, group)
         else:
             assert torch.equal(rlk.linear_w4(x, c, s, view, group), y)
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+def test_bounded_wait_runs_out_and_context_survives(mode):
+    """No copy is issued, or no stage is consumed after every copy was issued: the wait that
+    runs out is reported, every teardown wait ends in time, and the next call is right."""
+    import ctypes
+    import time
+
+    import invariant_token_logprob_gb300 as rlk
+    x, q, s, _ = make(1, 128, 1024, 128, "bf16", False, mode)
+    x, codes, s = x.cuda(), rlk.pack_w4(q.cuda()), s.cuda()
+    y = torch.full((1, 128), 7.0, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rlk.check_device_error()
+
+    def selftest(m):
+        return rlk.lib().rlk_selftest_wait_timeout_w4(*(ctypes.c_void_p(t.data_ptr()) for t in (x, codes, s, y)),
+                                                      m, stream)
+
+    assert selftest(0) == 1 and selftest(3) == 1
+    t0 = time.time()
+    assert selftest(mode) == 0
+    assert rlk.take_device_errors() == (1, 0)  # a wait ran out, and no teardown wait did
+    assert 1.0 < time.time() - t0 < 30.0
+    assert bool((y == 7).all())
+    rlk.check_device_error()
+    rlk.linear_w4(x, codes, s, out=y)
+    check_linear(y, x.cpu(), q, s.cpu(), None, 128, "fp32")

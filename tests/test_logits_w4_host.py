@@ -120,3 +120,12 @@ def test_linear_refuses_zero_points_off_a_word(L, zeros):
         assert L.rlk_linear_w4(A16, 0, A16, A16, A4, 2, 10, 64, 32, A16, 2, None) == 3
         assert L.rlk_quantize_w4(A16, 0, 4, 64, 32, A16, A16, zeros, None) == 3
         assert L.rlk_dequantize_w4(A16, A16, zeros, 0, 4, 64, 32, A16, 0, None) == 3
+
+
+def test_wait_selftest_refusals(L):
+    f = L.rlk_selftest_wait_timeout_w4
+    assert f(A16, A16, A16, A16, 0, None) == 1 and f(A16, A16, A16, A16, 3, None) == 1
+    assert f(None, A16, A16, A16, 1, None) == 1 and f(A16, A16, A16, None, 2, None) == 1
+    assert f(A4, A16, A16, A16, 1, None) == 2 and f(A16, A16, A16, A2, 1, None) == 2
+    if not torch.cuda.is_available():
+        assert f(A16, A16, A16, A16, 1, None) == 3

@@ -94,3 +94,16 @@ def test_tensor_memory_is_fenced_behind_every_wait():
     for at in accesses:
         wait = max(body.rfind("warp_wait(", 0, at), body.rfind("wait_bounded(", 0, at))
         assert "tc_fence_after_sync()" in body[wait:at], body[wait:at][:200]
+
+
+def test_copies_are_waited_for_whoever_gives_up():
+    """The producer's drain of its last copies stands under no condition: a consumer's wait may
+    run out after the last copy was issued, and the copies must not land in the shared memory
+    of the CTA that comes next.  (No run can show it without writing over that memory.)"""
+    text = open(os.path.join(CSRC, "rlk_w4_linear.cu")).read()
+    body = re.sub(r"//[^\n]*", "", text[text.index("linear_w4_kernel("):])
+    producer = body[body.index("if (warp == 0) {"):body.index("} else if (warp == 1) {")]
+    tail = producer[producer.rindex("++issued;"):]
+    drain = tail.index("wait_drain(")
+    assert "issued" in tail[tail.index("for ("):drain]
+    assert not re.search(r"if \(!ok\)", tail[:drain])
