@@ -599,7 +599,9 @@ rlk_status rlk_dequantize_w4(const uint32_t *codes_u32, const void *scales,
  * scales 16-byte aligned, zeros_u8 4-byte aligned (it is copied in words), y aligned to
  * its element; else RLK_ERR_ALIGNMENT.  T >= 0, N >= 0, T * N <= 2^39.
  * Asynchronous on `stream`; allocates nothing.  The order of the sums is fixed by N, K
- * and group: a row's bits depend on that row of x and the weight only, never on T.  A
+ * and group: a row's bits depend on that row of x and the weight only, never on T or the
+ * device.  (N counts: K is cut into parts where N is small, so a shard of a weight's rows
+ * may have other bits than the whole weight.)  A
  * bounded wait that runs out is reported by rlk_check_device_error.  Callers that capture
  * graphs make one call of each class before (T up to 8, 16, 32, more; group; with or
  * without zeros; types): the first one sets its kernel's shared-memory size.

@@ -61,7 +61,7 @@ constexpr int product_sets(int cols) { return cols < 64 ? 1 : 2; }
 constexpr int first_team_warp(int cols) { return kFirstProductWarp + 4 * product_sets(cols); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kABufCols = kStageK / 2;  // two 16-bit numbers per column
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = kW4MaxParts;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 
@@ -623,22 +623,6 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
     }
 }
 
-// Parts of K per tile: the fewest rounds of stages over the SMs, counting a few stages'
-// time for a part's beginning and end.  A function of the weight's shape alone.
-int num_splits(int tiles, int num_stages, int num_sms) {
-    int best = 1;
-    int64_t best_cost = INT64_MAX;
-    for (int s = 1; s <= kMaxSplits && s <= num_stages; ++s) {
-        const int64_t rounds = (int64_t(tiles) * s + num_sms - 1) / num_sms;
-        const int64_t cost = rounds * ((num_stages + s - 1) / s + 3 + (s > 1 ? 1 : 0));
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = s;
-        }
-    }
-    return best;
-}
-
 template <typename Elem, typename Out, int kCols, int kGroups, bool kZeros>
 cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, int num_sms,
                    cudaStream_t stream) {
@@ -716,7 +700,7 @@ cudaError_t launch_linear_w4(const void* x, ElemType type, const uint32_t* codes
     Args p = {scales, zeros, y, T, int(N), int((K + group - 1) / group), int(chunks),
               int(tiles * chunks), int((K + kStageK - 1) / kStageK), 1,
               int(T < mma_n(cols) ? T : mma_n(cols)), 0};
-    p.splits = num_splits(int(tiles), p.num_stages, num_sms);
+    p.splits = w4_parts_of_k(int(tiles), p.num_stages);
     CUtensorMap tw, tx;
     if (!encode_maps(codes, x, T, N, K, p.x_rows, &tw, &tx)) return cudaErrorInvalidValue;
     auto go = [&](auto elem, auto out) {

@@ -1,6 +1,6 @@
-// rlk_w4_plan.h -- which words of the scales and zero points the product with a 4-bit weight
-// (rlk_w4_linear.cu) copies: plain arithmetic without CUDA, so that a host compiler can check
-// it against the arrays' ends.
+// rlk_w4_plan.h -- how the product with a 4-bit weight (rlk_w4_linear.cu) cuts K, and which
+// words of the scales and zero points it copies: plain arithmetic without CUDA, so that a host
+// compiler can check it.
 #pragma once
 
 #include <stdint.h>
@@ -32,6 +32,25 @@ RLK_HOST_DEVICE int64_t w4_chunk_word(int64_t from, int row, int row_values, int
 RLK_HOST_DEVICE bool w4_chunk_inside(int64_t from, int row_values, int64_t n_rows, int size) {
     return w4_chunk_word(from, kW4TileN - 1, row_values, size, w4_chunk_words(size) - 1) + 4 <=
            n_rows * row_values * size;
+}
+
+// Parts of K per tile: the fewest rounds of stages over the SMs, counting a few stages'
+// time for a part's beginning and end.  The cut decides the order of the sums, so it follows
+// from the weight's shape alone: the number of SMs is the GB300's, whatever the device has.
+constexpr int kW4MaxParts = 8;
+constexpr int kW4PlanSms = 152;
+inline int w4_parts_of_k(int tiles, int num_stages) {
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; s <= kW4MaxParts && s <= num_stages; ++s) {
+        const int64_t rounds = (int64_t(tiles) * s + kW4PlanSms - 1) / kW4PlanSms;
+        const int64_t cost = rounds * ((num_stages + s - 1) / s + 3 + (s > 1 ? 1 : 0));
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 }  // namespace rlk

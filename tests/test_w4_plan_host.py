@@ -43,6 +43,7 @@ int counts(int n, int g, int size, int* held) {
         }
     return inside;
 }
+int parts_of_k(int n, int k) { return rlk::w4_parts_of_k((n + 127) / 128, (k + 255) / 256); }
 }
 """
 
@@ -107,3 +108,17 @@ def test_copies_are_waited_for_whoever_gives_up():
     drain = tail.index("wait_drain(")
     assert "issued" in tail[tail.index("for ("):drain]
     assert not re.search(r"if \(!ok\)", tail[:drain])
+
+
+@pytest.mark.parametrize("n,k,parts", [(151936, 4096, 1), (32768, 4096, 1), (40000, 1024, 1), (19584, 4096, 2),
+                                       (5119, 5152, 3), (5000, 4096, 3), (4864, 4096, 4), (4096, 4096, 4),
+                                       (1024, 2080, 5), (128, 4096, 8), (128, 256, 1)])
+def test_cut_of_k_is_pinned(plan, n, k, parts):
+    """The cut decides the order of a row's sums, hence its bits: a function of the weight's
+    shape, the same on every device."""
+    assert plan.parts_of_k(n, k) == parts
+
+
+def test_cut_of_k_does_not_ask_the_device():
+    text = open(os.path.join(CSRC, "rlk_w4_linear.cu")).read()
+    assert re.search(r"w4_parts_of_k\(int\(tiles\), p\.num_stages\);", text)
