@@ -12,6 +12,7 @@ The library is loaded on first use, so ``invariant_token_logprob_gb300.inputs``
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import NamedTuple, Optional
@@ -193,6 +194,22 @@ def _need(t, dtype, name, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims")
 
 
+def _empty(stream, *size, **kw):
+    """torch.empty in memory that belongs to `stream` (None: the current one), and that is not
+    handed on either before work queued on the current stream by then is through with it.  A
+    block of the current stream's may still be in use by work queued there when `stream` writes
+    to it, and a temporary would go to that stream's next work while `stream` still uses it."""
+    import torch
+    if stream is None:
+        return torch.empty(*size, **kw)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*size, **kw)
+    current = torch.cuda.current_stream()
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def row_tile() -> int:
     return lib().rlk_row_tile()
 
@@ -217,12 +234,12 @@ def _check_inputs(h, W, targets):
     return T, H, V
 
 
-def _outputs(T, device, out):
+def _outputs(T, device, out, stream):
     import torch
     if out is None:
-        return (torch.empty(T, dtype=torch.float32, device=device),
-                torch.empty(T, dtype=torch.float32, device=device),
-                torch.empty(T, dtype=torch.int32, device=device))
+        return (_empty(stream, T, dtype=torch.float32, device=device),
+                _empty(stream, T, dtype=torch.float32, device=device),
+                _empty(stream, T, dtype=torch.int32, device=device))
     lp, lse, am = out
     _need(lp, torch.float32, "out[0]", 1)
     _need(lse, torch.float32, "out[1]", 1)
@@ -233,7 +250,7 @@ def _outputs(T, device, out):
 def logprob(h, W, targets, inv_temp: float = 1.0, out=None, stream=None):
     """rlk_logprob: returns (logp f32[T], lse f32[T], argmax i32[T]) on h's device."""
     T, H, V = _check_inputs(h, W, targets)
-    lp, lse, am = _outputs(T, h.device, out)
+    lp, lse, am = _outputs(T, h.device, out, stream)
     _check(lib().rlk_logprob(_ptr(h), _ptr(W), _ptr(targets), T, H, V, ctypes.c_float(inv_temp),
                              _ptr(lp), _ptr(lse), _ptr(am), _stream(stream)), "rlk_logprob")
     return lp, lse, am
@@ -244,7 +261,7 @@ def logprob_ws(h, W, targets, workspace, inv_temp: float = 1.0, out=None, stream
     import torch
     T, H, V = _check_inputs(h, W, targets)
     _need(workspace, torch.uint8, "workspace", 1)
-    lp, lse, am = _outputs(T, h.device, out)
+    lp, lse, am = _outputs(T, h.device, out, stream)
     _check(lib().rlk_logprob_ws(_ptr(h), _ptr(W), _ptr(targets), T, H, V, ctypes.c_float(inv_temp),
                                 _ptr(lp), _ptr(lse), _ptr(am), _ptr(workspace),
                                 workspace.numel(), _stream(stream)), "rlk_logprob_ws")
@@ -258,7 +275,7 @@ def logprob_partials(h, W, targets, inv_temp: float = 1.0, out=None, stream=None
     T, H, V = _check_inputs(h, W, targets)
     nvt = (V + vocab_tile() - 1) // vocab_tile()
     if out is None:
-        out = torch.empty((T, nvt, 4), dtype=torch.float32, device=h.device)
+        out = _empty(stream, (T, nvt, 4), dtype=torch.float32, device=h.device)
     _need(out, torch.float32, "out")
     _check(lib().rlk_logprob_partials(_ptr(h), _ptr(W), _ptr(targets), T, H, V,
                                       ctypes.c_float(inv_temp), _ptr(out),
@@ -275,7 +292,7 @@ def lse_merge(partials, targets, V: int, out=None, stream=None):
     nvt = (V + vocab_tile() - 1) // vocab_tile()
     if partials.shape[1] != nvt or partials.shape[2] != 4 or targets.shape[0] != T:
         raise ValueError("partials must be [T, ceil(V/vocab_tile), 4] and targets [T]")
-    lp, lse, am = _outputs(T, partials.device, out)
+    lp, lse, am = _outputs(T, partials.device, out, stream)
     _check(lib().rlk_lse_merge(_ptr(partials), _ptr(targets), T, int(V), _ptr(lp), _ptr(lse),
                                _ptr(am), _stream(stream)), "rlk_lse_merge")
     return lp, lse, am
@@ -318,13 +335,13 @@ def consistency_stats_async(a, b, mask=None, out=None, workspace=None, stream=No
         mp = _ptr(mask)
     n = a.shape[0]
     if out is None:
-        out = torch.empty(8, dtype=torch.float64, device=a.device)
+        out = _empty(stream, 8, dtype=torch.float64, device=a.device)
     _need(out, torch.float64, "out", 1)
     if out.numel() < 8:
         raise ValueError("out must hold 8 doubles")
     need = lib().rlk_consistency_stats_workspace_size(n)
     if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=a.device)
+        workspace = _empty(stream, max(16, need), dtype=torch.uint8, device=a.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_consistency_stats_async(_ptr(a), _ptr(b), mp, n, _ptr(out), _ptr(workspace),
                                              workspace.numel(), _stream(stream)),
@@ -378,14 +395,14 @@ def logprob_backward(h, W, targets, lse, grad_logp, inv_temp: float = 1.0, need_
     T, H, V = _check_inputs(h, W, targets)
     _need(lse, torch.float32, "lse", 1)
     _need(grad_logp, torch.float32, "grad_logp", 1)
-    gh = torch.empty((T, H), dtype=torch.float32, device=h.device) if need_h else None
+    gh = _empty(stream, (T, H), dtype=torch.float32, device=h.device) if need_h else None
     accumulate = grad_W is not None
     if need_W and grad_W is None:
-        grad_W = torch.empty((V, H), dtype=torch.float32, device=h.device)
+        grad_W = _empty(stream, (V, H), dtype=torch.float32, device=h.device)
     if grad_W is not None:
         _need(grad_W, torch.float32, "grad_W", 2)
     if workspace is None:
-        workspace = torch.empty(backward_workspace_size(T, H, V), dtype=torch.uint8, device=h.device)
+        workspace = _empty(stream, backward_workspace_size(T, H, V), dtype=torch.uint8, device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_backward(
         _ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(grad_logp), T, H, V,
@@ -443,10 +460,10 @@ def logprob_entropy(h, W, targets, inv_temp: float = 1.0, workspace=None, stream
     """rlk_logprob_entropy: returns (logp, lse, argmax, entropy)."""
     import torch
     T, H, V = _check_inputs(h, W, targets)
-    lp, lse, am = _outputs(T, h.device, None)
-    ent = torch.empty(T, dtype=torch.float32, device=h.device)
+    lp, lse, am = _outputs(T, h.device, None, stream)
+    ent = _empty(stream, T, dtype=torch.float32, device=h.device)
     if workspace is None:
-        workspace = torch.empty(max(1, entropy_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = _empty(stream, max(1, entropy_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_entropy(_ptr(h), _ptr(W), _ptr(targets), T, H, V,
@@ -468,7 +485,7 @@ def logprob_partials_shard(h, W_shard, targets, V: int, shard_begin: int, inv_te
     rows = W_shard.shape[0]
     nvt_s = (rows + vocab_tile() - 1) // vocab_tile()
     if out is None:
-        out = torch.empty((T, nvt_s, 4), dtype=torch.float32, device=h.device)
+        out = _empty(stream, (T, nvt_s, 4), dtype=torch.float32, device=h.device)
     _need(out, torch.float32, "out")
     _check(lib().rlk_logprob_partials_shard(_ptr(h), _ptr(W_shard), _ptr(targets), T, H, int(V),
                                             int(shard_begin), rows, ctypes.c_float(inv_temp),
@@ -485,7 +502,7 @@ def lse_merge_sharded(partials, targets, V: int, out=None, stream=None):
     R, T, nvt_s, four = partials.shape
     if four != 4 or targets.shape[0] != T:
         raise ValueError("partials must be [R, T, tiles_per_shard, 4] and targets [T]")
-    lp, lse, am = _outputs(T, partials.device, out)
+    lp, lse, am = _outputs(T, partials.device, out, stream)
     _check(lib().rlk_lse_merge_sharded(_ptr(partials), R, nvt_s, _ptr(targets), T, int(V),
                                        _ptr(lp), _ptr(lse), _ptr(am), _stream(stream)),
            "rlk_lse_merge_sharded")
@@ -497,8 +514,8 @@ def quantize_fp8_rows(x, stream=None):
     import torch
     _need(x, torch.bfloat16, "x", 2)
     rows, H = x.shape
-    codes = torch.empty((rows, H), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    codes = _empty(stream, (rows, H), dtype=torch.uint8, device=x.device)
+    scales = _empty(stream, rows, dtype=torch.float32, device=x.device)
     _check(lib().rlk_quantize_fp8_rows(_ptr(x), rows, H, _ptr(codes), _ptr(scales),
                                        _stream(stream)), "rlk_quantize_fp8_rows")
     return codes, scales
@@ -515,8 +532,8 @@ def quantize_fp8_weight(W, out=None, stream=None):
     _need(W, torch.bfloat16, "W", 2)
     V, H = W.shape
     if out is None:
-        packed = torch.empty(lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
-        scales = torch.empty(V, dtype=torch.float32, device=W.device)
+        packed = _empty(stream, lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
+        scales = _empty(stream, V, dtype=torch.float32, device=W.device)
     else:
         packed, scales = out
         _need(packed, torch.uint8, "packed", 1)
@@ -549,9 +566,9 @@ def logprob_fp8(h, W_packed, W_scales, targets, inv_temp: float = 1.0, workspace
     V = W_scales.shape[0]
     if W_packed.numel() < lib().rlk_fp8_weight_bytes(V, H) or targets.shape[0] != T:
         raise ValueError("W_packed must hold rlk_fp8_weight_bytes(V, H) bytes; targets [T]")
-    lp, lse, am = _outputs(T, h.device, out)
+    lp, lse, am = _outputs(T, h.device, out, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, fp8_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = _empty(stream, max(1, fp8_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_fp8(_ptr(h), _ptr(W_packed), _ptr(W_scales), _ptr(targets), T, H, V,
@@ -567,8 +584,8 @@ def quantize_fp8_row_blocks(x, stream=None):
     import torch
     _need(x, torch.bfloat16, "x", 2)
     rows, H = x.shape
-    codes = torch.empty((rows, H), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, max(1, H // 128)), dtype=torch.float32, device=x.device)
+    codes = _empty(stream, (rows, H), dtype=torch.uint8, device=x.device)
+    scales = _empty(stream, (rows, max(1, H // 128)), dtype=torch.float32, device=x.device)
     _check(lib().rlk_quantize_fp8_row_blocks(_ptr(x), rows, H, _ptr(codes), _ptr(scales),
                                              _stream(stream)), "rlk_quantize_fp8_row_blocks")
     return codes, scales
@@ -581,8 +598,8 @@ def quantize_fp8_weight_blocks(W, out=None, stream=None):
     _need(W, torch.bfloat16, "W", 2)
     V, H = W.shape
     if out is None:
-        packed = torch.empty(lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
-        scales = torch.empty(((V + 127) // 128, max(1, H // 128)), dtype=torch.float32,
+        packed = _empty(stream, lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
+        scales = _empty(stream, ((V + 127) // 128, max(1, H // 128)), dtype=torch.float32,
                              device=W.device)
     else:
         packed, scales = out
@@ -613,9 +630,9 @@ def logprob_fp8_block(h, W_packed, W_scales, targets, V: int, inv_temp: float = 
     if (W_packed.numel() < lib().rlk_fp8_weight_bytes(V, H) or targets.shape[0] != T or
             W_scales.numel() < lib().rlk_fp8_block_weight_scale_count(V, H)):
         raise ValueError("W_packed / W_scales too small for (V, H), or targets not [T]")
-    lp, lse, am = _outputs(T, h.device, out)
+    lp, lse, am = _outputs(T, h.device, out, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, fp8_block_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = _empty(stream, max(1, fp8_block_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_fp8_block(_ptr(h), _ptr(W_packed), _ptr(W_scales), _ptr(targets), T,
@@ -731,10 +748,11 @@ def token_logprobs(logits, targets, top_k: int = 0, allowed=None, inv_temp: floa
     if out is None:
         # (five allocations: views of one cost five times as much on the host)
         dev = logits.device
-        lp, lse, ent = (torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev),
-                        torch.empty(T, dtype=f32, device=dev))
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        top = torch.empty((T, top_k), dtype=f32, device=dev)
+        empty = torch.empty if stream is None else functools.partial(_empty, stream)
+        lp, lse, ent = (empty(T, dtype=f32, device=dev), empty(T, dtype=f32, device=dev),
+                        empty(T, dtype=f32, device=dev))
+        ids = empty((T, top_k), dtype=torch.int32, device=dev)
+        top = empty((T, top_k), dtype=f32, device=dev)
         addresses = (lp.data_ptr(), lse.data_ptr(), ent.data_ptr(), ids.data_ptr(), top.data_ptr())
     else:
         lp, lse, ent, ids, top = out
@@ -784,7 +802,7 @@ def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, 
         if grad_top.shape[0] != T or top_ids.shape != grad_top.shape or top_k > MAX_TOP_K:
             raise ValueError(f"top_ids and grad_top must be [T, top_k], top_k <= {MAX_TOP_K}")
     if out is None:
-        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        out = _empty(stream, (T, V), dtype=logits.dtype, device=logits.device)
         out_stride = V
     else:
         _, out_stride = call.rows(out, "out")
@@ -908,9 +926,9 @@ def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=
         raise ValueError("group must be 32, 64 or 128")
     G = (K + group - 1) // group
     if out is None:
-        codes = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
-        scales = torch.empty((N, G), dtype=W.dtype, device=W.device)
-        zeros = torch.empty((N, G), dtype=torch.uint8, device=W.device) if asymmetric else None
+        codes = _empty(stream, (N, K // 8), dtype=torch.int32, device=W.device)
+        scales = _empty(stream, (N, G), dtype=W.dtype, device=W.device)
+        zeros = _empty(stream, (N, G), dtype=torch.uint8, device=W.device) if asymmetric else None
     else:
         codes, scales, zeros = out
         if (zeros is not None) != bool(asymmetric):
@@ -930,7 +948,7 @@ def dequantize_w4(codes, scales, zeros=None, group: int = 128, out_dtype=None, o
     call = _Call()
     c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
     if out is None:
-        out = call.torch.empty((N, K), dtype=out_dtype or scales.dtype, device=codes.device)
+        out = _empty(stream, (N, K), dtype=out_dtype or scales.dtype, device=codes.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
@@ -954,7 +972,7 @@ def linear_w4(x, codes, scales, zeros=None, group: int = 128, out_dtype=None, ou
     if x.shape[1] != K:
         raise ValueError("shape mismatch: x [T, K], codes [N, K/8]")
     if out is None:
-        out = call.torch.empty((T, N), dtype=out_dtype or call.torch.float32, device=x.device)
+        out = _empty(stream, (T, N), dtype=out_dtype or call.torch.float32, device=x.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
