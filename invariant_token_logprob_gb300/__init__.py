@@ -412,6 +412,26 @@ def logprob_backward(h, W, targets, lse, grad_logp, inv_temp: float = 1.0, need_
     return gh, (grad_W if (need_W or accumulate) else None), workspace
 
 
+def _first_derivatives(grads, inputs):
+    """Gradients out of a kernel that autograd does not see.  Under create_graph they get a
+    node that refuses to be differentiated: without one they would count as constants.
+    (torch's once_differentiable adds its own only where the incoming gradient needs one.)"""
+    import torch
+    if not torch.is_grad_enabled():
+        return grads
+
+    class FirstDerivative(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, grad, *inputs):
+            return grad.view_as(grad)
+
+        @staticmethod
+        def backward(ctx, grad):
+            raise RuntimeError("this operator has first derivatives only: its gradient cannot be differentiated")
+
+    return [None if g is None else FirstDerivative.apply(g, *inputs) for g in grads]
+
+
 def _autograd_function():
     import torch
 
@@ -434,7 +454,8 @@ def _autograd_function():
                 return None, None, None, None
             gh, gW, _ = logprob_backward(h, W, targets, lse, grad_lp.contiguous().float(),
                                          ctx.inv_temp, need_h=need_h, need_W=need_W)
-            return (gh.to(h.dtype) if need_h else None, gW.to(W.dtype) if need_W else None,
+            return (*_first_derivatives([gh.to(h.dtype) if need_h else None,
+                                         gW.to(W.dtype) if need_W else None], [h, W, grad_lp]),
                     None, None)
 
     return SelectedTokenLogprob
@@ -445,7 +466,8 @@ _SelectedTokenLogprob = None
 
 def selected_token_logprob(h, W, targets, inv_temp: float = 1.0):
     """Differentiable selected-token logprob (torch autograd): the forward is the
-    batch-invariant kernel, the backward recomputes the logits on the same tiles."""
+    batch-invariant kernel, the backward recomputes the logits on the same tiles.  First
+    derivatives only."""
     global _SelectedTokenLogprob
     if _SelectedTokenLogprob is None:
         _SelectedTokenLogprob = _autograd_function()
@@ -839,10 +861,12 @@ def _token_logprobs_function():
                 return None, None, None, None, None
             if g_top is not None and g_top.shape[1] == 0:
                 g_top = None
-            return (token_logprobs_backward(logits, targets, lse, entropy, dense(g_logp),
-                                            dense(g_lse), dense(g_entropy),
-                                            None if g_top is None else ids, dense(g_top), allowed,
-                                            ctx.inv_temp), None, None, None, None)
+            grad = token_logprobs_backward(logits, targets, lse, entropy, dense(g_logp),
+                                           dense(g_lse), dense(g_entropy),
+                                           None if g_top is None else ids, dense(g_top), allowed,
+                                           ctx.inv_temp)
+            return (*_first_derivatives([grad], [logits, g_logp, g_lse, g_entropy, g_top]),
+                    None, None, None, None)
 
     return TokenLogprobsFunction
 
@@ -853,7 +877,7 @@ _TokenLogprobsFunction = None
 def differentiable_token_logprobs(logits, targets, top_k: int = 0, allowed=None,
                                   inv_temp: float = 1.0):
     """token_logprobs under torch autograd: logp, lse, entropy and top_logp carry
-    gradients to the logits (top_ids does not)."""
+    gradients to the logits (top_ids does not).  First derivatives only."""
     global _TokenLogprobsFunction
     if _TokenLogprobsFunction is None:
         _TokenLogprobsFunction = _token_logprobs_function()
