@@ -540,9 +540,10 @@ rlk_status rlk_token_logprobs(const void *logits, int dtype, int64_t row_stride,
  * p = exp(z - lse) and G = grad_logp + sum_j grad_top[j]:
  *   grad[v] = inv_temp * ( p[v] (grad_lse - G - grad_entropy (z[v] - lse + entropy))
  *                          + [v == target] grad_logp + sum_j [v == top_ids[j]] grad_top[j] )
- * computed in fp32 and rounded once; 0 for masked tokens and tokens at -inf, and in
- * rows without tokens.  The grad_logp of a row whose target lies outside [0, V) and
- * the grad_top of an id outside [0, V) count as 0.  Rows whose lse is NaN give NaN.
+ * computed in fp32 and rounded once; 0 for masked tokens and tokens at -inf, whatever
+ * the gradients that come in and the row's lse, and in rows without tokens.  The grad_logp
+ * of a row whose target lies outside [0, V) and the grad_top of an id outside [0, V) count
+ * as 0.  Rows whose lse is NaN give NaN at all other tokens.
  *   logits, targets_i32, allowed_u32, T, V, inv_temp: as given to rlk_token_logprobs
  *   lse_f32                           device, [T]: its output
  *   entropy_f32                       device, [T]: its output (NULL without grad_entropy_f32)

@@ -793,6 +793,10 @@ __global__ void __launch_bounds__(kThreads, 4)
     f.b = p.inv_temp * g_ent;
     f.a = p.inv_temp * ((p.g_lse ? p.g_lse[t] : 0.0f) - total - g_ent * H);
     const bool empty = f.lse == -INFINITY;
+    // A token at -inf (masked or not) has gradient 0.  Its p is 0, but 0 times a factor that is
+    // not finite would not be: rows whose factors reach fp32's end at the cut, or whose lse is
+    // NaN, compare each element, one by one as the rows without tokens.
+    const bool special = empty || !(fabsf(f.a) - kFarBelow * fabsf(f.b) <= FLT_MAX) || f.lse != f.lse;
 
     // Tokens of this part with a gradient of their own: lane j the j-th alternative (the
     // first of equal ids for all of them), lane 0 of warp 1 the target.
@@ -844,24 +848,27 @@ __global__ void __launch_bounds__(kThreads, 4)
                     if (kMasked) raw[i].keep(eight_bits(bits, e0));
                     float x[8];
                     f(raw[i], x);
-                    if (empty) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-                    }
                     store_eight(out + e0, x);
                 } else {
                     for (int j = 0; j < 8 && e0 + j < p.V; ++j)
-                        out[e0 + j] = from_float<Elem>(empty ? 0.0f : f(element(row, bits, e0 + j)));
+                        out[e0 + j] = from_float<Elem>(f(element(row, bits, e0 + j)));
                 }
             }
         }
     };
-    if (shift == 0)
-        body(std::false_type());
-    else
-        body(std::true_type());
-    if (part == 0 && threadIdx.x < min(head, p.V))
-        out[threadIdx.x] = from_float<Elem>(empty ? 0.0f : f(element(row, bits, threadIdx.x)));
+    if (special) {
+        for (int64_t e = int64_t(begin) + threadIdx.x; e < end; e += kThreads) {
+            const float x = empty ? -INFINITY : element(row, bits, e);
+            out[e] = from_float<Elem>(x == -INFINITY ? 0.0f : f(x));
+        }
+    } else {
+        if (shift == 0)
+            body(std::false_type());
+        else
+            body(std::true_type());
+        if (part == 0 && threadIdx.x < min(head, p.V))
+            out[threadIdx.x] = from_float<Elem>(f(element(row, bits, threadIdx.x)));
+    }
 
     if (p.top_k > 0 || own_target) {
         __syncthreads();

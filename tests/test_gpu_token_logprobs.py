@@ -560,3 +560,38 @@ def test_refusals():
     e = rlk.token_logprobs(x[:0], tg[:0], 3)
     assert e.logp.shape == (0,) and e.top_ids.shape == (0, 3)
     assert rlk.token_logprobs_backward(x[:0], tg[:0], ok.lse[:0]).shape == (0, 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V,pad,offset", [(33, 0, 0), (2049, 3, 1), (5008, 0, 0), (70003, 5, 3)])
+def test_backward_is_zero_at_missing_tokens_whatever_comes_in(V, pad, offset, dtype):
+    """Infinite and NaN gradients, factors that overflow, a NaN lse: masked tokens and tokens at
+    -inf stay 0; where the row itself is NaN every other token is."""
+    import invariant_token_logprob_gb300 as rlk
+    T = 9
+    x, tg, keep = make(T, V, dtype, V, masked=True, pad=pad, offset=offset)
+    g = torch.Generator().manual_seed(V)
+    gone = (torch.rand(T, V, generator=g) < 0.2)
+    gone[:, 0] = False
+    keep[:, 0] = True
+    keep[T // 2] = False
+    x.masked_fill_(gone.cuda(), -math.inf)
+    x[7, 0] = math.nan  # allowed: the row is NaN
+    tg[1] = 0
+    bits = bits_of(keep)
+    r = rlk.token_logprobs(x, tg, 3, bits)
+    inf, nan, big = math.inf, math.nan, 3e38
+    c = dict(grad_logp=torch.tensor([inf, nan, 1, 1, inf, -inf, 1, 1, big]),
+             grad_lse=torch.tensor([0.0, 0, 0, inf, nan, 0, 1, 1, -big]),
+             grad_entropy=torch.tensor([0.0, 0, big, 0, inf, nan, 1, 1, 1e37]),
+             grad_top=torch.zeros(T, 3))
+    c["grad_top"][6, 0] = nan
+    c = {n: v.cuda() for n, v in c.items()}
+    got = rlk.token_logprobs_backward(x, tg, r.lse, r.entropy, top_ids=r.top_ids, allowed=bits, **c)
+    missing = gone | ~keep
+    assert bool((got.cpu()[missing] == 0).all())
+    assert bool(missing[T // 2].all())  # (a row without tokens)
+    for row in (1, 5, 6, 7):
+        assert bool(torch.isnan(got[row].cpu()[~missing[row]]).all()), row
+    rlk.token_logprobs_backward(x, tg, r.lse, r.entropy, top_ids=r.top_ids, allowed=bits, out=x, **c)
+    assert torch.equal(torch.isnan(x), torch.isnan(got)) and torch.equal(torch.nan_to_num(x), torch.nan_to_num(got))
