@@ -512,8 +512,11 @@ typedef enum rlk_dtype { RLK_BF16 = 0, RLK_FP16 = 1, RLK_FP32 = 2 } rlk_dtype;
  * an alternative; places left over hold id -1 and logp -inf.  A target that is
  * such a token has logp -inf.  A row without tokens has lse -inf, entropy 0 and
  * logp -inf.  A target outside [0, V) has logp 0.0f, and one >= V is counted as by
- * rlk_logprob.  A NaN or +inf logit that is not masked makes its row's floats NaN
- * (its alternatives are those of the tokens that are not NaN).
+ * rlk_logprob.  A NaN or +inf logit that is not masked makes its row's floats NaN, but
+ * for the -inf and 0.0f that these rules give to a missing target, to places left over
+ * and to a target outside [0, V) (its alternatives are those of the tokens that are not
+ * NaN).  A row whose z all lie below fp32's range counts as a row without tokens in its
+ * floats.
  *   logits      device, [T][V] of `dtype` (rlk_dtype), row t at element t * row_stride
  *               (row_stride >= V; not read for T == 1), aligned to its element
  *   targets_i32 device, [T]

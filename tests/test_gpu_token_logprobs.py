@@ -595,3 +595,26 @@ def test_backward_is_zero_at_missing_tokens_whatever_comes_in(V, pad, offset, dt
         assert bool(torch.isnan(got[row].cpu()[~missing[row]]).all()), row
     rlk.token_logprobs_backward(x, tg, r.lse, r.entropy, top_ids=r.top_ids, allowed=bits, out=x, **c)
     assert torch.equal(torch.isnan(x), torch.isnan(got)) and torch.equal(torch.nan_to_num(x), torch.nan_to_num(got))
+
+
+def test_special_targets_in_special_rows():
+    """In a row that a NaN makes NaN, a missing target keeps -inf, an ignored one 0 and places
+    left over -inf; rows at the type's lowest value whose z leave fp32 count as empty."""
+    import invariant_token_logprob_gb300 as rlk
+    V = 300
+    x = torch.randn(5, V, generator=torch.Generator().manual_seed(1))
+    keep = torch.ones(5, V, dtype=torch.bool)
+    x[:4, 7] = math.nan
+    keep[:4, 9:] = False
+    x[1, 3] = -math.inf
+    x[4] = torch.finfo(torch.float32).min
+    tg = torch.tensor([200, 3, -1, 2, 5], dtype=torch.int32)
+    r = [a.cpu() for a in call(x.cuda(), tg.cuda(), 12, keep, 2.0)]
+    logp, lse, entropy, ids, top = r
+    assert torch.isnan(lse[:4]).all() and torch.isnan(entropy[:4]).all()
+    assert logp[0] == -math.inf and logp[1] == -math.inf and logp[2] == 0 and torch.isnan(logp[3])
+    for t, n in ((0, 8), (1, 7), (2, 8), (3, 8)):  # the tokens that are not NaN
+        assert bool((ids[t, :n] >= 0).all()) and bool(torch.isnan(top[t, :n]).all())
+        assert bool((ids[t, n:] == -1).all()) and bool((top[t, n:] == -math.inf).all())
+    assert lse[4] == -math.inf and entropy[4] == 0 and logp[4] == -math.inf
+    assert ids[4].tolist() == list(range(12)) and bool((top[4] == -math.inf).all())
