@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<kShifted>)
     const Elem* row = static_cast<const Elem*>(p.logits) + t * p.row_stride;
     const uint8_t* bits =
         kMasked ? reinterpret_cast<const uint8_t*>(p.allowed + t * p.allowed_stride) : nullptr;
-    const float c2 = p.inv_temp * kLog2e;
+    // (below infinity, as 0 times it has to be 0; what the limit cuts off only logits that
+    // differ by less than 1e-36 could tell)
+    const float c2 = fminf(p.inv_temp * kLog2e, FLT_MAX);
     const int shift = kShifted ? row_shift(row) : 0;
     if (ranks > 1) cluster_arrive_relaxed();  // every CTA runs before another writes to it
     int32_t target = -1;

@@ -618,3 +618,32 @@ def test_special_targets_in_special_rows():
         assert bool((ids[t, n:] == -1).all()) and bool((top[t, n:] == -math.inf).all())
     assert lse[4] == -math.inf and entropy[4] == 0 and logp[4] == -math.inf
     assert ids[4].tolist() == list(range(12)) and bool((top[4] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [5, 257, 40001])
+def test_forward_at_the_ends_of_inv_temp(V, dtype):
+    """A temperature near 0 leaves the largest logit's tokens, equally likely; one near fp32's
+    largest value leaves a uniform row."""
+    T = 3
+    x = (torch.arange(V) * 37 % V % 64).float().repeat(T, 1)
+    x[1] *= -1
+    x[2] += 0.5
+    x = x.to(DTYPES[dtype])
+    tg = torch.tensor([0, 0, int(x[2].float().argmax())], dtype=torch.int32)
+    for it in (1e30, 2.3e38, 2.5e38, 3.4e38):
+        got = [a.cpu() for a in call(x.cuda(), tg.cuda(), 2, None, it)]
+        best = x.float().amax(1, keepdim=True)
+        n = (x.float() == best).sum(1)
+        logn = torch.log(n.double()).float()
+        hit = (x.float() == best)[torch.arange(T), tg.long()]
+        assert torch.allclose(got[2], logn, atol=1e-5), (it, got[2], logn)
+        assert torch.allclose(got[0][hit], -logn[hit], atol=1e-5), it
+        assert bool((got[0][~hit] < -1e25).all())
+        assert not torch.isnan(got[4]).any() and torch.allclose(got[4][:, 0], -logn, atol=1e-5)
+        assert not torch.isnan(got[1]).any()
+    for it in (1e-44, 1e-39, 1e-36):
+        got = [a.cpu() for a in call(x.cuda(), tg.cuda(), 2, None, it)]
+        want = math.log(V)
+        for a, w in ((got[0], -want), (got[1], want), (got[2], want), (got[4][:, 0], -want)):
+            assert torch.allclose(a, torch.full_like(a, w), atol=1e-4, rtol=1e-5), (it, a, w)
