@@ -32,6 +32,8 @@
 #include <float.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "rlk_logits.cuh"
 #include "rlk_logits_w4.h"
 #include "rlk_lse.cuh"
@@ -909,16 +911,17 @@ cudaError_t launch_token_logprobs(const void* logits, ElemType type, int64_t row
         ranks /= 2;
     auto go = [&](auto kernel, int slots, int which) {
         const int smem = kSharedBytes + slots;
-        static uint8_t configured[64];  // per device: the kernels that may have that much
+        // per device: the kernels that may have that much
+        static std::atomic<uint8_t> configured[64];
         if (slots > 0) {
             int dev = 0;
             cudaError_t e = cudaGetDevice(&dev);
             if (e != cudaSuccess) return e;
             if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-            if (!(configured[dev] >> which & 1)) {
+            if (!(configured[dev].load() >> which & 1)) {
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
                 if (e != cudaSuccess) return e;
-                configured[dev] |= uint8_t(1 << which);
+                configured[dev].fetch_or(uint8_t(1 << which));
             }
         }
         cudaLaunchConfig_t cfg = {};

@@ -40,6 +40,8 @@
 // x is one column of D.  So a row's bits do not depend on T.
 //
 // Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
+#include <atomic>
+
 #include "rlk_logits.cuh"
 #include "rlk_logits_w4.h"
 #include "rlk_ptx.cuh"
@@ -628,15 +630,15 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, 
                    cudaStream_t stream) {
     auto kernel = linear_w4_kernel<Elem, Out, kCols, kGroups, kZeros>;
     constexpr size_t smem = smem_bytes(kCols, kGroups);
-    static int configured[64];  // per device
+    static std::atomic<int> configured[64];  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
+    if (!configured[dev].load()) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
-        configured[dev] = 1;
+        configured[dev].store(1);
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
