@@ -647,3 +647,82 @@ def test_forward_at_the_ends_of_inv_temp(V, dtype):
         want = math.log(V)
         for a, w in ((got[0], -want), (got[1], want), (got[2], want), (got[4][:, 0], -want)):
             assert torch.allclose(a, torch.full_like(a, w), atol=1e-4, rtol=1e-5), (it, a, w)
+
+
+@pytest.mark.parametrize("V,dtype", [(151936, "fp32"), (600000, "fp32"), (151936, "bf16"), (300001, "fp16")])
+@pytest.mark.parametrize("order", ["up", "down", "any", "equal"])
+def test_many_candidates_where_one_lane_reads_them(V, dtype, order):
+    """Strip s gives its lane l the elements 256 s + 8 l + 16384 n + (0..7): all large logits lie
+    in one lane's place, in one strip's, or in the same lanes of all strips, where every token
+    is a candidate, more than the lists hold; in rows for one CTA and for clusters."""
+    i = torch.arange(V)
+    strip, lane = i // 256 % 64, i // 8 % 32
+    places = [(strip == 3) & (lane == 9), strip == 0, (strip == 62) | (strip == 17), lane == 31,
+              (strip < 40) & (lane < 7)]
+    x = torch.zeros(len(places), V)
+    g = torch.Generator().manual_seed(V)
+    for r, p in enumerate(places):
+        n = int(p.sum())
+        step = {"up": torch.arange(n), "down": -torch.arange(n), "any": torch.randperm(n, generator=g),
+                "equal": torch.zeros(n, dtype=torch.long)}[order]
+        x[r, p] = 4.0 + step.float() * (4.0 / n)
+    x = x.to(DTYPES[dtype])
+    tg = torch.zeros(len(places), dtype=torch.int32)
+    ref = ref_forward(x.double().numpy(), tg.numpy(), 1.0, 32)
+    for copies in (1, 8, 40):  # clusters of eight down to one CTA per row
+        got = call(x.cuda().repeat(copies, 1), tg.cuda().repeat(copies), 32, None, 1.0)
+        for c in {0, copies - 1}:
+            rows = slice(c * len(places), (c + 1) * len(places))
+            check_forward([a[rows] for a in got], ref, V, 1.0, f"{V} {dtype} {order} {copies}")
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.element_size() == 4 else torch.int16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [151936, 32761])
+def test_masked_row_bits_and_gradient_bits_do_not_depend_on_the_batch(V, dtype):
+    """Masked rows, and the gradient of all outputs: the same rows alone, in other batches, at
+    other alignments and strides, of the logits and of the gradient, and in place."""
+    import invariant_token_logprob_gb300 as rlk
+    T, top_k = 320, 8
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(T, V, generator=g, device="cuda") * 3).to(DTYPES[dtype])
+    x[5, ::3] = -math.inf
+    tg = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    allowed = torch.randint(-2 ** 31, 2 ** 31 - 1, (T, (V + 31) // 32), generator=g, device="cuda", dtype=torch.int32)
+    allowed[T - 3] = 0
+    allowed[T - 4] = 1 << 5
+    c = {n: v.cuda() for n, v in grads(T, top_k, 3).items()}
+
+    def grad(r, logits, sl, mask, **kw):
+        return rlk.token_logprobs_backward(
+            logits, tg[sl], r.lse, r.entropy, grad_logp=c["logp"][sl], grad_lse=c["lse"][sl], grad_entropy=c["entropy"][sl],
+            top_ids=r.top_ids, grad_top=c["top"][sl], allowed=mask, inv_temp=IT, **kw)
+
+    for mask in (allowed, None):
+        full = rlk.token_logprobs(x, tg, top_k, mask, IT)
+        full_grad = grad(full, x, slice(0, T), mask)
+        for n in (1, 2, 3, 7, 19, 38, 39, 76, 153, 304):
+            sl = slice(T - n, T)
+            part = None if mask is None else mask[sl]
+            r = rlk.token_logprobs(x[sl], tg[sl], top_k, part, IT)
+            for a, b in zip(r, full):
+                assert torch.equal(bits(a), bits(b[sl])), (n, "forward")
+            assert torch.equal(bits(grad(r, x[sl], sl, part)), bits(full_grad[sl])), (n, "gradient")
+        sl = slice(T - 5, T)
+        part = None if mask is None else mask[sl]
+        for off_in, off_out in ((0, 1), (1, 0), (3, 5), (7, 7), (2, 6)):
+            buf = torch.empty(5, V + 9, dtype=x.dtype, device="cuda")
+            view = buf[:, off_in:off_in + V]
+            view.copy_(x[sl])
+            r = rlk.token_logprobs(view, tg[sl], top_k, part, IT)
+            for a, b in zip(r, full):
+                assert torch.equal(bits(a), bits(b[sl])), (off_in, "forward")
+            out = torch.empty(5, V + 11, dtype=x.dtype, device="cuda")[:, off_out:off_out + V]
+            grad(r, view, sl, part, out=out)
+            assert torch.equal(bits(out), bits(full_grad[sl])), (off_in, off_out, "gradient")
+            grad(r, view, sl, part, out=view)
+            assert torch.equal(bits(view), bits(full_grad[sl])), (off_in, "in place")
+    rlk.check_device_error()
