@@ -195,19 +195,23 @@ def _need(t, dtype, name, ndim=None):
 
 
 def _empty(stream, *size, **kw):
-    """torch.empty in memory that belongs to `stream` (None: the current one), and that is not
-    handed on either before work queued on the current stream by then is through with it.  A
-    block of the current stream's may still be in use by work queued there when `stream` writes
-    to it, and a temporary would go to that stream's next work while `stream` still uses it."""
+    """torch.empty in memory that belongs to `stream`, and that is not handed on either before
+    work queued on the current stream by then is through with it.  A block of the current
+    stream's may still be in use by work queued there when `stream` writes to it, and a
+    temporary would go to that stream's next work while `stream` still uses it."""
     import torch
-    if stream is None:
-        return torch.empty(*size, **kw)
     with torch.cuda.stream(stream):
         t = torch.empty(*size, **kw)
-    current = torch.cuda.current_stream()
-    if current != stream:
-        t.record_stream(current)
+    t.record_stream(torch.cuda.current_stream())
     return t
+
+
+def _allocator(stream):
+    """For a given stream: torch.empty if it is the current one, else _empty for it."""
+    import torch
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()):
+        return torch.empty
+    return functools.partial(_empty, stream)
 
 
 def row_tile() -> int:
@@ -236,10 +240,11 @@ def _check_inputs(h, W, targets):
 
 def _outputs(T, device, out, stream):
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     if out is None:
-        return (_empty(stream, T, dtype=torch.float32, device=device),
-                _empty(stream, T, dtype=torch.float32, device=device),
-                _empty(stream, T, dtype=torch.int32, device=device))
+        return (empty(T, dtype=torch.float32, device=device),
+                empty(T, dtype=torch.float32, device=device),
+                empty(T, dtype=torch.int32, device=device))
     lp, lse, am = out
     _need(lp, torch.float32, "out[0]", 1)
     _need(lse, torch.float32, "out[1]", 1)
@@ -272,10 +277,11 @@ def logprob_partials(h, W, targets, inv_temp: float = 1.0, out=None, stream=None
     """rlk_logprob_partials: returns a float32 tensor [T, NVT, 4] of {m, s, a-bits, zt}
     (view column 2 as int32 for the argmax)."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     T, H, V = _check_inputs(h, W, targets)
     nvt = (V + vocab_tile() - 1) // vocab_tile()
     if out is None:
-        out = _empty(stream, (T, nvt, 4), dtype=torch.float32, device=h.device)
+        out = empty((T, nvt, 4), dtype=torch.float32, device=h.device)
     _need(out, torch.float32, "out")
     _check(lib().rlk_logprob_partials(_ptr(h), _ptr(W), _ptr(targets), T, H, V,
                                       ctypes.c_float(inv_temp), _ptr(out),
@@ -323,6 +329,7 @@ def consistency_stats_async(a, b, mask=None, out=None, workspace=None, stream=No
     float64 CUDA tensor of 8 (returned; pass `out` to reuse one).  No host sync and no
     allocation inside the library; read it with stats_dict() when needed."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(a, torch.float32, "a", 1)
     _need(b, torch.float32, "b", 1)
     if a.shape != b.shape:
@@ -335,13 +342,13 @@ def consistency_stats_async(a, b, mask=None, out=None, workspace=None, stream=No
         mp = _ptr(mask)
     n = a.shape[0]
     if out is None:
-        out = _empty(stream, 8, dtype=torch.float64, device=a.device)
+        out = empty(8, dtype=torch.float64, device=a.device)
     _need(out, torch.float64, "out", 1)
     if out.numel() < 8:
         raise ValueError("out must hold 8 doubles")
     need = lib().rlk_consistency_stats_workspace_size(n)
     if workspace is None:
-        workspace = _empty(stream, max(16, need), dtype=torch.uint8, device=a.device)
+        workspace = empty(max(16, need), dtype=torch.uint8, device=a.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_consistency_stats_async(_ptr(a), _ptr(b), mp, n, _ptr(out), _ptr(workspace),
                                              workspace.numel(), _stream(stream)),
@@ -392,17 +399,18 @@ def logprob_backward(h, W, targets, lse, grad_logp, inv_temp: float = 1.0, need_
     workspace).  Pass grad_W to accumulate into it.  dz (bf16 [T,V]) is left in the
     workspace afterwards: backward_dz(workspace, T, V)."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     T, H, V = _check_inputs(h, W, targets)
     _need(lse, torch.float32, "lse", 1)
     _need(grad_logp, torch.float32, "grad_logp", 1)
-    gh = _empty(stream, (T, H), dtype=torch.float32, device=h.device) if need_h else None
+    gh = empty((T, H), dtype=torch.float32, device=h.device) if need_h else None
     accumulate = grad_W is not None
     if need_W and grad_W is None:
-        grad_W = _empty(stream, (V, H), dtype=torch.float32, device=h.device)
+        grad_W = empty((V, H), dtype=torch.float32, device=h.device)
     if grad_W is not None:
         _need(grad_W, torch.float32, "grad_W", 2)
     if workspace is None:
-        workspace = _empty(stream, backward_workspace_size(T, H, V), dtype=torch.uint8, device=h.device)
+        workspace = empty(backward_workspace_size(T, H, V), dtype=torch.uint8, device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_backward(
         _ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(grad_logp), T, H, V,
@@ -481,11 +489,12 @@ def entropy_workspace_size(T: int, H: int, V: int) -> int:
 def logprob_entropy(h, W, targets, inv_temp: float = 1.0, workspace=None, stream=None):
     """rlk_logprob_entropy: returns (logp, lse, argmax, entropy)."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     T, H, V = _check_inputs(h, W, targets)
     lp, lse, am = _outputs(T, h.device, None, stream)
-    ent = _empty(stream, T, dtype=torch.float32, device=h.device)
+    ent = empty(T, dtype=torch.float32, device=h.device)
     if workspace is None:
-        workspace = _empty(stream, max(1, entropy_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = empty(max(1, entropy_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_entropy(_ptr(h), _ptr(W), _ptr(targets), T, H, V,
@@ -500,6 +509,7 @@ def logprob_partials_shard(h, W_shard, targets, V: int, shard_begin: int, inv_te
     """rlk_logprob_partials_shard: partials [T, ceil(rows/vocab_tile), 4] of one
     vocabulary shard W_shard = W[shard_begin : shard_begin + rows]."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(h, torch.bfloat16, "h", 2)
     _need(W_shard, torch.bfloat16, "W_shard", 2)
     _need(targets, torch.int32, "targets", 1)
@@ -507,7 +517,7 @@ def logprob_partials_shard(h, W_shard, targets, V: int, shard_begin: int, inv_te
     rows = W_shard.shape[0]
     nvt_s = (rows + vocab_tile() - 1) // vocab_tile()
     if out is None:
-        out = _empty(stream, (T, nvt_s, 4), dtype=torch.float32, device=h.device)
+        out = empty((T, nvt_s, 4), dtype=torch.float32, device=h.device)
     _need(out, torch.float32, "out")
     _check(lib().rlk_logprob_partials_shard(_ptr(h), _ptr(W_shard), _ptr(targets), T, H, int(V),
                                             int(shard_begin), rows, ctypes.c_float(inv_temp),
@@ -534,10 +544,11 @@ def lse_merge_sharded(partials, targets, V: int, out=None, stream=None):
 def quantize_fp8_rows(x, stream=None):
     """rlk_quantize_fp8_rows: bf16 [rows, H] -> (e4m3 codes as uint8 [rows, H], f32 scales [rows])."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(x, torch.bfloat16, "x", 2)
     rows, H = x.shape
-    codes = _empty(stream, (rows, H), dtype=torch.uint8, device=x.device)
-    scales = _empty(stream, rows, dtype=torch.float32, device=x.device)
+    codes = empty((rows, H), dtype=torch.uint8, device=x.device)
+    scales = empty(rows, dtype=torch.float32, device=x.device)
     _check(lib().rlk_quantize_fp8_rows(_ptr(x), rows, H, _ptr(codes), _ptr(scales),
                                        _stream(stream)), "rlk_quantize_fp8_rows")
     return codes, scales
@@ -551,11 +562,12 @@ def quantize_fp8_weight(W, out=None, stream=None):
     """rlk_quantize_fp8_weight: bf16 W [V, H] -> (tile-packed e4m3 codes as a flat uint8
     tensor, f32 scales [V]).  Pass out=(packed, scales) to reuse buffers."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(W, torch.bfloat16, "W", 2)
     V, H = W.shape
     if out is None:
-        packed = _empty(stream, lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
-        scales = _empty(stream, V, dtype=torch.float32, device=W.device)
+        packed = empty(lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
+        scales = empty(V, dtype=torch.float32, device=W.device)
     else:
         packed, scales = out
         _need(packed, torch.uint8, "packed", 1)
@@ -580,6 +592,7 @@ def logprob_fp8(h, W_packed, W_scales, targets, inv_temp: float = 1.0, workspace
     """rlk_logprob_fp8: (logp, lse, argmax) from bf16 h and a tile-packed e4m3 W
     (from quantize_fp8_weight); V = len(W_scales)."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(h, torch.bfloat16, "h", 2)
     _need(W_packed, torch.uint8, "W_packed", 1)
     _need(W_scales, torch.float32, "W_scales", 1)
@@ -590,7 +603,7 @@ def logprob_fp8(h, W_packed, W_scales, targets, inv_temp: float = 1.0, workspace
         raise ValueError("W_packed must hold rlk_fp8_weight_bytes(V, H) bytes; targets [T]")
     lp, lse, am = _outputs(T, h.device, out, stream)
     if workspace is None:
-        workspace = _empty(stream, max(1, fp8_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = empty(max(1, fp8_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_fp8(_ptr(h), _ptr(W_packed), _ptr(W_scales), _ptr(targets), T, H, V,
@@ -604,10 +617,11 @@ def quantize_fp8_row_blocks(x, stream=None):
     """rlk_quantize_fp8_row_blocks: bf16 [rows, H] -> (e4m3 codes uint8 [rows, H], f32
     scales [rows, H/128]) in 1 x 128 blocks."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(x, torch.bfloat16, "x", 2)
     rows, H = x.shape
-    codes = _empty(stream, (rows, H), dtype=torch.uint8, device=x.device)
-    scales = _empty(stream, (rows, max(1, H // 128)), dtype=torch.float32, device=x.device)
+    codes = empty((rows, H), dtype=torch.uint8, device=x.device)
+    scales = empty((rows, max(1, H // 128)), dtype=torch.float32, device=x.device)
     _check(lib().rlk_quantize_fp8_row_blocks(_ptr(x), rows, H, _ptr(codes), _ptr(scales),
                                              _stream(stream)), "rlk_quantize_fp8_row_blocks")
     return codes, scales
@@ -617,11 +631,12 @@ def quantize_fp8_weight_blocks(W, out=None, stream=None):
     """rlk_quantize_fp8_weight_blocks: bf16 W [V, H] -> (tile-packed e4m3 codes, flat
     uint8; f32 scales [ceil(V/128), H/128]) in 128 x 128 blocks."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(W, torch.bfloat16, "W", 2)
     V, H = W.shape
     if out is None:
-        packed = _empty(stream, lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
-        scales = _empty(stream, ((V + 127) // 128, max(1, H // 128)), dtype=torch.float32,
+        packed = empty(lib().rlk_fp8_weight_bytes(V, H), dtype=torch.uint8, device=W.device)
+        scales = empty(((V + 127) // 128, max(1, H // 128)), dtype=torch.float32,
                              device=W.device)
     else:
         packed, scales = out
@@ -644,6 +659,7 @@ def logprob_fp8_block(h, W_packed, W_scales, targets, V: int, inv_temp: float = 
     """rlk_logprob_fp8_block: (logp, lse, argmax) from bf16 h and a block-quantised
     tile-packed e4m3 W with its [ceil(V/128), H/128] block scales."""
     import torch
+    empty = torch.empty if stream is None else _allocator(stream)
     _need(h, torch.bfloat16, "h", 2)
     _need(W_packed, torch.uint8, "W_packed", 1)
     _need(W_scales, torch.float32, "W_scales")
@@ -654,7 +670,7 @@ def logprob_fp8_block(h, W_packed, W_scales, targets, V: int, inv_temp: float = 
         raise ValueError("W_packed / W_scales too small for (V, H), or targets not [T]")
     lp, lse, am = _outputs(T, h.device, out, stream)
     if workspace is None:
-        workspace = _empty(stream, max(1, fp8_block_workspace_size(T, H, V)), dtype=torch.uint8,
+        workspace = empty(max(1, fp8_block_workspace_size(T, H, V)), dtype=torch.uint8,
                                 device=h.device)
     _need(workspace, torch.uint8, "workspace", 1)
     _check(lib().rlk_logprob_fp8_block(_ptr(h), _ptr(W_packed), _ptr(W_scales), _ptr(targets), T,
@@ -770,7 +786,7 @@ def token_logprobs(logits, targets, top_k: int = 0, allowed=None, inv_temp: floa
     if out is None:
         # (five allocations: views of one cost five times as much on the host)
         dev = logits.device
-        empty = torch.empty if stream is None else functools.partial(_empty, stream)
+        empty = torch.empty if stream is None else _allocator(stream)
         lp, lse, ent = (empty(T, dtype=f32, device=dev), empty(T, dtype=f32, device=dev),
                         empty(T, dtype=f32, device=dev))
         ids = empty((T, top_k), dtype=torch.int32, device=dev)
@@ -801,6 +817,7 @@ def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, 
     with grad_top).  out may be a tensor to fill, `logits` itself included."""
     call = _Call()
     torch = call.torch
+    empty = torch.empty if stream is None else _allocator(stream)
     args, T, V = _logits_args(call, logits, targets, allowed)
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
@@ -824,7 +841,7 @@ def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, 
         if grad_top.shape[0] != T or top_ids.shape != grad_top.shape or top_k > MAX_TOP_K:
             raise ValueError(f"top_ids and grad_top must be [T, top_k], top_k <= {MAX_TOP_K}")
     if out is None:
-        out = _empty(stream, (T, V), dtype=logits.dtype, device=logits.device)
+        out = empty((T, V), dtype=logits.dtype, device=logits.device)
         out_stride = V
     else:
         _, out_stride = call.rows(out, "out")
@@ -940,6 +957,7 @@ def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=
     out=(codes, scales, zeros) to reuse tensors."""
     call = _Call()
     torch = call.torch
+    empty = torch.empty if stream is None else _allocator(stream)
     if not isinstance(W, torch.Tensor) or _dtype_code(W.dtype) not in (0, 1):
         raise TypeError("W must be a bfloat16 or float16 tensor")
     w = call.arg(W, W.dtype, "W", 2)
@@ -950,9 +968,9 @@ def quantize_w4(W, group: int = 128, asymmetric: bool = False, out=None, stream=
         raise ValueError("group must be 32, 64 or 128")
     G = (K + group - 1) // group
     if out is None:
-        codes = _empty(stream, (N, K // 8), dtype=torch.int32, device=W.device)
-        scales = _empty(stream, (N, G), dtype=W.dtype, device=W.device)
-        zeros = _empty(stream, (N, G), dtype=torch.uint8, device=W.device) if asymmetric else None
+        codes = empty((N, K // 8), dtype=torch.int32, device=W.device)
+        scales = empty((N, G), dtype=W.dtype, device=W.device)
+        zeros = empty((N, G), dtype=torch.uint8, device=W.device) if asymmetric else None
     else:
         codes, scales, zeros = out
         if (zeros is not None) != bool(asymmetric):
@@ -970,9 +988,10 @@ def dequantize_w4(codes, scales, zeros=None, group: int = 128, out_dtype=None, o
     """rlk_dequantize_w4: the values a 4-bit weight stands for, [N, K] as the scales' type
     (default) or float32."""
     call = _Call()
+    empty = call.torch.empty if stream is None else _allocator(stream)
     c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
     if out is None:
-        out = _empty(stream, (N, K), dtype=out_dtype or scales.dtype, device=codes.device)
+        out = empty((N, K), dtype=out_dtype or scales.dtype, device=codes.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
@@ -990,13 +1009,14 @@ def linear_w4(x, codes, scales, zeros=None, group: int = 128, out_dtype=None, ou
     y that type or float32 (out_dtype, default float32).  x, codes and scales start at
     16-byte boundaries, zeros at a 4-byte one."""
     call = _Call()
+    empty = call.torch.empty if stream is None else _allocator(stream)
     c, s, z, code, N, K = _w4_args(call, codes, scales, zeros, group)
     a = call.arg(x, scales.dtype, "x", 2)
     T = x.shape[0]
     if x.shape[1] != K:
         raise ValueError("shape mismatch: x [T, K], codes [N, K/8]")
     if out is None:
-        out = _empty(stream, (T, N), dtype=out_dtype or call.torch.float32, device=x.device)
+        out = empty((T, N), dtype=out_dtype or call.torch.float32, device=x.device)
     out_code = _dtype_code(out.dtype)
     if out_code not in (code, 2):
         raise TypeError("out_dtype must be the scales' type or float32")
