@@ -555,7 +555,8 @@ rlk_status rlk_token_logprobs(const void *logits, int dtype, int64_t row_stride,
  *                                     its top_logp (NULL for top_k == 0)
  *   out_grad                          device, [T][V] of `dtype`, row t at element
  *                                     t * grad_stride (>= V); may be `logits` itself
- *                                     with the same stride
+ *                                     with the same stride, and must not share elements
+ *                                     with it otherwise
  * Asynchronous on `stream`; allocates nothing.
  */
 rlk_status rlk_token_logprobs_backward(const void *logits, int dtype, int64_t row_stride,

@@ -814,7 +814,8 @@ def token_logprobs_backward(logits, targets, lse, entropy=None, grad_logp=None, 
     """rlk_token_logprobs_backward: the gradient with respect to the logits ([T, V] of
     their type) from those of token_logprobs' outputs (f32, each may be None).  lse and
     entropy are its outputs (entropy is needed with grad_entropy), top_ids its ids (needed
-    with grad_top).  out may be a tensor to fill, `logits` itself included."""
+    with grad_top).  out may be a tensor to fill: `logits` itself, or one that shares no
+    elements with it."""
     call = _Call()
     torch = call.torch
     empty = torch.empty if stream is None else _allocator(stream)

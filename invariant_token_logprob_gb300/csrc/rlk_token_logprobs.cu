@@ -26,9 +26,9 @@
 // that reach it, hardly more, are ranked by counting.
 //
 // The pass is bound by the reads of the logits where rows are many (T = 4096, V = 151936,
-// bf16: 205 us, 6.1 TB/s; with 20 alternatives 249 us; T = 1024, fp32: 94 us, 6.6 TB/s),
-// by the latency of its steps where they are few (T = 1, fp32, 20 alternatives: 8.5 us).
-// The gradient reads and writes each logit once (T = 4096, bf16: 366 us, 6.8 TB/s).
+// bf16: 206 us, 6.0 TB/s; with 20 alternatives 249 us; T = 1024, fp32: 95 us, 6.6 TB/s),
+// by the latency of its steps where they are few (T = 1, fp32, 20 alternatives: 8.4 us).
+// The gradient reads and writes each logit once (T = 4096, bf16: 361 us, 6.9 TB/s).
 #include <float.h>
 #include <limits.h>
 

@@ -15,10 +15,12 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t s
     return r;
 }
 
-// Eight codes as pairs of numbers kUnit (q - z) in 16 bits, exactly.  A code in the low places of a constant's pattern adds its value to the constant:
-// the multiply-add that subtracts the constant and the zero point brings the unit along.  A
-// code four places higher needs no shift: fp16's 1024 has room for it too (16 q), and in
-// bf16 the bare bits are a subnormal number, 16 q * 2^-133, that 2^127 brings to q / 4.  So a
+// Eight codes as pairs of numbers kUnit (q - z) in 16 bits, exactly.  A code in the low places
+// of a constant's pattern adds its value to the constant: the multiply-add that subtracts the
+// constant and the zero point brings the unit along.  A code four places higher needs no shift:
+// fp16's 1024 has room for it too (16 q).  (For fp16, with the even codes apart from the odd
+// ones, a published method: Y. J. Kim et al., Who Says Elephants Can't Run, 2022.)  In bf16
+// the bare bits are a subnormal number, 16 q * 2^-133, that 2^127 brings to q / 4.  So a
 // word takes one shift and four cuts; the integer pipe's time goes into nothing else.
 template <typename Elem>
 struct Numbers;

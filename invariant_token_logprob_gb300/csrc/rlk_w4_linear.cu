@@ -13,8 +13,8 @@
 // a thread owns one row of a 128-row tile, turns the row's codes into numbers in registers
 // and stores them to its TMEM lane, from where they are the A operand.  x is B (N = the
 // rows of x, 16, 32 or 64 at a time).
-// N = 151936, K = 4096, group 128, bf16: T = 1 59 us (5.5 TB/s, 0.81 of a copy), T = 32 65 us,
-// T = 64 80 us, where the x that comes in again for every tile, 32 KB a stage next to 16 KB of
+// N = 151936, K = 4096, group 128, bf16: T = 1 58 us (5.5 TB/s, 0.81 of a copy), T = 32 65 us,
+// T = 64 80 us (83 with zero points), where the x that comes in again for every tile, 32 KB a stage next to 16 KB of
 // codes, costs more than the codes.  N = K = 4096, T = 1: 6.4 us.
 //
 // One CTA per SM; a tile's K goes by in stages of 256 k:
@@ -36,10 +36,11 @@
 //
 // Few tiles (N of some thousands): the K range of a tile is cut into `splits` parts, one
 // per CTA of a cluster, whose sums meet through distributed shared memory in the order of k.
-// The cut follows from N and K; tiles, stages and the order of the sums are fixed; a row of
+// The cut follows from N and K (rlk_w4_plan.h); tiles, stages and the order of the sums are fixed; a row of
 // x is one column of D.  So a row's bits do not depend on T.
 //
-// Every wait is bounded (2 s); on expiry the kernel records it, drains and returns.
+// Every wait is bounded (2 s); on expiry the kernel records it, waits for its copies and
+// products under way and returns.
 #include <atomic>
 
 #include "rlk_logits.cuh"
