@@ -236,8 +236,9 @@ def _plain_gradient(s):
 
 
 def _quantized(x):
-    """Codes (as fp32 whole numbers) and scales of x's rows."""
-    scales = x.abs().amax(1) / 127
+    """Codes (as fp32 whole numbers) and scales of x's rows.  (By a tensor: torch multiplies by
+    the reciprocal of a plain number.)"""
+    scales = x.abs().amax(1) / torch.full((), 127.0, device=x.device)
     scales = torch.where(scales == 0, 1.0, scales)
     return torch.round(x / scales[:, None]).clamp(-127, 127), scales
 
