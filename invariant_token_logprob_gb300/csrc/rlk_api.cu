@@ -101,6 +101,19 @@ EncodeTiledFn encode_fn() {
     return g_encode;
 }
 
+// encode() of a tensor map.  The driver refuses a thread that has made no runtime call which needs
+// the device's context (autograd's worker, all its memory from a cache): cudaSetDevice makes it
+// current, then it is tried again.
+template <typename Encode>
+bool encode_in_context(Encode encode) {
+    CUresult r = encode();
+    int dev = -1;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = encode();
+    return r == CUDA_SUCCESS;
+}
+
 // 2-D tensor map over a row-major [rows][cols] matrix whose boxes are 128 bytes
 // wide (one swizzle row) and box_rows high, 128-byte swizzle, zero fill outside
 // the matrix: bf16 (64 elements per box row) or 8-bit codes (128 elements).
@@ -177,11 +190,12 @@ bool encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner, ui
     const cuuint64_t strides[1] = {cuuint64_t(row_bytes)};
     const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_outer)};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_in_context([&] {
+        return enc(map,
+                   bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 bool encode_tensor_map_2d_store(CUtensorMap* map, void* base, uint64_t inner, uint64_t outer,
                                 uint64_t row_bytes) {
@@ -191,10 +205,11 @@ bool encode_tensor_map_2d_store(CUtensorMap* map, void* base, uint64_t inner, ui
     const cuuint64_t strides[1] = {cuuint64_t(row_bytes)};
     const cuuint32_t box[2] = {32, 32};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_in_context([&] {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 bool encode_tensor_map_f32_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -205,10 +220,11 @@ bool encode_tensor_map_f32_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_
     const cuuint64_t strides[2] = {cuuint64_t(stride1_bytes), cuuint64_t(stride2_bytes)};
     const cuuint32_t box[3] = {32, 32, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_in_context([&] {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 }  // namespace rlk
 
