@@ -494,7 +494,7 @@ rlk_status rlk_selftest_wait_timeout_pair(const void *hidden_bf16, const void *w
                                           int mode, rlk_stream_t stream);
 
 /* Element types of the entry points below that take more than one. */
-typedef enum rlk_dtype { RLK_BF16 = 0, RLK_FP16 = 1, RLK_FP32 = 2 } rlk_dtype;
+typedef enum rlk_dtype { RLK_BF16 = 0, RLK_FP16 = 1, RLK_FP32 = 2, RLK_INT8 = 3 } rlk_dtype;
 
 /* Most alternatives rlk_token_logprobs gives per row. */
 #define RLK_MAX_TOP_K 32
@@ -630,6 +630,105 @@ rlk_status rlk_linear_w4(const void *x, int dtype, const uint32_t *codes_u32, co
 rlk_status rlk_selftest_wait_timeout_w4(const void *x_bf16, const uint32_t *codes_u32,
                                         const void *scales_bf16, float *y_f32, int mode,
                                         rlk_stream_t stream);
+
+/* What rlk_cross_entropy returns of the rows' losses. */
+typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduction;
+
+/*
+ * Softmax cross entropy of an LM head, without its logits in memory: the loss a model is
+ * trained or evaluated with.  With z, lse as in rlk_logprob, e = label_smoothing, per row
+ *   loss[t] = lse[t] - (1 - e) z[t][target[t]] - (e / V) sum_v z[t][v] + z_loss lse[t]^2
+ *   total   = sum_t w[t]            over the rows that count
+ *   RLK_NONE: out_loss[t] = w[t] loss[t];  RLK_SUM: their sum;  RLK_MEAN: that over total
+ * A row whose target lies outside [0, V) or whose weight is 0 does not count: its loss is 0
+ * whatever its logits, and so is its gradient (a target >= V is reported as by rlk_logprob).
+ * A mean over rows whose weights' sum is not above 0 is 0.
+ *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob
+ *   weights_f32   device, [T], w, finite and >= 0; NULL: 1 for every row
+ *   0 <= label_smoothing < 1, z_loss >= 0 and finite
+ *   out_loss_f32  device, [T] for RLK_NONE, else one value
+ *   out_lse_f32   device, [T], written for every row
+ *   out_total_f32 device, one value
+ *   workspace     device, 16-byte aligned, >= rlk_cross_entropy_workspace_size bytes
+ * lse has rlk_logprob's bits, and with e = z_loss = 0 a loss of weight 1 is -logp; a row's loss
+ * depends on its hidden state, target and weight, W, V, H and the options only.  The sum over
+ * rows is taken in an order fixed by T.  Asynchronous on `stream`; allocates nothing.  T == 0
+ * writes 0 to the sums.
+ */
+size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V);
+rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,
+                             const int32_t *targets_i32, const float *weights_f32, int64_t T,
+                             int64_t H, int64_t V, float inv_temp, float label_smoothing,
+                             float z_loss, int reduction, float *out_loss_f32, float *out_lse_f32,
+                             float *out_total_f32, void *workspace, size_t workspace_bytes,
+                             rlk_stream_t stream);
+
+/*
+ * Its gradient with respect to the hidden states and the weight.  With p = exp(z - lse) and
+ * a[t] = g w[t] / total (RLK_MEAN), g w[t] (RLK_SUM) or g[t] w[t] (RLK_NONE):
+ *   dz[t][v] = a[t] (p (1 + 2 z_loss lse[t]) - (1 - e) [v == target[t]] - e / V)
+ *   grad_hidden = inv_temp * dz . W      grad_weight (+)= inv_temp * dz^T . h
+ * The logits are computed again, a piece of the vocabulary at a time; of dz a piece and its
+ * transpose are held (256 MiB together, more only where 256 entries take more), rounded once to
+ * bf16, as an operand of the two products.  These sum in fp32 in an order fixed by (T, H, V).
+ *   lse_f32, total_f32   device: rlk_cross_entropy's outputs (total_f32 is read for RLK_MEAN)
+ *   grad_loss_f32        device: g, [T] for RLK_NONE, else one value
+ *   grad_hidden          device, [T][H] of grad_hidden_dtype; NULL: not wanted
+ *   grad_weight          device, [V][H] of grad_weight_dtype; NULL: not wanted
+ *                        (types RLK_BF16 or RLK_FP32; both 16-byte aligned)
+ *   accumulate_grad_weight != 0: grad_weight, of RLK_FP32, is added to
+ *   workspace            device, 16-byte aligned,
+ *                        >= rlk_cross_entropy_backward_workspace_size bytes
+ * Other arguments as given to rlk_cross_entropy.  Asynchronous on `stream`; allocates nothing.
+ * T == 0 sets an overwritten grad_weight to 0.
+ */
+size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V);
+rlk_status rlk_cross_entropy_backward(
+    const void *hidden_bf16, const void *weight_bf16, const int32_t *targets_i32,
+    const float *weights_f32, const float *lse_f32, const float *grad_loss_f32,
+    const float *total_f32, int64_t T, int64_t H, int64_t V, float inv_temp, float label_smoothing,
+    float z_loss, int reduction, void *grad_hidden, int grad_hidden_dtype, void *grad_weight,
+    int grad_weight_dtype, int accumulate_grad_weight, void *workspace, size_t workspace_bytes,
+    rlk_stream_t stream);
+
+/*
+ * Matrices in 8-bit whole numbers with an fp32 scale per row: a weight's channels, or tokens.
+ *   scale = max|x| / 127 (fp32; 1 for a row of zeros), code = clamp(rint(x / scale), -127, 127)
+ *   (fp32 division, rint to even);  an element stands for scale * code
+ * rlk_quantize_int8 makes codes [rows][K] and scales [rows] of x [rows][K] (`dtype` RLK_BF16,
+ * RLK_FP16 or RLK_FP32, finite); rlk_dequantize_int8 writes what they stand for, rounded once to
+ * out_dtype (any of the three).  K % 16 == 0 (else RLK_ERR_ALIGNMENT), rows * K <= 2^40; x, codes
+ * and out 16-byte aligned.  Asynchronous on `stream`; allocate nothing.
+ */
+rlk_status rlk_quantize_int8(const void *x, int dtype, int64_t rows, int64_t K, int8_t *codes_i8,
+                             float *scales_f32, rlk_stream_t stream);
+rlk_status rlk_dequantize_int8(const int8_t *codes_i8, const float *scales_f32, int64_t rows,
+                               int64_t K, void *out, int out_dtype, rlk_stream_t stream);
+
+/* Longest K of rlk_linear_int8: products of such length fit 32 bits whatever the codes. */
+#define RLK_INT8_MAX_K 131056
+
+/*
+ * y [T][N] = x [T][K] . W^T for such a weight, x of 16 or 32 bits, quantised per token as by
+ * rlk_quantize_int8 within the call, or given as codes with their scales:
+ *   y[t][n] = (float(sum_k qx[t][k] qw[n][k]) * x_scale[t]) * scale[n]
+ * The sum of whole numbers is exact, whatever the codes (-128 included); it is rounded once to
+ * fp32 and, behind the two fp32 products, once to out_dtype.  So a row's bits depend on that row
+ * of x and on the channel only: not on T, N, K's cut or the device.
+ *   x             device, [T][K] of x_dtype (RLK_BF16, RLK_FP16, RLK_FP32 or RLK_INT8), 16-byte
+ *                 aligned
+ *   x_scales_f32  device, [T] with RLK_INT8, else NULL
+ *   codes_i8, scales_f32   device, [N][K] and [N], codes 16-byte aligned
+ *   out_y         device, [T][N] of out_dtype (RLK_BF16, RLK_FP16 or RLK_FP32)
+ *   workspace     device, 16-byte aligned, >= rlk_linear_int8_workspace_size(T, K) bytes
+ *   K % 16 == 0, K <= RLK_INT8_MAX_K, N * K <= 2^40, T * N and T * K <= 2^39
+ * Asynchronous on `stream`; allocates nothing.
+ */
+size_t rlk_linear_int8_workspace_size(int64_t T, int64_t K);
+rlk_status rlk_linear_int8(const void *x, int x_dtype, const float *x_scales_f32,
+                           const int8_t *codes_i8, const float *scales_f32, int64_t T, int64_t N,
+                           int64_t K, void *out_y, int out_dtype, void *workspace,
+                           size_t workspace_bytes, rlk_stream_t stream);
 
 /* Release the library's cached workspaces on every device it used (waits for
  * them to be idle).  Safe to call more than once. */

@@ -28,6 +28,10 @@ __all__ = ["RlkError", "lib", "logprob", "logprob_ws", "logprob_partials", "lse_
            "TokenLogprobs", "token_logprobs", "token_logprobs_backward",
            "differentiable_token_logprobs", "MAX_TOP_K",
            "quantize_w4", "dequantize_w4", "pack_w4", "unpack_w4", "linear_w4", "logprob_w4",
+           "CrossEntropy", "cross_entropy", "cross_entropy_backward",
+           "differentiable_cross_entropy", "cross_entropy_workspace_size",
+           "cross_entropy_backward_workspace_size",
+           "quantize_int8", "dequantize_int8", "linear_int8", "logprob_int8",
            "header_functions", "STAT_NAMES", "LIB_PATH", "HEADER_PATH"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -148,6 +152,26 @@ def lib() -> ctypes.CDLL:
                                     ctypes.c_int, P]
         L.rlk_selftest_wait_timeout_w4.restype = st
         L.rlk_selftest_wait_timeout_w4.argtypes = [P, P, P, P, ctypes.c_int, P]
+        L.rlk_cross_entropy_workspace_size.restype = sz
+        L.rlk_cross_entropy_workspace_size.argtypes = [i64, i64, i64]
+        L.rlk_cross_entropy.restype = st
+        L.rlk_cross_entropy.argtypes = [P, P, P, P, i64, i64, i64, f32, f32, f32, ctypes.c_int,
+                                        P, P, P, P, sz, P]
+        L.rlk_cross_entropy_backward_workspace_size.restype = sz
+        L.rlk_cross_entropy_backward_workspace_size.argtypes = [i64, i64, i64]
+        L.rlk_cross_entropy_backward.restype = st
+        L.rlk_cross_entropy_backward.argtypes = [P, P, P, P, P, P, P, i64, i64, i64, f32, f32, f32,
+                                                 ctypes.c_int, P, ctypes.c_int, P, ctypes.c_int,
+                                                 ctypes.c_int, P, sz, P]
+        L.rlk_quantize_int8.restype = st
+        L.rlk_quantize_int8.argtypes = [P, ctypes.c_int, i64, i64, P, P, P]
+        L.rlk_dequantize_int8.restype = st
+        L.rlk_dequantize_int8.argtypes = [P, P, i64, i64, P, ctypes.c_int, P]
+        L.rlk_linear_int8_workspace_size.restype = sz
+        L.rlk_linear_int8_workspace_size.argtypes = [i64, i64]
+        L.rlk_linear_int8.restype = st
+        L.rlk_linear_int8.argtypes = [P, ctypes.c_int, P, P, P, i64, i64, i64, P, ctypes.c_int, P,
+                                      sz, P]
         _lib = L
     return _lib
 
@@ -1038,4 +1062,268 @@ def logprob_w4(h, codes, scales, targets, zeros=None, group: int = 128, top_k: i
         _need(logits, torch.float32, "logits", 2)
     logits = linear_w4(h, codes, scales, zeros, group, out=logits, out_dtype=torch.float32,
                        stream=stream)
+    return token_logprobs(logits, targets, top_k, allowed, inv_temp, out=out, stream=stream)
+
+
+# ---------------------------------------------------------------- cross entropy
+class CrossEntropy(NamedTuple):
+    """Results of cross_entropy: the loss (f32, a scalar, or [T] without reduction), every
+    row's log-sum-exp (f32 [T]) and the sum of the weights that count (f32 scalar)."""
+    loss: object
+    lse: object
+    total: object
+
+
+_REDUCTIONS = {"mean": 0, "sum": 1, "none": 2}
+
+
+def cross_entropy_workspace_size(T: int, H: int, V: int) -> int:
+    return lib().rlk_cross_entropy_workspace_size(int(T), int(H), int(V))
+
+
+def cross_entropy_backward_workspace_size(T: int, H: int, V: int) -> int:
+    return lib().rlk_cross_entropy_backward_workspace_size(int(T), int(H), int(V))
+
+
+def _cross_entropy_args(call, h, W, targets, weights, reduction):
+    """Checked (h, W, targets, weights) addresses, T, H, V and the reduction's code."""
+    torch = call.torch
+    if reduction not in _REDUCTIONS:
+        raise ValueError("reduction must be 'mean', 'sum' or 'none'")
+    pointers = [call.arg(h, torch.bfloat16, "h", 2), call.arg(W, torch.bfloat16, "W", 2),
+                call.arg(targets, torch.int32, "targets", 1)]
+    (T, H), (V, H2) = h.shape, W.shape
+    if H != H2 or targets.shape[0] != T:
+        raise ValueError("shape mismatch: h [T,H], W [V,H], targets [T]")
+    if weights is None:
+        return (*pointers, None), T, H, V, _REDUCTIONS[reduction]
+    pointers.append(call.arg(weights, torch.float32, "weights", 1))
+    if weights.shape[0] != T:
+        raise ValueError("weights must be [T]")
+    return pointers, T, H, V, _REDUCTIONS[reduction]
+
+
+def cross_entropy(h, W, targets, weights=None, inv_temp: float = 1.0, label_smoothing: float = 0.0,
+                  z_loss: float = 0.0, reduction: str = "mean", workspace=None, stream=None):
+    """rlk_cross_entropy: CrossEntropy(loss, lse, total) of an LM head's softmax, whose logits
+    never reach memory.
+
+    h bf16 [T, H], W bf16 [V, H], targets i32 [T] (negative: the row does not count), weights
+    None or f32 [T] (0: the row does not count).  Per row lse - (1 - e) z[target] - e mean(z) +
+    z_loss lse^2 with z = h . W^T * inv_temp and e = label_smoothing, times its weight;
+    reduction 'mean' (by the weights' sum), 'sum' or 'none'."""
+    call = _Call()
+    torch = call.torch
+    empty = torch.empty if stream is None else _allocator(stream)
+    pointers, T, H, V, code = _cross_entropy_args(call, h, W, targets, weights, reduction)
+    dev, f32 = h.device, torch.float32
+    loss = empty((T,) if code == 2 else (), dtype=f32, device=dev)
+    lse = empty(T, dtype=f32, device=dev)
+    total = empty((), dtype=f32, device=dev)
+    L = _lib or lib()
+    if workspace is None:
+        workspace = empty(max(16, L.rlk_cross_entropy_workspace_size(T, H, V)), dtype=torch.uint8,
+                          device=dev)
+    ws = call.arg(workspace, torch.uint8, "workspace", 1)
+    _check(L.rlk_cross_entropy(*pointers, T, H, V, inv_temp, label_smoothing, z_loss, code,
+                               loss.data_ptr(), lse.data_ptr(), total.data_ptr(), ws,
+                               workspace.shape[0], call.stream(stream)), "rlk_cross_entropy")
+    return CrossEntropy(loss, lse, total)
+
+
+def cross_entropy_backward(h, W, targets, lse, grad_loss, total=None, weights=None,
+                           inv_temp: float = 1.0, label_smoothing: float = 0.0,
+                           z_loss: float = 0.0, reduction: str = "mean", need_h: bool = True,
+                           need_W: bool = True, grad_W=None, grad_dtype=None, workspace=None,
+                           stream=None):
+    """rlk_cross_entropy_backward: (grad_h [T, H] or None, grad_W [V, H] or None) from the
+    gradient of cross_entropy's loss (f32, a scalar, or [T] for reduction 'none') and its lse
+    and total (needed for 'mean').  The gradients are bf16 (or float32: grad_dtype); pass grad_W
+    (float32) to add to it instead."""
+    call = _Call()
+    torch = call.torch
+    f32 = torch.float32
+    empty = torch.empty if stream is None else _allocator(stream)
+    pointers, T, H, V, code = _cross_entropy_args(call, h, W, targets, weights, reduction)
+    rows = [call.arg(lse, f32, "lse", 1)]
+    if lse.shape[0] != T:
+        raise ValueError("lse must be [T]")
+    rows.append(call.arg(grad_loss, f32, "grad_loss", 1 if code == 2 else 0))
+    if code == 2 and grad_loss.shape[0] != T:
+        raise ValueError("grad_loss must be [T] for reduction 'none'")
+    if code == 0 and total is None:
+        raise ValueError("reduction 'mean' needs total")
+    rows.append(None if total is None else call.arg(total, f32, "total", 0))
+    out = _dtype_code(grad_dtype or torch.bfloat16)
+    if out not in (0, 2):
+        raise TypeError("grad_dtype must be bfloat16 or float32")
+    dtype = torch.float32 if out == 2 else torch.bfloat16
+    dev = h.device
+    grad_h = empty((T, H), dtype=dtype, device=dev) if need_h else None
+    accumulate = grad_W is not None
+    if accumulate:
+        call.arg(grad_W, f32, "grad_W", 2)
+        if grad_W.shape != W.shape:
+            raise ValueError("grad_W must be [V, H]")
+    elif need_W:
+        grad_W = empty((V, H), dtype=dtype, device=dev)
+    L = _lib or lib()
+    if workspace is None:
+        workspace = empty(max(16, L.rlk_cross_entropy_backward_workspace_size(T, H, V)),
+                          dtype=torch.uint8, device=dev)
+    ws = call.arg(workspace, torch.uint8, "workspace", 1)
+    _check(L.rlk_cross_entropy_backward(
+        *pointers, *rows, T, H, V, inv_temp, label_smoothing, z_loss, code,
+        None if grad_h is None else grad_h.data_ptr(), out,
+        None if grad_W is None else grad_W.data_ptr(), 2 if accumulate else out,
+        1 if accumulate else 0, ws, workspace.shape[0], call.stream(stream)),
+        "rlk_cross_entropy_backward")
+    return grad_h, grad_W
+
+
+def _cross_entropy_function():
+    import torch
+
+    class CrossEntropyFunction(torch.autograd.Function):
+        """rlk_cross_entropy with rlk_cross_entropy_backward as its gradient."""
+
+        @staticmethod
+        def forward(ctx, h, W, targets, weights, options):
+            r = cross_entropy(h, W, targets, weights, **options)
+            ctx.save_for_backward(h, W, targets, weights, r.lse, r.total)
+            ctx.options = options
+            ctx.mark_non_differentiable(r.lse, r.total)
+            ctx.set_materialize_grads(False)
+            return tuple(r)
+
+        @staticmethod
+        def backward(ctx, g, *_):
+            h, W, targets, weights, lse, total = ctx.saved_tensors
+            need_h, need_W = ctx.needs_input_grad[:2]
+            if g is None or not (need_h or need_W):
+                return None, None, None, None, None
+            grads = cross_entropy_backward(h, W, targets, lse, g.contiguous().float(), total,
+                                           weights, need_h=need_h, need_W=need_W, **ctx.options)
+            return (*_first_derivatives(list(grads), [h, W, g]), None, None, None)
+
+    return CrossEntropyFunction
+
+
+_CrossEntropyFunction = None
+
+
+def differentiable_cross_entropy(h, W, targets, weights=None, inv_temp: float = 1.0,
+                                 label_smoothing: float = 0.0, z_loss: float = 0.0,
+                                 reduction: str = "mean"):
+    """cross_entropy under torch autograd: the loss carries gradients to h and W (lse, total and
+    the weights do not).  First derivatives only."""
+    global _CrossEntropyFunction
+    if _CrossEntropyFunction is None:
+        _CrossEntropyFunction = _cross_entropy_function()
+    options = dict(inv_temp=inv_temp, label_smoothing=label_smoothing, z_loss=z_loss,
+                   reduction=reduction)
+    return CrossEntropy(*_CrossEntropyFunction.apply(h, W, targets, weights, options))
+
+
+# ---------------------------------------------------------------- 8-bit integers
+def _int8_args(call, codes, scales):
+    """Checked (codes, scales) addresses, N, K of a matrix in 8-bit integers."""
+    torch = call.torch
+    c = call.arg(codes, torch.int8, "codes", 2)
+    s = call.arg(scales, torch.float32, "scales", 1)
+    N, K = codes.shape
+    if scales.shape[0] != N:
+        raise ValueError("scales must be [N], one per row of codes")
+    return c, s, N, K
+
+
+def quantize_int8(x, out=None, stream=None):
+    """rlk_quantize_int8: bf16, fp16 or fp32 x [N, K] (K % 16 == 0), a weight or tokens ->
+    (int8 codes [N, K], f32 scales [N]).  Pass out=(codes, scales) to reuse tensors."""
+    call = _Call()
+    torch = call.torch
+    empty = torch.empty if stream is None else _allocator(stream)
+    code = _dtype_code(x.dtype) if isinstance(x, torch.Tensor) else None
+    if code is None:
+        raise TypeError("x must be a bfloat16, float16 or float32 tensor")
+    a = call.arg(x, x.dtype, "x", 2)
+    if out is None:
+        codes = empty(x.shape, dtype=torch.int8, device=x.device)
+        scales = empty(x.shape[0], dtype=torch.float32, device=x.device)
+    else:
+        codes, scales = out
+    c, s, N, K = _int8_args(call, codes, scales)
+    if codes.shape != x.shape:
+        raise ValueError("out must hold codes [N, K] and scales [N]")
+    _check((_lib or lib()).rlk_quantize_int8(a, code, N, K, c, s, call.stream(stream)),
+           "rlk_quantize_int8")
+    return codes, scales
+
+
+def dequantize_int8(codes, scales, out_dtype=None, out=None, stream=None):
+    """rlk_dequantize_int8: the values that codes and scales stand for, [N, K] as float32
+    (default), bfloat16 or float16."""
+    call = _Call()
+    empty = call.torch.empty if stream is None else _allocator(stream)
+    c, s, N, K = _int8_args(call, codes, scales)
+    if out is None:
+        out = empty((N, K), dtype=out_dtype or call.torch.float32, device=codes.device)
+    code = _dtype_code(out.dtype)
+    if code is None:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16")
+    o = call.arg(out, out.dtype, "out", 2)
+    if out.shape != (N, K):
+        raise ValueError("out must be [N, K]")
+    _check((_lib or lib()).rlk_dequantize_int8(c, s, N, K, o, code, call.stream(stream)),
+           "rlk_dequantize_int8")
+    return out
+
+
+def linear_int8(x, codes, scales, x_scales=None, out_dtype=None, out=None, workspace=None,
+                stream=None):
+    """rlk_linear_int8: y [T, N] = x [T, K] . W^T for a weight in 8-bit integers, with a scale per
+    channel.  x is bf16, fp16 or fp32 and quantised per token within the call, or int8 with its
+    x_scales f32 [T]; y is float32 (default), bfloat16 or float16 (out_dtype)."""
+    call = _Call()
+    torch = call.torch
+    empty = torch.empty if stream is None else _allocator(stream)
+    c, s, N, K = _int8_args(call, codes, scales)
+    if not isinstance(x, torch.Tensor) or not (x.dtype is torch.int8 or _dtype_code(x.dtype) is not None):
+        raise TypeError("x must be a bfloat16, float16, float32 or int8 tensor")
+    given = x.dtype is torch.int8
+    a = call.arg(x, x.dtype, "x", 2)
+    T = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError("shape mismatch: x [T, K], codes [N, K]")
+    if given != (x_scales is not None):
+        raise ValueError("x_scales go with an int8 x, and only with one")
+    xs = call.arg(x_scales, torch.float32, "x_scales", 1) if given else None
+    if given and x_scales.shape[0] != T:
+        raise ValueError("x_scales must be [T]")
+    if out is None:
+        out = empty((T, N), dtype=out_dtype or torch.float32, device=x.device)
+    out_code = _dtype_code(out.dtype)
+    if out_code is None:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16")
+    o = call.arg(out, out.dtype, "out", 2)
+    if out.shape != (T, N):
+        raise ValueError("out must be [T, N]")
+    L = _lib or lib()
+    if workspace is None:
+        workspace = empty(max(16, L.rlk_linear_int8_workspace_size(T, K)), dtype=torch.uint8,
+                          device=x.device)
+    ws = call.arg(workspace, torch.uint8, "workspace", 1)
+    _check(L.rlk_linear_int8(a, 3 if given else _dtype_code(x.dtype), xs, c, s, T, N, K, o, out_code,
+                             ws, workspace.shape[0], call.stream(stream)), "rlk_linear_int8")
+    return out
+
+
+def logprob_int8(h, codes, scales, targets, top_k: int = 0, allowed=None, inv_temp: float = 1.0,
+                 logits=None, out=None, stream=None):
+    """A decode step of an LM head in 8-bit integers: linear_int8 into fp32 logits [T, V] (a
+    buffer to reuse may be given), then token_logprobs of them.  Returns its TokenLogprobs."""
+    import torch
+    if logits is not None:
+        _need(logits, torch.float32, "logits", 2)
+    logits = linear_int8(h, codes, scales, out=logits, out_dtype=torch.float32, stream=stream)
     return token_logprobs(logits, targets, top_k, allowed, inv_temp, out=out, stream=stream)

@@ -14,8 +14,10 @@
 #include <utility>
 
 #include "rlk.h"
+#include "rlk_ce_plan.h"
 #include "rlk_internal.h"
 #include "rlk_logits_w4.h"
+#include "rlk_train_int8.h"
 
 namespace {
 
@@ -222,6 +224,20 @@ bool encode_tensor_map_f32_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_
     const cuuint32_t estr[3] = {1, 1, 1};
     return encode_in_context([&] {
         return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+}
+bool encode_tensor_map_bf16_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_t d1,
+                               uint64_t d2, uint64_t stride1_bytes, uint64_t stride2_bytes) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2)};
+    const cuuint64_t strides[2] = {cuuint64_t(stride1_bytes), cuuint64_t(stride2_bytes)};
+    const cuuint32_t box[3] = {64, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_in_context([&] {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     });
@@ -940,6 +956,242 @@ rlk_status rlk_selftest_wait_timeout_w4(const void* x_bf16, const uint32_t* code
                                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+bool valid_ratio(float e) { return e >= 0.0f && e < 1.0f; }
+
+// Checks shared by the cross entropy and its gradient (host values only).
+rlk_status check_cross_entropy(int64_t T, int64_t H, int64_t V, float inv_temp, float smoothing,
+                               float z_loss, int reduction) {
+    rlk_status st = check_shape(T, H, V, inv_temp);
+    if (st != RLK_OK) return st;
+    if (!valid_ratio(smoothing) || !(z_loss >= 0.0f) || !isfinite(z_loss))
+        return RLK_ERR_INVALID_ARG;
+    if (reduction != RLK_MEAN && reduction != RLK_SUM && reduction != RLK_NONE)
+        return RLK_ERR_INVALID_ARG;
+    return RLK_OK;
+}
+
+size_t sum_z_bytes(int64_t T, int64_t V) {
+    return round16(size_t(T) * size_t(num_vocab_tiles(V)) * sizeof(float));
+}
+
+}  // namespace
+
+size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V) {
+    if (T <= 0 || V <= 0 || H <= 0) return 0;
+    return partial_bytes(T, V) + sum_z_bytes(T, V) + round16(size_t(T) * sizeof(float));
+}
+
+rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
+                             const int32_t* targets_i32, const float* weights_f32, int64_t T,
+                             int64_t H, int64_t V, float inv_temp, float label_smoothing,
+                             float z_loss, int reduction, float* out_loss_f32, float* out_lse_f32,
+                             float* out_total_f32, void* workspace, size_t workspace_bytes,
+                             rlk_stream_t stream) {
+    rlk_status st = check_cross_entropy(T, H, V, inv_temp, label_smoothing, z_loss, reduction);
+    if (st != RLK_OK) return st;
+    if (!out_total_f32 || (!out_loss_f32 && (T > 0 || reduction != RLK_NONE)))
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned4(out_loss_f32) || !aligned4(out_total_f32)) return RLK_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int dev, sms;
+    if (T == 0) {  // empty sums
+        if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+        cudaError_t e = cudaMemsetAsync(out_total_f32, 0, sizeof(float), s);
+        if (e == cudaSuccess && reduction != RLK_NONE)
+            e = cudaMemsetAsync(out_loss_f32, 0, sizeof(float), s);
+        return from_cuda(e);
+    }
+    if ((st = check_operands(hidden_bf16, weight_bf16, targets_i32, H)) != RLK_OK) return st;
+    if (!out_lse_f32) return RLK_ERR_INVALID_ARG;
+    if (!aligned4(out_lse_f32) || !aligned4(weights_f32)) return RLK_ERR_ALIGNMENT;
+    if (!workspace) return RLK_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return RLK_ERR_ALIGNMENT;
+    if (workspace_bytes < rlk_cross_entropy_workspace_size(T, H, V)) return RLK_ERR_WORKSPACE;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    CUtensorMap th, tw;
+    if ((st = prepare_maps(hidden_bf16, weight_bf16, T, H, V, &th, &tw)) != RLK_OK) return st;
+    char* base = static_cast<char*>(workspace);
+    float* sum_z = reinterpret_cast<float*>(base + partial_bytes(T, V));
+    float* rows = reinterpret_cast<float*>(base + partial_bytes(T, V) + sum_z_bytes(T, V));
+    if (label_smoothing == 0.0f) sum_z = nullptr;
+    cudaError_t e =
+        sum_z ? rlk::launch_lmhead_sum_z(&th, &tw, targets_i32, workspace, sum_z, T, V, H, inv_temp,
+                                         sms, s)
+              : rlk::launch_lmhead_partials(&th, &tw, targets_i32, workspace, T, V, H, inv_temp,
+                                            sms, s);
+    if (e != cudaSuccess) return from_cuda(e);
+    const bool none = reduction == RLK_NONE;
+    return from_cuda(rlk::launch_cross_entropy(
+        workspace, sum_z, targets_i32, weights_f32, T, V, label_smoothing, z_loss,
+        reduction == RLK_MEAN, none ? out_loss_f32 : rows, out_lse_f32,
+        none ? nullptr : out_loss_f32, out_total_f32, s));
+}
+
+size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V) {
+    if (T <= 0 || V <= 0 || H <= 0) return 0;
+    return rlk::ce_layout(T, H, rlk::ce_plan(T, H, V)).bytes;
+}
+
+rlk_status rlk_cross_entropy_backward(
+    const void* hidden_bf16, const void* weight_bf16, const int32_t* targets_i32,
+    const float* weights_f32, const float* lse_f32, const float* grad_loss_f32,
+    const float* total_f32, int64_t T, int64_t H, int64_t V, float inv_temp, float label_smoothing,
+    float z_loss, int reduction, void* grad_hidden, int grad_hidden_dtype, void* grad_weight,
+    int grad_weight_dtype, int accumulate_grad_weight, void* workspace, size_t workspace_bytes,
+    rlk_stream_t stream) {
+    rlk_status st = check_cross_entropy(T, H, V, inv_temp, label_smoothing, z_loss, reduction);
+    if (st != RLK_OK) return st;
+    if ((grad_hidden_dtype != RLK_BF16 && grad_hidden_dtype != RLK_FP32) ||
+        (grad_weight_dtype != RLK_BF16 && grad_weight_dtype != RLK_FP32))
+        return RLK_ERR_INVALID_ARG;
+    if (accumulate_grad_weight && grad_weight_dtype != RLK_FP32) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(grad_hidden) || !aligned16(grad_weight)) return RLK_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int dev, sms;
+    const size_t weight_row = size_t(H) * elem_size(grad_weight_dtype);
+    if (T == 0) {  // grad_h is empty and grad_W an empty sum
+        if (!grad_weight || accumulate_grad_weight) return RLK_OK;
+        if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+        return from_cuda(cudaMemsetAsync(grad_weight, 0, size_t(V) * weight_row, s));
+    }
+    if ((st = check_operands(hidden_bf16, weight_bf16, targets_i32, H)) != RLK_OK) return st;
+    if (!lse_f32 || !grad_loss_f32 || (reduction == RLK_MEAN && !total_f32))
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned4(lse_f32) || !aligned4(grad_loss_f32) || !aligned4(total_f32) ||
+        !aligned4(weights_f32))
+        return RLK_ERR_ALIGNMENT;
+    if (!workspace) return RLK_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return RLK_ERR_ALIGNMENT;
+    const rlk::CePlan plan = rlk::ce_plan(T, H, V);
+    const rlk::CeLayout layout = rlk::ce_layout(T, H, plan);
+    if (workspace_bytes < layout.bytes) return RLK_ERR_WORKSPACE;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    if (!grad_hidden && !grad_weight) return RLK_OK;
+    char* dz = static_cast<char*>(workspace);
+    char* dzt = dz + layout.dzt;
+    float* sums = reinterpret_cast<float*>(dz + layout.sums);
+    const rlk::CrossEntropyTerms terms = {weights_f32, reduction == RLK_MEAN ? total_f32 : nullptr,
+                                          reduction == RLK_NONE ? 1 : 0, int(V), label_smoothing,
+                                          z_loss};
+    const int64_t part_rows = rlk::ce_part_rows(plan);
+    for (int64_t v0 = 0; v0 < V; v0 += plan.rows) {
+        const int64_t rows = V - v0 < plan.rows ? V - v0 : plan.rows;
+        const char* w = static_cast<const char*>(weight_bf16) + size_t(v0) * size_t(H) * 2;
+        CUtensorMap th, tw, tdzt;
+        if ((st = prepare_maps(hidden_bf16, w, T, H, rows, &th, &tw)) != RLK_OK) return st;
+        if (grad_weight && !rlk::encode_dzt_store_map(&tdzt, dzt, T, rows)) return RLK_ERR_CUDA;
+        cudaError_t e = rlk::launch_lmhead_grad_loss(
+            &th, &tw, grad_weight ? &tdzt : nullptr, targets_i32, lse_f32, grad_loss_f32, terms, dz,
+            plan.rows, T, v0, rows, H, inv_temp, sms, s);
+        if (e == cudaSuccess && grad_weight)
+            e = rlk::launch_piece_grad_weight(
+                hidden_bf16, dzt, T, H, rows, inv_temp,
+                static_cast<char*>(grad_weight) + size_t(v0) * weight_row,
+                grad_weight_dtype == RLK_BF16, accumulate_grad_weight != 0, sms, s);
+        if (e == cudaSuccess && grad_hidden)
+            e = rlk::launch_piece_grad_hidden(w, dz, plan.rows, T, H, rows, part_rows, sums, v0 > 0,
+                                              sms, s);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    if (!grad_hidden) return RLK_OK;
+    const int64_t first = V < plan.rows ? V : plan.rows;
+    return from_cuda(rlk::launch_sum_parts(sums, grad_hidden, grad_hidden_dtype == RLK_BF16, T, H,
+                                           int((first + part_rows - 1) / part_rows), inv_temp, sms,
+                                           s));
+}
+
+namespace {
+
+// Checks shared by the 8-bit integer entry points (pointers only where N >= 1).
+rlk_status check_int8(int64_t N, int64_t K, const void* codes, const void* scales) {
+    if (N < 0 || N > INT32_MAX || K < 1 || K > INT32_MAX) return RLK_ERR_INVALID_ARG;
+    if (K % 16 != 0) return RLK_ERR_ALIGNMENT;
+    if (N > (int64_t(1) << 40) / K) return RLK_ERR_INVALID_ARG;
+    if (N == 0) return RLK_OK;
+    if (!codes || !scales) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned4(scales)) return RLK_ERR_ALIGNMENT;
+    return RLK_OK;
+}
+
+bool float_dtype(int dtype) {
+    return dtype == RLK_BF16 || dtype == RLK_FP16 || dtype == RLK_FP32;
+}
+
+}  // namespace
+
+rlk_status rlk_quantize_int8(const void* x, int dtype, int64_t rows, int64_t K, int8_t* codes_i8,
+                             float* scales_f32, rlk_stream_t stream) {
+    if (!float_dtype(dtype)) return RLK_ERR_INVALID_ARG;
+    rlk_status st = check_int8(rows, K, codes_i8, scales_f32);
+    if (st != RLK_OK) return st;
+    if (rows == 0) return RLK_OK;
+    if (!x) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(x)) return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_quantize_int8(x, ElemType(dtype), rows, K, codes_i8, scales_f32,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rlk_status rlk_dequantize_int8(const int8_t* codes_i8, const float* scales_f32, int64_t rows,
+                               int64_t K, void* out, int out_dtype, rlk_stream_t stream) {
+    if (!float_dtype(out_dtype)) return RLK_ERR_INVALID_ARG;
+    rlk_status st = check_int8(rows, K, codes_i8, scales_f32);
+    if (st != RLK_OK) return st;
+    if (rows == 0) return RLK_OK;
+    if (!out) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(out)) return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    return from_cuda(rlk::launch_dequantize_int8(codes_i8, scales_f32, rows, K, out,
+                                                 ElemType(out_dtype),
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t rlk_linear_int8_workspace_size(int64_t T, int64_t K) {
+    if (T <= 0 || K <= 0) return 0;
+    return round16(size_t(T) * size_t(K) * 2) + round16(size_t(T) * sizeof(float));
+}
+
+rlk_status rlk_linear_int8(const void* x, int x_dtype, const float* x_scales_f32,
+                           const int8_t* codes_i8, const float* scales_f32, int64_t T, int64_t N,
+                           int64_t K, void* out_y, int out_dtype, void* workspace,
+                           size_t workspace_bytes, rlk_stream_t stream) {
+    if (T < 0 || T > INT32_MAX) return RLK_ERR_INVALID_ARG;
+    rlk_status st = check_int8(N, K, codes_i8, scales_f32);
+    if (st != RLK_OK) return st;
+    if (K > RLK_INT8_MAX_K) return RLK_ERR_INVALID_ARG;
+    if ((x_dtype != RLK_INT8 && !float_dtype(x_dtype)) || !float_dtype(out_dtype))
+        return RLK_ERR_INVALID_ARG;
+    if (T > 0 && (N > (int64_t(1) << 39) / T || K > (int64_t(1) << 39) / T))
+        return RLK_ERR_INVALID_ARG;
+    if (N == 0 || T == 0) return RLK_OK;
+    if (!x || !out_y || (x_dtype == RLK_INT8) != (x_scales_f32 != nullptr))
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned4(x_scales_f32) || !aligned_to(out_y, elem_size(out_dtype)))
+        return RLK_ERR_ALIGNMENT;
+    if (!workspace) return RLK_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return RLK_ERR_ALIGNMENT;
+    if (workspace_bytes < rlk_linear_int8_workspace_size(T, K)) return RLK_ERR_WORKSPACE;
+    int dev, sms;
+    if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int8_t* xq = static_cast<const int8_t*>(x);
+    if (x_dtype != RLK_INT8) {
+        int8_t* q = static_cast<int8_t*>(workspace);
+        float* sc = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                             round16(size_t(T) * size_t(K) * 2));
+        cudaError_t e = rlk::launch_quantize_int8(x, ElemType(x_dtype), T, K, q, sc, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        xq = q;
+        x_scales_f32 = sc;
+    }
+    return from_cuda(rlk::launch_linear_int8(xq, x_scales_f32, codes_i8, scales_f32, T, N, K, out_y,
+                                             ElemType(out_dtype), sms, s));
+}
+
 rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits,
                                   uint64_t* target_range_rows) {
     int dev, sms;
@@ -958,7 +1210,9 @@ rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits
     unsigned long long rows_logits = 0;
     if (rlk::take_target_range_rows(&rows) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::token_logprobs_take_range_rows(&rows_logits) != cudaSuccess) return RLK_ERR_CUDA;
-    rows += rows_logits;
+    unsigned long long rows_ce = 0;
+    if (rlk::cross_entropy_take_range_rows(&rows_ce) != cudaSuccess) return RLK_ERR_CUDA;
+    rows += rows_logits + rows_ce;
     if (wait_error_bits) *wait_error_bits = word;
     if (target_range_rows) *target_range_rows = rows;
     return RLK_OK;

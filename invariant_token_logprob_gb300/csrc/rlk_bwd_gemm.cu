@@ -109,6 +109,7 @@ struct Args {
     int num_tiles;         // S * num_mu * num_n
     float alpha;
     int accumulate;        // D += alpha * acc instead of D = alpha * acc
+    int add_in_l2;         // the same by adding stores (no read here), fp32 D
     int stall_selftest;    // the producer issues no copies (bounded-wait self-test)
 };
 
@@ -158,7 +159,8 @@ __device__ __forceinline__ bool wait_limit(uint32_t bar, uint32_t parity, uint64
     return true;
 }
 
-template <bool kAMn, bool kBMn = true>
+// kBf16: D is bf16, rounded once from the fp32 accumulator.
+template <bool kAMn, bool kBMn = true, bool kBf16 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
@@ -419,14 +421,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const int col0 = n * kUN;
             const int ncols = min(kUN, p.N - col0);
-            float* drow = p.d + int64_t(s) * p.split_stride + (live ? row : 0) * p.ldd + col0;
+            float* drow =
+                kBf16 ? nullptr
+                      : p.d + int64_t(s) * p.split_stride + (live ? row : 0) * p.ldd + col0;
             const uint32_t t_addr = lane_base + acc * uint32_t(kUN);
             const int row0 = (2 * mu + int(rank)) * kUM + q * 32;  // this warp's first row
             for (int c = 0; c * 32 < ncols; ++c) {
                 uint32_t r[32];
                 tmem_ld32(t_addr + uint32_t(c * 32), r);
                 tmem_ld_wait();
-                if (!p.accumulate) {
+                if constexpr (kBf16) {
+                    // two chunks, 64 columns, make the staging block's 128-byte rows: 16-byte
+                    // piece i of row r at piece i ^ (r % 8), as for fp32
+                    const int half = c & 1;
+                    if (half == 0) {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(
+                                __fmul_rn(alpha, __uint_as_float(r[8 * i + 2 * j])),
+                                __fmul_rn(alpha, __uint_as_float(r[8 * i + 2 * j + 1])));
+                            v[j] = *reinterpret_cast<const uint32_t*>(&two);
+                        }
+                        *reinterpret_cast<uint4*>(out_row +
+                                                  (((4 * half + i) ^ (lane & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    if (half == 1 || (c + 1) * 32 >= ncols) {  // (the last chunk may stand alone:
+                        fence_proxy_async_shared();            // columns past N are not stored)
+                        __syncwarp();
+                        if (lane == 0 && row0 < p.M) {
+                            tma_store_3d_hint(&tmap_d, out_block, col0 + (c & ~1) * 32, row0, s,
+                                              store_policy);
+                            bulk_commit_group();
+                        }
+                    }
+                } else if (!p.accumulate) {
                     // stage the 32 x 32 block, then one tiled bulk store (clipped
                     // at M and N); the previous store must be done reading first
                     if (lane == 0) bulk_wait_group_read<0>();
@@ -441,8 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M) {
-                        tma_store_3d_hint(&tmap_d, out_block, col0 + c * 32, row0, s,
-                                          store_policy);
+                        if (p.add_in_l2)
+                            tma_add_3d(&tmap_d, out_block, col0 + c * 32, row0, s);
+                        else
+                            tma_store_3d_hint(&tmap_d, out_block, col0 + c * 32, row0, s,
+                                              store_policy);
                         bulk_commit_group();
                     }
                 } else if (live) {
@@ -493,8 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out[i] = alpha * (ws[0][i] + ws[1][i] + ... + ws[S-1][i]), added in that order.
+template <bool kBf16 = false>
 __global__ void __launch_bounds__(256)
-    split_reduce_kernel(const float4* __restrict__ ws, float4* __restrict__ out, int64_t n4,
+    split_reduce_kernel(const float4* __restrict__ ws, void* __restrict__ out, int64_t n4,
                         int64_t stride4, int splits, float alpha) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -508,24 +547,56 @@ __global__ void __launch_bounds__(256)
             a.z = __fadd_rn(a.z, b.z);
             a.w = __fadd_rn(a.w, b.w);
         }
-        out[i] = make_float4(__fmul_rn(alpha, a.x), __fmul_rn(alpha, a.y), __fmul_rn(alpha, a.z),
-                             __fmul_rn(alpha, a.w));
+        const float4 v = make_float4(__fmul_rn(alpha, a.x), __fmul_rn(alpha, a.y),
+                                     __fmul_rn(alpha, a.z), __fmul_rn(alpha, a.w));
+        if constexpr (kBf16) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+            static_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                     *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+            static_cast<float4*>(out)[i] = v;
+        }
     }
 }
 
-int g_max_clusters[4][64];  // co-resident CTA pairs per kernel variant and device
+template <bool kBf16>
+cudaError_t launch_split_reduce(const void* ws, void* out, int64_t T, int64_t H, int splits,
+                                float alpha, int num_sms, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t n4 = T * H / 4;
+    const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, int64_t(num_sms) * 8);
+    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, split_reduce_kernel<kBf16>,
+                                       static_cast<const float4*>(ws), out, n4, n4, splits, alpha);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
 
-template <bool kAMn, bool kBMn = true>
+int g_max_clusters[8][64];  // co-resident CTA pairs per kernel variant and device
+
+template <bool kAMn, bool kBMn = true, bool kBf16 = false>
 cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, int num_sms,
-                        cudaStream_t stream) {
-    // D as [S][M][ldd] fp32, stored in 32 x 32 blocks
+                        cudaStream_t stream, void* d_bf16 = nullptr) {
+    // D as [S][M][ldd] fp32, stored in 32 x 32 blocks; or bf16, in blocks of 32 x 64
     CUtensorMap td;
     const int64_t splits = (a.num_kb + a.kb_per_split - 1) / a.kb_per_split;
-    if (!encode_tensor_map_f32_3d(&td, a.d, uint64_t(a.N), uint64_t(a.M), uint64_t(splits),
-                                  uint64_t(a.ldd) * 4,
-                                  uint64_t(a.split_stride ? a.split_stride : a.M * a.ldd) * 4))
-        return cudaErrorInvalidValue;
-    auto kernel = bwd_gemm_kernel<kAMn, kBMn>;
+    const bool mapped =
+        kBf16 ? encode_tensor_map_bf16_3d(&td, d_bf16, uint64_t(a.N), uint64_t(a.M), 1,
+                                          uint64_t(a.ldd) * 2, uint64_t(a.M) * a.ldd * 2)
+              : encode_tensor_map_f32_3d(
+                    &td, a.d, uint64_t(a.N), uint64_t(a.M), uint64_t(splits),
+                    uint64_t(a.ldd) * 4,
+                    uint64_t(a.split_stride ? a.split_stride : a.M * a.ldd) * 4);
+    if (!mapped) return cudaErrorInvalidValue;
+    auto kernel = bwd_gemm_kernel<kAMn, kBMn, kBf16>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -543,7 +614,7 @@ cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, in
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    int& maxc = g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0)][dev];
+    int& maxc = g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0) + (kBf16 ? 4 : 0)][dev];
     if (maxc == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kSmemBytes));
@@ -667,24 +738,65 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
         a.alpha = 1.0f;
         cudaError_t e = launch_gemm<false>(ta, tb, a, num_sms, stream);
         if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        const int64_t n4 = T * H / 4;
-        const int64_t blocks = std::min<int64_t>(cdiv(n4, 256), int64_t(num_sms) * 8);
-        cfg.gridDim = dim3(unsigned(blocks), 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, split_reduce_kernel,
-                               static_cast<const float4*>(split_ws),
-                               reinterpret_cast<float4*>(grad_h), n4, n4, splits, inv_temp);
-        if (e != cudaSuccess) return e;
-        return cudaGetLastError();
+        return launch_split_reduce<false>(split_ws, grad_h, T, H, splits, inv_temp, num_sms,
+                                          stream);
     }
     return cudaSuccess;
+}
+
+cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, int64_t T, int64_t H,
+                                     int64_t rows, float alpha, void* grad, bool bf16,
+                                     bool accumulate, int num_sms, cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!encode_tensor_map_2d(&ta, dzt, uint64_t(T), uint64_t(rows),
+                              uint64_t(backward_dz_ld(T)) * 2, kBK, kUM, false) ||
+        !encode_tensor_map_2d(&tb, h, uint64_t(H), uint64_t(T), uint64_t(H) * 2, kMnAtom, kBK,
+                              false))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.d = bf16 ? nullptr : static_cast<float*>(grad);
+    a.ldd = H;
+    a.M = int(rows);
+    a.N = int(H);
+    a.num_kb = a.kb_per_split = int(cdiv(T, kBK));
+    a.num_mu = int(cdiv(rows, 2 * kUM));
+    a.num_n = int(cdiv(H, kUN));
+    a.num_tiles = a.num_mu * a.num_n;
+    a.alpha = alpha;
+    a.add_in_l2 = accumulate ? 1 : 0;
+    return bf16 ? launch_gemm<false, true, true>(ta, tb, a, num_sms, stream, grad)
+                : launch_gemm<false>(ta, tb, a, num_sms, stream);
+}
+
+cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
+                                     int64_t H, int64_t rows, int64_t part_rows, float* sums,
+                                     bool add, int num_sms, cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!encode_tensor_map_2d(&ta, dz, uint64_t(rows), uint64_t(T), uint64_t(ldz) * 2, kBK, kUM,
+                              false) ||
+        !encode_tensor_map_2d(&tb, W, uint64_t(H), uint64_t(rows), uint64_t(H) * 2, kMnAtom, kBK,
+                              false))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.d = sums;
+    a.split_stride = T * H;
+    a.ldd = H;
+    a.M = int(T);
+    a.N = int(H);
+    a.num_kb = int(cdiv(rows, kBK));
+    a.kb_per_split = int(cdiv(part_rows, kBK));
+    a.num_mu = int(cdiv(T, 2 * kUM));
+    a.num_n = int(cdiv(H, kUN));
+    a.num_tiles = int(cdiv(a.num_kb, a.kb_per_split)) * a.num_mu * a.num_n;
+    a.alpha = 1.0f;
+    a.add_in_l2 = add ? 1 : 0;
+    return launch_gemm<false>(ta, tb, a, num_sms, stream);
+}
+
+cudaError_t launch_sum_parts(const float* sums, void* out, bool bf16, int64_t T, int64_t H,
+                             int parts, float alpha, int num_sms, cudaStream_t stream) {
+    return bf16 ? launch_split_reduce<true>(sums, out, T, H, parts, alpha, num_sms, stream)
+                : launch_split_reduce<false>(sums, out, T, H, parts, alpha, num_sms, stream);
 }
 
 cudaError_t bwd_gemm_take_error(unsigned int* out) {

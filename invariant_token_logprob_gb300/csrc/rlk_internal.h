@@ -44,6 +44,10 @@ bool encode_tensor_map_2d_store(CUtensorMap* map, void* base, uint64_t inner, ui
 bool encode_tensor_map_f32_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                               uint64_t stride1_bytes, uint64_t stride2_bytes);
 
+// The same of bf16, boxes of 64 x 32 x 1 elements.
+bool encode_tensor_map_bf16_3d(CUtensorMap* map, void* base, uint64_t d0, uint64_t d1,
+                               uint64_t d2, uint64_t stride1_bytes, uint64_t stride2_bytes);
+
 // The smallest h box the LM-head kernel copies (rows); see lmhead_a_box_rows.
 constexpr int kMinTmaRows = 16;
 
@@ -79,6 +83,32 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
                                       int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
                                       cudaStream_t stream);
 
+// What the gradient of the cross entropy with respect to the logits depends on besides the
+// rows' lse and targets.  With a = g w (/ total):
+//   dz[v] = a (p[v] (1 + 2 z_loss lse) - (1 - smoothing) [v == target] - smoothing / V)
+struct CrossEntropyTerms {
+    const float* weights;  // [T], or null: 1
+    const float* total;    // the weights' sum, where the loss is their mean; else null
+    int per_row;           // the incoming gradient is [T], not one value
+    int V;                 // the whole vocabulary
+    float smoothing, z_loss;
+};
+
+// Forward records plus sum_z [T][NVT], the sum of z over each tile's columns.
+cudaError_t launch_lmhead_sum_z(const CUtensorMap* th, const CUtensorMap* tw,
+                                const int32_t* targets, void* partials, float* sum_z, int64_t T,
+                                int64_t V, int64_t H, float inv_temp, int num_sms,
+                                cudaStream_t stream);
+// dz [T][ldz] (and, with tdzt, its transpose) of the cross entropy for the vocabulary's entries
+// [first, first + rows), which tw maps; first is a multiple of kVocabTile.  0 in rows that do not
+// count (target outside the vocabulary, weight 0).
+cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
+                                    const CUtensorMap* tdzt, const int32_t* targets,
+                                    const float* lse, const float* grad,
+                                    const CrossEntropyTerms& terms, void* dz, int64_t ldz,
+                                    int64_t T, int64_t first, int64_t rows, int64_t H,
+                                    float inv_temp, int num_sms, cudaStream_t stream);
+
 // Row stride (elements) of dz: V rounded up to a multiple of 8 (of its
 // transposed copy: backward_dz_ld(T)).
 int64_t backward_dz_ld(int64_t V);
@@ -97,6 +127,19 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
                                int64_t T, int64_t H, int64_t V, float inv_temp, float* grad_h,
                                float* grad_W, bool accumulate_W, void* split_ws, int num_sms,
                                cudaStream_t stream);
+// The same products for a piece of `rows` vocabulary entries (the cross entropy's backward).
+// grad [rows][H] (+)= alpha * dzt . h as bf16 (overwritten) or fp32; dzt [rows][backward_dz_ld(T)].
+cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, int64_t T, int64_t H,
+                                     int64_t rows, float alpha, void* grad, bool bf16,
+                                     bool accumulate, int num_sms, cudaStream_t stream);
+// sums [.][T][H] (+)= dz . W, one sum per part_rows (a multiple of 64) of the piece's rows;
+// W [rows][H], dz [T][ldz].
+cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
+                                     int64_t H, int64_t rows, int64_t part_rows, float* sums,
+                                     bool add, int num_sms, cudaStream_t stream);
+// out [T][H] = alpha * (sums[0] + sums[1] + ...), in that order, as bf16 or fp32.
+cudaError_t launch_sum_parts(const float* sums, void* out, bool bf16, int64_t T, int64_t H,
+                             int parts, float alpha, int num_sms, cudaStream_t stream);
 // Reads and clears the backward GEMM kernel's per-device error word (bit 0: a
 // bounded wait ran out; bit 1: a teardown wait ran out).
 cudaError_t bwd_gemm_take_error(unsigned int* out);

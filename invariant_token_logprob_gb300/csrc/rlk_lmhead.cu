@@ -136,12 +136,13 @@ __device__ unsigned int g_lmhead_error;
 struct Args {
     const int32_t* targets;
     float4* partials;      // modes 0, 2: [T][num_n] records
-    float* ent_u;          // mode 2: [T][num_n] sum exp(z - m) (z - m) per tile
-    const float* lse;      // mode 1: forward LSE per row
-    const float* grad;     // mode 1: upstream gradient of logp per row
-    uint16_t* dz;          // mode 1: [T][ldz] bf16 gradient of logp w.r.t. the logits
-    int64_t ldz;           // mode 1: row stride of dz (a multiple of 8 elements)
-    int write_dzt;         // mode 1: also store dz transposed through tmap_x ([V][T])
+    float* ent_u;          // mode 2: [T][num_n] sum exp(z - m) (z - m) per tile; mode 3: sum z
+    const float* lse;      // modes 1, 4: forward LSE per row
+    const float* grad;     // mode 1: upstream gradient of logp per row; mode 4: of the loss
+    uint16_t* dz;          // modes 1, 4: [T][ldz] bf16 gradient w.r.t. the logits
+    int64_t ldz;           // modes 1, 4: row stride of dz (a multiple of 8 elements)
+    int write_dzt;         // modes 1, 4: also store dz transposed through tmap_x ([V][T])
+    CrossEntropyTerms ce;  // mode 4
     int64_t T;
     int64_t h_rows; // rows the h tensor map covers (>= T; padded copies are longer)
     int a_rows;     // rows of each h box (lmhead_a_box_rows(T))
@@ -225,6 +226,8 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity,
 constexpr int kModePartials = 0;   // forward: vocabulary-tile partial records
 constexpr int kModeGradLogits = 1; // backward: dz = g (onehot - exp(z - lse)) as bf16
 constexpr int kModeEntropy = 2;    // forward records plus the per-tile entropy statistic
+constexpr int kModeSumZ = 3;       // forward records plus the per-tile sum of z
+constexpr int kModeGradLoss = 4;   // cross entropy's backward: its dz for a piece of W's rows
 
 // kHq: the call's T (<= kHqMaxRows) h rows of H (<= kHqMaxH, a multiple of 128)
 // bf16 -> e4m3 codes in the resident block `hq` and the row scales in
@@ -692,13 +695,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after_sync();
 
-            if constexpr (kMode == kModePartials || kMode == kModeEntropy) {
+            if constexpr (kMode == kModePartials || kMode == kModeEntropy || kMode == kModeSumZ) {
                 const int col0 = n * kBN;
                 const int ncols = min(kBN, p.V - col0);
                 const int nchunks = (ncols + 31) >> 5;
                 float run_m = -INFINITY, run_s = 0.0f, zt = 0.0f;
                 int32_t run_a = INT_MAX;
-                float run_u = 0.0f;  // mode 2 only
+                float run_u = 0.0f;  // modes 2 and 3 only
                 const uint32_t t_addr = lane_base + acc * uint32_t(kBN);
                 for (int c = 0; c < nchunks; ++c) {
                     uint32_t r[32];
@@ -743,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cs += e;
                         if constexpr (kMode == kModeEntropy)
                             cu = (j < nvalid) ? fmaf(e, z[j] - cm, cu) : cu;
+                        if constexpr (kMode == kModeSumZ) cu = (j < nvalid) ? cu + z[j] : cu;
                     }
                     const int cbase = p.col_offset + col0 + c * 32;  // global column of j = 0
                     const int rel = tgt - cbase;
@@ -753,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if constexpr (kMode == kModeEntropy)
                         run_u = lse_combine_u(run_m, run_s, run_a, run_u, cm, cs, cbase + ca, cu);
+                    if constexpr (kMode == kModeSumZ) run_u += cu;
                     lse_combine(run_m, run_s, run_a, cm, cs, cbase + ca);
                 }
                 // Accumulator buffer fully read: hand it back to the MMA warp.
@@ -767,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (row < p.T) {
                     p.partials[row * p.num_n + n] =
                         make_float4(run_m, run_s, __int_as_float(run_a), zt);
-                    if constexpr (kMode == kModeEntropy) p.ent_u[row * p.num_n + n] = run_u;
+                    if constexpr (kMode != kModePartials) p.ent_u[row * p.num_n + n] = run_u;
                 }
             } else {
                 const int col0 = n * kBN;
@@ -775,9 +780,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nchunks = (ncols + 31) >> 5;
                 const uint32_t t_addr = lane_base + acc * uint32_t(kBN);
                 const bool live = row < p.T;
-                const bool valid = live && tgt >= 0 && tgt < p.V;
-                const float g = valid ? __ldg(p.grad + row) : 0.0f;
-                const float lse2 = live ? __ldg(p.lse + row) * kLog2e : 0.0f;
+                // mode 4's rows of W are a piece of the vocabulary that begins at col_offset
+                bool valid = live && tgt >= 0 && tgt < (kMode == kModeGradLoss ? p.ce.V : p.V);
+                const float lse_row = live ? __ldg(p.lse + row) : 0.0f;
+                const float lse2 = lse_row * kLog2e;
+                float g = 0.0f;                          // mode 1: d/dlogp
+                float gp = 0.0f, gt = 0.0f, ge = 0.0f;   // mode 4: dz = gp p - gt [target] - ge
+                if constexpr (kMode == kModeGradLoss) {
+                    const float w = valid ? (p.ce.weights ? __ldg(p.ce.weights + row) : 1.0f) : 0.0f;
+                    valid = w != 0.0f;
+                    float a = __ldg(p.grad + (p.ce.per_row ? (live ? row : 0) : 0)) * w;
+                    if (p.ce.total) {
+                        const float total = __ldg(p.ce.total);
+                        a = total > 0.0f ? a / total : 0.0f;
+                    }
+                    gp = a * fmaf(2.0f * p.ce.z_loss, lse_row, 1.0f);
+                    gt = a * (1.0f - p.ce.smoothing);
+                    ge = a * (p.ce.smoothing / float(p.ce.V));
+                } else {
+                    g = valid ? __ldg(p.grad + row) : 0.0f;
+                }
+                const int tgt_here = tgt - p.col_offset;
                 uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;  // 16-byte aligned rows
                 // transposed copy: this warp's 32 rows x 32 columns of a chunk are
                 // staged as 32 columns x 32 rows and stored in one piece
@@ -794,12 +817,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; j += 2) {
                         const float z0 = __uint_as_float(r[j]) * inv_temp;
                         const float z1 = __uint_as_float(r[j + 1]) * inv_temp;
-                        // p = exp(z - lse); dz = g * (onehot - p)
+                        // p = exp(z - lse); dz = g * (onehot - p), or the loss's
                         const float p0 = exp2f(fmaf(z0, kLog2e, -lse2));
                         const float p1 = exp2f(fmaf(z1, kLog2e, -lse2));
-                        const float d0 = valid ? g * ((cbase + j == tgt ? 1.0f : 0.0f) - p0) : 0.0f;
-                        const float d1 =
-                            valid ? g * ((cbase + j + 1 == tgt ? 1.0f : 0.0f) - p1) : 0.0f;
+                        float d0, d1;
+                        if constexpr (kMode == kModeGradLoss) {
+                            d0 = valid ? fmaf(gp, p0, -ge) - (cbase + j == tgt_here ? gt : 0.0f)
+                                       : 0.0f;
+                            d1 = valid ? fmaf(gp, p1, -ge) - (cbase + j + 1 == tgt_here ? gt : 0.0f)
+                                       : 0.0f;
+                        } else {
+                            d0 = valid ? g * ((cbase + j == tgt ? 1.0f : 0.0f) - p0) : 0.0f;
+                            d1 = valid ? g * ((cbase + j + 1 == tgt ? 1.0f : 0.0f) - p1) : 0.0f;
+                        }
                         packed[j / 2] = pack_bf16x2(d0, d1);
                     }
                     const int nvalid = ncols - c * 32;
@@ -846,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1u;
             }
         }
-        if constexpr (kMode == kModeGradLogits) {
+        if constexpr (kMode == kModeGradLogits || kMode == kModeGradLoss) {
             if (p.write_dzt && lane == 0) bulk_wait_group<0>();  // every store has completed
             __syncwarp();
         }
@@ -868,14 +898,16 @@ struct VariantState {
     int configured = 0;    // dynamic shared memory attribute set
     int max_clusters = 0;  // CTA pairs that fit at once (CTA-pair variants)
 };
-VariantState g_variant[9][64];  // per kernel variant and device
+VariantState g_variant[13][64];  // per kernel variant and device
 constexpr size_t kMaxSmemBytes = 227 * 1024;
 
 template <int kMode, bool kFp8, bool kPair, bool kHq = false>
 cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tx,
                            Args a, int64_t H, int num_sms, cudaStream_t stream) {
     using P = Pipe<kPair, kHq>;
-    constexpr int kVariant = kHq ? 8 : (kFp8 ? 3 : kMode) + (kPair ? 4 : 0);
+    constexpr int kVariant = kMode >= kModeSumZ ? 9 + 2 * (kMode - kModeSumZ) + (kPair ? 1 : 0)
+                             : kHq              ? 8
+                                                : (kFp8 ? 3 : kMode) + (kPair ? 4 : 0);
     constexpr int kBKE = kFp8 ? 2 * kBK : kBK;
     auto kernel = lmhead_kernel<kMode, kFp8, kPair, kHq>;
     int dev = 0;
@@ -981,6 +1013,20 @@ cudaError_t launch_lmhead_entropy(const CUtensorMap* th, const CUtensorMap* tw,
     return launch_mode<kModeEntropy>(th, tw, a, H, num_sms, stream);
 }
 
+cudaError_t launch_lmhead_sum_z(const CUtensorMap* th, const CUtensorMap* tw,
+                                const int32_t* targets, void* partials, float* sum_z, int64_t T,
+                                int64_t V, int64_t H, float inv_temp, int num_sms,
+                                cudaStream_t stream) {
+    Args a = {};
+    a.targets = targets;
+    a.partials = static_cast<float4*>(partials);
+    a.ent_u = sum_z;
+    a.T = T;
+    a.V = int(V);
+    a.inv_temp = inv_temp;
+    return launch_mode<kModeSumZ>(th, tw, a, H, num_sms, stream);
+}
+
 bool lmhead_fp8_quantises_h(int64_t T, int64_t H) {
     static_assert(Pipe<false, true>::kSmemBytes + size_t(kHqRows) * kHqMaxH <= kMaxSmemBytes,
                   "h codes and weight stages fit in shared memory");
@@ -1050,6 +1096,27 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
     a.V = int(V);
     a.inv_temp = inv_temp;
     return launch_mode<kModeGradLogits>(th, tw, a, H, num_sms, stream, tdzt);
+}
+
+cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
+                                    const CUtensorMap* tdzt, const int32_t* targets,
+                                    const float* lse, const float* grad,
+                                    const CrossEntropyTerms& terms, void* dz, int64_t ldz,
+                                    int64_t T, int64_t first, int64_t rows, int64_t H,
+                                    float inv_temp, int num_sms, cudaStream_t stream) {
+    Args a = {};
+    a.targets = targets;
+    a.lse = lse;
+    a.grad = grad;
+    a.ce = terms;
+    a.dz = static_cast<uint16_t*>(dz);
+    a.ldz = ldz;
+    a.write_dzt = tdzt ? 1 : 0;
+    a.T = T;
+    a.V = int(rows);
+    a.col_offset = int(first);
+    a.inv_temp = inv_temp;
+    return launch_mode<kModeGradLoss>(th, tw, a, H, num_sms, stream, tdzt);
 }
 
 cudaError_t lmhead_take_error(unsigned int* out) {

@@ -219,6 +219,16 @@ __device__ __forceinline__ void tma_store_3d_hint(const void* desc, uint32_t src
         : "memory");
 }
 
+// 3-D tiled bulk addition shared -> global: the box's fp32 values are added to the tensor's in
+// L2, one addition per element, rounded like add.rn.
+__device__ __forceinline__ void tma_add_3d(const void* desc, uint32_t src, int x, int y, int z) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+        " [%0, {%2, %3, %4}], [%1];" ::"l"(desc),
+        "r"(src), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
