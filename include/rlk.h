@@ -714,7 +714,10 @@ rlk_status rlk_dequantize_int8(const int8_t *codes_i8, const float *scales_f32, 
  *   y[t][n] = (float(sum_k qx[t][k] qw[n][k]) * x_scale[t]) * scale[n]
  * The sum of whole numbers is exact, whatever the codes (-128 included); it is rounded once to
  * fp32 and, behind the two fp32 products, once to out_dtype.  So a row's bits depend on that row
- * of x and on the channel only: not on T, N, K's cut or the device.
+ * of x and on the channel only: not on T, N, K's cut or the device.  A bounded wait that runs
+ * out is reported by rlk_check_device_error.  Callers that capture graphs make one call of each
+ * class before (T up to 16, 32, 64, 128, more; out_dtype): the first sets its kernel's
+ * shared-memory size.
  *   x             device, [T][K] of x_dtype (RLK_BF16, RLK_FP16, RLK_FP32 or RLK_INT8), 16-byte
  *                 aligned
  *   x_scales_f32  device, [T] with RLK_INT8, else NULL
@@ -729,6 +732,16 @@ rlk_status rlk_linear_int8(const void *x, int x_dtype, const float *x_scales_f32
                            const int8_t *codes_i8, const float *scales_f32, int64_t T, int64_t N,
                            int64_t K, void *out_y, int out_dtype, void *workspace,
                            size_t workspace_bytes, rlk_stream_t stream);
+
+/*
+ * Self-test of rlk_linear_int8's bounded waits, as rlk_selftest_wait_timeout_w4 (modes 1 and 2): a
+ * product with T = 1, N = 128, K = 512 that cannot end.
+ *   x_fp16 [1][512], codes_i8 [128][512] (16-byte aligned), x_scales_f32 [1], scales_f32 [128],
+ *   y_f32 [128] (left unwritten): device buffers.  Another mode: RLK_ERR_INVALID_ARG.
+ */
+rlk_status rlk_selftest_wait_timeout_int8(const void *x_fp16, const float *x_scales_f32,
+                                          const int8_t *codes_i8, const float *scales_f32,
+                                          float *y_f32, int mode, rlk_stream_t stream);
 
 /* Release the library's cached workspaces on every device it used (waits for
  * them to be idle).  Safe to call more than once. */

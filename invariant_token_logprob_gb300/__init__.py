@@ -172,6 +172,8 @@ def lib() -> ctypes.CDLL:
         L.rlk_linear_int8.restype = st
         L.rlk_linear_int8.argtypes = [P, ctypes.c_int, P, P, P, i64, i64, i64, P, ctypes.c_int, P,
                                       sz, P]
+        L.rlk_selftest_wait_timeout_int8.restype = st
+        L.rlk_selftest_wait_timeout_int8.argtypes = [P, P, P, P, P, ctypes.c_int, P]
         _lib = L
     return _lib
 

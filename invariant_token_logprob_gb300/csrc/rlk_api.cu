@@ -1178,18 +1178,34 @@ rlk_status rlk_linear_int8(const void* x, int x_dtype, const float* x_scales_f32
     int dev, sms;
     if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int8_t* xq = static_cast<const int8_t*>(x);
-    if (x_dtype != RLK_INT8) {
-        int8_t* q = static_cast<int8_t*>(workspace);
+    cudaError_t e;
+    if (x_dtype == RLK_INT8) {
+        e = rlk::launch_widen_int8(static_cast<const int8_t*>(x), T * K, workspace, s);
+    } else {
         float* sc = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                              round16(size_t(T) * size_t(K) * 2));
-        cudaError_t e = rlk::launch_quantize_int8(x, ElemType(x_dtype), T, K, q, sc, s);
-        if (e != cudaSuccess) return from_cuda(e);
-        xq = q;
+        e = rlk::launch_quantize_fp16(x, ElemType(x_dtype), T, K, workspace, sc, s);
         x_scales_f32 = sc;
     }
-    return from_cuda(rlk::launch_linear_int8(xq, x_scales_f32, codes_i8, scales_f32, T, N, K, out_y,
-                                             ElemType(out_dtype), sms, s));
+    if (e != cudaSuccess) return from_cuda(e);
+    return from_cuda(rlk::launch_linear_int8(workspace, x_scales_f32, codes_i8, scales_f32, T, N, K,
+                                             out_y, ElemType(out_dtype), sms, s));
+}
+
+rlk_status rlk_selftest_wait_timeout_int8(const void* x_fp16, const float* x_scales_f32,
+                                          const int8_t* codes_i8, const float* scales_f32,
+                                          float* y_f32, int mode, rlk_stream_t stream) {
+    if (mode != 1 && mode != 2) return RLK_ERR_INVALID_ARG;
+    if (!x_fp16 || !x_scales_f32 || !codes_i8 || !scales_f32 || !y_f32) return RLK_ERR_INVALID_ARG;
+    if (!aligned16(x_fp16) || !aligned16(codes_i8) || !aligned4(x_scales_f32) ||
+        !aligned4(scales_f32) || !aligned4(y_f32))
+        return RLK_ERR_ALIGNMENT;
+    int dev, sms;
+    rlk_status st = current_device(&dev, &sms);
+    if (st != RLK_OK) return st;
+    return from_cuda(rlk::launch_linear_int8_stall_selftest(
+        x_fp16, x_scales_f32, codes_i8, scales_f32, y_f32, mode, sms,
+        reinterpret_cast<cudaStream_t>(stream)));
 }
 
 rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits,
@@ -1206,7 +1222,9 @@ rlk_status rlk_take_device_errors(rlk_stream_t stream, uint32_t* wait_error_bits
     if (rlk::lmhead_fp8b_take_error(&word_fp8b) != cudaSuccess) return RLK_ERR_CUDA;
     unsigned int word_w4 = 0;
     if (rlk::linear_w4_take_error(&word_w4) != cudaSuccess) return RLK_ERR_CUDA;
-    word |= word_bwd | word_fp8b | word_w4;
+    unsigned int word_int8 = 0;
+    if (rlk::linear_int8_take_error(&word_int8) != cudaSuccess) return RLK_ERR_CUDA;
+    word |= word_bwd | word_fp8b | word_w4 | word_int8;
     unsigned long long rows_logits = 0;
     if (rlk::take_target_range_rows(&rows) != cudaSuccess) return RLK_ERR_CUDA;
     if (rlk::token_logprobs_take_range_rows(&rows_logits) != cudaSuccess) return RLK_ERR_CUDA;

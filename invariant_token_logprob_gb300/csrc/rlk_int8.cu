@@ -71,6 +71,25 @@ __device__ __forceinline__ void two_codes(float a, float b, float s, float r, ui
     q[1] = __float_as_uint(fminf(fmaxf(v.y, -127.0f), 127.0f) + kRint);
 }
 
+// The codes of a vector, as bytes or as fp16 numbers.
+template <typename Elem, bool kFast>
+__device__ __forceinline__ void store_codes(const uint4& v, float s, float r, __half* dst) {
+    constexpr int n = kVecElems<Elem>;
+    float f[n];
+    to_floats<Elem>(v, f);
+    uint32_t words[n / 2];
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+        uint32_t q[2];
+        two_codes<kFast>(f[i], f[i + 1], s, r, q);
+        const __half2 two = __floats2half2_rn(__uint_as_float(q[0]) - kRint, __uint_as_float(q[1]) - kRint);
+        words[i / 2] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    if constexpr (n == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(words[0], words[1], words[2], words[3]);
+    else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(words[0], words[1]);
+}
 template <typename Elem, bool kFast>
 __device__ __forceinline__ void store_codes(const uint4& v, float s, float r, int8_t* dst) {
     constexpr int n = kVecElems<Elem>;
@@ -92,10 +111,10 @@ __device__ __forceinline__ void store_codes(const uint4& v, float s, float r, in
 }
 
 // kWarps warps per row (1 or 8).  kHeld: the row fits in their registers; else it is read twice.
-template <typename Elem, int kWarps, bool kHeld>
+template <typename Elem, typename Code, int kWarps, bool kHeld>
 __global__ void __launch_bounds__(kThreads)
     quantize_int8_kernel(const uint4* __restrict__ x, int64_t rows, int vecs,
-                         int8_t* __restrict__ codes, float* __restrict__ scales) {
+                         Code* __restrict__ codes, float* __restrict__ scales) {
     constexpr int kRows = kThreads / 32 / kWarps;  // per CTA
     constexpr int kLanes = 32 * kWarps;
     constexpr int n = kVecElems<Elem>;
@@ -129,7 +148,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     const float s = scale_of(amax);
     if (at == 0) scales[row] = s;
-    int8_t* dst = codes + row * vecs * n;
+    Code* dst = codes + row * vecs * n;
     auto store = [&](auto fast) {
         constexpr bool kFast = decltype(fast)::value;
         const float r = kFast ? __frcp_rn(s) : 0.0f;
@@ -188,6 +207,26 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Codes as fp16 numbers, 16 per thread.
+__global__ void __launch_bounds__(kThreads)
+    widen_int8_kernel(const uint4* __restrict__ codes, int64_t vecs, uint4* __restrict__ out) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= vecs) return;
+    const uint4 v = __ldg(codes + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const __half2 two = __floats2half2_rn(float(int8_t(w[j / 4] >> (8 * (j % 4)))),
+                                              float(int8_t(w[j / 4] >> (8 * (j % 4) + 8))));
+        r[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    out[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
+    out[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
 cudaLaunchConfig_t config(int64_t blocks, cudaLaunchAttribute* attr, cudaStream_t stream) {
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr->val.programmaticStreamSerializationAllowed = 1;
@@ -200,29 +239,49 @@ cudaLaunchConfig_t config(int64_t blocks, cudaLaunchAttribute* attr, cudaStream_
     return cfg;
 }
 
-template <typename Elem>
-cudaError_t quantize(const void* x, int64_t rows, int64_t K, int8_t* codes, float* scales,
+template <typename Elem, typename Code>
+cudaError_t quantize(const void* x, int64_t rows, int64_t K, Code* codes, float* scales,
                      cudaStream_t stream) {
     const int vecs = int(K / kVecElems<Elem>);
     // one warp per row fills the GPU from some thousands of rows on
     const bool wide = rows >= 2048 && vecs <= 32 * kVecs;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(wide ? (rows + 7) / 8 : rows, &attr, stream);
-    auto kernel = wide                       ? quantize_int8_kernel<Elem, 1, true>
-                  : vecs <= kThreads * kVecs ? quantize_int8_kernel<Elem, 8, true>
-                                             : quantize_int8_kernel<Elem, 8, false>;
+    auto kernel = wide                       ? quantize_int8_kernel<Elem, Code, 1, true>
+                  : vecs <= kThreads * kVecs ? quantize_int8_kernel<Elem, Code, 8, true>
+                                             : quantize_int8_kernel<Elem, Code, 8, false>;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint4*>(x), rows, vecs,
                                        codes, scales);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename Code>
+cudaError_t quantize_typed(const void* x, ElemType type, int64_t rows, int64_t K, Code* codes,
+                           float* scales, cudaStream_t stream) {
+    if (type == ElemType::kBf16) return quantize<__nv_bfloat16>(x, rows, K, codes, scales, stream);
+    if (type == ElemType::kFp16) return quantize<__half>(x, rows, K, codes, scales, stream);
+    return quantize<float>(x, rows, K, codes, scales, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_int8(const void* x, ElemType type, int64_t rows, int64_t K,
                                  int8_t* codes, float* scales, cudaStream_t stream) {
-    if (type == ElemType::kBf16) return quantize<__nv_bfloat16>(x, rows, K, codes, scales, stream);
-    if (type == ElemType::kFp16) return quantize<__half>(x, rows, K, codes, scales, stream);
-    return quantize<float>(x, rows, K, codes, scales, stream);
+    return quantize_typed(x, type, rows, K, codes, scales, stream);
+}
+
+cudaError_t launch_quantize_fp16(const void* x, ElemType type, int64_t rows, int64_t K, void* codes,
+                                 float* scales, cudaStream_t stream) {
+    return quantize_typed(x, type, rows, K, static_cast<__half*>(codes), scales, stream);
+}
+
+cudaError_t launch_widen_int8(const int8_t* codes, int64_t count, void* out, cudaStream_t stream) {
+    const int64_t vecs = count / 16;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config((vecs + kThreads - 1) / kThreads, &attr, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, widen_int8_kernel, reinterpret_cast<const uint4*>(codes),
+                                       vecs, static_cast<uint4*>(out));
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_dequantize_int8(const int8_t* codes, const float* scales, int64_t N, int64_t K,

@@ -22,9 +22,21 @@ cudaError_t launch_quantize_int8(const void* x, ElemType type, int64_t rows, int
                                  int8_t* codes, float* scales, cudaStream_t stream);
 cudaError_t launch_dequantize_int8(const int8_t* codes, const float* scales, int64_t N, int64_t K,
                                    void* out, ElemType out_type, cudaStream_t stream);
-// y [T][N] from x's codes (rlk_linear_int8).
-cudaError_t launch_linear_int8(const int8_t* x, const float* x_scales, const int8_t* codes,
+// The same codes as fp16 whole numbers, an operand of the product: of x quantised, or of given codes.
+cudaError_t launch_quantize_fp16(const void* x, ElemType type, int64_t rows, int64_t K, void* codes,
+                                 float* scales, cudaStream_t stream);
+cudaError_t launch_widen_int8(const int8_t* codes, int64_t count, void* out, cudaStream_t stream);
+// y [T][N] from x's codes as fp16 (rlk_linear_int8).
+cudaError_t launch_linear_int8(const void* x_fp16, const float* x_scales, const int8_t* codes,
                                const float* scales, int64_t T, int64_t N, int64_t K, void* y,
                                ElemType y_type, int num_sms, cudaStream_t stream);
+// Its bounded-wait self-test (T = 1, N = 128, K = 512); mode 1: no copy is issued, 2: no stage is
+// consumed.
+cudaError_t launch_linear_int8_stall_selftest(const void* x_fp16, const float* x_scales,
+                                              const int8_t* codes, const float* scales, float* y,
+                                              int mode, int num_sms, cudaStream_t stream);
+// Reads and clears its per-device error word (bit 0: a bounded wait ran out; bit 1: a teardown
+// wait ran out).
+cudaError_t linear_int8_take_error(unsigned int* out);
 
 }  // namespace rlk

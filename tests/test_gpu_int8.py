@@ -238,3 +238,32 @@ def test_empty_and_refusals():
         rlk.linear_int8(x, qw, sw, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError):
         rlk.dequantize_int8(qw, sw, out_dtype=torch.int32)
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+def test_bounded_wait_runs_out_and_context_survives(mode):
+    """No copy is issued, or no stage is consumed after every copy was issued: the wait that runs
+    out is reported, every teardown wait ends in time, and the next call is right."""
+    import ctypes
+    import time
+
+    import invariant_token_logprob_gb300 as rlk
+    qx, sx = ref_quantize(normal(1, 512, "bf16", 1))
+    qw, sw = ref_quantize(normal(128, 512, "bf16", 2))
+    x, xs, w, s = qx.half().cuda(), sx.cuda(), qw.cuda(), sw.cuda()
+    y = torch.full((1, 128), 7.0, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rlk.check_device_error()
+
+    def selftest(m):
+        return rlk.lib().rlk_selftest_wait_timeout_int8(*(ctypes.c_void_p(t.data_ptr()) for t in (x, xs, w, s, y)), m,
+                                                        stream)
+
+    assert selftest(0) == 1 and selftest(3) == 1
+    t0 = time.time()
+    assert selftest(mode) == 0
+    assert rlk.take_device_errors() == (1, 0)  # a wait ran out, and no teardown wait did
+    assert 1.0 < time.time() - t0 < 30.0
+    assert bool((y == 7).all())
+    rlk.check_device_error()
+    assert torch.equal(rlk.linear_int8(qx.cuda(), w, s, x_scales=xs).cpu(), ref_linear(qx, sx, qw, sw, "fp32"))

@@ -85,6 +85,15 @@ def test_empty_problems_and_no_gpu(L):
     assert L.rlk_dequantize_int8(A16, A16, 4, 64, A16, 0, None) == 3
 
 
+def test_wait_selftest_refusals(L):
+    f = L.rlk_selftest_wait_timeout_int8
+    assert f(A16, A16, A16, A16, A16, 0, None) == 1 and f(A16, A16, A16, A16, A16, 3, None) == 1
+    assert f(None, A16, A16, A16, A16, 1, None) == 1 and f(A16, A16, A16, A16, None, 2, None) == 1
+    assert f(A4, A16, A16, A16, A16, 1, None) == 2 and f(A16, A16, A16, A16, A2, 1, None) == 2
+    if not torch.cuda.is_available():
+        assert f(A16, A16, A16, A16, A16, 1, None) == 3
+
+
 def test_binding_refuses_cpu_tensors():
     b = torch.zeros(2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
@@ -132,9 +141,37 @@ int main() {
 """
 
 
-def test_cut_of_the_vocabulary(tmp_path):
+INT8_PLAN = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "rlk_int8_plan.h"
+using namespace rlk;
+int main() {
+    for (int room : {16, 32, 64, 128, 192}) {
+        const size_t stages = size_t(int8_stages(room)) * int8_stage_bytes(room);
+        if (int8_smem_bytes(room) > 227 * 1024 || int8_tmem_cols(room) > 512 || int8_warps(room) > 32 ||
+            int8_stage_bytes(room) % 1024 || size_t(room + kInt8MaxParts) * kInt8TileN * 4 > stages)
+            return std::printf("room %d\n", room), 1;
+    }
+    for (long T : {1, 7, 16, 17, 32, 33, 64, 65, 128, 129, 192, 193, 300, 385, 4096, 100000})
+        for (long N : {1, 127, 128, 129, 5119, 151936})
+            for (long K : {16, 128, 144, 1024, 4096, 5152, 131056}) {
+                const Int8Plan p = int8_plan(T, N, K, 152);
+                const bool ok = long(p.chunks) * p.rows >= T && long(p.chunks - 1) * p.rows < T &&
+                                p.rows <= p.mma_n && p.mma_n <= p.room && p.mma_n % 16 == 0 && p.room <= 192 &&
+                                long(p.tiles) * 128 >= N && long(p.stages) * 128 >= K && p.parts >= 1 &&
+                                p.parts <= kInt8MaxParts && p.parts <= p.stages;
+                if (!ok) return std::printf("T=%ld N=%ld K=%ld\n", T, N, K), 1;
+            }
+    return 0;
+}
+"""
+
+
+@pytest.mark.parametrize("source", [PLAN, INT8_PLAN], ids=["vocabulary", "int8"])
+def test_plans(tmp_path, source):
     src = tmp_path / "plan.cpp"
-    src.write_text(PLAN)
+    src.write_text(source)
     csrc = os.path.join(os.path.dirname(rlk.__file__), "csrc")
     exe = str(tmp_path / "plan")
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", csrc, str(src), "-o", exe], check=True)
