@@ -641,7 +641,8 @@ typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduc
  *   total   = sum_t w[t]            over the rows that count
  *   RLK_NONE: out_loss[t] = w[t] loss[t];  RLK_SUM: their sum;  RLK_MEAN: that over total
  * A row whose target lies outside [0, V) or whose weight is 0 does not count: its loss is 0
- * whatever its logits, and so is its gradient (a target >= V is reported as by rlk_logprob).
+ * whatever its hidden state, NaN included, and so is its gradient (a target >= V is reported as by
+ * rlk_logprob).
  * A mean over rows whose weights' sum is not above 0 is 0.
  *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob
  *   weights_f32   device, [T], w, finite and >= 0; NULL: 1 for every row
@@ -650,9 +651,10 @@ typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduc
  *   out_lse_f32   device, [T], written for every row
  *   out_total_f32 device, one value
  *   workspace     device, 16-byte aligned, >= rlk_cross_entropy_workspace_size bytes
- * lse has rlk_logprob's bits, and with e = z_loss = 0 a loss of weight 1 is -logp; a row's loss
- * depends on its hidden state, target and weight, W, V, H and the options only.  The sum over
- * rows is taken in an order fixed by T.  Asynchronous on `stream`; allocates nothing.  T == 0
+ * Logits are summed in parts of 512 k, the parts' sums added in fp32: nearer to the exact sum than
+ * rlk_logprob's, whose bits lse therefore does not have.  The bits of a row's lse and loss depend on
+ * its hidden state, target and weight, W, V, H and the options only, as for rlk_logprob.  The sum
+ * over rows is taken in an order fixed by T.  Asynchronous on `stream`; allocates nothing.  T == 0
  * writes 0 to the sums.
  */
 size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V);
@@ -669,8 +671,11 @@ rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,
  *   dz[t][v] = a[t] (p (1 + 2 z_loss lse[t]) - (1 - e) [v == target[t]] - e / V)
  *   grad_hidden = inv_temp * dz . W      grad_weight (+)= inv_temp * dz^T . h
  * The logits are computed again, a piece of the vocabulary at a time; of dz a piece and its
- * transpose are held (256 MiB together, more only where 256 entries take more), rounded once to
- * bf16, as an operand of the two products.  These sum in fp32 in an order fixed by (T, H, V).
+ * transpose are held (256 MiB together, more only where 256 entries take more), 16 bits each, as
+ * operands of the two products: for grad_hidden rounded once to bf16 but for each row's element at
+ * its target, which a factor per row keeps whole; for grad_weight rounded once to fp16, under
+ * powers of two that keep it in range (h is exact there).  The products sum in fp32 in an order
+ * fixed by (T, H, V).
  *   lse_f32, total_f32   device: rlk_cross_entropy's outputs (total_f32 is read for RLK_MEAN)
  *   grad_loss_f32        device: g, [T] for RLK_NONE, else one value
  *   grad_hidden          device, [T][H] of grad_hidden_dtype; NULL: not wanted

@@ -972,15 +972,15 @@ rlk_status check_cross_entropy(int64_t T, int64_t H, int64_t V, float inv_temp, 
     return RLK_OK;
 }
 
-size_t sum_z_bytes(int64_t T, int64_t V) {
-    return round16(size_t(T) * size_t(num_vocab_tiles(V)) * sizeof(float));
-}
+// Workspace of the loss: records of half tiles, their sums of z, the targets' z, the rows' losses.
+size_t ce_records(int64_t T, int64_t V) { return size_t(T) * 2 * size_t(num_vocab_tiles(V)); }
 
 }  // namespace
 
 size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V) {
     if (T <= 0 || V <= 0 || H <= 0) return 0;
-    return partial_bytes(T, V) + sum_z_bytes(T, V) + round16(size_t(T) * sizeof(float));
+    return ce_records(T, V) * sizeof(float2) + round16(ce_records(T, V) * sizeof(float)) +
+           2 * round16(size_t(T) * sizeof(float));
 }
 
 rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
@@ -1012,19 +1012,17 @@ rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
     if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
     CUtensorMap th, tw;
     if ((st = prepare_maps(hidden_bf16, weight_bf16, T, H, V, &th, &tw)) != RLK_OK) return st;
-    char* base = static_cast<char*>(workspace);
-    float* sum_z = reinterpret_cast<float*>(base + partial_bytes(T, V));
-    float* rows = reinterpret_cast<float*>(base + partial_bytes(T, V) + sum_z_bytes(T, V));
+    float2* records = static_cast<float2*>(workspace);
+    float* sum_z = reinterpret_cast<float*>(records + ce_records(T, V));
+    float* zt = sum_z + round16(ce_records(T, V) * sizeof(float)) / sizeof(float);
+    float* rows = zt + round16(size_t(T) * sizeof(float)) / sizeof(float);
     if (label_smoothing == 0.0f) sum_z = nullptr;
-    cudaError_t e =
-        sum_z ? rlk::launch_lmhead_sum_z(&th, &tw, targets_i32, workspace, sum_z, T, V, H, inv_temp,
-                                         sms, s)
-              : rlk::launch_lmhead_partials(&th, &tw, targets_i32, workspace, T, V, H, inv_temp,
-                                            sms, s);
+    cudaError_t e = rlk::launch_lmhead_loss(&th, &tw, targets_i32, records, zt, sum_z, T, V, H,
+                                            inv_temp, sms, s);
     if (e != cudaSuccess) return from_cuda(e);
     const bool none = reduction == RLK_NONE;
     return from_cuda(rlk::launch_cross_entropy(
-        workspace, sum_z, targets_i32, weights_f32, T, V, label_smoothing, z_loss,
+        records, zt, sum_z, targets_i32, weights_f32, T, V, label_smoothing, z_loss,
         reduction == RLK_MEAN, none ? out_loss_f32 : rows, out_lse_f32,
         none ? nullptr : out_loss_f32, out_total_f32, s));
 }
@@ -1072,9 +1070,17 @@ rlk_status rlk_cross_entropy_backward(
     char* dz = static_cast<char*>(workspace);
     char* dzt = dz + layout.dzt;
     float* sums = reinterpret_cast<float*>(dz + layout.sums);
-    const rlk::CrossEntropyTerms terms = {weights_f32, reduction == RLK_MEAN ? total_f32 : nullptr,
-                                          reduction == RLK_NONE ? 1 : 0, int(V), label_smoothing,
-                                          z_loss};
+    rlk::CeRow* rows_info = reinterpret_cast<rlk::CeRow*>(dz + layout.rows);
+    int* top = reinterpret_cast<int*>(dz + layout.top);
+    void* h_fp16 = dz + layout.h;
+    static_assert(sizeof(rlk::CeRow) == 32, "the layout's row");
+    const rlk::CeTerms terms = {targets_i32, weights_f32, lse_f32, grad_loss_f32,
+                                reduction == RLK_MEAN ? total_f32 : nullptr,
+                                reduction == RLK_NONE ? 1 : 0, int(V), label_smoothing, z_loss,
+                                inv_temp};
+    cudaError_t e = rlk::launch_cross_entropy_rows(terms, hidden_bf16, weight_bf16, T, H, rows_info,
+                                                   grad_weight ? h_fp16 : nullptr, top, s);
+    if (e != cudaSuccess) return from_cuda(e);
     const int64_t part_rows = rlk::ce_part_rows(plan);
     for (int64_t v0 = 0; v0 < V; v0 += plan.rows) {
         const int64_t rows = V - v0 < plan.rows ? V - v0 : plan.rows;
@@ -1082,12 +1088,12 @@ rlk_status rlk_cross_entropy_backward(
         CUtensorMap th, tw, tdzt;
         if ((st = prepare_maps(hidden_bf16, w, T, H, rows, &th, &tw)) != RLK_OK) return st;
         if (grad_weight && !rlk::encode_dzt_store_map(&tdzt, dzt, T, rows)) return RLK_ERR_CUDA;
-        cudaError_t e = rlk::launch_lmhead_grad_loss(
-            &th, &tw, grad_weight ? &tdzt : nullptr, targets_i32, lse_f32, grad_loss_f32, terms, dz,
-            plan.rows, T, v0, rows, H, inv_temp, sms, s);
+        e = rlk::launch_lmhead_grad_loss(&th, &tw, grad_weight ? &tdzt : nullptr, targets_i32,
+                                         rows_info, top, dz, plan.rows, T, v0, rows, H, inv_temp,
+                                         sms, s);
         if (e == cudaSuccess && grad_weight)
             e = rlk::launch_piece_grad_weight(
-                hidden_bf16, dzt, T, H, rows, inv_temp,
+                h_fp16, dzt, top, T, H, rows, inv_temp,
                 static_cast<char*>(grad_weight) + size_t(v0) * weight_row,
                 grad_weight_dtype == RLK_BF16, accumulate_grad_weight != 0, sms, s);
         if (e == cudaSuccess && grad_hidden)
@@ -1097,7 +1103,8 @@ rlk_status rlk_cross_entropy_backward(
     }
     if (!grad_hidden) return RLK_OK;
     const int64_t first = V < plan.rows ? V : plan.rows;
-    return from_cuda(rlk::launch_sum_parts(sums, grad_hidden, grad_hidden_dtype == RLK_BF16, T, H,
+    return from_cuda(rlk::launch_sum_parts(sums, rows_info, grad_hidden,
+                                           grad_hidden_dtype == RLK_BF16, T, H,
                                            int((first + part_rows - 1) / part_rows), inv_temp, sms,
                                            s));
 }

@@ -110,6 +110,7 @@ struct Args {
     float alpha;
     int accumulate;        // D += alpha * acc instead of D = alpha * acc
     int add_in_l2;         // the same by adding stores (no read here), fp32 D
+    const int* top;        // fp16 operands: alpha counts times 2^(*top - 2 kCeTop)
     int stall_selftest;    // the producer issues no copies (bounded-wait self-test)
 };
 
@@ -159,13 +160,15 @@ __device__ __forceinline__ bool wait_limit(uint32_t bar, uint32_t parity, uint64
     return true;
 }
 
-// kBf16: D is bf16, rounded once from the fp32 accumulator.
-template <bool kAMn, bool kBMn = true, bool kBf16 = false>
+// kBf16: D is bf16, rounded once from the fp32 accumulator.  kFp16: A and B are fp16, scaled by
+// powers of two (CeRow).
+template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d, const Args p) {
-    constexpr uint32_t kIdesc = idesc_bf16_f32_major(2 * kUM, kUN, kAMn, kBMn);
+    constexpr uint32_t kIdesc = idesc_bf16_f32_major(2 * kUM, kUN, kAMn, kBMn) &
+                                (kFp16 ? ~((7u << 7) | (7u << 10)) : ~0u);  // (A, B format 0: fp16)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -399,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;  // TMEM lane quadrant this warp may access
         const int row_in_tile = q * 32 + lane;
         const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
-        const float alpha = p.alpha;
+        const float alpha =
+            kFp16 ? p.alpha * ce_power(*p.top - 2 * kCeTop) : p.alpha;
         // the output is written once and not read back here: evict it first
         const uint64_t store_policy = l2_policy_evict_first();
         // This warp's staging block: its 32 rows x 32 columns of one chunk,
@@ -531,10 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out[i] = alpha * (ws[0][i] + ws[1][i] + ... + ws[S-1][i]), added in that order.
+// With `rows`, also times inv_factor of the element's row (row4 float4s long), 0 where it is 0.
 template <bool kBf16 = false>
 __global__ void __launch_bounds__(256)
     split_reduce_kernel(const float4* __restrict__ ws, void* __restrict__ out, int64_t n4,
-                        int64_t stride4, int splits, float alpha) {
+                        int64_t stride4, int splits, float alpha,
+                        const CeRow* __restrict__ rows = nullptr, uint32_t row4 = 1) {
     grid_dependency_wait();
     grid_launch_dependents();
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
@@ -547,8 +553,14 @@ __global__ void __launch_bounds__(256)
             a.z = __fadd_rn(a.z, b.z);
             a.w = __fadd_rn(a.w, b.w);
         }
-        const float4 v = make_float4(__fmul_rn(alpha, a.x), __fmul_rn(alpha, a.y),
-                                     __fmul_rn(alpha, a.z), __fmul_rn(alpha, a.w));
+        float4 v = make_float4(__fmul_rn(alpha, a.x), __fmul_rn(alpha, a.y), __fmul_rn(alpha, a.z),
+                               __fmul_rn(alpha, a.w));
+        if (rows) {
+            const int64_t row = n4 <= UINT32_MAX ? int64_t(uint32_t(i) / row4) : i / row4;
+            const float f = __ldg(&rows[row].inv_factor);
+            v = f != 0.0f ? make_float4(v.x * f, v.y * f, v.z * f, v.w * f)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         if constexpr (kBf16) {
             const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
@@ -562,7 +574,8 @@ __global__ void __launch_bounds__(256)
 
 template <bool kBf16>
 cudaError_t launch_split_reduce(const void* ws, void* out, int64_t T, int64_t H, int splits,
-                                float alpha, int num_sms, cudaStream_t stream) {
+                                float alpha, int num_sms, cudaStream_t stream,
+                                const CeRow* rows = nullptr) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -575,14 +588,15 @@ cudaError_t launch_split_reduce(const void* ws, void* out, int64_t T, int64_t H,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, split_reduce_kernel<kBf16>,
-                                       static_cast<const float4*>(ws), out, n4, n4, splits, alpha);
+                                       static_cast<const float4*>(ws), out, n4, n4, splits, alpha,
+                                       rows, uint32_t(H / 4));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
-int g_max_clusters[8][64];  // co-resident CTA pairs per kernel variant and device
+int g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
 
-template <bool kAMn, bool kBMn = true, bool kBf16 = false>
+template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
 cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, int num_sms,
                         cudaStream_t stream, void* d_bf16 = nullptr) {
     // D as [S][M][ldd] fp32, stored in 32 x 32 blocks; or bf16, in blocks of 32 x 64
@@ -596,7 +610,7 @@ cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, in
                     uint64_t(a.ldd) * 4,
                     uint64_t(a.split_stride ? a.split_stride : a.M * a.ldd) * 4);
     if (!mapped) return cudaErrorInvalidValue;
-    auto kernel = bwd_gemm_kernel<kAMn, kBMn, kBf16>;
+    auto kernel = bwd_gemm_kernel<kAMn, kBMn, kBf16, kFp16>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -614,7 +628,7 @@ cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, in
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    int& maxc = g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0) + (kBf16 ? 4 : 0)][dev];
+    int& maxc = g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0) + (kBf16 ? 4 : 0) + (kFp16 ? 8 : 0)][dev];
     if (maxc == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kSmemBytes));
@@ -744,8 +758,8 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
     return cudaSuccess;
 }
 
-cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, int64_t T, int64_t H,
-                                     int64_t rows, float alpha, void* grad, bool bf16,
+cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, const int* top, int64_t T,
+                                     int64_t H, int64_t rows, float alpha, void* grad, bool bf16,
                                      bool accumulate, int num_sms, cudaStream_t stream) {
     CUtensorMap ta, tb;
     if (!encode_tensor_map_2d(&ta, dzt, uint64_t(T), uint64_t(rows),
@@ -764,8 +778,9 @@ cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, int64_t T, 
     a.num_tiles = a.num_mu * a.num_n;
     a.alpha = alpha;
     a.add_in_l2 = accumulate ? 1 : 0;
-    return bf16 ? launch_gemm<false, true, true>(ta, tb, a, num_sms, stream, grad)
-                : launch_gemm<false>(ta, tb, a, num_sms, stream);
+    a.top = top;
+    return bf16 ? launch_gemm<false, true, true, true>(ta, tb, a, num_sms, stream, grad)
+                : launch_gemm<false, true, false, true>(ta, tb, a, num_sms, stream);
 }
 
 cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
@@ -793,10 +808,10 @@ cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz,
     return launch_gemm<false>(ta, tb, a, num_sms, stream);
 }
 
-cudaError_t launch_sum_parts(const float* sums, void* out, bool bf16, int64_t T, int64_t H,
-                             int parts, float alpha, int num_sms, cudaStream_t stream) {
-    return bf16 ? launch_split_reduce<true>(sums, out, T, H, parts, alpha, num_sms, stream)
-                : launch_split_reduce<false>(sums, out, T, H, parts, alpha, num_sms, stream);
+cudaError_t launch_sum_parts(const float* sums, const CeRow* rows, void* out, bool bf16, int64_t T,
+                             int64_t H, int parts, float alpha, int num_sms, cudaStream_t stream) {
+    return bf16 ? launch_split_reduce<true>(sums, out, T, H, parts, alpha, num_sms, stream, rows)
+                : launch_split_reduce<false>(sums, out, T, H, parts, alpha, num_sms, stream, rows);
 }
 
 cudaError_t bwd_gemm_take_error(unsigned int* out) {

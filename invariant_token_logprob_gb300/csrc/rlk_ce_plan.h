@@ -65,17 +65,20 @@ inline CePlan ce_plan(int64_t T, int64_t H, int64_t V) {
     return best;
 }
 
-// Workspace of the backward: dz [T][rows] and its transpose, bf16, then grad_h's sums
-// [parts][T][H] in fp32.
+// Workspace of the backward: dz [T][rows] and its transpose, 16 bits each, grad_h's sums
+// [parts][T][H] in fp32, h in fp16, and what belongs to a row (32 bytes) and to all (16).
 struct CeLayout {
-    size_t dzt, sums, bytes;  // offsets; dz lies at 0
+    size_t dzt, sums, h, rows, top, bytes;  // offsets; dz lies at 0
 };
 inline CeLayout ce_layout(int64_t T, int64_t H, const CePlan& p) {
     auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     CeLayout l;
     l.dzt = round(size_t(T) * size_t(p.rows) * 2);
     l.sums = l.dzt + round(size_t(p.rows) * size_t(ce_row_stride(T)) * 2);
-    l.bytes = l.sums + round(size_t(p.parts) * size_t(T) * size_t(H) * 4);
+    l.h = l.sums + round(size_t(p.parts) * size_t(T) * size_t(H) * 4);
+    l.rows = l.h + round(size_t(T) * size_t(H) * 2);
+    l.top = l.rows + round(size_t(T) * 32);
+    l.bytes = l.top + 256;
     return l;
 }
 

@@ -1,16 +1,22 @@
-// rlk_cross_entropy.cu -- what the cross entropy does behind the LM-head kernel: from each row's
-// records of the vocabulary's tiles {max, exp-sum, ., target's logit} to its log-sum-exp and loss
+// rlk_cross_entropy.cu -- what the cross entropy does around the LM-head kernel.
+//
+// Loss: from each row's records {max, exp-sum} of the vocabulary's half tiles and its target's z to
 //   loss = lse - (1 - e) z[target] - (e / V) sum_v z[v] + l lse^2       (e smoothing, l z loss)
-// and from the rows' losses to their weighted sum or mean.
+// and from the rows' losses to their weighted sum or mean.  One warp per row: the largest maximum
+// first, then sum_j s_j exp(m_j - M), a lane's records in order, the lanes in a butterfly; the sum
+// of z likewise.  These orders follow from V alone.  The sum over rows is one CTA: thread i adds
+// rows i, i + 1024, ... in order, then a fixed tree.
 //
-// The row kernel is the merge kernel's shape, one warp per row with its fixed tree, so the lse is
-// the log probability's bit for bit and, without smoothing and z loss, a loss of weight 1 is minus
-// the log probability.  sum z comes from one fp32 number per tile: a lane adds its tiles in order,
-// then the lanes meet in a butterfly.  Both orders follow from V alone.
+// Gradient: what each row's gradient with respect to its logits is made of (CeRow), and h in fp16.
+// One warp per row reads h and its target's row of W, for the target's probability.
 //
-// The sum over rows is one CTA: thread i adds rows i, i + 1024, ... in order, then a fixed tree.
-// Two small kernels next to the LM-head GEMM's 2 T H V operations: latency-bound, a few us each.
-#include "rlk_merge_row.cuh"
+// Small kernels next to the LM-head products' 2 T H V operations: latency-bound, a few us each, at
+// T = 4096, H = 4096 bounded by HBM (100 MB for the gradient's rows).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rlk_logits.cuh"
+#include "rlk_lse.cuh"
 #include "rlk_sm103.cuh"
 #include "rlk_train_int8.h"
 
@@ -23,26 +29,38 @@ constexpr int kSumThreads = 1024;
 // Rows whose target was >= V, counted since the last read.
 __device__ unsigned long long g_ce_range_rows;
 
+// The weight a row counts with: 0 where its target lies outside the vocabulary.
+__device__ __forceinline__ float row_weight(const float* weights, int64_t row, int32_t target, int V) {
+    if (target < 0 || target >= V) return 0.0f;
+    return weights ? __ldg(weights + row) : 1.0f;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
 struct LossArgs {
-    const float4* partials;
-    const float* sum_z;  // [T][nvt], with smoothing
+    const float2* records;  // [T][n]
+    const float* zt;
+    const float* sum_z;     // [T][n], with smoothing
     const int32_t* targets;
-    const float* weights;  // [T], or null: 1
+    const float* weights;   // [T], or null: 1
     float* row_losses;
     float* lse;
     float* loss;  // or null
     float* total;
     int64_t T;
-    int V, nvt;
+    int V, n;
     float smoothing, z_loss;
     int mean;
 };
-
-// The weight a row counts with: 0 where its target lies outside the vocabulary.
-__device__ __forceinline__ float row_weight(const LossArgs& p, int64_t row, int32_t target) {
-    if (target < 0 || target >= p.V) return 0.0f;
-    return p.weights ? __ldg(p.weights + row) : 1.0f;
-}
 
 template <bool kSmooth>
 __global__ void __launch_bounds__(kRowWarps * 32) row_loss_kernel(const LossArgs p) {
@@ -51,24 +69,36 @@ __global__ void __launch_bounds__(kRowWarps * 32) row_loss_kernel(const LossArgs
     const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
     if (row >= p.T) return;  // whole warp leaves together
     const int lane = threadIdx.x & 31;
-    float sum_z = 0.0f;
-    if constexpr (kSmooth) {
-        for (int j = lane; j < p.nvt; j += 32) sum_z += __ldg(p.sum_z + row * p.nvt + j);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) sum_z += __shfl_xor_sync(0xffffffffu, sum_z, off);
+    const float2* records = p.records + row * p.n;
+    const int32_t target = __ldg(p.targets + row);
+    float top = -INFINITY, sum = 0.0f, sum_z = 0.0f;
+#pragma unroll 8
+    for (int j = lane; j < p.n; j += 32) top = fmaxf(top, __ldg(&records[j].x));
+    top = warp_max(top);
+#pragma unroll 8
+    for (int j = lane; j < p.n; j += 32) {
+        const float2 r = __ldg(records + j);
+        sum += r.y * exp2f((r.x - top) * kLog2e);
     }
-    const MergedRow r = merge_records<false, false>(p.partials, nullptr, p.targets, row, p.T, p.V,
-                                                    p.nvt, 0);
+    sum = warp_sum(sum);
+    if constexpr (kSmooth) {
+#pragma unroll 8
+        for (int j = lane; j < p.n; j += 32) sum_z += __ldg(p.sum_z + row * p.n + j);
+        sum_z = warp_sum(sum_z);
+    }
     if (lane == 0) {
-        const float lse = r.m + logf(r.s);
-        const float w = row_weight(p, row, r.target);
+        const float log_sum = logf(sum);
+        const float lse = top + log_sum;
+        const float w = row_weight(p.weights, row, target, p.V);
         float loss = 0.0f;
         if (w != 0.0f) {
-            loss = -(r.zt - lse);
-            if constexpr (kSmooth) loss = fmaf(p.smoothing, r.zt - sum_z / float(p.V), loss);
-            loss = fmaf(p.z_loss * lse, lse, loss) * w;
+            const float zt = p.zt[row];
+            loss = (top - zt) + log_sum;  // (the first difference is exact where they are near)
+            if constexpr (kSmooth) loss = fmaf(p.smoothing, zt - sum_z / float(p.V), loss);
+            if (p.z_loss != 0.0f) loss = fmaf(p.z_loss * lse, lse, loss);
+            loss *= w;
         }
-        if (r.target >= p.V) atomicAdd(&g_ce_range_rows, 1ull);
+        if (target >= p.V) atomicAdd(&g_ce_range_rows, 1ull);
         p.lse[row] = lse;
         p.row_losses[row] = loss;
     }
@@ -81,21 +111,14 @@ __global__ void __launch_bounds__(kSumThreads) sum_loss_kernel(const LossArgs p)
     float2 v = make_float2(0.0f, 0.0f);  // losses, weights
     for (int64_t row = threadIdx.x; row < p.T; row += kSumThreads) {
         v.x += p.row_losses[row];
-        v.y += row_weight(p, row, __ldg(p.targets + row));
+        v.y += row_weight(p.weights, row, __ldg(p.targets + row), p.V);
     }
-    auto meet = [&]() {
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
-        }
-    };
-    meet();
+    v = make_float2(warp_sum(v.x), warp_sum(v.y));
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
         v = warps[threadIdx.x];
-        meet();
+        v = make_float2(warp_sum(v.x), warp_sum(v.y));
         if (threadIdx.x == 0) {
             *p.total = v.y;
             if (p.loss) *p.loss = !p.mean ? v.x : v.y > 0.0f ? v.x / v.y : 0.0f;
@@ -103,32 +126,138 @@ __global__ void __launch_bounds__(kSumThreads) sum_loss_kernel(const LossArgs p)
     }
 }
 
-}  // namespace
+// The exponent e of the least power of two that |x| (finite) lies below: |x| < 2^e.
+__device__ __forceinline__ int exponent_above(float x) {
+    return int((__float_as_uint(x) >> 23) & 255u) - 126;
+}
 
-cudaError_t launch_cross_entropy(const void* partials, const float* sum_z, const int32_t* targets,
-                                 const float* weights, int64_t T, int64_t V, float smoothing,
-                                 float z_loss, bool mean, float* row_losses, float* lse,
-                                 float* loss, float* total, cudaStream_t stream) {
-    const LossArgs p = {static_cast<const float4*>(partials), sum_z, targets, weights, row_losses,
-                        lse, loss, total, T, int(V), int((V + kVocabTile - 1) / kVocabTile),
-                        smoothing, z_loss, mean ? 1 : 0};
+__global__ void __launch_bounds__(kRowWarps * 32)
+    gradient_rows_kernel(const CeTerms p, const uint4* __restrict__ h, const uint4* __restrict__ W,
+                         int64_t T, int vecs, CeRow* __restrict__ rows, uint4* __restrict__ h_fp16,
+                         int* __restrict__ top) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    if (row >= T) return;  // whole warp leaves together
+    const int lane = threadIdx.x & 31;
+    const int32_t target = __ldg(p.targets + row);
+    const float w = row_weight(p.weights, row, target, p.V);
+    float a = __ldg(p.grad + (p.per_row ? row : 0)) * w;
+    if (p.total) {
+        const float total = __ldg(p.total);
+        a = total > 0.0f ? a / total : 0.0f;
+    }
+    const bool counts = w != 0.0f && a != 0.0f;
+    const uint4* hr = h + row * vecs;
+    const uint4* wr = W + int64_t(counts ? target : 0) * vecs;
+    float dot = 0.0f, amax = 0.0f;
+    if (counts) {
+#pragma unroll 4
+        for (int i = lane; i < vecs; i += 32) {
+            const uint4 x = __ldg(hr + i), y = __ldg(wr + i);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = pair_to_float(xs[j], __nv_bfloat16());
+                const float2 g = pair_to_float(ys[j], __nv_bfloat16());
+                dot = fmaf(f.x, g.x, dot);
+                dot = fmaf(f.y, g.y, dot);
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+        dot = warp_sum(dot);
+        amax = warp_max(amax);
+    }
+    const int h_exponent = exponent_above(amax);
+    CeRow r = {};
+    if (counts) {
+        r.lse = __ldg(p.lse + row);
+        r.p = a * fmaf(2.0f * p.z_loss, r.lse, 1.0f);
+        r.target = a * (1.0f - p.smoothing);
+        r.rest = a * (p.smoothing / float(p.V));
+        const int most = exponent_above(fabsf(r.p) + fabsf(r.target) + fabsf(r.rest));
+        // the target's element, and the factor that makes it a bf16 number
+        const float at_target =
+            fmaf(r.p, exp2f((dot * p.inv_temp - r.lse) * kLog2e), -r.rest) - r.target;
+        const float rounded = __bfloat162float(__float2bfloat16_rn(at_target));
+        float factor = rounded / at_target;
+        if (!(factor > 0.99f && factor < 1.01f)) factor = 1.0f;  // (0, tiny, or not finite)
+        r.p *= factor;
+        r.target *= factor;
+        r.rest *= factor;
+        r.inv_factor = 1.0f / factor;
+        r.h_exponent = h_exponent;
+        if (lane == 0 && h_fp16 && amax > 0.0f) atomicMax(top, most + h_exponent);
+    }
+    if (lane == 0) rows[row] = r;
+    if (h_fp16) {
+        // (rows that do not count as zeros, whatever they hold)
+        const float scale = ce_power(kCeTop - h_exponent);
+        uint4* out = h_fp16 + row * vecs;
+#pragma unroll 4
+        for (int i = lane; i < vecs; i += 32) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (counts) {
+                const uint4 x = __ldg(hr + i);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = pair_to_float(xs[j], __nv_bfloat16());
+                    const __half2 two = __floats2half2_rn(f.x * scale, f.y * scale);
+                    o[j] = *reinterpret_cast<const uint32_t*>(&two);
+                }
+                v = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            out[i] = v;
+        }
+    }
+}
+
+cudaLaunchConfig_t config(int64_t blocks, int threads, cudaLaunchAttribute* attr,
+                          cudaStream_t stream) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(unsigned((T + kRowWarps - 1) / kRowWarps), 1, 1);
-    cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
+    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_entropy(const float2* records, const float* zt, const float* sum_z,
+                                 const int32_t* targets, const float* weights, int64_t T, int64_t V,
+                                 float smoothing, float z_loss, bool mean, float* row_losses,
+                                 float* lse, float* loss, float* total, cudaStream_t stream) {
+    const LossArgs p = {records, zt, sum_z, targets, weights, row_losses, lse, loss, total, T,
+                        int(V), 2 * int((V + kVocabTile - 1) / kVocabTile), smoothing, z_loss,
+                        mean ? 1 : 0};
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
     cudaError_t e = sum_z ? cudaLaunchKernelEx(&cfg, row_loss_kernel<true>, p)
                           : cudaLaunchKernelEx(&cfg, row_loss_kernel<false>, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(kSumThreads, 1, 1);
+    cfg = config(1, kSumThreads, &attr, stream);
     e = cudaLaunchKernelEx(&cfg, sum_loss_kernel, p);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_cross_entropy_rows(const CeTerms& terms, const void* h, const void* W, int64_t T,
+                                      int64_t H, CeRow* rows, void* h_fp16, int* top,
+                                      cudaStream_t stream) {
+    cudaError_t e;
+    // (below every sum of two exponents: 0x80 four times)
+    if (h_fp16 && (e = cudaMemsetAsync(top, 0x80, sizeof(int), stream)) != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
+    e = cudaLaunchKernelEx(&cfg, gradient_rows_kernel, terms, static_cast<const uint4*>(h),
+                           static_cast<const uint4*>(W), T, int(H / 8), rows,
+                           static_cast<uint4*>(h_fp16), top);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t cross_entropy_take_range_rows(unsigned long long* out) {

@@ -83,29 +83,40 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
                                       int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
                                       cudaStream_t stream);
 
-// What the gradient of the cross entropy with respect to the logits depends on besides the
-// rows' lse and targets.  With a = g w (/ total):
-//   dz[v] = a (p[v] (1 + 2 z_loss lse) - (1 - smoothing) [v == target] - smoothing / V)
-struct CrossEntropyTerms {
-    const float* weights;  // [T], or null: 1
-    const float* total;    // the weights' sum, where the loss is their mean; else null
-    int per_row;           // the incoming gradient is [T], not one value
-    int V;                 // the whole vocabulary
-    float smoothing, z_loss;
-};
+// Cross entropy: records [T][2 NVT] {max, exp-sum} of z over the halves (128 columns) of the
+// vocabulary's tiles, zt [T] the z of targets inside [0, V), and, unless null, sum_z [T][2 NVT]
+// the halves' sums of z.
+cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
+                               float2* records, float* zt, float* sum_z, int64_t T, int64_t V,
+                               int64_t H, float inv_temp, int num_sms, cudaStream_t stream);
 
-// Forward records plus sum_z [T][NVT], the sum of z over each tile's columns.
-cudaError_t launch_lmhead_sum_z(const CUtensorMap* th, const CUtensorMap* tw,
-                                const int32_t* targets, void* partials, float* sum_z, int64_t T,
-                                int64_t V, int64_t H, float inv_temp, int num_sms,
-                                cudaStream_t stream);
+// A row of the cross entropy's backward (rlk_cross_entropy.cu).  The gradient with respect to its
+// logits, times a factor f, is p e^{z - lse} - rest - target [v == target].  dz holds it as bf16; f
+// lies next to 1 and makes the target's element, by far the largest, a bf16 number, so that one
+// is not rounded.  dz's transpose holds the gradient itself in fp16 (three bits more), times
+// 2^(kCeTop - top + h_exponent); h there is 2^(kCeTop - h_exponent) h, of magnitude up to 2^kCeTop,
+// so that the rows' products are all times 2^(2 kCeTop - top).  top is the largest exponent of a
+// row's gradient plus h_exponent: no number leaves fp16's range.
+struct CeRow {
+    float p, target, rest;
+    float lse;
+    float inv_factor;  // 1 / f; 0: the row does not count
+    int h_exponent;
+    int pad[2];
+};
+constexpr int kCeTop = 14;
+#ifdef __CUDACC__
+// 2^e, e held within the normal numbers' exponents.
+__device__ __forceinline__ float ce_power(int e) {
+    return __int_as_float((min(max(e, -126), 127) + 127) << 23);
+}
+#endif
+
 // dz [T][ldz] (and, with tdzt, its transpose) of the cross entropy for the vocabulary's entries
-// [first, first + rows), which tw maps; first is a multiple of kVocabTile.  0 in rows that do not
-// count (target outside the vocabulary, weight 0).
+// [first, first + rows), which tw maps; first is a multiple of kVocabTile.
 cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
                                     const CUtensorMap* tdzt, const int32_t* targets,
-                                    const float* lse, const float* grad,
-                                    const CrossEntropyTerms& terms, void* dz, int64_t ldz,
+                                    const CeRow* ce_rows, const int* ce_top, void* dz, int64_t ldz,
                                     int64_t T, int64_t first, int64_t rows, int64_t H,
                                     float inv_temp, int num_sms, cudaStream_t stream);
 
@@ -128,18 +139,20 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
                                float* grad_W, bool accumulate_W, void* split_ws, int num_sms,
                                cudaStream_t stream);
 // The same products for a piece of `rows` vocabulary entries (the cross entropy's backward).
-// grad [rows][H] (+)= alpha * dzt . h as bf16 (overwritten) or fp32; dzt [rows][backward_dz_ld(T)].
-cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, int64_t T, int64_t H,
-                                     int64_t rows, float alpha, void* grad, bool bf16,
+// grad [rows][H] (+)= alpha 2^(*top - 2 kCeTop) dzt . h as bf16 (overwritten) or fp32; dzt
+// [rows][backward_dz_ld(T)] and h [T][H] in fp16, as CeRow has them.
+cudaError_t launch_piece_grad_weight(const void* h_fp16, const void* dzt, const int* top, int64_t T,
+                                     int64_t H, int64_t rows, float alpha, void* grad, bool bf16,
                                      bool accumulate, int num_sms, cudaStream_t stream);
 // sums [.][T][H] (+)= dz . W, one sum per part_rows (a multiple of 64) of the piece's rows;
 // W [rows][H], dz [T][ldz].
 cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
                                      int64_t H, int64_t rows, int64_t part_rows, float* sums,
                                      bool add, int num_sms, cudaStream_t stream);
-// out [T][H] = alpha * (sums[0] + sums[1] + ...), in that order, as bf16 or fp32.
-cudaError_t launch_sum_parts(const float* sums, void* out, bool bf16, int64_t T, int64_t H,
-                             int parts, float alpha, int num_sms, cudaStream_t stream);
+// out [T][H] = alpha * inv_factor of the row * (sums[0] + sums[1] + ...), in that order, as bf16
+// or fp32; 0 for rows that do not count.
+cudaError_t launch_sum_parts(const float* sums, const CeRow* rows, void* out, bool bf16, int64_t T,
+                             int64_t H, int parts, float alpha, int num_sms, cudaStream_t stream);
 // Reads and clears the backward GEMM kernel's per-device error word (bit 0: a
 // bounded wait ran out; bit 1: a teardown wait ran out).
 cudaError_t bwd_gemm_take_error(unsigned int* out);

@@ -42,6 +42,7 @@
 // The accumulator is double-buffered in TMEM (2 x 256 columns) so the epilogue
 // of tile i overlaps the MMAs of tile i+1.  Every wait is bounded in time.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <limits.h>
 
 #include "rlk_fp8_quant.cuh"
@@ -68,6 +69,12 @@ constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kABytes = kBM * kBK * 2;  // 16 KiB
 constexpr int kThreads = 192;
+constexpr int kLossThreads = 320;  // mode 3: eight epilogue warps
+// Mode 3 takes a tile's accumulator out of tensor memory every so many k-blocks (512 k) and adds
+// the parts up in registers.  The tensor core cuts its fp32 additions off towards zero, so an
+// accumulator that runs over all of K falls short: by 3e-6 of the loss at K = 4096 (256
+// additions), a part of 512 k by a tenth of that.  The parts' additions round to nearest.
+constexpr int kLossPartKb = 8;
 // kHq: calls of at most kHqMaxRows rows with H <= kHqMaxH quantise h in the
 // kernel; the codes sit in a block of kHqRows rows (the 16-row box layout)
 constexpr int kHqRows = kMinTmaRows;
@@ -86,7 +93,7 @@ constexpr int kHqMaxH = 4096;
 // kHq (single CTA, e4m3, a handful of rows): the CTA quantises the call's h
 // rows itself into a resident shared-memory block of kHqRows rows x H codes
 // (laid out as the 16-row TMA boxes would land), and the stages carry W only.
-template <bool kPair, bool kHq = false>
+template <bool kPair, bool kHq = false, int kEpiWarps = 4>
 struct Pipe {
     static_assert(!(kPair && kHq), "in-kernel h quantisation: single CTA only");
     static constexpr int kBRows = kPair ? kBN / 2 : kBN;  // W rows one CTA stages
@@ -112,7 +119,7 @@ struct Pipe {
                                          size_t(kStages) * kStageBytes + kTransBytes +
                                          kBarriers * 8 + kWords * 4 + 16;
     static constexpr int kMmaM = kPair ? 2 * kBM : kBM;
-    static constexpr int kEpiArrivals = kPair ? 8 : 4;  // epilogue warps releasing a buffer
+    static constexpr int kEpiArrivals = kPair ? 2 * kEpiWarps : kEpiWarps;  // warps releasing a buffer
     static_assert(kStageBytes % 1024 == 0, "stage tiles 1024-B aligned");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -136,13 +143,17 @@ __device__ unsigned int g_lmhead_error;
 struct Args {
     const int32_t* targets;
     float4* partials;      // modes 0, 2: [T][num_n] records
-    float* ent_u;          // mode 2: [T][num_n] sum exp(z - m) (z - m) per tile; mode 3: sum z
-    const float* lse;      // modes 1, 4: forward LSE per row
-    const float* grad;     // mode 1: upstream gradient of logp per row; mode 4: of the loss
+    float* ent_u;          // mode 2: [T][num_n] sum exp(z - m) (z - m) per tile; mode 3, unless
+                           // null: [T][2 num_n] sum z of each half tile
+    const float* lse;      // mode 1: forward LSE per row
+    const float* grad;     // mode 1: upstream gradient of logp per row
     uint16_t* dz;          // modes 1, 4: [T][ldz] bf16 gradient w.r.t. the logits
     int64_t ldz;           // modes 1, 4: row stride of dz (a multiple of 8 elements)
     int write_dzt;         // modes 1, 4: also store dz transposed through tmap_x ([V][T])
-    CrossEntropyTerms ce;  // mode 4
+    float2* records;       // mode 3: [T][2 num_n] {max, exp-sum} of each half tile
+    float* zt;             // mode 3: [T] the target's z
+    const CeRow* ce_rows;  // mode 4: [T]
+    const int* ce_top;     // mode 4: see CeRow
     int64_t T;
     int64_t h_rows; // rows the h tensor map covers (>= T; padded copies are longer)
     int a_rows;     // rows of each h box (lmhead_a_box_rows(T))
@@ -226,7 +237,7 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity,
 constexpr int kModePartials = 0;   // forward: vocabulary-tile partial records
 constexpr int kModeGradLogits = 1; // backward: dz = g (onehot - exp(z - lse)) as bf16
 constexpr int kModeEntropy = 2;    // forward records plus the per-tile entropy statistic
-constexpr int kModeSumZ = 3;       // forward records plus the per-tile sum of z
+constexpr int kModeLoss = 3;       // cross entropy: records of half tiles, parts of K summed apart
 constexpr int kModeGradLoss = 4;   // cross entropy's backward: its dz for a piece of W's rows
 
 // kHq: the call's T (<= kHqMaxRows) h rows of H (<= kHqMaxH, a multiple of 128)
@@ -343,13 +354,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // quantiser kernel's arithmetic (same codes, same row scales), so a decode call
 // needs no quantiser launch; tmap_h is then unused.
 template <int kMode, bool kFp8, bool kPair, bool kHq = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 1)
     lmhead_kernel(const __grid_constant__ CUtensorMap tmap_h,
                   const __grid_constant__ CUtensorMap tmap_w,
                   const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     static_assert(!kFp8 || kMode == kModePartials, "fp8 operands: forward partials only");
     static_assert(!kHq || (kFp8 && !kPair), "in-kernel h quantisation: e4m3, single CTA");
-    using P = Pipe<kPair, kHq>;
+    using P = Pipe<kPair, kHq, kMode == kModeLoss ? 8 : 4>;
     constexpr int kG = kPair ? 2 : 1;  // tcgen05 CTA group
     constexpr int kStages = P::kStages;
     constexpr int kStageBytes = P::kStageBytes;
@@ -604,8 +615,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int tile = slot; ok && tile < ntiles; tile += nslots) {
                 if (!wait_bounded<kPair>(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) break;
                 tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + acc * uint32_t(kBN);
+                uint32_t d_tmem = tmem_base + acc * uint32_t(kBN);
+                int part_kb = 0;  // first k-block of the accumulator's part (mode 3)
                 for (int kb0 = 0; kb0 < p.num_kb; kb0 += kKbs) {
+                    if (kMode == kModeLoss && kb0 == part_kb + kLossPartKb) {
+                        // this part goes to the epilogue, the next one to the other accumulator
+                        if constexpr (kPair)
+                            umma_commit_pair_multicast(tfull_bar(acc), 0x3);
+                        else
+                            umma_commit(tfull_bar(acc));
+                        if (++acc == kAccBufs) {
+                            acc = 0;
+                            acc_phase ^= 1u;
+                        }
+                        if (!wait_bounded<kPair>(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        d_tmem = tmem_base + acc * uint32_t(kBN);
+                        part_kb = kb0;
+                    }
                     if (!wait_bounded(full_bar(stage), phase, abort_flag)) {
                         ok = false;
                         break;
@@ -627,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (kb | kk) != 0 ? 1u : 0u);
                             else
                                 umma_bf16<kG>(d_tmem, a_desc + off, b_desc + off, kIdescT,
-                                              (kb | kk) != 0 ? 1u : 0u);
+                                              ((kb - part_kb) | kk) != 0 ? 1u : 0u);
                         }
                     }
                     // frees the smem stage (in both CTAs of a pair) when these MMAs finish
@@ -690,18 +720,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                     row_scale = row < p.T ? __ldg(p.sh + row) : 0.0f;
             }
             int ok = 1;
+            if constexpr (kMode == kModeLoss) {
+                // Two warps share a quadrant, 128 columns each.
+                constexpr int kHalf = kBN / 2;
+                const int half = (warp - 2) >> 2;
+                float acc_z[kHalf];
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) acc_z[j] = 0.0f;
+                for (int kb0 = 0; kb0 < p.num_kb; kb0 += kLossPartKb) {
+                    if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, abort_flag) ? 1 : 0;
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t t_addr = lane_base + acc * uint32_t(kBN) + half * kHalf;
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(t_addr + uint32_t(c), r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc_z[c + j] = __fadd_rn(acc_z[c + j], __uint_as_float(r[j]));
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair)
+                            mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+                        else
+                            mbar_arrive(tempty_bar(acc));
+                    }
+                    if (++acc == kAccBufs) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                const int col0 = n * kBN + half * kHalf;
+                float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f, zt = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kHalf / 32; ++c) {
+                    float* z = acc_z + 32 * c;
+                    const int nvalid = p.V - (col0 + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        z[j] = j < nvalid ? __fmul_rn(z[j], inv_temp) : -INFINITY;
+                    float cm = z[0];
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
+                    if (p.ent_u) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) run_z += j < nvalid ? z[j] : 0.0f;
+                    }
+                    const int rel = tgt - (col0 + 32 * c);
+                    if (unsigned(rel) < 32u) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j == rel) zt = z[j];
+                    }
+                    float cs = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) cs += exp2f((z[j] - cm) * kLog2e);
+                    if (nvalid > 0) {
+                        const float m = fmaxf(run_m, cm);
+                        run_s = run_s * exp2f((run_m - m) * kLog2e) + cs * exp2f((cm - m) * kLog2e);
+                        run_m = m;
+                    }
+                }
+                if (row < p.T) {
+                    const int64_t at = row * (2 * int64_t(p.num_n)) + 2 * n + half;
+                    p.records[at] = make_float2(run_m, run_s);
+                    if (p.ent_u) p.ent_u[at] = run_z;
+                    if (unsigned(tgt - col0) < unsigned(kHalf) && tgt < p.V) p.zt[row] = zt;
+                }
+                __syncwarp();
+                continue;
+            }
             if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, abort_flag) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             tc_fence_after_sync();
 
-            if constexpr (kMode == kModePartials || kMode == kModeEntropy || kMode == kModeSumZ) {
+            if constexpr (kMode == kModeLoss) {
+            } else if constexpr (kMode == kModePartials || kMode == kModeEntropy) {
                 const int col0 = n * kBN;
                 const int ncols = min(kBN, p.V - col0);
                 const int nchunks = (ncols + 31) >> 5;
                 float run_m = -INFINITY, run_s = 0.0f, zt = 0.0f;
                 int32_t run_a = INT_MAX;
-                float run_u = 0.0f;  // modes 2 and 3 only
+                float run_u = 0.0f;  // mode 2 only
                 const uint32_t t_addr = lane_base + acc * uint32_t(kBN);
                 for (int c = 0; c < nchunks; ++c) {
                     uint32_t r[32];
@@ -746,7 +853,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cs += e;
                         if constexpr (kMode == kModeEntropy)
                             cu = (j < nvalid) ? fmaf(e, z[j] - cm, cu) : cu;
-                        if constexpr (kMode == kModeSumZ) cu = (j < nvalid) ? cu + z[j] : cu;
                     }
                     const int cbase = p.col_offset + col0 + c * 32;  // global column of j = 0
                     const int rel = tgt - cbase;
@@ -757,7 +863,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if constexpr (kMode == kModeEntropy)
                         run_u = lse_combine_u(run_m, run_s, run_a, run_u, cm, cs, cbase + ca, cu);
-                    if constexpr (kMode == kModeSumZ) run_u += cu;
                     lse_combine(run_m, run_s, run_a, cm, cs, cbase + ca);
                 }
                 // Accumulator buffer fully read: hand it back to the MMA warp.
@@ -772,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (row < p.T) {
                     p.partials[row * p.num_n + n] =
                         make_float4(run_m, run_s, __int_as_float(run_a), zt);
-                    if constexpr (kMode != kModePartials) p.ent_u[row * p.num_n + n] = run_u;
+                    if constexpr (kMode == kModeEntropy) p.ent_u[row * p.num_n + n] = run_u;
                 }
             } else {
                 const int col0 = n * kBN;
@@ -780,26 +885,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nchunks = (ncols + 31) >> 5;
                 const uint32_t t_addr = lane_base + acc * uint32_t(kBN);
                 const bool live = row < p.T;
-                // mode 4's rows of W are a piece of the vocabulary that begins at col_offset
-                bool valid = live && tgt >= 0 && tgt < (kMode == kModeGradLoss ? p.ce.V : p.V);
-                const float lse_row = live ? __ldg(p.lse + row) : 0.0f;
-                const float lse2 = lse_row * kLog2e;
-                float g = 0.0f;                          // mode 1: d/dlogp
-                float gp = 0.0f, gt = 0.0f, ge = 0.0f;   // mode 4: dz = gp p - gt [target] - ge
+                bool valid;
+                float lse2, g = 0.0f;
+                CeRow ce;                 // mode 4: dz = ce.p p - ce.target [target] - ce.rest
+                float dzt_scale = 0.0f;   // mode 4: dz times this goes to the transpose, as fp16
                 if constexpr (kMode == kModeGradLoss) {
-                    const float w = valid ? (p.ce.weights ? __ldg(p.ce.weights + row) : 1.0f) : 0.0f;
-                    valid = w != 0.0f;
-                    float a = __ldg(p.grad + (p.ce.per_row ? (live ? row : 0) : 0)) * w;
-                    if (p.ce.total) {
-                        const float total = __ldg(p.ce.total);
-                        a = total > 0.0f ? a / total : 0.0f;
-                    }
-                    gp = a * fmaf(2.0f * p.ce.z_loss, lse_row, 1.0f);
-                    gt = a * (1.0f - p.ce.smoothing);
-                    ge = a * (p.ce.smoothing / float(p.ce.V));
+                    if (live) ce = p.ce_rows[row];
+                    valid = live && ce.inv_factor != 0.0f;
+                    lse2 = valid ? ce.lse * kLog2e : 0.0f;
+                    if (valid && p.write_dzt)
+                        dzt_scale = ce.inv_factor * ce_power(kCeTop - *p.ce_top + ce.h_exponent);
                 } else {
+                    valid = live && tgt >= 0 && tgt < p.V;
                     g = valid ? __ldg(p.grad + row) : 0.0f;
+                    lse2 = live ? __ldg(p.lse + row) * kLog2e : 0.0f;
                 }
+                // mode 4's rows of W are a piece of the vocabulary that begins at col_offset
                 const int tgt_here = tgt - p.col_offset;
                 uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;  // 16-byte aligned rows
                 // transposed copy: this warp's 32 rows x 32 columns of a chunk are
@@ -812,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(t_addr + uint32_t(c * 32), r);
                     tmem_ld_wait();
                     const int cbase = col0 + c * 32;
-                    uint32_t packed[16];
+                    uint32_t packed[16], packed_t[kMode == kModeGradLoss ? 16 : 1];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float z0 = __uint_as_float(r[j]) * inv_temp;
@@ -822,10 +923,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float p1 = exp2f(fmaf(z1, kLog2e, -lse2));
                         float d0, d1;
                         if constexpr (kMode == kModeGradLoss) {
-                            d0 = valid ? fmaf(gp, p0, -ge) - (cbase + j == tgt_here ? gt : 0.0f)
-                                       : 0.0f;
-                            d1 = valid ? fmaf(gp, p1, -ge) - (cbase + j + 1 == tgt_here ? gt : 0.0f)
-                                       : 0.0f;
+                            d0 = fmaf(ce.p, p0, -ce.rest) - (cbase + j == tgt_here ? ce.target : 0.0f);
+                            d1 = fmaf(ce.p, p1, -ce.rest) -
+                                 (cbase + j + 1 == tgt_here ? ce.target : 0.0f);
+                            d0 = valid ? d0 : 0.0f;
+                            d1 = valid ? d1 : 0.0f;
+                            const __half2 two = __floats2half2_rn(d0 * dzt_scale, d1 * dzt_scale);
+                            packed_t[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
                         } else {
                             d0 = valid ? g * ((cbase + j == tgt ? 1.0f : 0.0f) - p0) : 0.0f;
                             d1 = valid ? g * ((cbase + j + 1 == tgt ? 1.0f : 0.0f) - p1) : 0.0f;
@@ -838,8 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            tblk[j * 32 + lane] =
-                                uint16_t((packed[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+                            tblk[j * 32 + lane] = uint16_t(
+                                ((kMode == kModeGradLoss ? packed_t[j / 2] : packed[j / 2]) >>
+                                 (16 * (j & 1))) &
+                                0xFFFFu);
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) {
@@ -904,8 +1010,8 @@ constexpr size_t kMaxSmemBytes = 227 * 1024;
 template <int kMode, bool kFp8, bool kPair, bool kHq = false>
 cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tx,
                            Args a, int64_t H, int num_sms, cudaStream_t stream) {
-    using P = Pipe<kPair, kHq>;
-    constexpr int kVariant = kMode >= kModeSumZ ? 9 + 2 * (kMode - kModeSumZ) + (kPair ? 1 : 0)
+    using P = Pipe<kPair, kHq, kMode == kModeLoss ? 8 : 4>;
+    constexpr int kVariant = kMode >= kModeLoss ? 9 + 2 * (kMode - kModeLoss) + (kPair ? 1 : 0)
                              : kHq              ? 8
                                                 : (kFp8 ? 3 : kMode) + (kPair ? 4 : 0);
     constexpr int kBKE = kFp8 ? 2 * kBK : kBK;
@@ -924,7 +1030,7 @@ cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const C
     attr[1].val.clusterDim.x = kPair ? 2 : 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kMode == kModeLoss ? kLossThreads : kThreads, 1, 1);
     cfg.dynamicSmemBytes = P::kSmemBytes + (kHq ? size_t(kHqRows) * size_t(H) : 0);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1013,18 +1119,19 @@ cudaError_t launch_lmhead_entropy(const CUtensorMap* th, const CUtensorMap* tw,
     return launch_mode<kModeEntropy>(th, tw, a, H, num_sms, stream);
 }
 
-cudaError_t launch_lmhead_sum_z(const CUtensorMap* th, const CUtensorMap* tw,
-                                const int32_t* targets, void* partials, float* sum_z, int64_t T,
-                                int64_t V, int64_t H, float inv_temp, int num_sms,
-                                cudaStream_t stream) {
+cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
+                               float2* records, float* zt, float* sum_z, int64_t T, int64_t V,
+                               int64_t H, float inv_temp, int num_sms, cudaStream_t stream) {
+    static_assert(kLossPartKb % Pipe<true>::kKbPerStage == 0, "parts are whole stages");
     Args a = {};
     a.targets = targets;
-    a.partials = static_cast<float4*>(partials);
+    a.records = records;
+    a.zt = zt;
     a.ent_u = sum_z;
     a.T = T;
     a.V = int(V);
     a.inv_temp = inv_temp;
-    return launch_mode<kModeSumZ>(th, tw, a, H, num_sms, stream);
+    return launch_mode<kModeLoss>(th, tw, a, H, num_sms, stream);
 }
 
 bool lmhead_fp8_quantises_h(int64_t T, int64_t H) {
@@ -1100,15 +1207,13 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
 
 cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
                                     const CUtensorMap* tdzt, const int32_t* targets,
-                                    const float* lse, const float* grad,
-                                    const CrossEntropyTerms& terms, void* dz, int64_t ldz,
+                                    const CeRow* ce_rows, const int* ce_top, void* dz, int64_t ldz,
                                     int64_t T, int64_t first, int64_t rows, int64_t H,
                                     float inv_temp, int num_sms, cudaStream_t stream) {
     Args a = {};
     a.targets = targets;
-    a.lse = lse;
-    a.grad = grad;
-    a.ce = terms;
+    a.ce_rows = ce_rows;
+    a.ce_top = ce_top;
     a.dz = static_cast<uint16_t*>(dz);
     a.ldz = ldz;
     a.write_dzt = tdzt ? 1 : 0;

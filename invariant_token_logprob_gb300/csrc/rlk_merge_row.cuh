@@ -51,21 +51,13 @@ struct MergeOut {
     unsigned long long* range_rows;  // rows whose target was >= V
 };
 
-// A row's merged records, the same in every lane, and its target's logit.
-struct MergedRow {
-    float m, s, u;
-    int32_t a, target;
-    bool inside;  // the target lies in [0, V)
-    float zt;     // its logit (0 outside)
-};
-
-// One warp merges `row` (every lane must call it).
+// One warp merges `row` (every lane must call it; lane 0 writes the outputs).
 template <bool kEntropy, bool kSharded>
-__device__ __forceinline__ MergedRow merge_records(const float4* __restrict__ partials,
-                                                   const float* __restrict__ ent_u,
-                                                   const int32_t* __restrict__ targets,
-                                                   int64_t row, int64_t T, int V, int nvt,
-                                                   int nvt_shard) {
+__device__ __forceinline__ void merge_row(const float4* __restrict__ partials,
+                                          const float* __restrict__ ent_u,
+                                          const int32_t* __restrict__ targets, int64_t row,
+                                          int64_t T, int V, int nvt, int nvt_shard,
+                                          const MergeOut& o) {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, s = 0.0f, u = 0.0f;
     int32_t a = INT_MAX;
@@ -127,29 +119,17 @@ __device__ __forceinline__ MergedRow merge_records(const float4* __restrict__ pa
         }
         lse_combine(m, s, a, mo, so, ao);
     }
-    return {m, s, u, a, tgt, tgt_in, zt};  // (zt: lane 0 has it whatever nvt)
-}
-
-// The same, and lane 0 writes the outputs.
-template <bool kEntropy, bool kSharded>
-__device__ __forceinline__ void merge_row(const float4* __restrict__ partials,
-                                          const float* __restrict__ ent_u,
-                                          const int32_t* __restrict__ targets, int64_t row,
-                                          int64_t T, int V, int nvt, int nvt_shard,
-                                          const MergeOut& o) {
-    const MergedRow r =
-        merge_records<kEntropy, kSharded>(partials, ent_u, targets, row, T, V, nvt, nvt_shard);
-    if ((threadIdx.x & 31) == 0) {
-        const float lse = r.m + logf(r.s);
+    if (lane == 0) {
+        const float lse = m + logf(s);
         float logp = 0.0f;
-        if (r.inside)
-            logp = r.zt - lse;
-        else if (r.target >= V)
+        if (tgt_in)
+            logp = zt - lse;
+        else if (tgt >= V)
             atomicAdd(o.range_rows, 1ull);
         o.logp[row] = logp;
         o.lse[row] = lse;
-        o.argmax[row] = r.a;
-        if constexpr (kEntropy) o.entropy[row] = logf(r.s) - r.u / r.s;
+        o.argmax[row] = a;
+        if constexpr (kEntropy) o.entropy[row] = logf(s) - u / s;
     }
 }
 

@@ -7,13 +7,30 @@
 
 namespace rlk {
 
-// Cross entropy: the rows' records (and sum_z, with smoothing) to log-sum-exps and losses.
-// row_losses [T] gets each row's weighted loss; total the weights' sum; loss (unless null) the
-// rows' sum, divided by total with `mean`.
-cudaError_t launch_cross_entropy(const void* partials, const float* sum_z, const int32_t* targets,
-                                 const float* weights, int64_t T, int64_t V, float smoothing,
-                                 float z_loss, bool mean, float* row_losses, float* lse,
-                                 float* loss, float* total, cudaStream_t stream);
+// Cross entropy: what launch_lmhead_loss leaves (sum_z with smoothing, else null) to log-sum-exps
+// and losses.  row_losses [T] gets each row's weighted loss; total the weights' sum; loss (unless
+// null) the rows' sum, divided by total with `mean`.
+cudaError_t launch_cross_entropy(const float2* records, const float* zt, const float* sum_z,
+                                 const int32_t* targets, const float* weights, int64_t T, int64_t V,
+                                 float smoothing, float z_loss, bool mean, float* row_losses,
+                                 float* lse, float* loss, float* total, cudaStream_t stream);
+
+// What the gradient of the cross entropy depends on.  With a = g w (/ total):
+//   dz[v] = a (p[v] (1 + 2 z_loss lse) - (1 - smoothing) [v == target] - smoothing / V)
+struct CeTerms {
+    const int32_t* targets;
+    const float* weights;  // [T], or null: 1
+    const float* lse;
+    const float* grad;     // [T], or one value
+    const float* total;    // where the loss is a mean; else null
+    int per_row;           // grad is [T]
+    int V;
+    float smoothing, z_loss, inv_temp;
+};
+// The rows of the backward, and, unless h_fp16 is null, h in fp16 and *top (see CeRow).
+cudaError_t launch_cross_entropy_rows(const CeTerms& terms, const void* h, const void* W, int64_t T,
+                                      int64_t H, CeRow* rows, void* h_fp16, int* top,
+                                      cudaStream_t stream);
 // Reads and clears the per-device count of rows whose target was >= V.  Synchronous.
 cudaError_t cross_entropy_take_range_rows(unsigned long long* out);
 

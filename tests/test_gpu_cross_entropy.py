@@ -2,17 +2,22 @@
 
 Tolerances.  A logit sums H exact products of bf16 numbers on the tensor core, 16 to an
 instruction; each of its additions loses at most 2^-22 of the magnitudes added so far (it may cut
-instead of rounding), the instruction's own sum included, so with A = inv_temp sum |h||W|
-  |z - z64| <= A (H/16 + 16) 2^-22 =: E_t                    (A: the row's largest)
-The log-sum-exp moves by at most E_t, and its own fp32 steps (exponentials of arguments rounded to
+instead of rounding), the instruction's own sum included.  The loss takes parts of 512 k, which
+fp32 additions join, the gradient's logits all of H: with A = inv_temp sum |h||W| (a row's largest)
+  loss:     |z - z64| <= A ((32 + 16) 2^-22 + (H/512 + 1) 2^-24) =: E
+  gradient: |z - z64| <= A (H/16 + 16) 2^-22                     =: G
+The log-sum-exp moves by at most E, and its own fp32 steps (exponentials of arguments rounded to
 2^-23 of their size, a tree of additions of positive numbers, one logarithm) by at most
-2^-19 (1 + |lse|).  The loss adds the target's logit (E_t), smoothing's mean (E_t and an fp32 sum of
-V numbers in chunks of 32, tiles and lanes: 2^-19 of the mean magnitude) and z_loss lse^2.
-In the gradients dz is rounded to bf16 (2^-8 of its value at most) and p is off by a relative
-E_t + 2^-18; the products' sums lose 2^-22 per instruction of 16, 2^-12 in all for the sizes here.
-With |dz| <= D := |a| (p (1 + 2 l lse) + (1 - e) [target] + e / V):
-  |grad_h - grad_h64| <= inv_temp (2^-8 + 2^-11 + E) D |W| + 2^-8 |grad_h64|
-and likewise for grad_W; 2^-11 is there for the terms above, the last term for bf16 outputs."""
+2^-19 (1 + |lse|).  The loss adds the target's logit (E), smoothing's mean (E and an fp32 sum of
+V numbers in chunks of 128, tiles and lanes: 2^-19 of the mean magnitude) and z_loss lse^2.
+In the gradients p is off by a relative G + 2^-18, and the products' sums lose 2^-22 per instruction
+of 16, 2^-12 in all for the sizes here.  For grad_h the gradient with respect to the logits is
+rounded to bf16 (2^-8 at most) but for the target's element, which is kept; for grad_W to fp16
+(2^-11), h is not, and what lies 2^-39 below the largest product of a row's gradient and hidden
+state may be lost.  With P := |a| (p (1 + 2 l lse) + e / V) and D := P + |a| (1 - e) [target]:
+  |grad_h - grad_h64| <= inv_temp (2^-8 P + (2^-11 + G) D) |W|
+  |grad_W - grad_W64| <= inv_temp ((2^-10 + G) D^T |h| + T 2^-36 max D max |h|)
+(2^-11 in each for the terms above), and the output's rounding, 2^-8 for bf16."""
 import math
 
 import numpy as np
@@ -62,7 +67,9 @@ class Ref:
         nll = self.lse - (1 - self.e) * self.zt - self.e * self.z.mean(1) + self.l * self.lse ** 2
         self.row = torch.where(self.w != 0, self.w * nll, torch.zeros_like(nll))
         self.total = self.w.sum()
-        self.E = ((self.h.abs() @ self.W.abs().T).amax(1) * it) * (h.shape[1] / 16 + 16) * 2.0 ** -22
+        A = (self.h.abs() @ self.W.abs().T).amax(1) * it
+        self.E = A * (48 * 2.0 ** -22 + (h.shape[1] / 512 + 1) * 2.0 ** -24)
+        self.G = A * (h.shape[1] / 16 + 16) * 2.0 ** -22
 
     def loss_bound(self):
         rows = 2 * self.E * (1 + 2 * self.l * self.lse.abs()) + 2.0 ** -19 * (
@@ -85,9 +92,12 @@ class Ref:
         hit = torch.zeros_like(p).scatter_(1, self.t[:, None], 1 - self.e)
         V = p.shape[1]
         dz = a[:, None] * (up - hit - self.e / V)
-        D = a.abs()[:, None] * (up.abs() + hit + self.e / V) * (2.0 ** -8 + 2.0 ** -11 + self.E)[:, None]
-        it = self.it
-        return (it * dz @ self.W, it * D @ self.W.abs()), (it * dz.T @ self.h, it * D.T @ self.h.abs())
+        P = a.abs()[:, None] * (up.abs() + self.e / V)
+        D = P + a.abs()[:, None] * hit
+        it, G = self.it, self.G[:, None]
+        floor = p.shape[0] * 2.0 ** -36 * (D.amax(1) * self.h.abs().amax(1)).max()
+        return ((it * dz @ self.W, it * (2.0 ** -8 * P + (2.0 ** -11 + G) * D) @ self.W.abs()),
+                (it * dz.T @ self.h, it * (((2.0 ** -10 + G) * D).T @ self.h.abs() + floor)))
 
 
 def within(got, want, bound, rounding=0.0, what=""):
@@ -162,18 +172,57 @@ def test_pieces_of_the_vocabulary(T, H, V):
     assert torch.equal(gh, again[0]) and torch.equal(gW, again[1])
 
 
-def test_bits_are_the_log_probabilities():
+def test_row_bits_do_not_depend_on_the_batch():
     import invariant_token_logprob_gb300 as rlk
-    h, W, t, _ = (None if x is None else x.cuda() for x in make(300, 256, 5003, 3, weighted=False))
-    lp, lse, _ = rlk.logprob(h, W, t, 0.8)
-    r = rlk.cross_entropy(h, W, t, inv_temp=0.8, reduction="none")
-    assert torch.equal(r.lse, lse) and torch.equal(r.loss, -lp + 0.0)
-    s = rlk.cross_entropy(h, W, t, inv_temp=0.8, label_smoothing=0.2, z_loss=1e-3, reduction="none")
-    assert torch.equal(s.lse, lse)
-    for n in (1, 7, 128, 200):  # single rows and both launch shapes
-        part = rlk.cross_entropy(h[:n].contiguous(), W, t[:n].contiguous(), inv_temp=0.8, label_smoothing=0.2,
-                                 z_loss=1e-3, reduction="none")
-        assert torch.equal(part.loss, s.loss[:n]) and torch.equal(part.lse, lse[:n])
+    for H in (256, 1032):
+        h, W, t, _ = (None if x is None else x.cuda() for x in make(300, H, 5003, 3, weighted=False))
+        lp, lse, _ = rlk.logprob(h, W, t, 0.8)
+        opts = dict(inv_temp=0.8, reduction="none")
+        r = rlk.cross_entropy(h, W, t, **opts)
+        ref = Ref(h, W, t, None, 0.8, 0.0, 0.0)
+        within(r.lse, lse.double(), ref.E + ref.G + 2.0 ** -19 * (1 + lse.double().abs()), what="the log probability's lse")
+        s = rlk.cross_entropy(h, W, t, label_smoothing=0.2, z_loss=1e-3, **opts)
+        assert torch.equal(s.lse, r.lse)
+        for n in (1, 7, 128, 200):  # single rows and both launch shapes
+            for o, full in ((dict(), r), (dict(label_smoothing=0.2, z_loss=1e-3), s)):
+                part = rlk.cross_entropy(h[:n].contiguous(), W, t[:n].contiguous(), **opts, **o)
+                assert torch.equal(part.loss, full.loss[:n]) and torch.equal(part.lse, full.lse[:n])
+
+
+def test_long_sums_stay_near():
+    """Logits that add up to one side over a long H, where cut additions would show: the loss keeps
+    fp32's nearness."""
+    import invariant_token_logprob_gb300 as rlk
+    g = torch.Generator().manual_seed(0)
+    T, H, V = 64, 8192, 600
+    W = (torch.rand(V, H, generator=g) / 64).bfloat16().cuda()
+    h = torch.rand(T, H, generator=g).bfloat16().cuda()
+    t = torch.randint(0, V, (T,), generator=g).to(torch.int32).cuda()
+    r = rlk.cross_entropy(h, W, t, reduction="none")
+    ref = Ref(h, W, t, None, 1.0, 0.0, 0.0)
+    assert ((r.lse.double() - ref.lse).abs() / ref.lse).max() < 1e-6  # 32 cuts of 2^-24 and the rest
+
+
+@pytest.mark.parametrize("spread", [0, 20, 60])
+def test_gradients_of_rows_far_apart(spread):
+    """Incoming gradients, hidden states and weights' rows that lie many powers of two apart, and
+    rows of zeros: every row keeps its own nearness."""
+    import invariant_token_logprob_gb300 as rlk
+    T, H, V = 140, 72, 515
+    h, W, t, _ = (None if x is None else x.cuda() for x in make(T, H, V, 6, weighted=False))
+    g = torch.Generator().manual_seed(spread)
+    rows = (2.0 ** torch.randint(-spread // 2, spread // 2 + 1, (T, 1), generator=g)).cuda()
+    grad = torch.randn(T, generator=g).cuda() * (2.0 ** torch.randint(-spread, spread + 1, (T,), generator=g)).cuda()
+    grad[4] = 0
+    h[5] = 0
+    h = torch.where(rows > 1, h, h * rows).bfloat16()  # (large ones would make one-hot softmaxes alone)
+    opts = dict(label_smoothing=0.1, reduction="none")
+    r = rlk.cross_entropy(h, W, t, **opts)
+    ref = Ref(h, W, t, None, 1.0, 0.1, 0.0, lse=r.lse)
+    (wh, bh), (wW, bW) = ref.grads(grad, "none")
+    gh, gW = rlk.cross_entropy_backward(h, W, t, r.lse, grad, **opts)
+    within(gh, wh, bh * (1 + 2.0 ** -8) + 1e-38, 2.0 ** -8, "grad_h")
+    within(gW, wW, bW * (1 + 2.0 ** -8) + 1e-38, 2.0 ** -8, "grad_W")
 
 
 def test_rows_that_do_not_count():
@@ -196,6 +245,13 @@ def test_rows_that_do_not_count():
     lse[idle] = float("nan")  # what such a row's logits gave does not matter
     gh, gW = rlk.cross_entropy_backward(h, W, t, lse, g, m.total, w, **opts)
     assert (gh[idle] == 0).all() and torch.isfinite(gW).all()
+    padded = h.clone()
+    padded[idle] = float("nan")  # nor what it holds
+    again = rlk.cross_entropy(padded, W, t, w, **opts)
+    rlk.take_device_errors()
+    assert torch.equal(again.loss, m.loss) and torch.equal(again.lse[~idle], m.lse[~idle])
+    ph, pW = rlk.cross_entropy_backward(padded, W, t, lse, g, m.total, w, **opts)
+    assert torch.equal(ph, gh) and torch.equal(pW, gW)
     nothing = torch.full_like(t, -100)
     for reduction in ("mean", "sum"):
         z = rlk.cross_entropy(h, W, nothing, w, reduction=reduction, **opts)
