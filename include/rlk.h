@@ -671,7 +671,7 @@ rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,
  *   dz[t][v] = a[t] (p (1 + 2 z_loss lse[t]) - (1 - e) [v == target[t]] - e / V)
  *   grad_hidden = inv_temp * dz . W      grad_weight (+)= inv_temp * dz^T . h
  * The logits are computed again, a piece of the vocabulary at a time; of dz a piece and its
- * transpose are held (256 MiB together, more only where 256 entries take more), 16 bits each, as
+ * transpose are held (512 MiB together, more only where 256 entries take more), 16 bits each, as
  * operands of the two products: for grad_hidden rounded once to bf16 but for each row's element at
  * its target, which a factor per row keeps whole; for grad_weight rounded once to fp16, under
  * powers of two that keep it in range (h is exact there).  The products sum in fp32 in an order

@@ -972,7 +972,8 @@ rlk_status check_cross_entropy(int64_t T, int64_t H, int64_t V, float inv_temp, 
     return RLK_OK;
 }
 
-// Workspace of the loss: records of half tiles, their sums of z, the targets' z, the rows' losses.
+// Workspace of the loss: records of half tiles, their sums of z, the targets' z, the rows' losses,
+// a counter.
 size_t ce_records(int64_t T, int64_t V) { return size_t(T) * 2 * size_t(num_vocab_tiles(V)); }
 
 }  // namespace
@@ -980,7 +981,7 @@ size_t ce_records(int64_t T, int64_t V) { return size_t(T) * 2 * size_t(num_voca
 size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V) {
     if (T <= 0 || V <= 0 || H <= 0) return 0;
     return ce_records(T, V) * sizeof(float2) + round16(ce_records(T, V) * sizeof(float)) +
-           2 * round16(size_t(T) * sizeof(float));
+           2 * round16(size_t(T) * sizeof(float)) + 16;
 }
 
 rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
@@ -1016,15 +1017,17 @@ rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
     float* sum_z = reinterpret_cast<float*>(records + ce_records(T, V));
     float* zt = sum_z + round16(ce_records(T, V) * sizeof(float)) / sizeof(float);
     float* rows = zt + round16(size_t(T) * sizeof(float)) / sizeof(float);
+    unsigned int* done =
+        reinterpret_cast<unsigned int*>(rows + round16(size_t(T) * sizeof(float)) / sizeof(float));
     if (label_smoothing == 0.0f) sum_z = nullptr;
-    cudaError_t e = rlk::launch_lmhead_loss(&th, &tw, targets_i32, records, zt, sum_z, T, V, H,
+    cudaError_t e = rlk::launch_lmhead_loss(&th, &tw, targets_i32, records, zt, sum_z, done, T, V, H,
                                             inv_temp, sms, s);
     if (e != cudaSuccess) return from_cuda(e);
     const bool none = reduction == RLK_NONE;
     return from_cuda(rlk::launch_cross_entropy(
         records, zt, sum_z, targets_i32, weights_f32, T, V, label_smoothing, z_loss,
         reduction == RLK_MEAN, none ? out_loss_f32 : rows, out_lse_f32,
-        none ? nullptr : out_loss_f32, out_total_f32, s));
+        none ? nullptr : out_loss_f32, out_total_f32, done, s));
 }
 
 size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V) {
@@ -1071,6 +1074,7 @@ rlk_status rlk_cross_entropy_backward(
     char* dzt = dz + layout.dzt;
     float* sums = reinterpret_cast<float*>(dz + layout.sums);
     rlk::CeRow* rows_info = reinterpret_cast<rlk::CeRow*>(dz + layout.rows);
+    int* tops = reinterpret_cast<int*>(dz + layout.tops);
     int* top = reinterpret_cast<int*>(dz + layout.top);
     void* h_fp16 = dz + layout.h;
     static_assert(sizeof(rlk::CeRow) == 32, "the layout's row");
@@ -1079,9 +1083,10 @@ rlk_status rlk_cross_entropy_backward(
                                 reduction == RLK_NONE ? 1 : 0, int(V), label_smoothing, z_loss,
                                 inv_temp};
     cudaError_t e = rlk::launch_cross_entropy_rows(terms, hidden_bf16, weight_bf16, T, H, rows_info,
-                                                   grad_weight ? h_fp16 : nullptr, top, s);
+                                                   grad_weight ? h_fp16 : nullptr, tops, s);
     if (e != cudaSuccess) return from_cuda(e);
     const int64_t part_rows = rlk::ce_part_rows(plan);
+    const bool whole = plan.pieces == 1 && plan.parts == 1;  // grad_h in one product, no sums
     for (int64_t v0 = 0; v0 < V; v0 += plan.rows) {
         const int64_t rows = V - v0 < plan.rows ? V - v0 : plan.rows;
         const char* w = static_cast<const char*>(weight_bf16) + size_t(v0) * size_t(H) * 2;
@@ -1089,19 +1094,22 @@ rlk_status rlk_cross_entropy_backward(
         if ((st = prepare_maps(hidden_bf16, w, T, H, rows, &th, &tw)) != RLK_OK) return st;
         if (grad_weight && !rlk::encode_dzt_store_map(&tdzt, dzt, T, rows)) return RLK_ERR_CUDA;
         e = rlk::launch_lmhead_grad_loss(&th, &tw, grad_weight ? &tdzt : nullptr, targets_i32,
-                                         rows_info, top, dz, plan.rows, T, v0, rows, H, inv_temp,
-                                         sms, s);
+                                         rows_info, tops, top, dz, plan.rows, T, v0, rows, H,
+                                         inv_temp, sms, s);
         if (e == cudaSuccess && grad_weight)
             e = rlk::launch_piece_grad_weight(
                 h_fp16, dzt, top, T, H, rows, inv_temp,
                 static_cast<char*>(grad_weight) + size_t(v0) * weight_row,
                 grad_weight_dtype == RLK_BF16, accumulate_grad_weight != 0, sms, s);
-        if (e == cudaSuccess && grad_hidden)
+        if (e == cudaSuccess && grad_hidden && whole)
+            e = rlk::launch_grad_hidden(w, dz, plan.rows, rows_info, T, H, rows, inv_temp,
+                                        grad_hidden, grad_hidden_dtype == RLK_BF16, sms, s);
+        else if (e == cudaSuccess && grad_hidden)
             e = rlk::launch_piece_grad_hidden(w, dz, plan.rows, T, H, rows, part_rows, sums, v0 > 0,
                                               sms, s);
         if (e != cudaSuccess) return from_cuda(e);
     }
-    if (!grad_hidden) return RLK_OK;
+    if (!grad_hidden || whole) return RLK_OK;
     const int64_t first = V < plan.rows ? V : plan.rows;
     return from_cuda(rlk::launch_sum_parts(sums, rows_info, grad_hidden,
                                            grad_hidden_dtype == RLK_BF16, T, H,

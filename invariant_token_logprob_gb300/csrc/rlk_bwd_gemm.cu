@@ -111,6 +111,7 @@ struct Args {
     int accumulate;        // D += alpha * acc instead of D = alpha * acc
     int add_in_l2;         // the same by adding stores (no read here), fp32 D
     const int* top;        // fp16 operands: alpha counts times 2^(*top - 2 kCeTop)
+    const CeRow* rows;     // unless null: alpha counts times the row's inv_factor (not accumulating)
     int stall_selftest;    // the producer issues no copies (bounded-wait self-test)
 };
 
@@ -402,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;  // TMEM lane quadrant this warp may access
         const int row_in_tile = q * 32 + lane;
         const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16);
-        const float alpha =
-            kFp16 ? p.alpha * ce_power(*p.top - 2 * kCeTop) : p.alpha;
+        const float alpha_all = kFp16 ? p.alpha * ce_power(*p.top - 2 * kCeTop) : p.alpha;
         // the output is written once and not read back here: evict it first
         const uint64_t store_policy = l2_policy_evict_first();
         // This warp's staging block: its 32 rows x 32 columns of one chunk,
@@ -418,6 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             unit_coords(p, tile, s, mu, n);
             const int64_t row = int64_t(2 * mu + int(rank)) * kUM + row_in_tile;
             const bool live = row < p.M;
+            const float alpha =
+                p.rows ? (live ? alpha_all * __ldg(&p.rows[row].inv_factor) : 0.0f) : alpha_all;
             int ok = 1;
             if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, abort_flag) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -781,6 +783,30 @@ cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, const int* 
     a.top = top;
     return bf16 ? launch_gemm<false, true, true, true>(ta, tb, a, num_sms, stream, grad)
                 : launch_gemm<false, true, false, true>(ta, tb, a, num_sms, stream);
+}
+
+cudaError_t launch_grad_hidden(const void* W, const void* dz, int64_t ldz, const CeRow* row_info,
+                               int64_t T, int64_t H, int64_t rows, float alpha, void* out, bool bf16,
+                               int num_sms, cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!encode_tensor_map_2d(&ta, dz, uint64_t(rows), uint64_t(T), uint64_t(ldz) * 2, kBK, kUM,
+                              false) ||
+        !encode_tensor_map_2d(&tb, W, uint64_t(H), uint64_t(rows), uint64_t(H) * 2, kMnAtom, kBK,
+                              false))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.d = bf16 ? nullptr : static_cast<float*>(out);
+    a.ldd = H;
+    a.M = int(T);
+    a.N = int(H);
+    a.num_kb = a.kb_per_split = int(cdiv(rows, kBK));
+    a.num_mu = int(cdiv(T, 2 * kUM));
+    a.num_n = int(cdiv(H, kUN));
+    a.num_tiles = a.num_mu * a.num_n;
+    a.alpha = alpha;
+    a.rows = row_info;
+    return bf16 ? launch_gemm<false, true, true>(ta, tb, a, num_sms, stream, out)
+                : launch_gemm<false>(ta, tb, a, num_sms, stream);
 }
 
 cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,

@@ -4,8 +4,8 @@
 //   loss = lse - (1 - e) z[target] - (e / V) sum_v z[v] + l lse^2       (e smoothing, l z loss)
 // and from the rows' losses to their weighted sum or mean.  One warp per row: the largest maximum
 // first, then sum_j s_j exp(m_j - M), a lane's records in order, the lanes in a butterfly; the sum
-// of z likewise.  These orders follow from V alone.  The sum over rows is one CTA: thread i adds
-// rows i, i + 1024, ... in order, then a fixed tree.
+// of z likewise.  These orders follow from V alone.  The rows' sum is the last CTA's, in an order
+// fixed by T, whichever CTA that is.
 //
 // Gradient: what each row's gradient with respect to its logits is made of (CeRow), and h in fp16.
 // One warp per row reads h and its target's row of W, for the target's probability.
@@ -14,6 +14,7 @@
 // T = 4096, H = 4096 bounded by HBM (100 MB for the gradient's rows).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 
 #include "rlk_logits.cuh"
 #include "rlk_lse.cuh"
@@ -24,7 +25,6 @@ namespace rlk {
 namespace {
 
 constexpr int kRowWarps = 8;
-constexpr int kSumThreads = 1024;
 
 // Rows whose target was >= V, counted since the last read.
 __device__ unsigned long long g_ce_range_rows;
@@ -60,15 +60,12 @@ struct LossArgs {
     int V, n;
     float smoothing, z_loss;
     int mean;
+    unsigned int* done;  // CTAs whose rows are written; the LM-head kernel before has set it to 0
 };
 
+// By one warp.
 template <bool kSmooth>
-__global__ void __launch_bounds__(kRowWarps * 32) row_loss_kernel(const LossArgs p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (row >= p.T) return;  // whole warp leaves together
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void row_loss(const LossArgs& p, int64_t row, int lane) {
     const float2* records = p.records + row * p.n;
     const int32_t target = __ldg(p.targets + row);
     float top = -INFINITY, sum = 0.0f, sum_z = 0.0f;
@@ -104,25 +101,36 @@ __global__ void __launch_bounds__(kRowWarps * 32) row_loss_kernel(const LossArgs
     }
 }
 
-__global__ void __launch_bounds__(kSumThreads) sum_loss_kernel(const LossArgs p) {
-    __shared__ float2 warps[kSumThreads / 32];
+template <bool kSmooth>
+__global__ void __launch_bounds__(kRowWarps * 32) row_loss_kernel(const LossArgs p) {
     grid_dependency_wait();
     grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    if (row < p.T) row_loss<kSmooth>(p, row, lane);
+    // The last CTA to get here adds the rows up, thread i rows i, i + 256, ... in order.
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    __shared__ float2 warps[kRowWarps];
     float2 v = make_float2(0.0f, 0.0f);  // losses, weights
-    for (int64_t row = threadIdx.x; row < p.T; row += kSumThreads) {
-        v.x += p.row_losses[row];
-        v.y += row_weight(p.weights, row, __ldg(p.targets + row), p.V);
+#pragma unroll 4
+    for (int64_t r = threadIdx.x; r < p.T; r += kRowWarps * 32) {
+        v.x += __ldcg(p.row_losses + r);
+        v.y += row_weight(p.weights, r, __ldg(p.targets + r), p.V);
     }
     v = make_float2(warp_sum(v.x), warp_sum(v.y));
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+    if (lane == 0) warps[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        v = warps[threadIdx.x];
-        v = make_float2(warp_sum(v.x), warp_sum(v.y));
-        if (threadIdx.x == 0) {
-            *p.total = v.y;
-            if (p.loss) *p.loss = !p.mean ? v.x : v.y > 0.0f ? v.x / v.y : 0.0f;
-        }
+    if (threadIdx.x == 0) {
+        v = warps[0];
+        for (int w = 1; w < kRowWarps; ++w) v = make_float2(v.x + warps[w].x, v.y + warps[w].y);
+        *p.total = v.y;
+        if (p.loss) *p.loss = !p.mean ? v.x : v.y > 0.0f ? v.x / v.y : 0.0f;
     }
 }
 
@@ -134,7 +142,7 @@ __device__ __forceinline__ int exponent_above(float x) {
 __global__ void __launch_bounds__(kRowWarps * 32)
     gradient_rows_kernel(const CeTerms p, const uint4* __restrict__ h, const uint4* __restrict__ W,
                          int64_t T, int vecs, CeRow* __restrict__ rows, uint4* __restrict__ h_fp16,
-                         int* __restrict__ top) {
+                         int* __restrict__ tops) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
@@ -170,6 +178,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     }
     const int h_exponent = exponent_above(amax);
     CeRow r = {};
+    int top = INT_MIN;
     if (counts) {
         r.lse = __ldg(p.lse + row);
         r.p = a * fmaf(2.0f * p.z_loss, r.lse, 1.0f);
@@ -187,9 +196,12 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         r.rest *= factor;
         r.inv_factor = 1.0f / factor;
         r.h_exponent = h_exponent;
-        if (lane == 0 && h_fp16 && amax > 0.0f) atomicMax(top, most + h_exponent);
+        if (amax > 0.0f) top = most + h_exponent;
     }
-    if (lane == 0) rows[row] = r;
+    if (lane == 0) {
+        rows[row] = r;
+        tops[row] = top;
+    }
     if (h_fp16) {
         // (rows that do not count as zeros, whatever they hold)
         const float scale = ce_power(kCeTop - h_exponent);
@@ -232,31 +244,26 @@ cudaLaunchConfig_t config(int64_t blocks, int threads, cudaLaunchAttribute* attr
 cudaError_t launch_cross_entropy(const float2* records, const float* zt, const float* sum_z,
                                  const int32_t* targets, const float* weights, int64_t T, int64_t V,
                                  float smoothing, float z_loss, bool mean, float* row_losses,
-                                 float* lse, float* loss, float* total, cudaStream_t stream) {
+                                 float* lse, float* loss, float* total, unsigned int* done,
+                                 cudaStream_t stream) {
     const LossArgs p = {records, zt, sum_z, targets, weights, row_losses, lse, loss, total, T,
                         int(V), 2 * int((V + kVocabTile - 1) / kVocabTile), smoothing, z_loss,
-                        mean ? 1 : 0};
+                        mean ? 1 : 0, done};
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
+    const cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
     cudaError_t e = sum_z ? cudaLaunchKernelEx(&cfg, row_loss_kernel<true>, p)
                           : cudaLaunchKernelEx(&cfg, row_loss_kernel<false>, p);
-    if (e != cudaSuccess) return e;
-    cfg = config(1, kSumThreads, &attr, stream);
-    e = cudaLaunchKernelEx(&cfg, sum_loss_kernel, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_cross_entropy_rows(const CeTerms& terms, const void* h, const void* W, int64_t T,
-                                      int64_t H, CeRow* rows, void* h_fp16, int* top,
+                                      int64_t H, CeRow* rows, void* h_fp16, int* tops,
                                       cudaStream_t stream) {
-    cudaError_t e;
-    // (below every sum of two exponents: 0x80 four times)
-    if (h_fp16 && (e = cudaMemsetAsync(top, 0x80, sizeof(int), stream)) != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
-    e = cudaLaunchKernelEx(&cfg, gradient_rows_kernel, terms, static_cast<const uint4*>(h),
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gradient_rows_kernel, terms, static_cast<const uint4*>(h),
                            static_cast<const uint4*>(W), T, int(H / 8), rows,
-                           static_cast<uint4*>(h_fp16), top);
+                           static_cast<uint4*>(h_fp16), tops);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -28,6 +28,15 @@ __device__ __forceinline__ float scale_of(float amax) {
     return s > 0.0f ? s : 1.0f;
 }
 
+__device__ __forceinline__ uint32_t pack_pair(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&two);
+}
+__device__ __forceinline__ uint32_t pack_pair(float a, float b, __half) {
+    const __half2 two = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&two);
+}
+
 // A vector's elements as fp32.
 template <typename Elem>
 __device__ __forceinline__ void to_floats(const uint4& v, float (&f)[kVecElems<Elem>]) {
@@ -44,14 +53,35 @@ __device__ __forceinline__ void to_floats(const uint4& v, float (&f)[kVecElems<E
     }
 }
 
-// The largest magnitude of a vector's elements and of m.
+// The largest magnitude of elements, as they lie in memory: of 16-bit ones by pairs, which keeps
+// their fp32 values out of the registers until the codes (146 registers, one row's warps fewer per
+// SM, 371 us for N = 151936, K = 4096 otherwise).
 template <typename Elem>
-__device__ __forceinline__ float max_abs(const uint4& v, float m) {
-    float f[kVecElems<Elem>];
-    to_floats<Elem>(v, f);
-#pragma unroll
-    for (int i = 0; i < kVecElems<Elem>; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
+struct MaxAbs {
+    using Pair = typename PairOf<Elem>::type;
+    uint32_t w = 0;
+    __device__ __forceinline__ void add(uint32_t x) {
+        const uint32_t a = x & 0x7fff7fffu;
+        const Pair m = max_pair(*reinterpret_cast<const Pair*>(&w), *reinterpret_cast<const Pair*>(&a));
+        w = *reinterpret_cast<const uint32_t*>(&m);
+    }
+    __device__ __forceinline__ float value() const {
+        const float2 f = pair_to_float(w, Elem());
+        return fmaxf(f.x, f.y);
+    }
+};
+template <>
+struct MaxAbs<float> {
+    float m = 0.0f;
+    __device__ __forceinline__ void add(uint32_t x) { m = fmaxf(m, fabsf(__uint_as_float(x))); }
+    __device__ __forceinline__ float value() const { return m; }
+};
+template <typename Elem>
+__device__ __forceinline__ void add_vector(MaxAbs<Elem>& m, const uint4& v) {
+    m.add(v.x);
+    m.add(v.y);
+    m.add(v.z);
+    m.add(v.w);
 }
 
 // Two quotients x / s, rounded to whole numbers that stand in the low bits.
@@ -82,8 +112,7 @@ __device__ __forceinline__ void store_codes(const uint4& v, float s, float r, __
     for (int i = 0; i < n; i += 2) {
         uint32_t q[2];
         two_codes<kFast>(f[i], f[i + 1], s, r, q);
-        const __half2 two = __floats2half2_rn(__uint_as_float(q[0]) - kRint, __uint_as_float(q[1]) - kRint);
-        words[i / 2] = *reinterpret_cast<const uint32_t*>(&two);
+        words[i / 2] = pack_pair(__uint_as_float(q[0]) - kRint, __uint_as_float(q[1]) - kRint, __half());
     }
     if constexpr (n == 8)
         *reinterpret_cast<uint4*>(dst) = make_uint4(words[0], words[1], words[2], words[3]);
@@ -110,9 +139,9 @@ __device__ __forceinline__ void store_codes(const uint4& v, float s, float r, in
         *reinterpret_cast<uint32_t*>(dst) = words[0];
 }
 
-// kWarps warps per row (1 or 8).  kHeld: the row fits in their registers; else it is read twice.
+// kWarps warps per row (1, 2, 4 or 8).  kHeld: the row fits in their registers; else it is read twice.
 template <typename Elem, typename Code, int kWarps, bool kHeld>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 3 : 2)
     quantize_int8_kernel(const uint4* __restrict__ x, int64_t rows, int vecs,
                          Code* __restrict__ codes, float* __restrict__ scales) {
     constexpr int kRows = kThreads / 32 / kWarps;  // per CTA
@@ -123,20 +152,22 @@ __global__ void __launch_bounds__(kThreads)
     grid_launch_dependents();
     const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes;
     if (kWarps == 1 && row >= rows) return;
+    if (row >= rows) vecs = 0;  // (its warps are there for the barrier)
     const int at = threadIdx.x % kLanes;
     const uint4* src = x + row * vecs;
     uint4 v[kHeld ? kVecs : 1];
-    float amax = 0.0f;
+    MaxAbs<Elem> largest;
     if constexpr (kHeld) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
             v[i] = at + i * kLanes < vecs ? __ldg(src + at + i * kLanes) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) amax = max_abs<Elem>(v[i], amax);
+        for (int i = 0; i < kVecs; ++i) add_vector(largest, v[i]);
     } else {
 #pragma unroll 8
-        for (int i = at; i < vecs; i += kLanes) amax = max_abs<Elem>(__ldg(src + i), amax);
+        for (int i = at; i < vecs; i += kLanes) add_vector(largest, __ldg(src + i));
     }
+    float amax = largest.value();
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -144,10 +175,11 @@ __global__ void __launch_bounds__(kThreads)
         if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = amax;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, warp_max[w]);
+        for (int w = 0; w < kWarps; ++w)
+            amax = fmaxf(amax, warp_max[threadIdx.x / kLanes * kWarps + w]);
     }
     const float s = scale_of(amax);
-    if (at == 0) scales[row] = s;
+    if (at == 0 && row < rows) scales[row] = s;
     Code* dst = codes + row * vecs * n;
     auto store = [&](auto fast) {
         constexpr bool kFast = decltype(fast)::value;
@@ -169,41 +201,52 @@ __global__ void __launch_bounds__(kThreads)
         store(std::false_type());
 }
 
-// One warp per row, 16 codes per lane and step.
+// Byte j of `codes`, which hold codes plus 128, as fp32: under the exponent of 2^23, less 2^23 + 128.
+__device__ __forceinline__ float code_to_float(uint32_t codes, int j) {
+    return __uint_as_float(__byte_perm(codes, 0x4b000000u, 0x7440 + j)) - 8388736.0f;
+}
+
+// One warp per row, sixteen vectors of 8 codes per lane in flight, so that a 16-bit output's stores
+// are whole lines (16 codes per lane leave half lines per store: 325 us for N = 151936, K = 4096).
 template <typename Out>
 __global__ void __launch_bounds__(kThreads)
-    dequantize_int8_kernel(const uint4* __restrict__ codes, const float* __restrict__ scales,
+    dequantize_int8_kernel(const uint2* __restrict__ codes, const float* __restrict__ scales,
                            int64_t rows, int vecs, Out* __restrict__ out) {
     const int64_t row = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
     grid_dependency_wait();
     grid_launch_dependents();
     if (row >= rows) return;
     const float s = __ldg(scales + row);
-    const uint4* src = codes + row * vecs;
-    Out* dst = out + row * vecs * 16;
-#pragma unroll 4
-    for (int i = threadIdx.x % 32; i < vecs; i += 32) {
-        const uint4 v = __ldg(src + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        constexpr int kWords = 4 * sizeof(Out);
-        uint32_t r[kWords];
+    const uint2* src = codes + row * vecs;
+    Out* dst = out + row * vecs * 8;
+    constexpr int kFlight = 16;
+    for (int i0 = threadIdx.x % 32; i0 < vecs; i0 += 32 * kFlight) {
+        uint2 v[kFlight];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float a = __fmul_rn(float(int8_t(w[j / 4] >> (8 * (j % 4)))), s);
-            const float b = __fmul_rn(float(int8_t(w[j / 4] >> (8 * (j % 4) + 8))), s);
-            if constexpr (sizeof(Out) == 4) {
-                r[j] = __float_as_uint(a);
-                r[j + 1] = __float_as_uint(b);
-            } else {
-                const Out two[2] = {from_float<Out>(a), from_float<Out>(b)};
-                r[j / 2] = uint32_t(*reinterpret_cast<const uint16_t*>(&two[0])) |
-                           uint32_t(*reinterpret_cast<const uint16_t*>(&two[1])) << 16;
+        for (int f = 0; f < kFlight; ++f)
+            if (i0 + 32 * f < vecs) v[f] = __ldg(src + i0 + 32 * f);
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            if (i0 + 32 * f >= vecs) break;
+            const uint32_t w[2] = {v[f].x ^ 0x80808080u, v[f].y ^ 0x80808080u};
+            constexpr int kWords = 2 * sizeof(Out);
+            uint32_t r[kWords];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float a = __fmul_rn(code_to_float(w[j / 4], j % 4), s);
+                const float b = __fmul_rn(code_to_float(w[j / 4], j % 4 + 1), s);
+                if constexpr (sizeof(Out) == 4) {
+                    r[j] = __float_as_uint(a);
+                    r[j + 1] = __float_as_uint(b);
+                } else {
+                    r[j / 2] = pack_pair(a, b, Out());
+                }
             }
-        }
-        uint4* to = reinterpret_cast<uint4*>(dst + int64_t(i) * 16);
+            uint4* to = reinterpret_cast<uint4*>(dst + int64_t(i0 + 32 * f) * 8);
 #pragma unroll
-        for (int j = 0; j < kWords / 4; ++j)
-            to[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            for (int j = 0; j < kWords / 4; ++j)
+                to[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        }
     }
 }
 
@@ -215,14 +258,12 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     if (i >= vecs) return;
     const uint4 v = __ldg(codes + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u,
+                           v.w ^ 0x80808080u};
     uint32_t r[8];
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        const __half2 two = __floats2half2_rn(float(int8_t(w[j / 4] >> (8 * (j % 4)))),
-                                              float(int8_t(w[j / 4] >> (8 * (j % 4) + 8))));
-        r[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
-    }
+    for (int j = 0; j < 16; j += 2)
+        r[j / 2] = pack_pair(code_to_float(w[j / 4], j % 4), code_to_float(w[j / 4], j % 4 + 1), __half());
     out[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
     out[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
@@ -243,11 +284,15 @@ template <typename Elem, typename Code>
 cudaError_t quantize(const void* x, int64_t rows, int64_t K, Code* codes, float* scales,
                      cudaStream_t stream) {
     const int vecs = int(K / kVecElems<Elem>);
-    // one warp per row fills the GPU from some thousands of rows on
-    const bool wide = rows >= 2048 && vecs <= 32 * kVecs;
+    // The fewest warps that hold a row have the most bytes in flight each (N = 100000, K = 5152:
+    // two warps @@ us, eight 526); eight warps fill the GPU where rows are fewer than some thousands.
+    int warps = 1;
+    while (warps < 8 && (rows < 2048 || vecs > 32 * kVecs * warps)) warps *= 2;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(wide ? (rows + 7) / 8 : rows, &attr, stream);
-    auto kernel = wide                       ? quantize_int8_kernel<Elem, Code, 1, true>
+    const cudaLaunchConfig_t cfg = config((rows * warps + 7) / 8, &attr, stream);
+    auto kernel = warps == 1                 ? quantize_int8_kernel<Elem, Code, 1, true>
+                  : warps == 2               ? quantize_int8_kernel<Elem, Code, 2, true>
+                  : warps == 4               ? quantize_int8_kernel<Elem, Code, 4, true>
                   : vecs <= kThreads * kVecs ? quantize_int8_kernel<Elem, Code, 8, true>
                                              : quantize_int8_kernel<Elem, Code, 8, false>;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint4*>(x), rows, vecs,
@@ -288,8 +333,8 @@ cudaError_t launch_dequantize_int8(const int8_t* codes, const float* scales, int
                                    void* out, ElemType out_type, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config((N + 7) / 8, &attr, stream);
-    const uint4* c = reinterpret_cast<const uint4*>(codes);
-    const int vecs = int(K / 16);
+    const uint2* c = reinterpret_cast<const uint2*>(codes);
+    const int vecs = int(K / 8);
     cudaError_t e;
     if (out_type == ElemType::kBf16)
         e = cudaLaunchKernelEx(&cfg, dequantize_int8_kernel<__nv_bfloat16>, c, scales, N, vecs,

@@ -16,7 +16,7 @@
 //   warp 1     MMA issuer: 8 MMAs per stage, accumulators for 1024 k, two of them
 //   sets       of four warps, 64 columns each: a thread adds its channel's sums up in integers
 //   teams      of four warps, which take the stages in turn: a thread turns its channel's codes
-//              into numbers and stores them to the team's A buffer
+//              into numbers and stores them to one of two or four A buffers
 // Few tiles: K is cut into parts, one per CTA of a cluster, whose integers meet through
 // distributed shared memory.
 //
@@ -38,7 +38,7 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;
 
 constexpr bool fits(int room) {
     return int8_smem_bytes(room) <= 227 * 1024 && int8_tmem_cols(room) <= int(kTmemCols) &&
-           2 * (int8_stages(room) + int8_teams(room) + 2) + 1 <= kInt8MaxBarriers &&
+           2 * (int8_stages(room) + int8_number_bufs(room) + 2) + 1 <= kInt8MaxBarriers &&
            (room + kInt8MaxParts) * kInt8TileN * 4 <= int8_stages(room) * int8_stage_bytes(room);
 }
 static_assert(fits(16) && fits(32) && fits(64) && fits(128) && fits(192), "memory per CTA");
@@ -106,10 +106,12 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
     constexpr int kStages = int8_stages(kRoom);
     constexpr int kStageBytes = int8_stage_bytes(kRoom);
     constexpr int kTeams = int8_teams(kRoom), kSets = int8_sets(kRoom);
+    constexpr int kBufs = int8_number_bufs(kRoom);
+    constexpr uint32_t kNumberCols = kInt8NumberCols;
     constexpr int kMine = kRoom / kSets;  // columns of a set
     constexpr int kPiece = kSets > 1 ? 8 : 16;  // (registers)
     constexpr int kFirstTeamWarp = 2 + 4 * kSets;
-    constexpr uint32_t kDBase = kTeams * kInt8NumberCols;
+    constexpr uint32_t kDBase = kBufs * kNumberCols;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -120,11 +122,11 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const uint32_t bar0 = smem_u32(bars);
-    constexpr int kA = 2 * kStages, kD = kA + 2 * kTeams;
+    constexpr int kA = 2 * kStages, kD = kA + 2 * kBufs;
     auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
     auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (kStages + s); };
-    auto a_full = [&](uint32_t team) { return bar0 + 8 * (kA + team); };
-    auto a_empty = [&](uint32_t team) { return bar0 + 8 * (kA + kTeams + team); };
+    auto a_full = [&](uint32_t buf) { return bar0 + 8 * (kA + buf); };
+    auto a_empty = [&](uint32_t buf) { return bar0 + 8 * (kA + kBufs + buf); };
     auto d_full = [&](uint32_t d) { return bar0 + 8 * (kD + d); };
     auto d_empty = [&](uint32_t d) { return bar0 + 8 * (kD + 2 + d); };
     const uint32_t drain_bar = bar0 + 8 * (kD + 4);
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 4 + 1);  // the codes' readers, and the MMAs
         }
-        for (int i = 0; i < kTeams; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(a_full(i), 4);
             mbar_init(a_empty(i), 1);
         }
@@ -223,32 +225,38 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
         // (the whole warp runs the loop, so addresses are warp-uniform; one lane issues)
         const bool leader = elect_one();
         const uint32_t idesc = idesc_f16_f32(kInt8TileN, plan.mma_n);
-        uint32_t stage = 0, phase = 0, team = 0, team_phase = 0, d = 0, d_phase = 0;
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0, d = 0, d_phase = 0;
         bool ok = true;
         const int items = p.stall_selftest == 2 ? 0 : p.items;
         for (int item = first_item; ok && item < items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
                 const bool opens = (ks - k_first) % kInt8SumStages == 0;
                 const bool closes = (ks - k_first) % kInt8SumStages == kInt8SumStages - 1 || ks + 1 == k_last;
-                ok = warp_wait(full_bar(stage), phase) && warp_wait(a_full(team), team_phase) &&
+                ok = warp_wait(full_bar(stage), phase) &&
                      (!opens || warp_wait(d_empty(d), d_phase ^ 1u));
+                if (!ok) break;
+                const uint64_t x_desc =
+                    sw128_kmajor_desc(stage0 + stage * kStageBytes + kInt8CodeBytes);
+                const uint32_t d_tmem = tmem_base + kDBase + d * kRoom;
+                ok = warp_wait(a_full(buf), buf_phase);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (leader) {
-                    const uint64_t x_desc =
-                        sw128_kmajor_desc(stage0 + stage * kStageBytes + kInt8CodeBytes);
-                    const uint32_t a_tmem = tmem_base + team * kInt8NumberCols;
-                    const uint32_t d_tmem = tmem_base + kDBase + d * kRoom;
+                    const uint32_t a_tmem = tmem_base + buf * kNumberCols;
 #pragma unroll
                     for (int i = 0; i < kInt8StageK / 16; ++i)
                         umma_f16_tmem_a(d_tmem, a_tmem + i * 8,
                                         x_desc + uint64_t((i / 4 * kRoom * 128 + i % 4 * 32) >> 4),
                                         idesc, opens && i == 0 ? 0u : 1u);
-                    umma_commit(a_empty(team));
+                    umma_commit(a_empty(buf));
                     umma_commit(empty_bar(stage));
                     if (closes) umma_commit(d_full(d));
                 }
                 __syncwarp();
+                if (++buf == kBufs) {
+                    buf = 0;
+                    buf_phase ^= 1u;
+                }
                 if (closes && ++d == 2) {
                     d = 0;
                     d_phase ^= 1u;
@@ -256,10 +264,6 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
-                }
-                if (++team == kTeams) {
-                    team = 0;
-                    team_phase ^= 1u;
                 }
             }
         }
@@ -318,20 +322,20 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
     } else {
         // ------------------------------------------------------------ numbers
         const uint32_t team = uint32_t(warp - kFirstTeamWarp) / 4;
-        const uint32_t a_tmem = lane_base + team * kInt8NumberCols;
-        // The CTA's stages are numbered through all items; number i lies in ring place
-        // i % kStages and belongs to team i % kTeams.
-        uint32_t stage = 0, phase = 0, turn = 0, a_phase = 0;
+        // The CTA's stages are numbered through all items; number i lies in ring place i % kStages,
+        // belongs to team i % kTeams and goes to buffer i % kBufs.
+        uint32_t stage = 0, phase = 0, turn = 0, buf = 0, buf_phase = 0;
         bool ok = true;
         for (int item = first_item; ok && item < p.items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
                 if (turn == team) {
-                    ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
-                    if (!ok) break;
-                    tc_fence_after_sync();  // the MMAs that read the buffer come before the stores
                     // 16-byte pieces of the row, swizzled by its place among eight
                     const uint32_t codes = stage0 + stage * kStageBytes + row_in_tile * 128 +
                                            ((row_in_tile & 7) << 4);
+                    const uint32_t a_tmem = lane_base + buf * kNumberCols;
+                    ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(buf), buf_phase ^ 1u);
+                    if (!ok) break;
+                    tc_fence_after_sync();  // the MMAs that read the buffer come before the stores
 #pragma unroll
                     for (int c = 0; c < 8; c += 2) {
                         const uint4 v[2] = {load_shared_v4(codes ^ (c << 4)),
@@ -350,14 +354,17 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(a_full(team));
+                        mbar_arrive(a_full(buf));
                         mbar_arrive(empty_bar(stage));
                     }
-                    a_phase ^= 1u;
                 }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
+                }
+                if (++buf == kBufs) {
+                    buf = 0;
+                    buf_phase ^= 1u;
                 }
                 if (++turn == kTeams) turn = 0;
             }

@@ -21,15 +21,16 @@ constexpr int int8_room(int64_t rows) {
 constexpr int int8_sets(int room) { return room <= 64 ? 1 : room / 64; }
 constexpr int int8_teams(int room) { return room <= 128 ? 3 : 2; }
 constexpr int int8_warps(int room) { return 2 + 4 * (int8_sets(room) + int8_teams(room)); }
-constexpr int kInt8NumberCols = kInt8StageK / 2;
-constexpr int int8_tmem_cols(int room) { return 2 * room + int8_teams(room) * kInt8NumberCols; }
+constexpr int kInt8NumberCols = kInt8StageK / 2;  // a stage's numbers, two to a column
+constexpr int int8_number_bufs(int room) { return room <= 128 ? 4 : 2; }
+constexpr int int8_tmem_cols(int room) { return 2 * room + int8_number_bufs(room) * kInt8NumberCols; }
 
 constexpr int kInt8CodeBytes = kInt8TileN * kInt8StageK;
 constexpr int int8_stage_bytes(int room) { return kInt8CodeBytes + room * kInt8StageK * 2; }
 constexpr int int8_stages(int room) {
     return room == 16 ? 10 : room == 32 ? 8 : room == 64 ? 6 : room == 128 ? 4 : 3;
 }
-constexpr int kInt8MaxBarriers = 2 * 10 + 2 * 3 + 2 * 2 + 1;
+constexpr int kInt8MaxBarriers = 2 * 10 + 2 * 4 + 2 * 2 + 1;
 constexpr size_t int8_smem_bytes(int room) {
     return 1024 + size_t(int8_stages(room)) * int8_stage_bytes(room) + kInt8MaxBarriers * 8 + 16;
 }

@@ -85,10 +85,11 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
 
 // Cross entropy: records [T][2 NVT] {max, exp-sum} of z over the halves (128 columns) of the
 // vocabulary's tiles, zt [T] the z of targets inside [0, V), and, unless null, sum_z [T][2 NVT]
-// the halves' sums of z.
+// the halves' sums of z.  Sets *done to 0.
 cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
-                               float2* records, float* zt, float* sum_z, int64_t T, int64_t V,
-                               int64_t H, float inv_temp, int num_sms, cudaStream_t stream);
+                               float2* records, float* zt, float* sum_z, unsigned int* done,
+                               int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
+                               cudaStream_t stream);
 
 // A row of the cross entropy's backward (rlk_cross_entropy.cu).  The gradient with respect to its
 // logits, times a factor f, is p e^{z - lse} - rest - target [v == target].  dz holds it as bf16; f
@@ -113,10 +114,11 @@ __device__ __forceinline__ float ce_power(int e) {
 #endif
 
 // dz [T][ldz] (and, with tdzt, its transpose) of the cross entropy for the vocabulary's entries
-// [first, first + rows), which tw maps; first is a multiple of kVocabTile.
+// [first, first + rows), which tw maps; first is a multiple of kVocabTile.  With tdzt, writes the
+// largest of tops [T] to *top.
 cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
                                     const CUtensorMap* tdzt, const int32_t* targets,
-                                    const CeRow* ce_rows, const int* ce_top, void* dz, int64_t ldz,
+                                    const CeRow* ce_rows, const int* tops, int* top, void* dz, int64_t ldz,
                                     int64_t T, int64_t first, int64_t rows, int64_t H,
                                     float inv_temp, int num_sms, cudaStream_t stream);
 
@@ -144,6 +146,10 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
 cudaError_t launch_piece_grad_weight(const void* h_fp16, const void* dzt, const int* top, int64_t T,
                                      int64_t H, int64_t rows, float alpha, void* grad, bool bf16,
                                      bool accumulate, int num_sms, cudaStream_t stream);
+// out [T][H] = alpha * inv_factor of the row * dz . W, as bf16 or fp32; 0 for rows that do not count.
+cudaError_t launch_grad_hidden(const void* W, const void* dz, int64_t ldz, const CeRow* row_info,
+                               int64_t T, int64_t H, int64_t rows, float alpha, void* out, bool bf16,
+                               int num_sms, cudaStream_t stream);
 // sums [.][T][H] (+)= dz . W, one sum per part_rows (a multiple of 64) of the piece's rows;
 // W [rows][H], dz [T][ldz].
 cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,

@@ -153,7 +153,9 @@ struct Args {
     float2* records;       // mode 3: [T][2 num_n] {max, exp-sum} of each half tile
     float* zt;             // mode 3: [T] the target's z
     const CeRow* ce_rows;  // mode 4: [T]
-    const int* ce_top;     // mode 4: see CeRow
+    const int* ce_tops;    // mode 4: [T], whose largest is CeRow's top
+    int* ce_top;           // mode 4: where it is written
+    unsigned int* done;    // mode 3: set to 0
     int64_t T;
     int64_t h_rows; // rows the h tensor map covers (>= T; padded copies are longer)
     int a_rows;     // rows of each h box (lmhead_a_box_rows(T))
@@ -465,6 +467,9 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
     // written before this wait.
     grid_dependency_wait();
     grid_launch_dependents();
+    if constexpr (kMode == kModeLoss) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0u;
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -698,6 +703,22 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                             hq_scale);
             if (warp == 2 && lane == 0) mbar_arrive(hq_bar);  // after quantise_h_rows' barrier
         }
+        int ce_top = 0;
+        if constexpr (kMode == kModeGradLoss) {
+            if (p.write_dzt) {  // the largest of tops, by the four warps, while the first MMAs run
+                int* found = reinterpret_cast<int*>(trans);
+                ce_top = INT_MIN;
+#pragma unroll 8
+                for (int64_t r = threadIdx.x - 64; r < p.T; r += 128) ce_top = max(ce_top, __ldg(p.ce_tops + r));
+                ce_top = __reduce_max_sync(0xffffffffu, ce_top);
+                if (lane == 0) found[warp - 2] = ce_top;
+                named_barrier_sync(1, 128);
+                ce_top = max(max(found[0], found[1]), max(found[2], found[3]));
+                named_barrier_sync(1, 128);  // (read before the blocks go there)
+                if (ce_top == INT_MIN) ce_top = 0;
+                if (blockIdx.x == 0 && threadIdx.x == 64) *p.ce_top = ce_top;
+            }
+        }
         for (int tile = slot; tile < p.num_tiles; tile += nslots) {
             int mu, n;
             tile_coords(p, tile, mu, n);
@@ -894,7 +915,7 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                     valid = live && ce.inv_factor != 0.0f;
                     lse2 = valid ? ce.lse * kLog2e : 0.0f;
                     if (valid && p.write_dzt)
-                        dzt_scale = ce.inv_factor * ce_power(kCeTop - *p.ce_top + ce.h_exponent);
+                        dzt_scale = ce.inv_factor * ce_power(kCeTop - ce_top + ce.h_exponent);
                 } else {
                     valid = live && tgt >= 0 && tgt < p.V;
                     g = valid ? __ldg(p.grad + row) : 0.0f;
@@ -1120,14 +1141,16 @@ cudaError_t launch_lmhead_entropy(const CUtensorMap* th, const CUtensorMap* tw,
 }
 
 cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
-                               float2* records, float* zt, float* sum_z, int64_t T, int64_t V,
-                               int64_t H, float inv_temp, int num_sms, cudaStream_t stream) {
+                               float2* records, float* zt, float* sum_z, unsigned int* done,
+                               int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
+                               cudaStream_t stream) {
     static_assert(kLossPartKb % Pipe<true>::kKbPerStage == 0, "parts are whole stages");
     Args a = {};
     a.targets = targets;
     a.records = records;
     a.zt = zt;
     a.ent_u = sum_z;
+    a.done = done;
     a.T = T;
     a.V = int(V);
     a.inv_temp = inv_temp;
@@ -1207,13 +1230,14 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
 
 cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
                                     const CUtensorMap* tdzt, const int32_t* targets,
-                                    const CeRow* ce_rows, const int* ce_top, void* dz, int64_t ldz,
-                                    int64_t T, int64_t first, int64_t rows, int64_t H,
+                                    const CeRow* ce_rows, const int* tops, int* top, void* dz,
+                                    int64_t ldz, int64_t T, int64_t first, int64_t rows, int64_t H,
                                     float inv_temp, int num_sms, cudaStream_t stream) {
     Args a = {};
     a.targets = targets;
     a.ce_rows = ce_rows;
-    a.ce_top = ce_top;
+    a.ce_tops = tops;
+    a.ce_top = top;
     a.dz = static_cast<uint16_t*>(dz);
     a.ldz = ldz;
     a.write_dzt = tdzt ? 1 : 0;

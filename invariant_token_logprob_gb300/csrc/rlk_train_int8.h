@@ -9,11 +9,12 @@ namespace rlk {
 
 // Cross entropy: what launch_lmhead_loss leaves (sum_z with smoothing, else null) to log-sum-exps
 // and losses.  row_losses [T] gets each row's weighted loss; total the weights' sum; loss (unless
-// null) the rows' sum, divided by total with `mean`.
+// null) the rows' sum, divided by total with `mean`; done is the counter launch_lmhead_loss zeroes.
 cudaError_t launch_cross_entropy(const float2* records, const float* zt, const float* sum_z,
                                  const int32_t* targets, const float* weights, int64_t T, int64_t V,
                                  float smoothing, float z_loss, bool mean, float* row_losses,
-                                 float* lse, float* loss, float* total, cudaStream_t stream);
+                                 float* lse, float* loss, float* total, unsigned int* done,
+                                 cudaStream_t stream);
 
 // What the gradient of the cross entropy depends on.  With a = g w (/ total):
 //   dz[v] = a (p[v] (1 + 2 z_loss lse) - (1 - smoothing) [v == target] - smoothing / V)
@@ -27,9 +28,10 @@ struct CeTerms {
     int V;
     float smoothing, z_loss, inv_temp;
 };
-// The rows of the backward, and, unless h_fp16 is null, h in fp16 and *top (see CeRow).
+// The rows of the backward with tops [T], whose largest is `top` (see CeRow), and, unless h_fp16 is
+// null, h in fp16.
 cudaError_t launch_cross_entropy_rows(const CeTerms& terms, const void* h, const void* W, int64_t T,
-                                      int64_t H, CeRow* rows, void* h_fp16, int* top,
+                                      int64_t H, CeRow* rows, void* h_fp16, int* tops,
                                       cudaStream_t stream);
 // Reads and clears the per-device count of rows whose target was >= V.  Synchronous.
 cudaError_t cross_entropy_take_range_rows(unsigned long long* out);

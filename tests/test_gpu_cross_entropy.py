@@ -149,7 +149,7 @@ def test_loss_and_gradients(shape, e, l, it, reduction):
     assert rlk.take_device_errors() == (0, 0)
 
 
-@pytest.mark.parametrize("T,H,V", [(2048, 64, 50000), (1100, 72, 77777), (4096, 256, 20001)])
+@pytest.mark.parametrize("T,H,V", [(2048, 64, 100000), (1100, 72, 150777), (4096, 256, 40001)])
 def test_pieces_of_the_vocabulary(T, H, V):
     """More than one piece, the last one short; every column counts exactly once."""
     import invariant_token_logprob_gb300 as rlk

@@ -132,8 +132,10 @@ int main() {
         }
         if (V <= 100 * p.rows && covered != V) return fail("covered", T, H, V);
         const CeLayout l = ce_layout(T, H, p);
-        if (l.dzt % 256 || l.sums % 256 || l.dzt < size_t(T) * p.rows * 2 ||
-            l.sums - l.dzt < size_t(p.rows) * ce_row_stride(T) * 2 || l.bytes - l.sums < size_t(p.parts) * T * H * 4)
+        if (l.dzt % 256 || l.sums % 256 || l.h % 256 || l.rows % 256 || l.tops % 256 || l.top % 256 ||
+            l.h - l.sums < size_t(p.parts) * T * H * 4 || l.rows - l.h < size_t(T) * H * 2 ||
+            l.tops - l.rows < size_t(T) * 32 || l.top - l.tops < size_t(T) * 4 || l.bytes - l.top < 4 || l.dzt < size_t(T) * p.rows * 2 ||
+            l.sums - l.dzt < size_t(p.rows) * ce_row_stride(T) * 2)
             return fail("layout", T, H, V);
     }
     return 0;
