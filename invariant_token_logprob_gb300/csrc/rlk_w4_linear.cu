@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
     constexpr float kUnit = Numbers<Elem>::kUnit;  // (a power of two: dividing is exact)
     constexpr uint32_t kIdesc =
         std::is_same<Elem, __half>::value ? idesc_f16_f32(kTileN, kN) : idesc_bf16_f32(kTileN, kN);
+    static_assert(kStages >= kTeams, "a team's wait for a stage is for the next phase");
     static_assert(kDs >= 2 && kGroups % kDGroups == 0 && kDBase + kDs * kDBufCols <= kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -541,7 +542,12 @@ __global__ void __launch_bounds__(32 * (first_team_warp(kCols) + kTeamWarps * nu
                         zero[g] = kZeros ? zeros[((row_first + uint32_t((ks - in_chunk) * kGroups)) & 3u) +
                                                  in_chunk * kGroups + g]
                                          : 8u;
-                    ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(team), a_phase ^ 1u);
+                    // A team skips the stages between its own, and a barrier tells two phases apart,
+                    // not three: that the stage that was in this place of the ring before has come
+                    // must be known before this one is waited for.  The team's buffer is free only
+                    // once the products of stage i - kTeams are done, hence that one's, and all
+                    // earlier stages', copies.
+                    ok = warp_wait(a_empty(team), a_phase ^ 1u) && warp_wait(full_bar(stage), phase);
                     if (!ok) break;
                     tc_fence_after_sync();  // the MMAs that read the buffer come before the stores
                     // 16-byte pieces of the row, swizzled by its place among eight
