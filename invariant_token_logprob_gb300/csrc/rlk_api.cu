@@ -1096,17 +1096,27 @@ rlk_status rlk_cross_entropy_backward(
         e = rlk::launch_lmhead_grad_loss(&th, &tw, grad_weight ? &tdzt : nullptr, targets_i32,
                                          rows_info, tops, top, dz, plan.rows, T, v0, rows, H,
                                          inv_temp, sms, s);
-        if (e == cudaSuccess && grad_weight)
-            e = rlk::launch_piece_grad_weight(
-                h_fp16, dzt, top, T, H, rows, inv_temp,
-                static_cast<char*>(grad_weight) + size_t(v0) * weight_row,
-                grad_weight_dtype == RLK_BF16, accumulate_grad_weight != 0, sms, s);
-        if (e == cudaSuccess && grad_hidden && whole)
-            e = rlk::launch_grad_hidden(w, dz, plan.rows, rows_info, T, H, rows, inv_temp,
-                                        grad_hidden, grad_hidden_dtype == RLK_BF16, sms, s);
-        else if (e == cudaSuccess && grad_hidden)
-            e = rlk::launch_piece_grad_hidden(w, dz, plan.rows, T, H, rows, part_rows, sums, v0 > 0,
-                                              sms, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        rlk::CePiece piece = {};
+        piece.T = T;
+        piece.H = H;
+        piece.rows = rows;
+        piece.alpha = inv_temp;
+        piece.h_fp16 = h_fp16;
+        piece.dzt = dzt;
+        piece.top = top;
+        if (grad_weight) piece.grad_weight = static_cast<char*>(grad_weight) + size_t(v0) * weight_row;
+        piece.weight_bf16 = grad_weight_dtype == RLK_BF16;
+        piece.accumulate_weight = accumulate_grad_weight != 0;
+        piece.W = w;
+        piece.dz = dz;
+        piece.ldz = plan.rows;
+        piece.row_info = rows_info;
+        if (grad_hidden) piece.grad_hidden = whole ? grad_hidden : sums;
+        piece.hidden_bf16 = whole && grad_hidden_dtype == RLK_BF16;
+        piece.add_hidden = v0 > 0;
+        piece.part_rows = whole ? 0 : part_rows;
+        e = rlk::launch_piece_products(piece, sms, s);
         if (e != cudaSuccess) return from_cuda(e);
     }
     if (!grad_hidden || whole) return RLK_OK;

@@ -163,11 +163,11 @@ __device__ __forceinline__ bool wait_limit(uint32_t bar, uint32_t parity, uint64
 
 // kBf16: D is bf16, rounded once from the fp32 accumulator.  kFp16: A and B are fp16, scaled by
 // powers of two (CeRow).
-template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
-__global__ void __launch_bounds__(kThreads, 1)
-    bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                    const __grid_constant__ CUtensorMap tmap_b,
-                    const __grid_constant__ CUtensorMap tmap_d, const Args p) {
+// A pair that is number `slot` of the `nslots` that share the product's units.
+template <bool kAMn, bool kBMn, bool kBf16, bool kFp16>
+__device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b,
+                                         const CUtensorMap& tmap_d, const Args& p, const int slot,
+                                         const int nslots) {
     constexpr uint32_t kIdesc = idesc_bf16_f32_major(2 * kUM, kUN, kAMn, kBMn) &
                                 (kFp16 ? ~((7u << 7) | (7u << 10)) : ~0u);  // (A, B format 0: fp16)
     extern __shared__ uint8_t smem_raw[];
@@ -227,8 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t rank = cluster_ctarank();
-    const int slot = int(cluster_id_x());
-    const int nslots = int(num_clusters_x());
     // Only shared memory, TMEM and parameters were touched so far: the launch
     // may overlap the previous kernel in the stream up to here.
     grid_dependency_wait();
@@ -536,6 +534,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
 }
 
+template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                    const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_d, const Args p) {
+    bwd_gemm<kAMn, kBMn, kBf16, kFp16>(tmap_a, tmap_b, tmap_d, p, int(cluster_id_x()),
+                                       int(num_clusters_x()));
+}
+
+struct Maps {
+    CUtensorMap a, b, d;
+};
+
+// Both products of the cross entropy's backward side by side, which do not depend on each other: the
+// first `pairs_w` pairs take grad_W's units, the others grad_h's.
+template <bool kWBf16, bool kHBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_two_kernel(const __grid_constant__ Maps mw, const __grid_constant__ Maps mh, const Args w,
+                   const Args h, const int pairs_w) {
+    const int pair = int(cluster_id_x());
+    if (pair < pairs_w)
+        bwd_gemm<false, true, kWBf16, true>(mw.a, mw.b, mw.d, w, pair, pairs_w);
+    else
+        bwd_gemm<false, true, kHBf16, false>(mh.a, mh.b, mh.d, h, pair - pairs_w,
+                                             int(num_clusters_x()) - pairs_w);
+}
+
 // out[i] = alpha * (ws[0][i] + ws[1][i] + ... + ws[S-1][i]), added in that order.
 // With `rows`, also times inv_factor of the element's row (row4 float4s long), 0 where it is 0.
 template <bool kBf16 = false>
@@ -596,58 +621,125 @@ cudaError_t launch_split_reduce(const void* ws, void* out, int64_t T, int64_t H,
     return cudaGetLastError();
 }
 
-int g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
-
-template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
-cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, int num_sms,
-                        cudaStream_t stream, void* d_bf16 = nullptr) {
-    // D as [S][M][ldd] fp32, stored in 32 x 32 blocks; or bf16, in blocks of 32 x 64
-    CUtensorMap td;
+// D as [S][M][ldd] fp32, stored in 32 x 32 blocks; or bf16, in blocks of 32 x 64.
+bool encode_output(CUtensorMap* td, const Args& a, void* d_bf16) {
     const int64_t splits = (a.num_kb + a.kb_per_split - 1) / a.kb_per_split;
-    const bool mapped =
-        kBf16 ? encode_tensor_map_bf16_3d(&td, d_bf16, uint64_t(a.N), uint64_t(a.M), 1,
-                                          uint64_t(a.ldd) * 2, uint64_t(a.M) * a.ldd * 2)
-              : encode_tensor_map_f32_3d(
-                    &td, a.d, uint64_t(a.N), uint64_t(a.M), uint64_t(splits),
-                    uint64_t(a.ldd) * 4,
-                    uint64_t(a.split_stride ? a.split_stride : a.M * a.ldd) * 4);
-    if (!mapped) return cudaErrorInvalidValue;
-    auto kernel = bwd_gemm_kernel<kAMn, kBMn, kBf16, kFp16>;
+    return d_bf16 ? encode_tensor_map_bf16_3d(td, d_bf16, uint64_t(a.N), uint64_t(a.M), 1,
+                                              uint64_t(a.ldd) * 2, uint64_t(a.M) * a.ldd * 2)
+                  : encode_tensor_map_f32_3d(
+                        td, a.d, uint64_t(a.N), uint64_t(a.M), uint64_t(splits),
+                        uint64_t(a.ldd) * 4,
+                        uint64_t(a.split_stride ? a.split_stride : a.M * a.ldd) * 4);
+}
+
+// The launch of `kernel` in pairs of CTAs, and how many pairs are resident at once (found once per
+// device, into max_pairs[dev]).
+template <typename Kernel>
+cudaError_t pair_config(Kernel kernel, int* max_pairs, int num_sms, cudaStream_t stream,
+                        cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int* pairs) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
+    *cfg = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    int& maxc = g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0) + (kBf16 ? 4 : 0) + (kFp16 ? 8 : 0)][dev];
+    cfg->blockDim = dim3(kThreads, 1, 1);
+    cfg->dynamicSmemBytes = kSmemBytes;
+    cfg->stream = stream;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+    int& maxc = max_pairs[dev];
     if (maxc == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kSmemBytes));
         if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+        cfg->gridDim = dim3(2 * (num_sms / 2), 1, 1);
         int nc = 0;
-        e = cudaOccupancyMaxActiveClusters(&nc, kernel, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&nc, kernel, cfg);
         if (e != cudaSuccess || nc < 1) {
             cudaGetLastError();
             nc = num_sms / 2;
         }
         maxc = nc;
     }
+    *pairs = maxc;
+    return cudaSuccess;
+}
+
+int g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
+
+template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
+cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, int num_sms,
+                        cudaStream_t stream, void* d_bf16 = nullptr) {
+    CUtensorMap td;
+    if (!encode_output(&td, a, d_bf16)) return cudaErrorInvalidValue;
+    auto kernel = bwd_gemm_kernel<kAMn, kBMn, kBf16, kFp16>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    int maxc = 0;
+    cudaError_t e = pair_config(
+        kernel, g_max_clusters[(kAMn ? 1 : 0) + (kBMn ? 2 : 0) + (kBf16 ? 4 : 0) + (kFp16 ? 8 : 0)],
+        num_sms, stream, &cfg, attr, &maxc);
+    if (e != cudaSuccess) return e;
     const int clusters = a.num_tiles < maxc ? a.num_tiles : maxc;
     if (clusters < 1) return cudaSuccess;
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, td, a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+int g_max_pairs_two[4][64];
+
+// Time of a product's units on `pairs` pairs, in blocks of k: a unit takes no less than its epilogue.
+int64_t rounds_time(const Args& a, int pairs) {
+    const int64_t unit = a.kb_per_split > 8 ? a.kb_per_split : 8;
+    return (a.num_tiles + pairs - 1) / pairs * unit;
+}
+
+// The split of the pairs that ends both products first; 0 where one after the other is as good.
+int pairs_for_first(const Args& w, const Args& h, int pairs) {
+    constexpr int64_t kLaunch = 11;  // blocks of k that a launch of its own takes
+    int best = 0;
+    int64_t best_time = (rounds_time(w, pairs) + rounds_time(h, pairs) + kLaunch) * 31 / 32;
+    for (int first = 1; first < pairs; ++first) {
+        const int64_t a = rounds_time(w, first), b = rounds_time(h, pairs - first);
+        const int64_t time = a > b ? a : b;
+        if (time < best_time) {
+            best_time = time;
+            best = first;
+        }
+    }
+    return best;
+}
+
+template <bool kWBf16, bool kHBf16>
+cudaError_t launch_both(Maps& mw, Maps& mh, const Args& w, const Args& h, void* w_bf16,
+                        void* h_bf16, int num_sms, cudaStream_t stream) {
+    auto kernel = bwd_two_kernel<kWBf16, kHBf16>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    int pairs = 0;
+    cudaError_t e = pair_config(kernel, g_max_pairs_two[(kWBf16 ? 1 : 0) + (kHBf16 ? 2 : 0)], num_sms,
+                                stream, &cfg, attr, &pairs);
+    if (e != cudaSuccess) return e;
+    const int first = pairs_for_first(w, h, pairs);
+    if (first == 0) {
+        e = launch_gemm<false, true, kWBf16, true>(mw.a, mw.b, w, num_sms, stream, w_bf16);
+        if (e != cudaSuccess) return e;
+        return launch_gemm<false, true, kHBf16, false>(mh.a, mh.b, h, num_sms, stream, h_bf16);
+    }
+    if (!encode_output(&mw.d, w, w_bf16) || !encode_output(&mh.d, h, h_bf16))
+        return cudaErrorInvalidValue;
+    const int pairs_w = w.num_tiles < first ? w.num_tiles : first;
+    const int pairs_h = h.num_tiles < pairs - first ? h.num_tiles : pairs - first;
+    cfg.gridDim = dim3(2 * (pairs_w + pairs_h), 1, 1);
+    e = cudaLaunchKernelEx(&cfg, kernel, mw, mh, w, h, pairs_w);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -760,78 +852,62 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
     return cudaSuccess;
 }
 
-cudaError_t launch_piece_grad_weight(const void* h, const void* dzt, const int* top, int64_t T,
-                                     int64_t H, int64_t rows, float alpha, void* grad, bool bf16,
-                                     bool accumulate, int num_sms, cudaStream_t stream) {
-    CUtensorMap ta, tb;
-    if (!encode_tensor_map_2d(&ta, dzt, uint64_t(T), uint64_t(rows),
-                              uint64_t(backward_dz_ld(T)) * 2, kBK, kUM, false) ||
-        !encode_tensor_map_2d(&tb, h, uint64_t(H), uint64_t(T), uint64_t(H) * 2, kMnAtom, kBK,
-                              false))
-        return cudaErrorInvalidValue;
-    Args a = {};
-    a.d = bf16 ? nullptr : static_cast<float*>(grad);
-    a.ldd = H;
-    a.M = int(rows);
-    a.N = int(H);
-    a.num_kb = a.kb_per_split = int(cdiv(T, kBK));
-    a.num_mu = int(cdiv(rows, 2 * kUM));
-    a.num_n = int(cdiv(H, kUN));
-    a.num_tiles = a.num_mu * a.num_n;
-    a.alpha = alpha;
-    a.add_in_l2 = accumulate ? 1 : 0;
-    a.top = top;
-    return bf16 ? launch_gemm<false, true, true, true>(ta, tb, a, num_sms, stream, grad)
-                : launch_gemm<false, true, false, true>(ta, tb, a, num_sms, stream);
-}
-
-cudaError_t launch_grad_hidden(const void* W, const void* dz, int64_t ldz, const CeRow* row_info,
-                               int64_t T, int64_t H, int64_t rows, float alpha, void* out, bool bf16,
-                               int num_sms, cudaStream_t stream) {
-    CUtensorMap ta, tb;
-    if (!encode_tensor_map_2d(&ta, dz, uint64_t(rows), uint64_t(T), uint64_t(ldz) * 2, kBK, kUM,
-                              false) ||
-        !encode_tensor_map_2d(&tb, W, uint64_t(H), uint64_t(rows), uint64_t(H) * 2, kMnAtom, kBK,
-                              false))
-        return cudaErrorInvalidValue;
-    Args a = {};
-    a.d = bf16 ? nullptr : static_cast<float*>(out);
-    a.ldd = H;
-    a.M = int(T);
-    a.N = int(H);
-    a.num_kb = a.kb_per_split = int(cdiv(rows, kBK));
-    a.num_mu = int(cdiv(T, 2 * kUM));
-    a.num_n = int(cdiv(H, kUN));
-    a.num_tiles = a.num_mu * a.num_n;
-    a.alpha = alpha;
-    a.rows = row_info;
-    return bf16 ? launch_gemm<false, true, true>(ta, tb, a, num_sms, stream, out)
-                : launch_gemm<false>(ta, tb, a, num_sms, stream);
-}
-
-cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
-                                     int64_t H, int64_t rows, int64_t part_rows, float* sums,
-                                     bool add, int num_sms, cudaStream_t stream) {
-    CUtensorMap ta, tb;
-    if (!encode_tensor_map_2d(&ta, dz, uint64_t(rows), uint64_t(T), uint64_t(ldz) * 2, kBK, kUM,
-                              false) ||
-        !encode_tensor_map_2d(&tb, W, uint64_t(H), uint64_t(rows), uint64_t(H) * 2, kMnAtom, kBK,
-                              false))
-        return cudaErrorInvalidValue;
-    Args a = {};
-    a.d = sums;
-    a.split_stride = T * H;
-    a.ldd = H;
-    a.M = int(T);
-    a.N = int(H);
-    a.num_kb = int(cdiv(rows, kBK));
-    a.kb_per_split = int(cdiv(part_rows, kBK));
-    a.num_mu = int(cdiv(T, 2 * kUM));
-    a.num_n = int(cdiv(H, kUN));
-    a.num_tiles = int(cdiv(a.num_kb, a.kb_per_split)) * a.num_mu * a.num_n;
-    a.alpha = 1.0f;
-    a.add_in_l2 = add ? 1 : 0;
-    return launch_gemm<false>(ta, tb, a, num_sms, stream);
+cudaError_t launch_piece_products(const CePiece& p, int num_sms, cudaStream_t stream) {
+    Maps mw, mh;
+    Args w = {}, h = {};
+    if (p.grad_weight) {
+        if (!encode_tensor_map_2d(&mw.a, p.dzt, uint64_t(p.T), uint64_t(p.rows),
+                                  uint64_t(backward_dz_ld(p.T)) * 2, kBK, kUM, false) ||
+            !encode_tensor_map_2d(&mw.b, p.h_fp16, uint64_t(p.H), uint64_t(p.T), uint64_t(p.H) * 2,
+                                  kMnAtom, kBK, false))
+            return cudaErrorInvalidValue;
+        w.d = p.weight_bf16 ? nullptr : static_cast<float*>(p.grad_weight);
+        w.ldd = p.H;
+        w.M = int(p.rows);
+        w.N = int(p.H);
+        w.num_kb = w.kb_per_split = int(cdiv(p.T, kBK));
+        w.num_mu = int(cdiv(p.rows, 2 * kUM));
+        w.num_n = int(cdiv(p.H, kUN));
+        w.num_tiles = w.num_mu * w.num_n;
+        w.alpha = p.alpha;
+        w.add_in_l2 = p.accumulate_weight ? 1 : 0;
+        w.top = p.top;
+    }
+    if (p.grad_hidden) {
+        if (!encode_tensor_map_2d(&mh.a, p.dz, uint64_t(p.rows), uint64_t(p.T), uint64_t(p.ldz) * 2,
+                                  kBK, kUM, false) ||
+            !encode_tensor_map_2d(&mh.b, p.W, uint64_t(p.H), uint64_t(p.rows), uint64_t(p.H) * 2,
+                                  kMnAtom, kBK, false))
+            return cudaErrorInvalidValue;
+        h.d = p.hidden_bf16 ? nullptr : static_cast<float*>(p.grad_hidden);
+        h.ldd = p.H;
+        h.M = int(p.T);
+        h.N = int(p.H);
+        h.num_kb = int(cdiv(p.rows, kBK));
+        h.kb_per_split = p.part_rows ? int(cdiv(p.part_rows, kBK)) : h.num_kb;
+        h.split_stride = p.part_rows ? p.T * p.H : 0;
+        h.num_mu = int(cdiv(p.T, 2 * kUM));
+        h.num_n = int(cdiv(p.H, kUN));
+        h.num_tiles = int(cdiv(h.num_kb, h.kb_per_split)) * h.num_mu * h.num_n;
+        h.alpha = p.part_rows ? 1.0f : p.alpha;
+        h.rows = p.part_rows ? nullptr : p.row_info;
+        h.add_in_l2 = p.add_hidden ? 1 : 0;
+    }
+    void* w16 = p.weight_bf16 ? p.grad_weight : nullptr;
+    void* h16 = p.hidden_bf16 ? p.grad_hidden : nullptr;
+    if (p.grad_weight && p.grad_hidden) {
+        if (p.weight_bf16)
+            return p.hidden_bf16 ? launch_both<true, true>(mw, mh, w, h, w16, h16, num_sms, stream)
+                                 : launch_both<true, false>(mw, mh, w, h, w16, h16, num_sms, stream);
+        return p.hidden_bf16 ? launch_both<false, true>(mw, mh, w, h, w16, h16, num_sms, stream)
+                             : launch_both<false, false>(mw, mh, w, h, w16, h16, num_sms, stream);
+    }
+    if (p.grad_weight)
+        return p.weight_bf16
+                   ? launch_gemm<false, true, true, true>(mw.a, mw.b, w, num_sms, stream, w16)
+                   : launch_gemm<false, true, false, true>(mw.a, mw.b, w, num_sms, stream);
+    return p.hidden_bf16 ? launch_gemm<false, true, true>(mh.a, mh.b, h, num_sms, stream, h16)
+                         : launch_gemm<false>(mh.a, mh.b, h, num_sms, stream);
 }
 
 cudaError_t launch_sum_parts(const float* sums, const CeRow* rows, void* out, bool bf16, int64_t T,

@@ -285,7 +285,7 @@ cudaError_t quantize(const void* x, int64_t rows, int64_t K, Code* codes, float*
                      cudaStream_t stream) {
     const int vecs = int(K / kVecElems<Elem>);
     // The fewest warps that hold a row have the most bytes in flight each (N = 100000, K = 5152:
-    // two warps @@ us, eight 526); eight warps fill the GPU where rows are fewer than some thousands.
+    // two warps 231 us, eight 526); eight warps fill the GPU where rows are fewer than some thousands.
     int warps = 1;
     while (warps < 8 && (rows < 2048 || vecs > 32 * kVecs * warps)) warps *= 2;
     cudaLaunchAttribute attr;

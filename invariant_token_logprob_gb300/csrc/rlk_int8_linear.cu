@@ -17,6 +17,11 @@
 //   sets       of four warps, 64 columns each: a thread adds its channel's sums up in integers
 //   teams      of four warps, which take the stages in turn: a thread turns its channel's codes
 //              into numbers and stores them to one of two or four A buffers
+// A team meets only every second or third stage, and a barrier tells two phases apart, not three: that
+// the phase before the one it waits for is over must be known.  So it waits for its buffer first.
+// That the MMAs of the stage that had the buffer before are done (stage i - buffers) says that all
+// copies up to that stage's have come, and the ring place of stage i held no later one (i - stages).
+//
 // Few tiles: K is cut into parts, one per CTA of a cluster, whose integers meet through
 // distributed shared memory.
 //
@@ -42,6 +47,14 @@ constexpr bool fits(int room) {
            (room + kInt8MaxParts) * kInt8TileN * 4 <= int8_stages(room) * int8_stage_bytes(room);
 }
 static_assert(fits(16) && fits(32) && fits(64) && fits(128) && fits(192), "memory per CTA");
+// (see above; and for the buffers' own phases: a team's last buffer was freed by stage
+// i - teams - buffers)
+constexpr bool phases_known(int room) {
+    return int8_stages(room) >= int8_number_bufs(room) && int8_number_bufs(room) >= int8_teams(room);
+}
+static_assert(phases_known(16) && phases_known(32) && phases_known(64) && phases_known(128) &&
+                  phases_known(192),
+              "a team's waits are for the next phase");
 
 __device__ unsigned int g_int8_error;  // bit 0: a wait ran out; bit 1: a teardown wait ran out
 
@@ -329,12 +342,13 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
         for (int item = first_item; ok && item < p.items; item += item_step) {
             for (int ks = k_first; ks < k_last; ++ks) {
                 if (turn == team) {
+                    // (the buffer first: see the top)
+                    ok = warp_wait(a_empty(buf), buf_phase ^ 1u) && warp_wait(full_bar(stage), phase);
+                    if (!ok) break;
                     // 16-byte pieces of the row, swizzled by its place among eight
                     const uint32_t codes = stage0 + stage * kStageBytes + row_in_tile * 128 +
                                            ((row_in_tile & 7) << 4);
                     const uint32_t a_tmem = lane_base + buf * kNumberCols;
-                    ok = warp_wait(full_bar(stage), phase) && warp_wait(a_empty(buf), buf_phase ^ 1u);
-                    if (!ok) break;
                     tc_fence_after_sync();  // the MMAs that read the buffer come before the stores
 #pragma unroll
                     for (int c = 0; c < 8; c += 2) {

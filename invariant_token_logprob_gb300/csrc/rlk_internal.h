@@ -140,21 +140,30 @@ cudaError_t run_backward_gemms(const void* h, const void* W, const void* dz, con
                                int64_t T, int64_t H, int64_t V, float inv_temp, float* grad_h,
                                float* grad_W, bool accumulate_W, void* split_ws, int num_sms,
                                cudaStream_t stream);
-// The same products for a piece of `rows` vocabulary entries (the cross entropy's backward).
-// grad [rows][H] (+)= alpha 2^(*top - 2 kCeTop) dzt . h as bf16 (overwritten) or fp32; dzt
-// [rows][backward_dz_ld(T)] and h [T][H] in fp16, as CeRow has them.
-cudaError_t launch_piece_grad_weight(const void* h_fp16, const void* dzt, const int* top, int64_t T,
-                                     int64_t H, int64_t rows, float alpha, void* grad, bool bf16,
-                                     bool accumulate, int num_sms, cudaStream_t stream);
-// out [T][H] = alpha * inv_factor of the row * dz . W, as bf16 or fp32; 0 for rows that do not count.
-cudaError_t launch_grad_hidden(const void* W, const void* dz, int64_t ldz, const CeRow* row_info,
-                               int64_t T, int64_t H, int64_t rows, float alpha, void* out, bool bf16,
-                               int num_sms, cudaStream_t stream);
-// sums [.][T][H] (+)= dz . W, one sum per part_rows (a multiple of 64) of the piece's rows;
-// W [rows][H], dz [T][ldz].
-cudaError_t launch_piece_grad_hidden(const void* W, const void* dz, int64_t ldz, int64_t T,
-                                     int64_t H, int64_t rows, int64_t part_rows, float* sums,
-                                     bool add, int num_sms, cudaStream_t stream);
+// The same products for a piece of the vocabulary (the cross entropy's backward), of which either
+// may be left out; both run side by side where that is quicker.
+//   grad_weight [rows][H] (+)= alpha 2^(*top - 2 kCeTop) dzt . h, dzt and h in fp16 as CeRow has them,
+//                bf16 (overwritten) or fp32
+//   grad_hidden  part_rows != 0 (a multiple of 64): sums [.][T][H] in fp32 (+)= dz . W, one per
+//                part_rows of the piece's rows;
+//                0: [T][H] = alpha * inv_factor of the row * dz . W, bf16 or fp32
+struct CePiece {
+    int64_t T, H, rows;
+    float alpha;
+    const void* h_fp16;   // [T][H]
+    const void* dzt;      // [rows][backward_dz_ld(T)]
+    const int* top;
+    void* grad_weight;    // or null
+    bool weight_bf16, accumulate_weight;
+    const void* W;        // the piece's rows, [rows][H] bf16
+    const void* dz;       // [T][ldz] bf16
+    int64_t ldz;
+    const CeRow* row_info;
+    void* grad_hidden;    // or null
+    bool hidden_bf16, add_hidden;
+    int64_t part_rows;
+};
+cudaError_t launch_piece_products(const CePiece& piece, int num_sms, cudaStream_t stream);
 // out [T][H] = alpha * inv_factor of the row * (sums[0] + sums[1] + ...), in that order, as bf16
 // or fp32; 0 for rows that do not count.
 cudaError_t launch_sum_parts(const float* sums, const CeRow* rows, void* out, bool bf16, int64_t T,
