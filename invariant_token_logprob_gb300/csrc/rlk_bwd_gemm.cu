@@ -28,7 +28,9 @@
 // buffered, 2 x 256 columns).  Persistent grid (pairs = co-resident clusters),
 // static round-robin over units; 3 pipeline stages of two k-blocks (64 KB).
 // Warp roles as in the LM-head kernel: TMA producer, single-thread MMA issuer,
-// four epilogue warps (one thread per row: TMEM -> registers -> alpha * acc).
+// eight epilogue warps (a thread has half a row: TMEM -> registers -> alpha * acc;
+// with four, a product over few k, whose time is its output's, took 310 us for
+// T = 64, H = 4096, V = 151936 in bf16, with eight @@).
 // The epilogue stages each warp's 32 x 32 block in shared memory and writes it
 // with one tiled bulk store (full 128-byte lines; scattered per-thread 16-byte
 // stores measured 2x the crossbar traffic); when adding to D it loads, adds
@@ -75,15 +77,16 @@ constexpr int kMnBoxBytes = kMnAtom * kBK * 2;     // 8 KB: one 64 (M/N) x 64 (k
 constexpr uint32_t kKAtomBytes = 1024;             // 8 k rows of an MN-major tile
 constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kThreads = 192;
-constexpr int kEpiArrivals = 8;                    // epilogue warps of both CTAs
+constexpr int kEpiWarps = 8;                       // two per quadrant of TMEM lanes, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiArrivals = 2 * kEpiWarps;        // epilogue warps of both CTAs
 // full[kStages], empty[kStages], tfull[2], tempty[2], drain, odd_done, drained
 constexpr int kBarriers = 2 * kStages + 2 * kAccBufs + 3;
 // after the barriers: tmem slot, abort flag, odd CTA's issue count, its bytes per stage slot
 constexpr int kWords = 3 + kStages;
 // output staging: one 32 x 32 fp32 block (4 KB, 128-byte swizzled) per epilogue warp
 constexpr int kOutBlockBytes = 32 * 32 * 4;
-constexpr int kOutBytes = 4 * kOutBlockBytes;
+constexpr int kOutBytes = kEpiWarps * kOutBlockBytes;
 constexpr size_t kSmemBytes =
     1024 + size_t(kStages) * kStageBytes + kOutBytes + kBarriers * 8 + kWords * 4 + 16;
 static_assert(kStageBytes % 1024 == 0 && kABytes % 1024 == 0 && kMnBoxBytes % 1024 == 0,
@@ -408,8 +411,10 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
         // written in the 128-byte-swizzled layout the tensor store reads
         // (16-byte piece i of row r at piece i ^ (r % 8)), which also keeps
         // the 8 lanes of each store phase on distinct banks.
-        uint8_t* out_row = out_stage + q * kOutBlockBytes + lane * 128;
-        const uint32_t out_block = smem_u32(out_stage + q * kOutBlockBytes);
+        uint8_t* out_row = out_stage + (warp - 2) * kOutBlockBytes + lane * 128;
+        const uint32_t out_block = smem_u32(out_stage + (warp - 2) * kOutBlockBytes);
+        constexpr int kMine = kUN / (kEpiWarps / 4);  // this warp's columns of the unit
+        const int mine0 = (warp - 2) / 4 * kMine;
         uint32_t acc = 0, acc_phase = 0;
         for (int tile = slot; tile < p.num_tiles; tile += nslots) {
             int s, mu, n;
@@ -423,12 +428,12 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             tc_fence_after_sync();
-            const int col0 = n * kUN;
-            const int ncols = min(kUN, p.N - col0);
+            const int col0 = n * kUN + mine0;
+            const int ncols = min(kMine, p.N - col0);  // (none or less: nothing is stored)
             float* drow =
                 kBf16 ? nullptr
                       : p.d + int64_t(s) * p.split_stride + (live ? row : 0) * p.ldd + col0;
-            const uint32_t t_addr = lane_base + acc * uint32_t(kUN);
+            const uint32_t t_addr = lane_base + acc * uint32_t(kUN) + mine0;
             const int row0 = (2 * mu + int(rank)) * kUM + q * 32;  // this warp's first row
             for (int c = 0; c * 32 < ncols; ++c) {
                 uint32_t r[32];

@@ -1,14 +1,16 @@
 // rlk_cross_entropy.cu -- what the cross entropy does around the LM-head kernel.
 //
-// Loss: from each row's records {max, exp-sum} of the vocabulary's half tiles and its target's z to
+// Loss: from each row's records {m, sum 2^(z log2 e - m)} of the vocabulary's half tiles (m whole) and
+// its target's z to
 //   loss = lse - (1 - e) z[target] - (e / V) sum_v z[v] + l lse^2       (e smoothing, l z loss)
 // and from the rows' losses to their weighted sum or mean.  One warp per row: the largest maximum
-// first, then sum_j s_j exp(m_j - M), a lane's records in order, the lanes in a butterfly; the sum
+// first, then sum_j s_j 2^(m_j - M), a lane's records in order, the lanes in a butterfly; the sum
 // of z likewise.  These orders follow from V alone.  The rows' sum is the last CTA's, in an order
 // fixed by T, whichever CTA that is.
 //
 // Gradient: what each row's gradient with respect to its logits is made of (CeRow), and h in fp16.
-// One warp per row reads h and its target's row of W, for the target's probability.
+// One warp per row (a CTA, where rows are few) reads h and its target's row of W, for the target's
+// probability.
 //
 // Small kernels next to the LM-head products' 2 T H V operations: latency-bound, a few us each, at
 // T = 4096, H = 4096 bounded by HBM (100 MB for the gradient's rows).
@@ -75,7 +77,7 @@ __device__ __forceinline__ void row_loss(const LossArgs& p, int64_t row, int lan
 #pragma unroll 8
     for (int j = lane; j < p.n; j += 32) {
         const float2 r = __ldg(records + j);
-        sum += r.y * exp2f((r.x - top) * kLog2e);
+        sum += r.y * exp2f(r.x - top);
     }
     sum = warp_sum(sum);
     if constexpr (kSmooth) {
@@ -84,13 +86,15 @@ __device__ __forceinline__ void row_loss(const LossArgs& p, int64_t row, int lan
         sum_z = warp_sum(sum_z);
     }
     if (lane == 0) {
-        const float log_sum = logf(sum);
-        const float lse = top + log_sum;
+        // top log 2 in two numbers, the first times a whole number up to 2^9 exact
+        const float top_log = top * 0.693145751953125f;
+        const float log_sum = fmaf(top, 1.42860677e-6f, logf(sum));
+        const float lse = top_log + log_sum;
         const float w = row_weight(p.weights, row, target, p.V);
         float loss = 0.0f;
         if (w != 0.0f) {
             const float zt = p.zt[row];
-            loss = (top - zt) + log_sum;  // (the first difference is exact where they are near)
+            loss = (top_log - zt) + log_sum;  // (the first difference is exact where they are near)
             if constexpr (kSmooth) loss = fmaf(p.smoothing, zt - sum_z / float(p.V), loss);
             if (p.z_loss != 0.0f) loss = fmaf(p.z_loss * lse, lse, loss);
             loss *= w;
@@ -139,15 +143,18 @@ __device__ __forceinline__ int exponent_above(float x) {
     return int((__float_as_uint(x) >> 23) & 255u) - 126;
 }
 
+// kWarps warps per row (1 or 8).
+template <int kWarps>
 __global__ void __launch_bounds__(kRowWarps * 32)
     gradient_rows_kernel(const CeTerms p, const uint4* __restrict__ h, const uint4* __restrict__ W,
                          int64_t T, int vecs, CeRow* __restrict__ rows, uint4* __restrict__ h_fp16,
                          int* __restrict__ tops) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t row = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (row >= T) return;  // whole warp leaves together
-    const int lane = threadIdx.x & 31;
+    constexpr int kLanes = 32 * kWarps;
+    const int64_t row = (int64_t(blockIdx.x) * (kRowWarps * 32) + threadIdx.x) / kLanes;
+    if (row >= T) return;  // (whole warps; with eight per row there is no such row)
+    const int lane = threadIdx.x % kLanes;
     const int32_t target = __ldg(p.targets + row);
     const float w = row_weight(p.weights, row, target, p.V);
     float a = __ldg(p.grad + (p.per_row ? row : 0)) * w;
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     float dot = 0.0f, amax = 0.0f;
     if (counts) {
 #pragma unroll 4
-        for (int i = lane; i < vecs; i += 32) {
+        for (int i = lane; i < vecs; i += kLanes) {
             const uint4 x = __ldg(hr + i), y = __ldg(wr + i);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -175,6 +182,18 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         }
         dot = warp_sum(dot);
         amax = warp_max(amax);
+        if constexpr (kWarps > 1) {
+            __shared__ float2 warps[kWarps];
+            if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = make_float2(dot, amax);
+            __syncthreads();
+            dot = warps[0].x;
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) {
+                dot += warps[i].x;
+                amax = fmaxf(amax, warps[i].y);
+            }
+            amax = fmaxf(amax, warps[0].y);
+        }
     }
     const int h_exponent = exponent_above(amax);
     CeRow r = {};
@@ -207,7 +226,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         const float scale = ce_power(kCeTop - h_exponent);
         uint4* out = h_fp16 + row * vecs;
 #pragma unroll 4
-        for (int i = lane; i < vecs; i += 32) {
+        for (int i = lane; i < vecs; i += kLanes) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (counts) {
                 const uint4 x = __ldg(hr + i);
@@ -260,8 +279,12 @@ cudaError_t launch_cross_entropy_rows(const CeTerms& terms, const void* h, const
                                       int64_t H, CeRow* rows, void* h_fp16, int* tops,
                                       cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config((T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gradient_rows_kernel, terms, static_cast<const uint4*>(h),
+    // (long rows, and few of them: one CTA each)
+    const bool wide = T <= 512 && H >= 1024;
+    const cudaLaunchConfig_t cfg =
+        config(wide ? T : (T + kRowWarps - 1) / kRowWarps, kRowWarps * 32, &attr, stream);
+    auto kernel = wide ? gradient_rows_kernel<8> : gradient_rows_kernel<1>;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, terms, static_cast<const uint4*>(h),
                            static_cast<const uint4*>(W), T, int(H / 8), rows,
                            static_cast<uint4*>(h_fp16), tops);
     return e != cudaSuccess ? e : cudaGetLastError();

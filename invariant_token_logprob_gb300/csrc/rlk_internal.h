@@ -83,8 +83,8 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
                                       int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
                                       cudaStream_t stream);
 
-// Cross entropy: records [T][2 NVT] {max, exp-sum} of z over the halves (128 columns) of the
-// vocabulary's tiles, zt [T] the z of targets inside [0, V), and, unless null, sum_z [T][2 NVT]
+// Cross entropy: records [T][2 NVT] {m, sum 2^(z log2 e - m)}, m a whole number next to the largest
+// z log2 e, of the halves (128 columns) of the vocabulary's tiles, zt [T] the z of targets inside [0, V), and, unless null, sum_z [T][2 NVT]
 // the halves' sums of z.  Sets *done to 0.
 cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
                                float2* records, float* zt, float* sum_z, unsigned int* done,

@@ -48,6 +48,7 @@
 #include "rlk_fp8_quant.cuh"
 #include "rlk_internal.h"
 #include "rlk_lse.cuh"
+#include "rlk_ptx.cuh"
 #include "rlk_sm103.cuh"
 
 namespace rlk {
@@ -69,7 +70,7 @@ constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kABytes = kBM * kBK * 2;  // 16 KiB
 constexpr int kThreads = 192;
-constexpr int kLossThreads = 320;  // mode 3: eight epilogue warps
+constexpr int kWideThreads = 320;  // modes 3 and 4: eight epilogue warps, two per quadrant
 // Mode 3 takes a tile's accumulator out of tensor memory every so many k-blocks (512 k) and adds
 // the parts up in registers.  The tensor core cuts its fp32 additions off towards zero, so an
 // accumulator that runs over all of K falls short: by 3e-6 of the loss at K = 4096 (256
@@ -113,7 +114,7 @@ struct Pipe {
     static constexpr int kWords = 3 + kStages + (kHq ? kHqRows + 4 * kHqMaxRows : 0);
     // backward only: one 32 x 32 bf16 block per epilogue warp, the transposed
     // copy of dz on its way to a tiled bulk store
-    static constexpr int kTransBytes = 4 * 32 * 32 * 2;
+    static constexpr int kTransBytes = kEpiWarps * 32 * 32 * 2;
     // kHq adds kHqRows * H bytes of h codes in front of the stages
     static constexpr size_t kSmemBytes = 1024 /*alignment slack*/ +
                                          size_t(kStages) * kStageBytes + kTransBytes +
@@ -150,7 +151,7 @@ struct Args {
     uint16_t* dz;          // modes 1, 4: [T][ldz] bf16 gradient w.r.t. the logits
     int64_t ldz;           // modes 1, 4: row stride of dz (a multiple of 8 elements)
     int write_dzt;         // modes 1, 4: also store dz transposed through tmap_x ([V][T])
-    float2* records;       // mode 3: [T][2 num_n] {max, exp-sum} of each half tile
+    float2* records;       // mode 3: [T][2 num_n] {m, sum 2^(z log2 e - m)} of each half tile
     float* zt;             // mode 3: [T] the target's z
     const CeRow* ce_rows;  // mode 4: [T]
     const int* ce_tops;    // mode 4: [T], whose largest is CeRow's top
@@ -356,13 +357,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // quantiser kernel's arithmetic (same codes, same row scales), so a decode call
 // needs no quantiser launch; tmap_h is then unused.
 template <int kMode, bool kFp8, bool kPair, bool kHq = false>
-__global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 1)
+__global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 1)
     lmhead_kernel(const __grid_constant__ CUtensorMap tmap_h,
                   const __grid_constant__ CUtensorMap tmap_w,
                   const __grid_constant__ CUtensorMap tmap_x, const Args p) {
     static_assert(!kFp8 || kMode == kModePartials, "fp8 operands: forward partials only");
     static_assert(!kHq || (kFp8 && !kPair), "in-kernel h quantisation: e4m3, single CTA");
-    using P = Pipe<kPair, kHq, kMode == kModeLoss ? 8 : 4>;
+    using P = Pipe<kPair, kHq, kMode >= kModeLoss ? 8 : 4>;
     constexpr int kG = kPair ? 2 : 1;  // tcgen05 CTA group
     constexpr int kStages = P::kStages;
     constexpr int kStageBytes = P::kStageBytes;
@@ -705,16 +706,17 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
         }
         int ce_top = 0;
         if constexpr (kMode == kModeGradLoss) {
-            if (p.write_dzt) {  // the largest of tops, by the four warps, while the first MMAs run
+            if (p.write_dzt) {  // the largest of tops, by the eight warps, while the first MMAs run
                 int* found = reinterpret_cast<int*>(trans);
                 ce_top = INT_MIN;
 #pragma unroll 8
-                for (int64_t r = threadIdx.x - 64; r < p.T; r += 128) ce_top = max(ce_top, __ldg(p.ce_tops + r));
+                for (int64_t r = threadIdx.x - 64; r < p.T; r += 256) ce_top = max(ce_top, __ldg(p.ce_tops + r));
                 ce_top = __reduce_max_sync(0xffffffffu, ce_top);
                 if (lane == 0) found[warp - 2] = ce_top;
-                named_barrier_sync(1, 128);
-                ce_top = max(max(found[0], found[1]), max(found[2], found[3]));
-                named_barrier_sync(1, 128);  // (read before the blocks go there)
+                named_barrier_sync(1, 256);
+#pragma unroll
+                for (int w = 0; w < 8; ++w) ce_top = max(ce_top, found[w]);
+                named_barrier_sync(1, 256);  // (read before the blocks go there)
                 if (ce_top == INT_MIN) ce_top = 0;
                 if (blockIdx.x == 0 && threadIdx.x == 64) *p.ce_top = ce_top;
             }
@@ -745,9 +747,9 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                 // Two warps share a quadrant, 128 columns each.
                 constexpr int kHalf = kBN / 2;
                 const int half = (warp - 2) >> 2;
-                float acc_z[kHalf];
+                F2 z[kHalf / 2];  // the logits over inv_temp
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) acc_z[j] = 0.0f;
+                for (int j = 0; j < kHalf / 2; ++j) z[j] = pack2(0.0f, 0.0f);
                 for (int kb0 = 0; kb0 < p.num_kb; kb0 += kLossPartKb) {
                     if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, abort_flag) ? 1 : 0;
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -760,8 +762,9 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                         tmem_ld16(t_addr + uint32_t(c), r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            acc_z[c + j] = __fadd_rn(acc_z[c + j], __uint_as_float(r[j]));
+                        for (int j = 0; j < 16; j += 2)
+                            z[(c + j) / 2] = add2(z[(c + j) / 2], pack2(__uint_as_float(r[j]),
+                                                                        __uint_as_float(r[j + 1])));
                     }
                     tc_fence_before_sync();
                     __syncwarp();
@@ -778,41 +781,58 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                 }
                 if (!ok) break;
                 const int col0 = n * kBN + half * kHalf;
-                float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f, zt = 0.0f;
+                const int ncols = p.V - col0;  // of these, kHalf at most
+                auto fill_behind_end = [&](float value) {
 #pragma unroll
-                for (int c = 0; c < kHalf / 32; ++c) {
-                    float* z = acc_z + 32 * c;
-                    const int nvalid = p.V - (col0 + 32 * c);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        z[j] = j < nvalid ? __fmul_rn(z[j], inv_temp) : -INFINITY;
-                    float cm = z[0];
-#pragma unroll
-                    for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
-                    if (p.ent_u) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) run_z += j < nvalid ? z[j] : 0.0f;
+                    for (int j = 0; j < kHalf / 2; ++j) {
+                        const float2 v = unpack2(z[j]);
+                        z[j] = pack2(2 * j < ncols ? v.x : value, 2 * j + 1 < ncols ? v.y : value);
                     }
-                    const int rel = tgt - (col0 + 32 * c);
-                    if (unsigned(rel) < 32u) {
+                };
+                if (ncols < kHalf) fill_behind_end(0.0f);
+                float sum_z = 0.0f;
+                if (p.ent_u) {
+                    F2 part[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j == rel) zt = z[j];
-                    }
-                    float cs = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) cs += exp2f((z[j] - cm) * kLog2e);
-                    if (nvalid > 0) {
-                        const float m = fmaxf(run_m, cm);
-                        run_s = run_s * exp2f((run_m - m) * kLog2e) + cs * exp2f((cm - m) * kLog2e);
-                        run_m = m;
-                    }
+                    for (int j = 0; j < kHalf / 2; ++j) part[j & 1] = add2(part[j & 1], z[j]);
+                    const float2 v = unpack2(add2(part[0], part[1]));
+                    sum_z = (v.x + v.y) * inv_temp;
                 }
+                if (ncols < kHalf) fill_behind_end(-INFINITY);
+                const int rel = tgt - col0;
+                if (unsigned(rel) < unsigned(kHalf) && rel < ncols) {  // (a target inside: row < T)
+                    float zt = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kHalf / 2; ++j) {
+                        const float2 v = unpack2(z[j]);
+                        if (2 * j == rel) zt = v.x;
+                        if (2 * j + 1 == rel) zt = v.y;
+                    }
+                    p.zt[row] = zt * inv_temp;
+                }
+                // The record is in powers of two about a whole number m2, so that neither m2 nor the
+                // factors between records are rounded: sum exp z = 2^m2 sum 2^(z log2 e - m2).
+                float m = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kHalf / 2; ++j) {
+                    const float2 v = unpack2(z[j]);
+                    m = max3(m, v.x, v.y);
+                }
+                const float to_log2 = inv_temp * kLog2e;
+                const float m2 = ceilf(m * to_log2);
+                const F2 scale = pack2(to_log2, to_log2), shift = pack2(-m2, -m2);
+                F2 part[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+#pragma unroll
+                for (int j = 0; j < kHalf / 2; ++j) {
+                    const float2 v = unpack2(fma2(z[j], scale, shift));
+                    part[j & 1] = add2(part[j & 1], pack2(ex2(v.x), ex2(v.y)));
+                }
+                const float2 sums = unpack2(add2(part[0], part[1]));
                 if (row < p.T) {
                     const int64_t at = row * (2 * int64_t(p.num_n)) + 2 * n + half;
-                    p.records[at] = make_float2(run_m, run_s);
-                    if (p.ent_u) p.ent_u[at] = run_z;
-                    if (unsigned(tgt - col0) < unsigned(kHalf) && tgt < p.V) p.zt[row] = zt;
+                    p.records[at] = ncols > 0 ? make_float2(m2, sums.x + sums.y)
+                                              : make_float2(-INFINITY, 0.0f);
+                    if (p.ent_u) p.ent_u[at] = sum_z;
                 }
                 __syncwarp();
                 continue;
@@ -823,6 +843,99 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
             tc_fence_after_sync();
 
             if constexpr (kMode == kModeLoss) {
+            } else if constexpr (kMode == kModeGradLoss) {
+                // dz = ce.p p - ce.rest - ce.target [target], p = exp(z - lse), as bf16, and, times
+                // dzt_scale, transposed as fp16
+                constexpr int kHalf = kBN / 2;
+                const int half = (warp - 2) >> 2;
+                const int col0 = n * kBN + half * kHalf;
+                const int ncols = min(kHalf, p.V - col0);
+                const int nchunks = (ncols + 31) >> 5;  // (0 or less: nothing of this half is there)
+                const uint32_t t_addr = lane_base + acc * uint32_t(kBN) + half * kHalf;
+                const bool live = row < p.T;
+                CeRow ce = {};
+                if (live) ce = p.ce_rows[row];
+                const bool valid = ce.inv_factor != 0.0f;  // (another row's logits may be anything)
+                const float dzt_scale =
+                    p.write_dzt ? ce.inv_factor * ce_power(kCeTop - ce_top + ce.h_exponent) : 0.0f;
+                const float to_log2 = inv_temp * kLog2e, shift = -ce.lse * kLog2e;
+                const F2 scale2 = pack2(to_log2, to_log2), shift2 = pack2(shift, shift);
+                const F2 p2 = pack2(ce.p, ce.p), rest2 = pack2(-ce.rest, -ce.rest);
+                const F2 dzt2 = pack2(dzt_scale, dzt_scale);
+                uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;  // 16-byte aligned rows
+                uint16_t* tblk = trans + (warp - 2) * 32 * 32;
+                const int row0 = int(int64_t(m) * kBM + q * 32);  // this warp's first row
+                const bool warp_live = int64_t(row0) < p.T;
+                for (int c = 0; c < nchunks; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(t_addr + uint32_t(c * 32), r);
+                    tmem_ld_wait();
+                    const int cbase = col0 + c * 32;
+                    F2 d[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 v = unpack2(fma2(
+                            pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), scale2, shift2));
+                        d[j] = fma2(pack2(ex2(v.x), ex2(v.y)), p2, rest2);
+                    }
+                    // the rows of W are a piece of the vocabulary that begins at col_offset
+                    const int rel = tgt - p.col_offset - cbase;
+                    if (__any_sync(0xffffffffu, unsigned(rel) < 32u)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = unpack2(d[j]);
+                            d[j] = pack2(v.x - (rel == 2 * j ? ce.target : 0.0f),
+                                         v.y - (rel == 2 * j + 1 ? ce.target : 0.0f));
+                        }
+                    }
+                    if (p.write_dzt && warp_live) {
+                        if (lane == 0) bulk_wait_group_read<0>();  // previous block read out
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = unpack2(mul2(d[j], dzt2));
+                            const __half2 two = __floats2half2_rn(v.x, v.y);
+                            const uint32_t w = valid ? *reinterpret_cast<const uint32_t*>(&two) : 0u;
+                            tblk[2 * j * 32 + lane] = uint16_t(w);
+                            tblk[(2 * j + 1) * 32 + lane] = uint16_t(w >> 16);
+                        }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmap_x, smem_u32(tblk), row0, cbase);
+                            bulk_commit_group();
+                        }
+                    }
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 v = unpack2(d[j]);
+                        packed[j] = valid ? pack_bf16x2(v.x, v.y) : 0u;
+                    }
+                    const int nvalid = ncols - c * 32;
+                    if (live && nvalid >= 32) {
+                        uint4* dst = reinterpret_cast<uint4*>(dz_row + cbase);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4)
+                            dst[q4] = make_uint4(packed[4 * q4], packed[4 * q4 + 1],
+                                                 packed[4 * q4 + 2], packed[4 * q4 + 3]);
+                    } else if (live) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < nvalid)
+                                dz_row[cbase + j] =
+                                    uint16_t((packed[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+                    }
+                    __syncwarp();  // reconverge before the next warp-wide TMEM load
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair)  // the even CTA's accumulator-empty barrier
+                        mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+                    else
+                        mbar_arrive(tempty_bar(acc));
+                }
             } else if constexpr (kMode == kModePartials || kMode == kModeEntropy) {
                 const int col0 = n * kBN;
                 const int ncols = min(kBN, p.V - col0);
@@ -906,23 +1019,9 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                 const int nchunks = (ncols + 31) >> 5;
                 const uint32_t t_addr = lane_base + acc * uint32_t(kBN);
                 const bool live = row < p.T;
-                bool valid;
-                float lse2, g = 0.0f;
-                CeRow ce;                 // mode 4: dz = ce.p p - ce.target [target] - ce.rest
-                float dzt_scale = 0.0f;   // mode 4: dz times this goes to the transpose, as fp16
-                if constexpr (kMode == kModeGradLoss) {
-                    if (live) ce = p.ce_rows[row];
-                    valid = live && ce.inv_factor != 0.0f;
-                    lse2 = valid ? ce.lse * kLog2e : 0.0f;
-                    if (valid && p.write_dzt)
-                        dzt_scale = ce.inv_factor * ce_power(kCeTop - ce_top + ce.h_exponent);
-                } else {
-                    valid = live && tgt >= 0 && tgt < p.V;
-                    g = valid ? __ldg(p.grad + row) : 0.0f;
-                    lse2 = live ? __ldg(p.lse + row) * kLog2e : 0.0f;
-                }
-                // mode 4's rows of W are a piece of the vocabulary that begins at col_offset
-                const int tgt_here = tgt - p.col_offset;
+                const bool valid = live && tgt >= 0 && tgt < p.V;
+                const float g = valid ? __ldg(p.grad + row) : 0.0f;
+                const float lse2 = live ? __ldg(p.lse + row) * kLog2e : 0.0f;
                 uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;  // 16-byte aligned rows
                 // transposed copy: this warp's 32 rows x 32 columns of a chunk are
                 // staged as 32 columns x 32 rows and stored in one piece
@@ -934,27 +1033,17 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                     tmem_ld32(t_addr + uint32_t(c * 32), r);
                     tmem_ld_wait();
                     const int cbase = col0 + c * 32;
-                    uint32_t packed[16], packed_t[kMode == kModeGradLoss ? 16 : 1];
+                    uint32_t packed[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float z0 = __uint_as_float(r[j]) * inv_temp;
                         const float z1 = __uint_as_float(r[j + 1]) * inv_temp;
-                        // p = exp(z - lse); dz = g * (onehot - p), or the loss's
+                        // p = exp(z - lse); dz = g * (onehot - p)
                         const float p0 = exp2f(fmaf(z0, kLog2e, -lse2));
                         const float p1 = exp2f(fmaf(z1, kLog2e, -lse2));
-                        float d0, d1;
-                        if constexpr (kMode == kModeGradLoss) {
-                            d0 = fmaf(ce.p, p0, -ce.rest) - (cbase + j == tgt_here ? ce.target : 0.0f);
-                            d1 = fmaf(ce.p, p1, -ce.rest) -
-                                 (cbase + j + 1 == tgt_here ? ce.target : 0.0f);
-                            d0 = valid ? d0 : 0.0f;
-                            d1 = valid ? d1 : 0.0f;
-                            const __half2 two = __floats2half2_rn(d0 * dzt_scale, d1 * dzt_scale);
-                            packed_t[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
-                        } else {
-                            d0 = valid ? g * ((cbase + j == tgt ? 1.0f : 0.0f) - p0) : 0.0f;
-                            d1 = valid ? g * ((cbase + j + 1 == tgt ? 1.0f : 0.0f) - p1) : 0.0f;
-                        }
+                        const float d0 = valid ? g * ((cbase + j == tgt ? 1.0f : 0.0f) - p0) : 0.0f;
+                        const float d1 =
+                            valid ? g * ((cbase + j + 1 == tgt ? 1.0f : 0.0f) - p1) : 0.0f;
                         packed[j / 2] = pack_bf16x2(d0, d1);
                     }
                     const int nvalid = ncols - c * 32;
@@ -963,10 +1052,8 @@ __global__ void __launch_bounds__(kMode == kModeLoss ? kLossThreads : kThreads, 
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            tblk[j * 32 + lane] = uint16_t(
-                                ((kMode == kModeGradLoss ? packed_t[j / 2] : packed[j / 2]) >>
-                                 (16 * (j & 1))) &
-                                0xFFFFu);
+                            tblk[j * 32 + lane] =
+                                uint16_t((packed[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) {
@@ -1031,7 +1118,7 @@ constexpr size_t kMaxSmemBytes = 227 * 1024;
 template <int kMode, bool kFp8, bool kPair, bool kHq = false>
 cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tx,
                            Args a, int64_t H, int num_sms, cudaStream_t stream) {
-    using P = Pipe<kPair, kHq, kMode == kModeLoss ? 8 : 4>;
+    using P = Pipe<kPair, kHq, kMode >= kModeLoss ? 8 : 4>;
     constexpr int kVariant = kMode >= kModeLoss ? 9 + 2 * (kMode - kModeLoss) + (kPair ? 1 : 0)
                              : kHq              ? 8
                                                 : (kFp8 ? 3 : kMode) + (kPair ? 4 : 0);
@@ -1051,7 +1138,7 @@ cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const C
     attr[1].val.clusterDim.x = kPair ? 2 : 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kMode == kModeLoss ? kLossThreads : kThreads, 1, 1);
+    cfg.blockDim = dim3(kMode >= kModeLoss ? kWideThreads : kThreads, 1, 1);
     cfg.dynamicSmemBytes = P::kSmemBytes + (kHq ? size_t(kHqRows) * size_t(H) : 0);
     cfg.stream = stream;
     cfg.attrs = attr;
