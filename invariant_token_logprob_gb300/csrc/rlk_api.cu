@@ -1032,7 +1032,7 @@ rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
 
 size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V) {
     if (T <= 0 || V <= 0 || H <= 0) return 0;
-    return rlk::ce_layout(T, H, rlk::ce_plan(T, H, V)).bytes;
+    return rlk::ce_layout(T, H, rlk::ce_plan(T, H, V)).bytes + rlk::kCeAlign;
 }
 
 rlk_status rlk_cross_entropy_backward(
@@ -1067,10 +1067,11 @@ rlk_status rlk_cross_entropy_backward(
     if (!aligned16(workspace)) return RLK_ERR_ALIGNMENT;
     const rlk::CePlan plan = rlk::ce_plan(T, H, V);
     const rlk::CeLayout layout = rlk::ce_layout(T, H, plan);
-    if (workspace_bytes < layout.bytes) return RLK_ERR_WORKSPACE;
+    if (workspace_bytes < layout.bytes + rlk::kCeAlign) return RLK_ERR_WORKSPACE;
     if ((st = current_device(&dev, &sms)) != RLK_OK) return st;
     if (!grad_hidden && !grad_weight) return RLK_OK;
-    char* dz = static_cast<char*>(workspace);
+    char* dz = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + rlk::kCeAlign - 1) /
+                                       rlk::kCeAlign * rlk::kCeAlign);
     char* dzt = dz + layout.dzt;
     float* sums = reinterpret_cast<float*>(dz + layout.sums);
     rlk::CeRow* rows_info = reinterpret_cast<rlk::CeRow*>(dz + layout.rows);

@@ -114,8 +114,9 @@ __device__ __forceinline__ float ce_power(int e) {
 #endif
 
 // dz [T][ldz] (and, with tdzt, its transpose) of the cross entropy for the vocabulary's entries
-// [first, first + rows), which tw maps; first is a multiple of kVocabTile.  With tdzt, writes the
-// largest of tops [T] to *top.
+// [first, first + rows), which tw maps; first is a multiple of kVocabTile.  dz is 32-byte aligned and
+// ldz a multiple of 256 with room for whole groups of 32 entries.  With tdzt, writes the largest of
+// tops [T] to *top.
 cudaError_t launch_lmhead_grad_loss(const CUtensorMap* th, const CUtensorMap* tw,
                                     const CUtensorMap* tdzt, const int32_t* targets,
                                     const CeRow* ce_rows, const int* tops, int* top, void* dz, int64_t ldz,

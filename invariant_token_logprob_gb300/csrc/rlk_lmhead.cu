@@ -112,9 +112,9 @@ struct Pipe {
     // its bytes per stage slot (written into the even CTA's words at teardown);
     // kHq: then the row scales and the epilogue warps' partial row maxima
     static constexpr int kWords = 3 + kStages + (kHq ? kHqRows + 4 * kHqMaxRows : 0);
-    // backward only: one 32 x 32 bf16 block per epilogue warp, the transposed
-    // copy of dz on its way to a tiled bulk store
-    static constexpr int kTransBytes = kEpiWarps * 32 * 32 * 2;
+    // backward only: one 32 x 32 bf16 block per epilogue warp (two with eight warps, in turn), the
+    // transposed copy of dz on its way to a tiled bulk store
+    static constexpr int kTransBytes = kEpiWarps * (kEpiWarps == 8 ? 2 : 1) * 32 * 32 * 2;
     // kHq adds kHqRows * H bytes of h codes in front of the stages
     static constexpr size_t kSmemBytes = 1024 /*alignment slack*/ +
                                          size_t(kStages) * kStageBytes + kTransBytes +
@@ -862,8 +862,7 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                 const F2 scale2 = pack2(to_log2, to_log2), shift2 = pack2(shift, shift);
                 const F2 p2 = pack2(ce.p, ce.p), rest2 = pack2(-ce.rest, -ce.rest);
                 const F2 dzt2 = pack2(dzt_scale, dzt_scale);
-                uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;  // 16-byte aligned rows
-                uint16_t* tblk = trans + (warp - 2) * 32 * 32;
+                uint16_t* dz_row = p.dz + (live ? row : 0) * p.ldz;
                 const int row0 = int(int64_t(m) * kBM + q * 32);  // this warp's first row
                 const bool warp_live = int64_t(row0) < p.T;
                 for (int c = 0; c < nchunks; ++c) {
@@ -889,7 +888,8 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                         }
                     }
                     if (p.write_dzt && warp_live) {
-                        if (lane == 0) bulk_wait_group_read<0>();  // previous block read out
+                        uint16_t* tblk = trans + (2 * (warp - 2) + (c & 1)) * 32 * 32;
+                        if (lane == 0) bulk_wait_group_read<1>();  // the block before last read out
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -912,19 +912,9 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                         const float2 v = unpack2(d[j]);
                         packed[j] = valid ? pack_bf16x2(v.x, v.y) : 0u;
                     }
-                    const int nvalid = ncols - c * 32;
-                    if (live && nvalid >= 32) {
-                        uint4* dst = reinterpret_cast<uint4*>(dz_row + cbase);
-#pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4)
-                            dst[q4] = make_uint4(packed[4 * q4], packed[4 * q4 + 1],
-                                                 packed[4 * q4 + 2], packed[4 * q4 + 3]);
-                    } else if (live) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < nvalid)
-                                dz_row[cbase + j] =
-                                    uint16_t((packed[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+                    if (live) {  // (ldz is a multiple of 256: room for whole chunks, whole sectors)
+                        store_global_v8(dz_row + cbase, packed);
+                        store_global_v8(dz_row + cbase + 16, packed + 8);
                     }
                     __syncwarp();  // reconverge before the next warp-wide TMEM load
                 }

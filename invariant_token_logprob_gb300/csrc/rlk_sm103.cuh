@@ -200,6 +200,13 @@ __device__ __forceinline__ void tma_store_3d(const void* desc, uint32_t src, int
         "r"(src), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+// 32 bytes of registers to global memory (32-byte aligned), a whole sector.
+__device__ __forceinline__ void store_global_v8(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // An L2 cache policy under which the lines an access brings in or writes are
 // the first to be evicted: for output the kernel does not read again, so it
 // does not push out operands that other CTAs are about to reuse.

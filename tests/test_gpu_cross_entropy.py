@@ -377,6 +377,11 @@ def test_reads_and_writes_stay_inside():
     x, y = rlk.cross_entropy_backward(*ins[:3], r.lse, g, r.total, ins[3], workspace=w2, **opts)
     assert torch.equal(r.loss, e.loss) and torch.equal(x, gh) and torch.equal(y, gW)
     assert (b1[w1.numel():] == 0xAB).all() and (b2[w2.numel():] == 0xAB).all()
+    for off in (16, 48, 240):  # a workspace at any 16-byte boundary
+        b2, _ = guarded(w2.numel() + off)
+        x, y = rlk.cross_entropy_backward(*ins[:3], r.lse, g, r.total, ins[3], workspace=b2[off:off + w2.numel()], **opts)
+        assert torch.equal(x, gh) and torch.equal(y, gW)
+        assert (b2[:off] == 0xAB).all() and (b2[off + w2.numel():] == 0xAB).all()
 
 
 def test_refusals():
