@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        // (the whole warp runs the loop, so addresses are warp-uniform; one lane issues)
+        // (the whole warp runs the loop and one lane issues: addresses from outside that lane's branch
+        // are warp-uniform, as the instructions want them)
         const bool leader = elect_one();
         const uint32_t idesc = idesc_f16_f32(kInt8TileN, plan.mma_n);
         uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0, d = 0, d_phase = 0;
@@ -245,25 +246,25 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
             for (int ks = k_first; ks < k_last; ++ks) {
                 const bool opens = (ks - k_first) % kInt8SumStages == 0;
                 const bool closes = (ks - k_first) % kInt8SumStages == kInt8SumStages - 1 || ks + 1 == k_last;
-                ok = warp_wait(full_bar(stage), phase) &&
+                ok = warp_wait(full_bar(stage), phase) && warp_wait(a_full(buf), buf_phase) &&
                      (!opens || warp_wait(d_empty(d), d_phase ^ 1u));
                 if (!ok) break;
+                tc_fence_after_sync();
                 const uint64_t x_desc =
                     sw128_kmajor_desc(stage0 + stage * kStageBytes + kInt8CodeBytes);
+                const uint32_t a_tmem = tmem_base + buf * kNumberCols;
                 const uint32_t d_tmem = tmem_base + kDBase + d * kRoom;
-                ok = warp_wait(a_full(buf), buf_phase);
-                if (!ok) break;
-                tc_fence_after_sync();
+                const uint32_t a_done = a_empty(buf), stage_done = empty_bar(stage), d_done = d_full(d);
+                const uint32_t more = opens ? 0u : 1u;
                 if (leader) {
-                    const uint32_t a_tmem = tmem_base + buf * kNumberCols;
 #pragma unroll
                     for (int i = 0; i < kInt8StageK / 16; ++i)
                         umma_f16_tmem_a(d_tmem, a_tmem + i * 8,
                                         x_desc + uint64_t((i / 4 * kRoom * 128 + i % 4 * 32) >> 4),
-                                        idesc, opens && i == 0 ? 0u : 1u);
-                    umma_commit(a_empty(buf));
-                    umma_commit(empty_bar(stage));
-                    if (closes) umma_commit(d_full(d));
+                                        idesc, i == 0 ? more : 1u);
+                    umma_commit(a_done);
+                    umma_commit(stage_done);
+                    if (closes) umma_commit(d_done);
                 }
                 __syncwarp();
                 if (++buf == kBufs) {
