@@ -15,6 +15,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 from typing import NamedTuple, Optional
 
 __all__ = ["RlkError", "lib", "logprob", "logprob_ws", "logprob_partials", "lse_merge",
@@ -775,6 +776,29 @@ class _Call:
         return self.torch._C._cuda_getCurrentRawStream(self.device)
 
 
+_SCRATCH_MOST = 2 << 20
+_scratch = threading.local()
+
+
+def _workspace(call, size, device, stream):
+    """A workspace of at least `size` bytes for one call.  A small one is kept, per thread, device
+    and stream, as an allocation takes longer than a small call's checks (4 us on Grace): the calls of a
+    thread on a stream run one after the other.  Not for a stream other than the current one, nor while it
+    is captured: a graph's launches must not share their memory with calls outside it."""
+    torch = call.torch
+    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(call.device):
+        return _empty(stream, max(16, size), dtype=torch.uint8, device=device)
+    if size > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(max(16, size), dtype=torch.uint8, device=device)
+    kept = _scratch.__dict__
+    key = call.device, torch._C._cuda_getCurrentRawStream(call.device)
+    workspace = kept.get(key)
+    if workspace is None or workspace.shape[0] < size:
+        workspace = torch.empty(max(1 << 16, 1 << (size - 1).bit_length()), dtype=torch.uint8, device=device)
+        kept[key] = workspace
+    return workspace
+
+
 def _logits_args(call, logits, targets, allowed):
     """Checked leading arguments of the two entry points, and T, V."""
     code, stride = call.rows(logits, "logits")
@@ -1124,8 +1148,7 @@ def cross_entropy(h, W, targets, weights=None, inv_temp: float = 1.0, label_smoo
     total = empty((), dtype=f32, device=dev)
     L = _lib or lib()
     if workspace is None:
-        workspace = empty(max(16, L.rlk_cross_entropy_workspace_size(T, H, V)), dtype=torch.uint8,
-                          device=dev)
+        workspace = _workspace(call, L.rlk_cross_entropy_workspace_size(T, H, V), dev, stream)
     ws = call.arg(workspace, torch.uint8, "workspace", 1)
     _check(L.rlk_cross_entropy(*pointers, T, H, V, inv_temp, label_smoothing, z_loss, code,
                                loss.data_ptr(), lse.data_ptr(), total.data_ptr(), ws,
@@ -1171,8 +1194,7 @@ def cross_entropy_backward(h, W, targets, lse, grad_loss, total=None, weights=No
         grad_W = empty((V, H), dtype=dtype, device=dev)
     L = _lib or lib()
     if workspace is None:
-        workspace = empty(max(16, L.rlk_cross_entropy_backward_workspace_size(T, H, V)),
-                          dtype=torch.uint8, device=dev)
+        workspace = _workspace(call, L.rlk_cross_entropy_backward_workspace_size(T, H, V), dev, stream)
     ws = call.arg(workspace, torch.uint8, "workspace", 1)
     _check(L.rlk_cross_entropy_backward(
         *pointers, *rows, T, H, V, inv_temp, label_smoothing, z_loss, code,
@@ -1312,8 +1334,7 @@ def linear_int8(x, codes, scales, x_scales=None, out_dtype=None, out=None, works
         raise ValueError("out must be [T, N]")
     L = _lib or lib()
     if workspace is None:
-        workspace = empty(max(16, L.rlk_linear_int8_workspace_size(T, K)), dtype=torch.uint8,
-                          device=x.device)
+        workspace = _workspace(call, L.rlk_linear_int8_workspace_size(T, K), x.device, stream)
     ws = call.arg(workspace, torch.uint8, "workspace", 1)
     _check(L.rlk_linear_int8(a, 3 if given else _dtype_code(x.dtype), xs, c, s, T, N, K, o, out_code,
                              ws, workspace.shape[0], call.stream(stream)), "rlk_linear_int8")
