@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
     constexpr int kBufs = int8_number_bufs(kRoom);
     constexpr uint32_t kNumberCols = kInt8NumberCols;
     constexpr int kMine = kRoom / kSets;  // columns of a set
+    constexpr int kLaneRows = (kMine + 31) / 32;
     constexpr int kPiece = kSets > 1 ? 8 : 16;  // (registers)
     constexpr int kFirstTeamWarp = 2 + 4 * kSets;
     constexpr uint32_t kDBase = kBufs * kNumberCols;
@@ -177,7 +178,9 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
 
     // A cluster takes one item, a CTA alone every gridDim.x-th; either way these stages of K.
     const Int8Plan& plan = p.plan;
-    const int rank = plan.parts > 1 ? int(cluster_ctarank()) : 0;
+    // (from blockIdx: the compiler then knows that all that follows is the same in a warp, which the
+    // issue of MMAs needs to be quick)
+    const int rank = int(blockIdx.x) % plan.parts;
     const int first_item = plan.parts > 1 ? int(blockIdx.x) / plan.parts : int(blockIdx.x);
     const int item_step = plan.parts > 1 ? p.items : int(gridDim.x);
     const int k_first = int(int64_t(plan.stages) * rank / plan.parts);
@@ -294,6 +297,16 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
             const int tile = item / plan.chunks;
             const int chunk = item - tile * plan.chunks;
             const int n = tile * kInt8TileN + row_in_tile;
+            const int first = chunk * plan.rows + mine0;
+            const int rows = int(min(int64_t(plan.rows), p.T - chunk * plan.rows)) - mine0;  // mine
+            // the scales that the stores will want, a lane one of every 32 rows'
+            float scale = 0.0f, x_scale[kLaneRows];
+            if (plan.parts == 1) {
+                scale = n < p.N ? __ldg(p.scales + n) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kLaneRows; ++j)
+                    x_scale[j] = 32 * j + lane < rows ? __ldg(p.x_scales + first + 32 * j + lane) : 0.0f;
+            }
 #pragma unroll
             for (int t = 0; t < kMine; ++t) sum[t] = 0;
             for (int ks = k_first; ks < k_last; ks += kInt8SumStages) {
@@ -320,17 +333,17 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
                     d_phase ^= 1u;
                 }
             }
-            if (plan.parts == 1 && n < p.N && ok) {
-                const float s = __ldg(p.scales + n);
-                const int first = chunk * plan.rows;
-                const int rows = int(min(int64_t(plan.rows), p.T - first)) - mine0;  // mine
-                Out* y = static_cast<Out*>(p.y) + int64_t(first + mine0) * p.N + n;
-                const float* xs = p.x_scales + first + mine0;
+            if (plan.parts == 1 && ok) {
+                // (stores one after the other, without a load or a branch between: the next item's
+                // sums wait for them)
+                Out* y = static_cast<Out*>(p.y) + int64_t(first) * p.N + n;
+                const bool there = n < p.N;
 #pragma unroll
-                for (int t = 0; t < kMine; ++t)
-                    if (t < rows)
-                        y[int64_t(t) * p.N] =
-                            from_float<Out>(__fmul_rn(__fmul_rn(float(sum[t]), __ldg(xs + t)), s));
+                for (int t = 0; t < kMine; ++t) {
+                    const float xs = __shfl_sync(0xffffffffu, x_scale[t / 32], t % 32);
+                    if (there && t < rows) *y = from_float<Out>(__fmul_rn(__fmul_rn(float(sum[t]), xs), scale));
+                    y += p.N;
+                }
             }
         }
     } else {
