@@ -674,7 +674,8 @@ rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,
  * transpose are held (512 MiB together, more only where 256 entries take more), 16 bits each, as
  * operands of the two products: for grad_hidden rounded once to bf16 but for each row's element at
  * its target, which a factor per row keeps whole; for grad_weight rounded once to fp16, under
- * powers of two that keep it in range (h is exact there).  The products sum in fp32 in an order
+ * powers of two that keep it in range (h is exact there; a product of the two that lies 2^-28 below the
+ * largest row's keeps fewer bits, one 2^-39 below is lost).  The products sum in fp32 in an order
  * fixed by (T, H, V).
  *   lse_f32, total_f32   device: rlk_cross_entropy's outputs (total_f32 is read for RLK_MEAN)
  *   grad_loss_f32        device: g, [T] for RLK_NONE, else one value

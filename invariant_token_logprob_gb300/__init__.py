@@ -1240,7 +1240,8 @@ def differentiable_cross_entropy(h, W, targets, weights=None, inv_temp: float = 
                                  label_smoothing: float = 0.0, z_loss: float = 0.0,
                                  reduction: str = "mean"):
     """cross_entropy under torch autograd: the loss carries gradients to h and W (lse, total and
-    the weights do not).  First derivatives only."""
+    the weights do not).  First derivatives only.  A step captured in a CUDA graph follows torch's
+    own rules: warmed up on a side stream, and no eager graph of the same leaves alive."""
     global _CrossEntropyFunction
     if _CrossEntropyFunction is None:
         _CrossEntropyFunction = _cross_entropy_function()

@@ -84,8 +84,8 @@ cudaError_t launch_lmhead_grad_logits(const CUtensorMap* th, const CUtensorMap* 
                                       cudaStream_t stream);
 
 // Cross entropy: records [T][2 NVT] {m, sum 2^(z log2 e - m)}, m a whole number next to the largest
-// z log2 e, of the halves (128 columns) of the vocabulary's tiles, zt [T] the z of targets inside [0, V), and, unless null, sum_z [T][2 NVT]
-// the halves' sums of z.  Sets *done to 0.
+// z log2 e, of the halves (128 columns) of the vocabulary's tiles, zt [T] the z of targets inside
+// [0, V), and, unless null, sum_z [T][2 NVT] the halves' sums of z.  Sets *done to 0.
 cudaError_t launch_lmhead_loss(const CUtensorMap* th, const CUtensorMap* tw, const int32_t* targets,
                                float2* records, float* zt, float* sum_z, unsigned int* done,
                                int64_t T, int64_t V, int64_t H, float inv_temp, int num_sms,
@@ -106,6 +106,10 @@ struct CeRow {
     int pad[2];
 };
 constexpr int kCeTop = 14;
+// What the exponents are held to, so that 2^(kCeTop - h_exponent) and 2^(top - 2 kCeTop) are normal
+// numbers (with the gradient's own exponent at kCeTop - 127 or more, the third power is one too, or
+// so small that 0 stands for it).
+constexpr int kCeLeastH = kCeTop - 126, kCeLeastTop = 2 * kCeTop - 126, kCeMostTop = 127 + 2 * kCeTop;
 #ifdef __CUDACC__
 // 2^e, e held within the normal numbers' exponents.
 __device__ __forceinline__ float ce_power(int e) {

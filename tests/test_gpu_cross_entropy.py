@@ -225,6 +225,28 @@ def test_gradients_of_rows_far_apart(spread):
     within(gW, wW, bW * (1 + 2.0 ** -8) + 1e-38, 2.0 ** -8, "grad_W")
 
 
+@pytest.mark.parametrize("grad,hidden", [(2.0 ** -100, 1.0), (2.0 ** -112, 1.0), (1.0, 2.0 ** -100),
+                                         (2.0 ** -4, 2.0 ** -116), (2.0 ** 90, 1.0), (2.0 ** -120, 2.0 ** 20)])
+def test_gradients_near_the_ends_of_the_range(grad, hidden):
+    """Incoming gradients and hidden states near the ends of fp32's range: powers of two that go in
+    come out.  Numbers below 2^-126 may be lost at each step: of the softmax's part of a gradient
+    (times |W| or |h|), of h under the power that lifts it and of the result."""
+    import invariant_token_logprob_gb300 as rlk
+    T, H, V = 130, 72, 300
+    h, W, t, _ = (None if x is None else x.cuda() for x in make(T, H, V, 16, weighted=False))
+    h = (h.float() * hidden).bfloat16()
+    if hidden > 1:
+        W = (W.float() / hidden).bfloat16()
+    g = torch.tensor(grad, device="cuda")
+    r = rlk.cross_entropy(h, W, t, reduction="sum")
+    ref = Ref(h, W, t, None, 1.0, 0.0, 0.0, lse=r.lse)
+    (wh, bh), (wW, bW) = ref.grads(g, "sum")
+    gh, gW = rlk.cross_entropy_backward(h, W, t, r.lse, g, reduction="sum", grad_dtype=torch.float32)
+    least = 2.0 ** -126
+    within(gh, wh, bh + least * (2 + W.double().abs().sum(0)), what="grad_h")
+    within(gW, wW, bW + least * (2 + 2 * h.double().abs().sum(0)), what="grad_W")
+
+
 def test_rows_that_do_not_count():
     """Ignored targets, weights of 0 and targets outside the vocabulary, with any logits."""
     import invariant_token_logprob_gb300 as rlk
@@ -304,6 +326,37 @@ def test_gradient_against_differences():
         tol = float(((bh * (1 + 2.0 ** -8) + 2.0 ** -8 * wh.abs()) * dh.abs()).sum() +
                     ((bW * (1 + 2.0 ** -8) + 2.0 ** -8 * wW.abs()) * dW.abs()).sum())
         assert abs(got - slope) <= tol + 1e-5
+
+
+def test_training_step_in_a_graph():
+    """Loss and backward pass under autograd, captured as torch asks for (warmed up on a side stream,
+    the eager graphs gone) and replayed on other inputs."""
+    import invariant_token_logprob_gb300 as rlk
+    h, W, t, w = (x.cuda() for x in make(150, 136, 3001, 18))
+    opts = dict(label_smoothing=0.05, z_loss=1e-4)
+    hp, Wp = h.clone().requires_grad_(), W.clone().requires_grad_()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            hp.grad = Wp.grad = None
+            rlk.differentiable_cross_entropy(hp, Wp, t, w, **opts).loss.backward()
+    torch.cuda.current_stream().wait_stream(s)
+    first = hp.grad, Wp.grad
+    hp.grad = Wp.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        loss = rlk.differentiable_cross_entropy(hp, Wp, t, w, **opts).loss
+        loss.backward()
+    graph.replay()
+    assert torch.equal(hp.grad, first[0]) and torch.equal(Wp.grad, first[1])
+    other = h.flip(1).contiguous()
+    with torch.no_grad():
+        hp.copy_(other)
+    graph.replay()
+    e = rlk.cross_entropy(other, W, t, w, **opts)
+    gh, gW = rlk.cross_entropy_backward(other, W, t, e.lse, torch.tensor(1.0, device="cuda"), e.total, w, **opts)
+    assert torch.equal(loss, e.loss) and torch.equal(hp.grad, gh) and torch.equal(Wp.grad, gW)
 
 
 def test_autograd_step_and_graph():
