@@ -67,8 +67,9 @@ inline CePlan ce_plan(int64_t T, int64_t H, int64_t V) {
     return best;
 }
 
-// Workspace of the backward, from the first address in it that is a multiple of kCeAlign: dz [T][rows] and its transpose, 16 bits each, grad_h's sums
-// [parts][T][H] in fp32, h in fp16, and what belongs to a row (32 bytes and 4) and to all.
+// Workspace of the backward, from the first address in it that is a multiple of kCeAlign: dz
+// [T][rows] and its transpose, 16 bits each, grad_h's sums [parts][T][H] in fp32, h in fp16, and
+// what belongs to a row (32 bytes and 4) and to all.
 constexpr size_t kCeAlign = 256;
 struct CeLayout {
     size_t dzt, sums, h, rows, tops, top, bytes;  // offsets; dz lies at 0

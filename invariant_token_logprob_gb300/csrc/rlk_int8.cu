@@ -11,6 +11,8 @@
 // What bounds it: HBM, 3 bytes per 16-bit element.  A row stays in registers between the
 // maximum and the codes (16 vectors of 16 bytes per lane): in one warp's where rows are many, in
 // eight warps' where they are few or long.
+// Measured for N = 151936, K = 4096, bf16: codes and scales 259 us (7.2 TB/s, 1.06 of a copy, whose
+// bytes are written by half, not by a third), read back as bf16 266 us.
 #include "rlk_logits.cuh"
 #include "rlk_ptx.cuh"
 #include "rlk_train_int8.h"
