@@ -475,8 +475,12 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
     // parameters (and issued L2 prefetches); the launch may overlap the
     // previous kernel in the stream up to here.  No global memory is read or
     // written before this wait.
-    grid_dependency_wait();
-    grid_launch_dependents();
+    // (Mode 4 follows a kernel of the same call, which has itself waited for whatever wrote h and W and
+    // does not write them: only its epilogue waits, products begin meanwhile.)
+    if (kMode != kModeGradLoss || warp >= 2) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
     if constexpr (kMode == kModeLoss) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0u;
     }

@@ -142,6 +142,37 @@ def test_row_bits_do_not_depend_on_the_batch():
     assert torch.equal(rlk.linear_int8(x, qw[100:300].contiguous(), sw[100:300].contiguous()), y[:, 100:300])
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 512, 4096), (3, 20000, 1040), (150, 1000, 2064)])
+def test_codes_written_by_the_call_before(T, N, K):
+    """Two weights in turn, quantised into the same codes and multiplied at once, without a wait and
+    from a graph: every product is of the codes that were written last."""
+    import invariant_token_logprob_gb300 as rlk
+    g = torch.Generator().manual_seed(T)
+    W = [torch.randn(N, K, generator=g).bfloat16().cuda() for _ in range(2)]
+    x = torch.randn(T, K, generator=g).bfloat16().cuda()
+    want = [rlk.linear_int8(x, *rlk.quantize_int8(w)) for w in W]
+    assert not torch.equal(*want)
+    buffers = rlk.quantize_int8(W[0])
+    out = [torch.empty_like(want[0]) for _ in range(20)]
+    workspace = torch.empty(rlk.lib().rlk_linear_int8_workspace_size(T, K), dtype=torch.uint8, device="cuda")
+
+    def run():
+        for i, o in enumerate(out):
+            rlk.quantize_int8(W[i % 2], out=buffers)
+            rlk.linear_int8(x, *buffers, out=o, workspace=workspace)
+    run()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(out))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run()
+    for o in out:
+        o.zero_()
+    graph.replay()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(out))
+
+
 def test_reads_and_writes_stay_inside():
     """Operands in the middle of poisoned memory, an output and a workspace with guards behind."""
     import invariant_token_logprob_gb300 as rlk
