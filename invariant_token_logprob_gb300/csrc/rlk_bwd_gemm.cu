@@ -28,9 +28,11 @@
 // buffered, 2 x 256 columns).  Persistent grid (pairs = co-resident clusters),
 // static round-robin over units; 3 pipeline stages of two k-blocks (64 KB).
 // Warp roles as in the LM-head kernel: TMA producer, single-thread MMA issuer,
-// eight epilogue warps (a thread has half a row: TMEM -> registers -> alpha * acc;
-// with four, a product over few k, whose time is its output's, took 310 us for
-// T = 64, H = 4096, V = 151936 in bf16, with eight 298 us; a memset of the same 1.24 GB takes 305).
+// four epilogue warps (a thread has a row: TMEM -> registers -> alpha * acc), or eight (half a row
+// each) for units of fewer than 16 blocks of k, whose time is their output's: T = 64, H = 4096,
+// V = 151936 in bf16, 310 us with four, 298 with eight; a memset of the same 1.24 GB takes 305.  Over
+// more k eight only draw power: T = 4096, the whole backward, 9.25 ms with eight, 9.10 with four; T = 512
+// (8 blocks) 349 and 341 us, T = 1024 (16) 507 and 518.
 // The epilogue stages each warp's 32 x 32 block in shared memory and writes it
 // with one tiled bulk store (full 128-byte lines; scattered per-thread 16-byte
 // stores measured 2x the crossbar traffic); when adding to D it loads, adds
@@ -86,9 +88,9 @@ constexpr int kMnBoxBytes = kMnAtom * kBK * 2;     // 8 KB: one 64 (M/N) x 64 (k
 constexpr uint32_t kKAtomBytes = 1024;             // 8 k rows of an MN-major tile
 constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpiWarps = 8;                       // two per quadrant of TMEM lanes, 128 columns each
+constexpr int kEpiWarps = 8;                       // at most; two per quadrant of TMEM lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kEpiArrivals = 2 * kEpiWarps;        // epilogue warps of both CTAs
+constexpr int kFewBlocks = 16;                     // fewer k-blocks per unit: eight epilogue warps
 // full[kStages], empty[kStages], tfull[2], tempty[2], drain, odd_done, drained
 constexpr int kBarriers = 2 * kStages + 2 * kAccBufs + 3;
 // after the barriers: tmem slot, abort flag, odd CTA's issue count, its bytes per stage slot
@@ -182,6 +184,7 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
                                          const int nslots) {
     constexpr uint32_t kIdesc = idesc_bf16_f32_major(2 * kUM, kUN, kAMn, kBMn) &
                                 (kFp16 ? ~((7u << 7) | (7u << 10)) : ~0u);  // (A, B format 0: fp16)
+    const int epi_warps = int(blockDim.x) / 32 - 2;  // 4 or 8
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -216,7 +219,7 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
         }
         for (int b = 0; b < kAccBufs; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), kEpiArrivals);
+            mbar_init(tempty_bar(b), 2 * epi_warps);  // of both CTAs
         }
         mbar_init(drain_bar, 1);
         mbar_init(odd_done_bar, 1);
@@ -422,8 +425,8 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
         // the 8 lanes of each store phase on distinct banks.
         uint8_t* out_row = out_stage + (warp - 2) * kOutBlockBytes + lane * 128;
         const uint32_t out_block = smem_u32(out_stage + (warp - 2) * kOutBlockBytes);
-        constexpr int kMine = kUN / (kEpiWarps / 4);  // this warp's columns of the unit
-        const int mine0 = (warp - 2) / 4 * kMine;
+        const int mine = kUN / (epi_warps / 4);  // this warp's columns of the unit
+        const int mine0 = (warp - 2) / 4 * mine;
         uint32_t acc = 0, acc_phase = 0;
         for (int tile = slot; tile < p.num_tiles; tile += nslots) {
             int s, mu, n;
@@ -438,7 +441,7 @@ __device__ __forceinline__ void bwd_gemm(const CUtensorMap& tmap_a, const CUtens
             if (!ok) break;
             tc_fence_after_sync();
             const int col0 = n * kUN + mine0;
-            const int ncols = min(kMine, p.N - col0);  // (none or less: nothing is stored)
+            const int ncols = min(mine, p.N - col0);  // (none or less: nothing is stored)
             float* drow =
                 kBf16 ? nullptr
                       : p.d + int64_t(s) * p.split_stride + (live ? row : 0) * p.ldd + col0;
@@ -685,6 +688,12 @@ cudaError_t pair_config(Kernel kernel, int* max_pairs, int num_sms, cudaStream_t
     return cudaSuccess;
 }
 
+// Threads of a CTA: the epilogue of few blocks of k has eight warps, else four (at the top).
+unsigned epilogue_threads(const Args& a) {
+    const int blocks = std::min(a.kb_per_split, a.num_kb);
+    return 64u + 32u * (blocks < kFewBlocks ? kEpiWarps : 4);
+}
+
 int g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
 
 template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
@@ -702,6 +711,7 @@ cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, in
     if (e != cudaSuccess) return e;
     const int clusters = a.num_tiles < maxc ? a.num_tiles : maxc;
     if (clusters < 1) return cudaSuccess;
+    cfg.blockDim = dim3(epilogue_threads(a), 1, 1);
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, td, a);
     if (e != cudaSuccess) return e;
@@ -753,6 +763,7 @@ cudaError_t launch_both(Maps& mw, Maps& mh, const Args& w, const Args& h, void* 
     const int pairs_w = w.num_tiles < first ? w.num_tiles : first;
     const int pairs_h = h.num_tiles < pairs - first ? h.num_tiles : pairs - first;
     cfg.gridDim = dim3(2 * (pairs_w + pairs_h), 1, 1);
+    cfg.blockDim = dim3(std::max(epilogue_threads(w), epilogue_threads(h)), 1, 1);
     e = cudaLaunchKernelEx(&cfg, kernel, mw, mh, w, h, pairs_w);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
