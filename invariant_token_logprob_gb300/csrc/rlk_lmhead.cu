@@ -717,6 +717,9 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                             hq_scale);
             if (warp == 2 && lane == 0) mbar_arrive(hq_bar);  // after quantise_h_rows' barrier
         }
+        // Mode 4: the staging block that the next chunk takes.  It changes with every store, from one tile
+        // to the next too (a tile may have an odd number of chunks): only the newest store may still read.
+        int trans_block = 0;
         int ce_top = 0;
         if constexpr (kMode == kModeGradLoss) {
             if (p.write_dzt) {  // the largest of tops, by the eight warps, while the first MMAs run
@@ -903,8 +906,8 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                         }
                     }
                     if (p.write_dzt && warp_live) {
-                        uint16_t* tblk = trans + (2 * (warp - 2) + (c & 1)) * 32 * 32;
-                        if (lane == 0) bulk_wait_group_read<1>();  // the block before last read out
+                        uint16_t* tblk = trans + (2 * (warp - 2) + trans_block) * 32 * 32;
+                        if (lane == 0) bulk_wait_group_read<1>();  // the store before last has read it
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -920,6 +923,7 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
                             tma_store_2d(&tmap_x, smem_u32(tblk), row0, cbase);
                             bulk_commit_group();
                         }
+                        trans_block ^= 1;
                     }
                     uint32_t packed[16];
 #pragma unroll
