@@ -193,6 +193,29 @@ def test_bands_of_rows_behind_a_short_tile(T, H, V):
     assert rlk.take_device_errors() == (0, 0)
 
 
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+@pytest.mark.parametrize("T,H,V", SHAPES + [(130, 1032, 50001), (64, 256, 20000), (2048, 64, 100000), (1100, 72, 150777),
+                                            (8192, 64, 32001)])
+def test_adding_to_a_gradient_beside_grad_h(T, H, V, reduction):
+    """grad_W added to a given fp32 tensor with grad_h wanted in the same call, bf16 and fp32, of one piece
+    of the vocabulary and of several: grad_h as without adding, one fp32 addition per element of grad_W."""
+    import invariant_token_logprob_gb300 as rlk
+    h, W, t, w = (x.cuda() if x is not None else None for x in make(T, H, V, T + H, weighted=T > 3))
+    opts = dict(inv_temp=1.25, label_smoothing=0.1, z_loss=1e-4, reduction=reduction)
+    r = rlk.cross_entropy(h, W, t, w, **opts)
+    gen = torch.Generator().manual_seed(3)
+    g = torch.randn(T, generator=gen).cuda() if reduction == "none" else torch.tensor(0.3, device="cuda")
+    start = torch.randn(V, H, generator=gen).cuda() * 1e-3
+    full = rlk.cross_entropy_backward(h, W, t, r.lse, g, r.total, w, grad_dtype=torch.float32, **opts)
+    for dtype in (torch.bfloat16, torch.float32):
+        alone = rlk.cross_entropy_backward(h, W, t, r.lse, g, r.total, w, grad_dtype=dtype, **opts)
+        acc = start.clone()
+        gh, same = rlk.cross_entropy_backward(h, W, t, r.lse, g, r.total, w, grad_dtype=dtype, grad_W=acc, **opts)
+        assert same is acc and gh.dtype == dtype
+        assert torch.equal(gh, alone[0]) and torch.equal(acc, start + full[1])
+    assert rlk.take_device_errors() == (0, 0)
+
+
 def test_row_bits_do_not_depend_on_the_batch():
     import invariant_token_logprob_gb300 as rlk
     for H in (256, 1032):
