@@ -644,7 +644,7 @@ typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduc
  * whatever its hidden state, NaN included, and so is its gradient (a target >= V is reported as by
  * rlk_logprob).
  * A mean over rows whose weights' sum is not above 0 is 0.
- *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob
+ *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob; T H and V H <= 2^44
  *   weights_f32   device, [T], w, finite and >= 0; NULL: 1 for every row
  *   0 <= label_smoothing < 1, z_loss >= 0 and finite
  *   out_loss_f32  device, [T] for RLK_NONE, else one value
@@ -655,7 +655,8 @@ typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduc
  * rlk_logprob's, whose bits lse therefore does not have.  The bits of a row's lse and loss depend on
  * its hidden state, target and weight, W, V, H and the options only, as for rlk_logprob.  The sum
  * over rows is taken in an order fixed by T.  Asynchronous on `stream`; allocates nothing.  T == 0
- * writes 0 to the sums.
+ * writes 0 to the sums.  The workspace queries, here and below, answer 0 for T == 0 and for sizes that
+ * the calls refuse.
  */
 size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V);
 rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,

@@ -9,6 +9,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -961,10 +962,19 @@ namespace {
 
 bool valid_ratio(float e) { return e >= 0.0f && e < 1.0f; }
 
+// Shapes that the cross entropy takes: within the LM head's, hidden states and weight of up to 2^44
+// elements (so that no size below leaves 64 bits).
+rlk_status check_cross_entropy_shape(int64_t T, int64_t H, int64_t V, float inv_temp) {
+    rlk_status st = check_shape(T, H, V, inv_temp);
+    if (st != RLK_OK) return st;
+    if (std::max(T, V) > (int64_t(1) << 44) / H) return RLK_ERR_INVALID_ARG;
+    return RLK_OK;
+}
+
 // Checks shared by the cross entropy and its gradient (host values only).
 rlk_status check_cross_entropy(int64_t T, int64_t H, int64_t V, float inv_temp, float smoothing,
                                float z_loss, int reduction) {
-    rlk_status st = check_shape(T, H, V, inv_temp);
+    rlk_status st = check_cross_entropy_shape(T, H, V, inv_temp);
     if (st != RLK_OK) return st;
     if (!valid_ratio(smoothing) || !(z_loss >= 0.0f) || !isfinite(z_loss))
         return RLK_ERR_INVALID_ARG;
@@ -980,7 +990,7 @@ size_t ce_records(int64_t T, int64_t V) { return size_t(T) * 2 * size_t(num_voca
 }  // namespace
 
 size_t rlk_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V) {
-    if (T <= 0 || V <= 0 || H <= 0) return 0;
+    if (T == 0 || check_cross_entropy_shape(T, H, V, 1.0f) != RLK_OK) return 0;
     return ce_records(T, V) * sizeof(float2) + round16(ce_records(T, V) * sizeof(float)) +
            2 * round16(size_t(T) * sizeof(float)) + 16;
 }
@@ -1032,7 +1042,7 @@ rlk_status rlk_cross_entropy(const void* hidden_bf16, const void* weight_bf16,
 }
 
 size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V) {
-    if (T <= 0 || V <= 0 || H <= 0) return 0;
+    if (T == 0 || check_cross_entropy_shape(T, H, V, 1.0f) != RLK_OK) return 0;
     return rlk::ce_layout(T, H, rlk::ce_plan(T, H, V)).bytes + rlk::kCeAlign;
 }
 
@@ -1178,7 +1188,8 @@ rlk_status rlk_dequantize_int8(const int8_t* codes_i8, const float* scales_f32, 
 }
 
 size_t rlk_linear_int8_workspace_size(int64_t T, int64_t K) {
-    if (T <= 0 || K <= 0) return 0;
+    if (T <= 0 || T > INT32_MAX || K <= 0 || K > RLK_INT8_MAX_K) return 0;
+    if (K > (int64_t(1) << 39) / T) return 0;
     return round16(size_t(T) * size_t(K) * 2) + round16(size_t(T) * sizeof(float));
 }
 

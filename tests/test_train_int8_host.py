@@ -179,3 +179,35 @@ def test_plans(tmp_path, source):
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", csrc, str(src), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+REFUSED_SHAPES = [(-1, 64, 100), (0, 64, 100), (4, 64, 0), (4, 0, 100), (1 << 31, 64, 100), (4, 64, 1 << 31), (4, 1 << 31, 100),
+                  (4, 64, 1 << 60), (1 << 60, 64, 100), (1 << 62, 1 << 62, 1 << 62), (1 << 30, 64, 1 << 20),
+                  ((1 << 31) - 1, (1 << 31) - 8, 1), (1, (1 << 31) - 8, (1 << 31) - 1)]
+
+
+@pytest.mark.timeout(60)
+@pytest.mark.parametrize("T,H,V", REFUSED_SHAPES)
+def test_no_workspace_for_refused_shapes(L, T, H, V):
+    """Sizes that the calls refuse: the queries answer 0, at once."""
+    assert L.rlk_cross_entropy_workspace_size(T, H, V) == 0
+    assert L.rlk_cross_entropy_backward_workspace_size(T, H, V) == 0
+    if T != 0:
+        assert loss(L, T=T, H=H, V=V) == grad(L, T=T, H=H, V=V) == 1
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 8, (1 << 31) - 1), (1 << 20, 8192, 250000), ((1 << 31) - 1, 8, 1), (32768, 16384, 1 << 20)])
+def test_largest_shapes_have_a_workspace(L, T, H, V):
+    """What the loss keeps: 12 bytes per row and half tile, 8 per row; the gradient at least its dz and
+    its transpose's smallest piece, and h in fp16."""
+    halves = 2 * ((V + 255) // 256)
+    assert L.rlk_cross_entropy_workspace_size(T, H, V) >= 12 * T * halves + 8 * T
+    assert L.rlk_cross_entropy_backward_workspace_size(T, H, V) >= T * 256 * 4 + 6 * T * H
+
+
+@pytest.mark.parametrize("T,K", [(-1, 64), (0, 64), (4, 0), (1 << 31, 16), (4, 131072), (1 << 62, 1 << 62), (1 << 30, 4096)])
+def test_no_workspace_for_refused_products(L, T, K):
+    assert L.rlk_linear_int8_workspace_size(T, K) == 0
+    if T != 0:
+        assert linear(L, T=T, K=K) != 0
+    assert L.rlk_linear_int8_workspace_size(13, 131056) >= 13 * 131056 * 2 + 13 * 4
