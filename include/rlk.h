@@ -644,7 +644,8 @@ typedef enum rlk_reduction { RLK_MEAN = 0, RLK_SUM = 1, RLK_NONE = 2 } rlk_reduc
  * whatever its hidden state, NaN included, and so is its gradient (a target >= V is reported as by
  * rlk_logprob).
  * A mean over rows whose weights' sum is not above 0 is 0.
- *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob; T H and V H <= 2^44
+ *   hidden_bf16, weight_bf16, targets_i32, T, H, V, inv_temp: as rlk_logprob; T H and V H <= 2^44,
+ *                 inv_temp up to 2.358e38 (times log2 e within fp32's range)
  *   weights_f32   device, [T], w, finite and >= 0; NULL: 1 for every row
  *   0 <= label_smoothing < 1, z_loss >= 0 and finite
  *   out_loss_f32  device, [T] for RLK_NONE, else one value

@@ -976,6 +976,7 @@ rlk_status check_cross_entropy(int64_t T, int64_t H, int64_t V, float inv_temp, 
                                float z_loss, int reduction) {
     rlk_status st = check_cross_entropy_shape(T, H, V, inv_temp);
     if (st != RLK_OK) return st;
+    if (!isfinite(inv_temp * 1.44269504f)) return RLK_ERR_INVALID_ARG;  // (the exponentials' factor)
     if (!valid_ratio(smoothing) || !(z_loss >= 0.0f) || !isfinite(z_loss))
         return RLK_ERR_INVALID_ARG;
     if (reduction != RLK_MEAN && reduction != RLK_SUM && reduction != RLK_NONE)

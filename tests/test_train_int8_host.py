@@ -211,3 +211,15 @@ def test_no_workspace_for_refused_products(L, T, K):
     if T != 0:
         assert linear(L, T=T, K=K) != 0
     assert L.rlk_linear_int8_workspace_size(13, 131056) >= 13 * 131056 * 2 + 13 * 4
+
+
+@pytest.mark.parametrize("it,taken", [(2.358e38, True), (2.37e38, False), (3.4e38, False), (1e-45, True)])
+def test_largest_inverse_temperature(L, it, taken):
+    """The kernels' exponentials take logits times inv_temp log2 e, which has to be finite in fp32: behind
+    it every logit would be infinite or NaN, a row of zeros too."""
+    assert (grad(L, T=0, it=it, h=None, gW=None) == 0) == taken
+    assert loss(L, it=it, h=None) == grad(L, it=it, h=None) == 1
+    if not taken:
+        assert loss(L, T=0, it=it) == 1
+    if not torch.cuda.is_available():
+        assert (loss(L, it=it) == 3) == (grad(L, it=it) == 3) == taken
