@@ -66,6 +66,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "rlk_internal.h"
 #include "rlk_sm103.cuh"
@@ -652,7 +653,7 @@ bool encode_output(CUtensorMap* td, const Args& a, void* d_bf16) {
 // The launch of `kernel` in pairs of CTAs, and how many pairs are resident at once (found once per
 // device, into max_pairs[dev]).
 template <typename Kernel>
-cudaError_t pair_config(Kernel kernel, int* max_pairs, int num_sms, cudaStream_t stream,
+cudaError_t pair_config(Kernel kernel, std::atomic<int>* max_pairs, int num_sms, cudaStream_t stream,
                         cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int* pairs) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -670,21 +671,20 @@ cudaError_t pair_config(Kernel kernel, int* max_pairs, int num_sms, cudaStream_t
     cfg->stream = stream;
     cfg->attrs = attr;
     cfg->numAttrs = 2;
-    int& maxc = max_pairs[dev];
-    if (maxc == 0) {
+    int most = max_pairs[dev].load();
+    if (most == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kSmemBytes));
         if (e != cudaSuccess) return e;
         cfg->gridDim = dim3(2 * (num_sms / 2), 1, 1);
-        int nc = 0;
-        e = cudaOccupancyMaxActiveClusters(&nc, kernel, cfg);
-        if (e != cudaSuccess || nc < 1) {
+        e = cudaOccupancyMaxActiveClusters(&most, kernel, cfg);
+        if (e != cudaSuccess || most < 1) {
             cudaGetLastError();
-            nc = num_sms / 2;
+            most = num_sms / 2;
         }
-        maxc = nc;
+        max_pairs[dev].store(most);
     }
-    *pairs = maxc;
+    *pairs = most;
     return cudaSuccess;
 }
 
@@ -694,7 +694,7 @@ unsigned epilogue_threads(const Args& a) {
     return 64u + 32u * (blocks < kFewBlocks ? kEpiWarps : 4);
 }
 
-int g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
+std::atomic<int> g_max_clusters[16][64];  // co-resident CTA pairs per kernel variant and device
 
 template <bool kAMn, bool kBMn = true, bool kBf16 = false, bool kFp16 = false>
 cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, int num_sms,
@@ -718,7 +718,7 @@ cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, Args a, in
     return cudaGetLastError();
 }
 
-int g_max_pairs_two[4][64];
+std::atomic<int> g_max_pairs_two[4][64];
 
 // Time of a product's units on `pairs` pairs, in blocks of k: a unit takes no less than its epilogue.
 int64_t rounds_time(const Args& a, int pairs) {

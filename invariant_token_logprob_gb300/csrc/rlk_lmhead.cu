@@ -54,6 +54,8 @@
 #include <cuda_fp16.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "rlk_fp8_quant.cuh"
 #include "rlk_internal.h"
 #include "rlk_lse.cuh"
@@ -1118,8 +1120,8 @@ __global__ void __launch_bounds__(kMode >= kModeLoss ? kWideThreads : kThreads, 
 }
 
 struct VariantState {
-    int configured = 0;    // dynamic shared memory attribute set
-    int max_clusters = 0;  // CTA pairs that fit at once (CTA-pair variants)
+    std::atomic<int> configured{0};    // dynamic shared memory attribute set; behind max_clusters
+    std::atomic<int> max_clusters{0};  // CTA pairs that fit at once (CTA-pair variants)
 };
 VariantState g_variant[13][64];  // per kernel variant and device
 constexpr size_t kMaxSmemBytes = 227 * 1024;
@@ -1153,7 +1155,7 @@ cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const C
     cfg.attrs = attr;
     cfg.numAttrs = kPair ? 2 : 1;
 
-    if (!vs.configured) {
+    if (!vs.configured.load()) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kHq ? kMaxSmemBytes : P::kSmemBytes));
         if (e != cudaSuccess) return e;
@@ -1167,9 +1169,9 @@ cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const C
                 cudaGetLastError();
                 n = num_sms / 2;
             }
-            vs.max_clusters = n;
+            vs.max_clusters.store(n);
         }
-        vs.configured = 1;
+        vs.configured.store(1);
     }
     a.num_m = int((a.T + kBM - 1) / kBM);
     a.num_mu = kPair ? (a.num_m + 1) / 2 : a.num_m;
@@ -1178,7 +1180,8 @@ cudaError_t launch_variant(const CUtensorMap* th, const CUtensorMap* tw, const C
     a.band = kPair ? (a.num_mu < 16 ? a.num_mu : 16) : (a.num_mu < 32 ? a.num_mu : 32);
     a.num_tiles = a.num_mu * a.num_n;
     if constexpr (kPair) {
-        const int clusters = a.num_tiles < vs.max_clusters ? a.num_tiles : vs.max_clusters;
+        const int most = vs.max_clusters.load();
+        const int clusters = a.num_tiles < most ? a.num_tiles : most;
         cfg.gridDim = dim3(2 * clusters, 1, 1);
     } else {
         cfg.gridDim = dim3(a.num_tiles < num_sms ? a.num_tiles : num_sms, 1, 1);

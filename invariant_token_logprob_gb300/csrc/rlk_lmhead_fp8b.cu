@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "rlk_fp8_quant.cuh"
 #include "rlk_internal.h"
 #include "rlk_lse.cuh"
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-int g_configured[2][64];  // per variant (kHq) and device
+std::atomic<int> g_configured[2][64];  // per variant (kHq) and device
 
 template <bool kHq>
 cudaError_t launch_fp8b(const CUtensorMap* th, const CUtensorMap* tw, const Args& a, int num_sms,
@@ -503,11 +505,11 @@ cudaError_t launch_fp8b(const CUtensorMap* th, const CUtensorMap* tw, const Args
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     auto kernel = lmhead_fp8b_kernel<kHq>;
-    if (!g_configured[kHq ? 1 : 0][dev]) {
+    if (!g_configured[kHq ? 1 : 0][dev].load()) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(smem_bytes<kHq>()));
         if (e != cudaSuccess) return e;
-        g_configured[kHq ? 1 : 0][dev] = 1;
+        g_configured[kHq ? 1 : 0][dev].store(1);
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
