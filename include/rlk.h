@@ -724,8 +724,7 @@ rlk_status rlk_dequantize_int8(const int8_t *codes_i8, const float *scales_f32, 
  * fp32 and, behind the two fp32 products, once to out_dtype.  So a row's bits depend on that row
  * of x and on the channel only: not on T, N, K's cut or the device.  A bounded wait that runs
  * out is reported by rlk_check_device_error.  Callers that capture graphs make one call of each
- * class before (T up to 16, 32, 64, 128, more; out_dtype): the first sets its kernel's
- * shared-memory size.
+ * out_dtype before, with any T: the first sets the kernels' shared-memory sizes.
  *   x             device, [T][K] of x_dtype (RLK_BF16, RLK_FP16, RLK_FP32 or RLK_INT8), 16-byte
  *                 aligned
  *   x_scales_f32  device, [T] with RLK_INT8, else NULL

@@ -450,21 +450,37 @@ __global__ void __launch_bounds__(32 * int8_warps(kRoom), 1)
     }
 }
 
-template <typename Out, int kRoom>
-cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, int num_sms,
-                   cudaStream_t stream) {
-    auto kernel = linear_int8_kernel<Out, kRoom>;
-    constexpr size_t smem = int8_smem_bytes(kRoom);
+// The kernels of an output type may have their shared memory: set for every room by the type's first call
+// on a device, whichever room it takes (a call in a graph's capture then meets no kernel for the first time).
+template <typename Out>
+cudaError_t configure() {
     static std::atomic<int> configured[64];  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev].load()) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-        configured[dev].store(1);
-    }
+    if (configured[dev].load()) return cudaSuccess;
+    auto allow = [&](auto kernel, int room) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(int8_smem_bytes(room)));
+    };
+    allow(linear_int8_kernel<Out, 16>, 16);
+    allow(linear_int8_kernel<Out, 32>, 32);
+    allow(linear_int8_kernel<Out, 64>, 64);
+    allow(linear_int8_kernel<Out, 128>, 128);
+    allow(linear_int8_kernel<Out, 192>, 192);
+    if (e == cudaSuccess) configured[dev].store(1);
+    return e;
+}
+
+template <typename Out, int kRoom>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Args& p, int num_sms,
+                   cudaStream_t stream) {
+    auto kernel = linear_int8_kernel<Out, kRoom>;
+    constexpr size_t smem = int8_smem_bytes(kRoom);
+    cudaError_t e = configure<Out>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -298,3 +298,42 @@ def test_bounded_wait_runs_out_and_context_survives(mode):
     assert bool((y == 7).all())
     rlk.check_device_error()
     assert torch.equal(rlk.linear_int8(qx.cuda(), w, s, x_scales=xs).cpu(), ref_linear(qx, sx, qw, sw, "fp32"))
+
+
+CAPTURE = """
+import torch
+import invariant_token_logprob_gb300 as rlk
+g = torch.Generator().manual_seed(0)
+N, K = 300, 528
+codes, scales = rlk.quantize_int8(torch.randn(N, K, generator=g).cuda())
+rows = [1, 17, 40, 100, 192, 193, 200, 256, 257, 300, 400]
+xs = [torch.randint(-127, 128, (T, K), generator=g, dtype=torch.int8).cuda() for T in rows]
+ss = [torch.rand(T, generator=g).cuda() for T in rows]
+for dtype in (torch.float32, torch.bfloat16, torch.float16):
+    call = lambda i: rlk.linear_int8(xs[i], codes, scales, ss[i], out_dtype=dtype)
+    call(%d)  # the only call of this type before
+    graphs = []
+    for i in range(len(rows)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call(i)
+        graphs.append((graph, out))
+    for graph, _ in graphs:
+        graph.replay()
+    for i, (_, out) in enumerate(graphs):
+        assert torch.equal(out, call(i)), rows[i]
+assert rlk.take_device_errors() == (0, 0)
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("first", [0, 9])
+def test_one_call_of_a_type_before_a_capture(first):
+    """In a process of its own: one eager call per output type, of 1 or 300 rows, then captures with other
+    numbers of rows, the first calls with those."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE % first], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
