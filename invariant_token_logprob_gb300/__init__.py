@@ -784,14 +784,18 @@ def _workspace(call, size, device, stream):
     """A workspace of at least `size` bytes for one call.  A small one is kept, per thread, device
     and stream, as an allocation takes longer than a small call's checks (4 us on Grace): the calls of a
     thread on a stream run one after the other.  Not for a stream other than the current one, nor while it
-    is captured: a graph's launches must not share their memory with calls outside it."""
+    is captured: a graph's launches must not share their memory with calls outside it.  Nor for a stream
+    that torch has not made (its id is then its address): torch's live as long as the process and are few,
+    but another's address may be that of a later stream, whose work does not wait for the first one's."""
     torch = call.torch
-    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(call.device):
+    raw = torch._C._cuda_getCurrentRawStream(call.device)
+    if stream is not None and stream.cuda_stream != raw:
         return _empty(stream, max(16, size), dtype=torch.uint8, device=device)
-    if size > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
+    if (size > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing()
+            or (raw and torch._C._cuda_getCurrentStream(call.device)[0] == raw)):
         return torch.empty(max(16, size), dtype=torch.uint8, device=device)
     kept = _scratch.__dict__
-    key = call.device, torch._C._cuda_getCurrentRawStream(call.device)
+    key = call.device, raw
     workspace = kept.get(key)
     if workspace is None or workspace.shape[0] < size:
         workspace = torch.empty(max(1 << 16, 1 << (size - 1).bit_length()), dtype=torch.uint8, device=device)

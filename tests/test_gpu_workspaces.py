@@ -89,3 +89,24 @@ def test_graphs_and_eager_calls(made):
         assert torch.equal(eager, want[1]) and torch.equal(eager2, want[0])
         for (g, outs), w in zip(graphs, want[2:]):
             assert all(torch.equal(o, w) for o in outs)
+
+
+def test_streams_that_torch_has_not_made(made):
+    """A stream given by its address alone may be gone, and its address another stream's, by the next call:
+    no workspace is kept for it; torch's own streams have one each."""
+    import invariant_token_logprob_gb300 as rlk
+    codes, scales, xs, want = made
+    rlk._scratch.__dict__.clear()
+    own = torch.cuda.Stream()
+    other = torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream)
+    for stream in (other, own, torch.cuda.default_stream()):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            got = [rlk.linear_int8(x, codes, scales) for x in xs]
+            got += [rlk.linear_int8(x, codes, scales, stream=stream) for x in xs]
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, 2 * want))
+    got = [rlk.linear_int8(x, codes, scales, stream=other) for x in xs]
+    other.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert {raw for _, raw in rlk._scratch.__dict__} == {own.cuda_stream, 0}
