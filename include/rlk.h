@@ -687,8 +687,10 @@ rlk_status rlk_cross_entropy(const void *hidden_bf16, const void *weight_bf16,
  *   accumulate_grad_weight != 0: grad_weight, of RLK_FP32, is added to
  *   workspace            device, 16-byte aligned,
  *                        >= rlk_cross_entropy_backward_workspace_size bytes
+ * fp32 outputs hold these roundings too.
  * Other arguments as given to rlk_cross_entropy.  Asynchronous on `stream`; allocates nothing.
- * T == 0 sets an overwritten grad_weight to 0.
+ * T == 0 sets an overwritten grad_weight to 0.  Callers that capture graphs make the same call, of the
+ * same sizes and types, before: which kernels run follows from them.
  */
 size_t rlk_cross_entropy_backward_workspace_size(int64_t T, int64_t H, int64_t V);
 rlk_status rlk_cross_entropy_backward(

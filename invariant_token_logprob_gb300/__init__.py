@@ -1167,8 +1167,8 @@ def cross_entropy_backward(h, W, targets, lse, grad_loss, total=None, weights=No
                            stream=None):
     """rlk_cross_entropy_backward: (grad_h [T, H] or None, grad_W [V, H] or None) from the
     gradient of cross_entropy's loss (f32, a scalar, or [T] for reduction 'none') and its lse
-    and total (needed for 'mean').  The gradients are bf16 (or float32: grad_dtype); pass grad_W
-    (float32) to add to it instead."""
+    and total (needed for 'mean').  The gradients are bf16 (or float32: grad_dtype, in which the logits'
+    gradient, an operand of 16 bits, still has its rounding); pass grad_W (float32) to add to it instead."""
     call = _Call()
     torch = call.torch
     f32 = torch.float32

@@ -30,9 +30,9 @@
 // Warp roles as in the LM-head kernel: TMA producer, single-thread MMA issuer,
 // four epilogue warps (a thread has a row: TMEM -> registers -> alpha * acc), or eight (half a row
 // each) for units of fewer than 16 blocks of k, whose time is their output's: T = 64, H = 4096,
-// V = 151936 in bf16, 310 us with four, 298 with eight; a memset of the same 1.24 GB takes 305.  Over
-// more k eight only draw power: T = 4096, the whole backward, 9.25 ms with eight, 9.10 with four; T = 512
-// (8 blocks) 349 and 341 us, T = 1024 (16) 507 and 518.
+// V = 151936 in bf16, 310 us with four, 298 with eight (the 1.24 GB alone take 183).  Over more k eight
+// only draw power: T = 4096, the whole backward called back to back, 9.25 ms with eight, 9.10 with four;
+// T = 512 (8 blocks) 349 and 341 us, T = 1024 (16) 507 and 518.
 // The epilogue stages each warp's 32 x 32 block in shared memory and writes it
 // with one tiled bulk store (full 128-byte lines; scattered per-thread 16-byte
 // stores measured 2x the crossbar traffic); when adding to D it loads, adds
@@ -53,8 +53,9 @@
 // (staged in 64-column blocks: by 32-byte register stores 339 us instead of 298 at T = 64) or fp32.
 // Where their units leave pairs idle at the ends, one launch runs both products side by side, its
 // pairs divided by the estimate in pairs_for_first.  At T = 4096, H = 4096, V = 151936 the whole
-// backward takes 8.65-8.98 ms, 1.70-1.75 PFLOP/s over its 6 T H V operations; at T = 1024 grad_W has
-// the tensor pipe 75% busy, grad_h 89%.
+// backward takes 8.4-8.8 ms in a graph (1.74-1.82 PFLOP/s over its 6 T H V operations) and 9.0-9.2 ms a
+// call on inputs that change, at the power limit either way; at T = 1024 grad_W has the tensor pipe 75%
+// busy, grad_h 89%.
 //
 // Failure handling: every wait is bounded in time.  When a wait runs out the
 // kernel records it in a per-device error word and both CTAs of a pair drain

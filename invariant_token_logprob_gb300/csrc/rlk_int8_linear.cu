@@ -32,7 +32,7 @@
 // A product of N columns takes about 60 + N/4 cycles here (A from tensor memory), so tiles are as
 // wide as fit: 160 columns, with three buffers of numbers, were slower at T = 4096.
 // Measured (codes rotated past L2; us), N = 151936, K = 4096: T = 1 94 (6.6 TB/s, 0.97 of a copy),
-// 16 99, 32 101, 64 112, 128 143; N = 16384, K = 4096: T = 512 64, T = 4096 339 (1.62 PFLOP/s,
+// 16 99, 32 101, 64 112-114, 128 143; N = 16384, K = 4096: T = 512 64, T = 4096 339 (1.62 PFLOP/s,
 // 0.86 of the measured bf16 rate); N = K = 4096: T = 4096 104.  By dot products of codes on the CUDA
 // cores: T = 1 196, T = 64 2149, T = 4096 21735.
 #include <atomic>

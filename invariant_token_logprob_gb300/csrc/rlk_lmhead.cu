@@ -46,10 +46,10 @@
 // two epilogue warps share a quadrant of TMEM lanes, 128 columns each, and use packed fp32 arithmetic.
 // Mode 3 takes the accumulator out every 512 k (kLossPartKb), so that its epilogue runs H/512 times
 // per tile; with four warps and scalar arithmetic it, not the tensor core, set the pace (T = 4096,
-// H = 4096, V = 151936: 3.04 ms, so 2.69, the floor at the measured bf16 rate; a whole-K accumulator
-// has 10 times the error).  Mode 4 writes dz in whole 32-byte sectors from registers and its
+// H = 4096, V = 151936: 3.04 ms, so 2.5-2.8 in a graph and 2.9-3.0 a call; the floor at the measured bf16
+// rate is 2.69; a whole-K accumulator has 10 times the error).  Mode 4 writes dz in whole 32-byte sectors from registers and its
 // transpose by tiled stores from two blocks per warp in turn (T = 1024, H = 1024, V = 32768, the
-// whole backward: 182 -> 166 us; T = 1024, H = 4096: 163 us under ncu, tensor pipe 81% of active).
+// whole backward: 182 -> 160-166 us; T = 1024, H = 4096: 163 us under ncu, tensor pipe 81% of active).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
